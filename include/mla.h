@@ -322,6 +322,107 @@ int mla_decode_sparse(const mla_dims* dims, const void* q_nope, const void* q_pe
                       float softmax_scale, int32_t num_splits, void* workspace, size_t workspace_bytes,
                       void* out, float* lse_out, mla_stream_t stream);
 
+/*
+ * mla_cache_read -- read cached rows back out of their pages, dequantised to
+ * bf16: the inverse of mla_cache_append for the rows of a packed batch ("KV
+ * Cache Optimization", section 3: x = scale * (code - zero point); "The
+ * Architecture of Memory", "PagedAttention").  With mla_expand_kv it turns a
+ * cached prefix into the keys and values of mla_prompt_attention.
+ *
+ * Row r of the outputs belongs to the sequence b with cu_rows[b] <= r <
+ * cu_rows[b + 1] and is the cached row at position starts[b] + r - cu_rows[b].
+ *
+ *   cache, cache_scale_zero, block_table  as for mla_cache_append
+ *   starts      optional int32 [num_seqs] (device): first position read of
+ *               each sequence; NULL: 0
+ *   cu_rows     int32 [num_seqs + 1] (device): non-decreasing offsets of the
+ *               sequences in the packed rows; equal neighbours are an empty
+ *               sequence
+ *   n_rows      rows of the outputs; 0 is a no-op
+ *   c_kv        bf16 [n_rows, 512] latents;  k_pe bf16 [n_rows, 64] RoPE keys
+ *               (rotated, as the append stored them); both 16-byte aligned.
+ *               bf16 caches are copied bit for bit; 1-byte caches are
+ *               dequantised in fp32 and rounded once to bf16.
+ *   device_status  optional int32 (device); a row whose position or page-table
+ *               entry is out of range is left as it was, and that, decreasing
+ *               offsets, or offsets outside [0, n_rows] store
+ *               MLA_ERR_DEVICE_BOUNDS here.
+ * Rows before cu_rows[0] and from cu_rows[num_seqs] on are left as they were.
+ */
+int mla_cache_read(const mla_dims* dims, const void* cache, const float* cache_scale_zero, int32_t num_pages,
+                   const int32_t* block_table, int32_t num_seqs, int32_t max_pages_per_seq, const int32_t* starts,
+                   const int32_t* cu_rows, int32_t n_rows, void* c_kv, void* k_pe, int32_t* device_status,
+                   mla_stream_t stream);
+
+/*
+ * mla_expand_kv -- latents to per-head keys and values, the un-absorbed form
+ * ("Beyond the Attention Bottleneck", "Down-Projection and Up-Projection
+ * Mechanics": K_t = W^UK c_t, V_t = W^UV c_t):
+ *   k_nope[n][h] = W_UK[h] c_kv[n],  v[n][h] = W_UV[h] c_kv[n]
+ * accumulated in fp32 and rounded once to bf16.
+ *
+ *   c_kv        bf16 [n_rows, 512] (new latents, or mla_cache_read's)
+ *   W_UK, W_UV  bf16 [H, 128, 512]
+ *   k_nope, v   bf16 [n_rows, H, 128]
+ *   n_rows      n_rows * H <= MLA_MAX_QUERY_ROWS; 0 is a no-op
+ *   device_status  optional int32 (device): MLA_ERR_DEVICE_TIMEOUT is stored
+ *               here if a bounded wait runs out
+ * All pointers to tensors 16-byte aligned.
+ */
+int mla_expand_kv(const mla_dims* dims, const void* c_kv, int32_t n_rows, const void* W_UK, const void* W_UV,
+                  void* k_nope, void* v, int32_t* device_status, mla_stream_t stream);
+
+/* Largest number of sequences of one mla_prompt_attention call. */
+#define MLA_MAX_PROMPT_SEQS (1 << 20)
+
+/* Bytes of workspace mla_prompt_attention needs for (dims, num_seqs, n_q); 0
+ * if the arguments are invalid. */
+size_t mla_prompt_attention_workspace_size(const mla_dims* dims, int32_t num_seqs, int32_t n_q);
+
+/*
+ * mla_prompt_attention -- causal attention over packed prompts of different
+ * lengths in the un-absorbed form ("The Architecture of Memory", "The Prefill
+ * Phase"; "Beyond the Attention Bottleneck", "Down-Projection and
+ * Up-Projection Mechanics" and "The RoPE Compatibility Problem"): 320
+ * multiply-adds per query, key and head where mla_prefill's absorbed form
+ * takes 1,088, for keys and values that mla_expand_kv made (or any others of
+ * this shape, with grouped heads).
+ *
+ * Sequence b has the query rows cu_q[b] .. cu_q[b + 1] - 1 and the key rows
+ * cu_k[b] .. cu_k[b + 1] - 1 (Lq and Lk of them).  Its queries are its last Lq
+ * positions: query t (from 0) sees the keys 0 .. t + Lk - Lq of its sequence,
+ * none if that is negative.  For head h with g = h / (H / num_kv_heads):
+ *   s_j = softmax_scale * (q_nope[i][h] . k_nope[j][g] + q_pe[i][h] . k_pe[j])
+ *   out[i][h] = sum_j softmax(s)_j v[j][g],  lse[i][h] = ln sum_j exp(s_j)
+ * A query that sees no key gets out = 0 and lse = -inf.
+ *
+ *   q_nope      bf16 [n_q, H, 128];  q_pe bf16 [n_q, H, 64], rotated
+ *   k_nope      bf16 [n_k, num_kv_heads, 128];  k_pe bf16 [n_k, 64], rotated,
+ *               shared by all heads;  v bf16 [n_k, num_kv_heads, 128]
+ *   n_q, n_k    rows of the query and key tensors, 0 included;
+ *               n_q * H and n_k * num_kv_heads <= MLA_MAX_QUERY_ROWS
+ *   num_kv_heads  a divisor of H
+ *   cu_q, cu_k  int32 [num_seqs + 1] (device): non-decreasing offsets within
+ *               [0, n_q] and [0, n_k].  The first sequence that breaks this,
+ *               and every one after it, is skipped and
+ *               MLA_ERR_DEVICE_BOUNDS is recorded.
+ *   workspace   device scratch, 256-byte aligned, at least
+ *               mla_prompt_attention_workspace_size bytes; its first 4 bytes
+ *               hold the device status of this call
+ *   out         bf16 [n_q, H, 128];  lse_out optional fp32 [n_q, H]
+ * Rows of no sequence (before cu_q[0], from cu_q[num_seqs] on, or skipped) are
+ * left as they were, and no row of another sequence or of none ever reaches a
+ * result, whatever it holds.  Within a sequence a NaN or infinity in a key
+ * reaches only the queries that see it; one in a value may also reach the
+ * queries up to 127 positions before it.  Tensors are 16-byte aligned.
+ * Results are bit-identical between runs; calls sharing one workspace must not
+ * overlap on the device.  dims' page_size and cache_dtype are not used.
+ */
+int mla_prompt_attention(const mla_dims* dims, const void* q_nope, const void* q_pe, int32_t n_q, const void* k_nope,
+                         const void* k_pe, const void* v, int32_t n_k, int32_t num_kv_heads, const int32_t* cu_q,
+                         const int32_t* cu_k, int32_t num_seqs, float softmax_scale, void* workspace,
+                         size_t workspace_bytes, void* out, float* lse_out, mla_stream_t stream);
+
 /* Size of the fixed scratch array used by mla_decode_no_alloc. */
 #define MLA_NO_ALLOC_WORKSPACE_BYTES (16u << 20)
 

@@ -19,11 +19,12 @@ from . import build as _build
 __all__ = [
     "MLAError", "Dims", "dims", "load_library", "check_dims", "cache_append", "auto_num_splits",
     "decode_workspace_size", "decode", "decode_multi_workspace_size", "decode_multi", "decode_sparse_workspace_size",
-    "decode_sparse", "decode_no_alloc", "combine", "read_device_status", "read_status_word",
+    "decode_sparse", "cache_read", "expand_kv", "prompt_attention_workspace_size", "prompt_attention",
+    "decode_no_alloc", "combine", "read_device_status", "read_status_word",
     "set_timing_events", "status_string", "version",
     "MLA_OK", "MLA_ERR_INVALID_ARG", "MLA_ERR_UNSUPPORTED", "MLA_ERR_WORKSPACE", "MLA_ERR_CUDA",
     "MLA_ERR_DEVICE_TIMEOUT", "MLA_ERR_DEVICE_BOUNDS", "MLA_CACHE_BF16", "MLA_CACHE_INT8", "MLA_CACHE_FP8",
-    "MAX_Q_LEN", "MAX_TOP_K", "MAX_PREFILL_CHUNK",
+    "MAX_Q_LEN", "MAX_TOP_K", "MAX_PREFILL_CHUNK", "MAX_PROMPT_SEQS",
 ]
 
 MLA_OK = 0
@@ -39,6 +40,7 @@ MLA_CACHE_FP8 = 2
 MAX_Q_LEN = 8  # MLA_MAX_Q_LEN in include/mla.h
 MAX_PREFILL_CHUNK = 2048  # MLA_MAX_PREFILL_CHUNK in include/mla.h
 MAX_TOP_K = 1 << 20  # MLA_MAX_TOP_K in include/mla.h
+MAX_PROMPT_SEQS = 1 << 20  # MLA_MAX_PROMPT_SEQS in include/mla.h
 
 # every function include/mla.h declares
 EXPORTED_SYMBOLS = (
@@ -47,7 +49,8 @@ EXPORTED_SYMBOLS = (
     "mla_status_string", "mla_set_timing_events", "mla_version", "mla_decode_no_alloc",
     "mla_test_inject_wait_timeout", "mla_decode_multi_workspace_size", "mla_decode_multi",
     "mla_decode_sparse_workspace_size", "mla_decode_sparse", "mla_test_force_single_cta",
-    "mla_prefill_workspace_size", "mla_prefill",
+    "mla_prefill_workspace_size", "mla_prefill", "mla_cache_read", "mla_expand_kv",
+    "mla_prompt_attention_workspace_size", "mla_prompt_attention",
 )
 NO_ALLOC_WORKSPACE_BYTES = 16 << 20  # MLA_NO_ALLOC_WORKSPACE_BYTES in include/mla.h
 
@@ -118,6 +121,11 @@ def load_library(build_if_missing: bool = False, path: str | None = None):
         "mla_prefill_workspace_size": (ctypes.c_size_t, [DP, _I, _I, _I]),
         "mla_prefill": (_I, [DP, _P, _P, _I, _P, _I, _P, _I, _I, _P, _P, ctypes.c_double, _P, _P, _P, _P,
                              ctypes.c_float, _I, _P, ctypes.c_size_t, _P, _P, _P]),
+        "mla_cache_read": (_I, [DP, _P, _P, _I, _P, _I, _I, _P, _P, _I, _P, _P, _P, _P]),
+        "mla_expand_kv": (_I, [DP, _P, _I, _P, _P, _P, _P, _P, _P]),
+        "mla_prompt_attention_workspace_size": (ctypes.c_size_t, [DP, _I, _I]),
+        "mla_prompt_attention": (_I, [DP, _P, _P, _I, _P, _P, _P, _I, _I, _P, _P, _I, ctypes.c_float, _P,
+                                      ctypes.c_size_t, _P, _P, _P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -342,6 +350,132 @@ def decode_sparse(d: Dims, q_nope, q_pe, cache, scale_zero, block_table, seq_len
         int(num_splits), _ptr(workspace, None, "workspace", dev), workspace.numel() * workspace.element_size(),
         _ptr(out, torch.bfloat16, "out", dev), _ptr(lse_out, torch.float32, "lse_out", dev), _stream(stream))
     _check(st, "mla_decode_sparse")
+    return out, lse_out
+
+
+def _rows(t: torch.Tensor, shape: tuple, name: str):
+    """Check a tensor's shape; None in ``shape`` matches any size."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != len(shape) or any(want is not None and have != want for have, want in zip(t.shape, shape)):
+        want = ", ".join("*" if n is None else str(n) for n in shape)
+        raise ValueError(f"{name} must have shape [{want}], got {list(t.shape)}")
+
+
+def _call_on(dev: torch.device, stream, call) -> int:
+    """call(stream pointer) with ``dev`` current, on ``stream`` or dev's current stream."""
+    if dev.type != "cuda":
+        raise ValueError(f"tensors must be CUDA tensors, got {dev}")
+    if dev.index == torch.cuda.current_device():
+        return call(_stream(stream))
+    with torch.cuda.device(dev):
+        return call(_stream(stream))
+
+
+def cache_read(d: Dims, cache: torch.Tensor, scale_zero: torch.Tensor | None, block_table: torch.Tensor,
+               cu_rows: torch.Tensor, starts: torch.Tensor | None = None, n_rows: int | None = None,
+               c_kv: torch.Tensor | None = None, k_pe: torch.Tensor | None = None,
+               device_status: torch.Tensor | None = None, stream=None):
+    """mla_cache_read: the cached rows of a packed batch, dequantised to bf16.
+    Sequence b's rows are cu_rows[b] .. cu_rows[b + 1] - 1 of the outputs, read
+    from position starts[b] (0 without ``starts``) on.  Returns (c_kv bf16
+    [n_rows, 512], k_pe bf16 [n_rows, 64]); ``n_rows`` may be left out where
+    an output is given."""
+    dev = cache.device
+    B = block_table.shape[0]
+    _rows(cu_rows, (B + 1,), "cu_rows")
+    if starts is not None:
+        _rows(starts, (B,), "starts")
+    if n_rows is None:
+        given = c_kv if c_kv is not None else k_pe
+        if given is None:
+            raise ValueError("n_rows is needed where neither c_kv nor k_pe is given")
+        n_rows = given.shape[0]
+    _rows(cache, (None, d.page_size, d.kv_lora_rank + d.rope_dim), "cache")
+    if scale_zero is not None and d.cache_dtype != MLA_CACHE_BF16:
+        _rows(scale_zero, tuple(cache.shape[:2]) + ((2,) if d.cache_dtype == MLA_CACHE_INT8 else ()), "scale_zero")
+    if c_kv is None:
+        c_kv = torch.empty((n_rows, d.kv_lora_rank), dtype=torch.bfloat16, device=dev)
+    if k_pe is None:
+        k_pe = torch.empty((n_rows, d.rope_dim), dtype=torch.bfloat16, device=dev)
+    _rows(c_kv, (n_rows, d.kv_lora_rank), "c_kv")
+    _rows(k_pe, (n_rows, d.rope_dim), "k_pe")
+    args = (ctypes.byref(d), *_cache_ptrs(d, cache, scale_zero, dev), cache.shape[0],
+            _ptr(block_table, torch.int32, "block_table", dev), B, block_table.shape[1],
+            _ptr(starts, torch.int32, "starts", dev), _ptr(cu_rows, torch.int32, "cu_rows", dev), int(n_rows),
+            _ptr(c_kv, torch.bfloat16, "c_kv", dev), _ptr(k_pe, torch.bfloat16, "k_pe", dev),
+            _ptr(device_status, torch.int32, "device_status", dev))
+    _check(_call_on(dev, stream, lambda s: _L().mla_cache_read(*args, s)), "mla_cache_read")
+    return c_kv, k_pe
+
+
+def expand_kv(d: Dims, c_kv: torch.Tensor, W_UK: torch.Tensor, W_UV: torch.Tensor, k_nope: torch.Tensor | None = None,
+              v: torch.Tensor | None = None, device_status: torch.Tensor | None = None, stream=None):
+    """mla_expand_kv: latents c_kv bf16 [n, 512] to per-head keys and values.
+    Returns (k_nope bf16 [n, H, 128], v bf16 [n, H, 128])."""
+    dev = c_kv.device
+    H = d.num_heads
+    _rows(c_kv, (None, d.kv_lora_rank), "c_kv")
+    _rows(W_UK, (H, d.qk_nope_dim, d.kv_lora_rank), "W_UK")
+    _rows(W_UV, (H, d.v_head_dim, d.kv_lora_rank), "W_UV")
+    n = c_kv.shape[0]
+    if k_nope is None:
+        k_nope = torch.empty((n, H, d.qk_nope_dim), dtype=torch.bfloat16, device=dev)
+    if v is None:
+        v = torch.empty((n, H, d.v_head_dim), dtype=torch.bfloat16, device=dev)
+    _rows(k_nope, (n, H, d.qk_nope_dim), "k_nope")
+    _rows(v, (n, H, d.v_head_dim), "v")
+    args = (ctypes.byref(d), _ptr(c_kv, torch.bfloat16, "c_kv"), n, _ptr(W_UK, torch.bfloat16, "W_UK", dev),
+            _ptr(W_UV, torch.bfloat16, "W_UV", dev), _ptr(k_nope, torch.bfloat16, "k_nope", dev),
+            _ptr(v, torch.bfloat16, "v", dev), _ptr(device_status, torch.int32, "device_status", dev))
+    _check(_call_on(dev, stream, lambda s: _L().mla_expand_kv(*args, s)), "mla_expand_kv")
+    return k_nope, v
+
+
+def prompt_attention_workspace_size(d: Dims, num_seqs: int, n_q: int) -> int:
+    n = _L().mla_prompt_attention_workspace_size(ctypes.byref(d), int(num_seqs), int(n_q))
+    if n == 0:
+        raise MLAError(MLA_ERR_INVALID_ARG, "mla_prompt_attention_workspace_size")
+    return n
+
+
+def prompt_attention(d: Dims, q_nope: torch.Tensor, q_pe: torch.Tensor, k_nope: torch.Tensor, k_pe: torch.Tensor,
+                     v: torch.Tensor, cu_q: torch.Tensor, cu_k: torch.Tensor, softmax_scale: float,
+                     workspace: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                     lse_out: torch.Tensor | None = None, want_lse: bool = True, stream=None):
+    """mla_prompt_attention: causal attention of packed queries q_nope bf16
+    [n_q, H, 128], q_pe [n_q, H, 64] over packed keys k_nope bf16 [n_k, H_kv,
+    128], k_pe [n_k, 64] and values v [n_k, H_kv, 128]; sequence b has the
+    query rows cu_q[b] .. cu_q[b + 1] - 1 and the key rows cu_k[b] ..
+    cu_k[b + 1] - 1, its queries being its last positions.  Returns (out bf16
+    [n_q, H, 128], lse fp32 [n_q, H] or None)."""
+    dev = q_nope.device
+    H = d.num_heads
+    _rows(q_nope, (None, H, d.qk_nope_dim), "q_nope")
+    _rows(k_nope, (None, None, d.qk_nope_dim), "k_nope")
+    n_q, n_k, kv_heads = q_nope.shape[0], k_nope.shape[0], k_nope.shape[1]
+    _rows(q_pe, (n_q, H, d.rope_dim), "q_pe")
+    _rows(k_pe, (n_k, d.rope_dim), "k_pe")
+    _rows(v, (n_k, kv_heads, d.v_head_dim), "v")
+    B = cu_q.shape[0] - 1
+    _rows(cu_q, (B + 1,), "cu_q")
+    _rows(cu_k, (B + 1,), "cu_k")
+    if workspace is None:
+        workspace = torch.empty(prompt_attention_workspace_size(d, B, n_q), dtype=torch.uint8, device=dev)
+    if out is None:
+        out = torch.empty((n_q, H, d.v_head_dim), dtype=torch.bfloat16, device=dev)
+    if lse_out is None and want_lse:
+        lse_out = torch.empty((n_q, H), dtype=torch.float32, device=dev)
+    _rows(out, (n_q, H, d.v_head_dim), "out")
+    if lse_out is not None:
+        _rows(lse_out, (n_q, H), "lse_out")
+    args = (ctypes.byref(d), _ptr(q_nope, torch.bfloat16, "q_nope"), _ptr(q_pe, torch.bfloat16, "q_pe", dev), n_q,
+            _ptr(k_nope, torch.bfloat16, "k_nope", dev), _ptr(k_pe, torch.bfloat16, "k_pe", dev),
+            _ptr(v, torch.bfloat16, "v", dev), n_k, kv_heads, _ptr(cu_q, torch.int32, "cu_q", dev),
+            _ptr(cu_k, torch.int32, "cu_k", dev), B, float(softmax_scale), _ptr(workspace, None, "workspace", dev),
+            workspace.numel() * workspace.element_size(), _ptr(out, torch.bfloat16, "out", dev),
+            _ptr(lse_out, torch.float32, "lse_out", dev))
+    _check(_call_on(dev, stream, lambda s: _L().mla_prompt_attention(*args, s)), "mla_prompt_attention")
     return out, lse_out
 
 

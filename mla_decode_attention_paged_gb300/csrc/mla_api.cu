@@ -404,6 +404,23 @@ SparseLayout sparse_layout(const mla_dims* d, int batch, int top_k, size_t decod
   return L;
 }
 
+// Workspace of mla_prompt_attention: the status word and item count, the
+// first block of every sequence, the list of items (a sequence of n rows has
+// at most n / 256 + 1 blocks).
+struct PromptLayout {
+  size_t status, block_start, items, total;
+};
+
+PromptLayout prompt_layout(int num_seqs, int n_q) {
+  PromptLayout L;
+  size_t off = 0;
+  L.status = off;       off = align256(off + 8);
+  L.block_start = off;  off = align256(off + 4 * (size_t(num_seqs) + 1));
+  L.items = off;        off = align256(off + sizeof(PromptItem) * (size_t(n_q) / 256 + num_seqs));
+  L.total = off;
+  return L;
+}
+
 }  // namespace
 
 extern "C" {
@@ -465,6 +482,117 @@ int mla_decode_sparse(const mla_dims* d, const void* q_nope, const void* q_pe, c
   return decode_rows(d, q_nope, q_pe, gp.out_cache, gp.out_scale_zero, batch * L.pps, gp.out_table, L.pps,
                      gp.out_lens, batch, 1, W_UK, W_UV, softmax_scale, num_splits, ws + L.decode, dec, out, lse_out,
                      stream, false);
+}
+
+int mla_cache_read(const mla_dims* d, const void* cache, const float* cache_scale_zero, int32_t num_pages,
+                   const int32_t* block_table, int32_t num_seqs, int32_t max_pages_per_seq, const int32_t* starts,
+                   const int32_t* cu_rows, int32_t n_rows, void* c_kv, void* k_pe, int32_t* device_status,
+                   mla_stream_t stream) {
+  int st = mla_check_dims(d);
+  if (st != MLA_OK) return st;
+  if (n_rows < 0 || num_pages <= 0 || num_seqs <= 0 || max_pages_per_seq <= 0) return MLA_ERR_INVALID_ARG;
+  if (n_rows == 0) return MLA_OK;
+  const int code = cache_code(d);
+  const bool byte = code != kCodeBf16;
+  if (!cache || !block_table || !cu_rows || !c_kv || !k_pe || (byte && !cache_scale_zero)) return MLA_ERR_INVALID_ARG;
+  if (!aligned(cache, 16) || !aligned(c_kv, 16) || !aligned(k_pe, 16) || !aligned(block_table, 4) ||
+      !aligned(cu_rows, 4) || (starts && !aligned(starts, 4)) || (device_status && !aligned(device_status, 4)) ||
+      (byte && !aligned(cache_scale_zero, 8)))
+    return MLA_ERR_INVALID_ARG;
+  CacheReadParams p;
+  p.cache = cache;
+  p.scale_zero = cache_scale_zero;
+  p.block_table = block_table;
+  p.starts = starts;
+  p.cu_rows = cu_rows;
+  p.c_kv = static_cast<__nv_bfloat16*>(c_kv);
+  p.k_pe = static_cast<__nv_bfloat16*>(k_pe);
+  p.status = device_status;
+  p.num_seqs = num_seqs;
+  p.max_pages = max_pages_per_seq;
+  p.num_pages = num_pages;
+  p.page_size = d->page_size;
+  p.n_rows = n_rows;
+  return launch_cache_read(p, code, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+int mla_expand_kv(const mla_dims* d, const void* c_kv, int32_t n_rows, const void* W_UK, const void* W_UV,
+                  void* k_nope, void* v, int32_t* device_status, mla_stream_t stream) {
+  int st = mla_check_dims(d);
+  if (st != MLA_OK) return st;
+  if (n_rows < 0) return MLA_ERR_INVALID_ARG;
+  if (n_rows == 0) return MLA_OK;
+  if ((long long)n_rows * d->num_heads > kMaxQueryRows) return MLA_ERR_INVALID_ARG;
+  if (!c_kv || !W_UK || !W_UV || !k_nope || !v) return MLA_ERR_INVALID_ARG;
+  if (!aligned(c_kv, 16) || !aligned(W_UK, 16) || !aligned(W_UV, 16) || !aligned(k_nope, 16) || !aligned(v, 16) ||
+      (device_status && !aligned(device_status, 4)))
+    return MLA_ERR_INVALID_ARG;
+  ExpandParams p;
+  p.c_kv = static_cast<const __nv_bfloat16*>(c_kv);
+  p.W_UK = static_cast<const __nv_bfloat16*>(W_UK);
+  p.W_UV = static_cast<const __nv_bfloat16*>(W_UV);
+  p.k_nope = static_cast<__nv_bfloat16*>(k_nope);
+  p.v = static_cast<__nv_bfloat16*>(v);
+  p.status = device_status;
+  p.n_rows = n_rows;
+  p.heads = d->num_heads;
+  p.sm_count = sm_count();
+  if (p.sm_count <= 0) return MLA_ERR_CUDA;
+  return launch_expand(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+size_t mla_prompt_attention_workspace_size(const mla_dims* d, int32_t num_seqs, int32_t n_q) {
+  if (mla_check_dims(d) != MLA_OK || num_seqs <= 0 || num_seqs > MLA_MAX_PROMPT_SEQS || n_q < 0) return 0;
+  if ((long long)n_q * d->num_heads > kMaxQueryRows) return 0;
+  return prompt_layout(num_seqs, n_q).total;
+}
+
+int mla_prompt_attention(const mla_dims* d, const void* q_nope, const void* q_pe, int32_t n_q, const void* k_nope,
+                         const void* k_pe, const void* v, int32_t n_k, int32_t num_kv_heads, const int32_t* cu_q,
+                         const int32_t* cu_k, int32_t num_seqs, float softmax_scale, void* workspace,
+                         size_t workspace_bytes, void* out, float* lse_out, mla_stream_t stream) {
+  int st = mla_check_dims(d);
+  if (st != MLA_OK) return st;
+  if (n_q < 0 || n_k < 0 || num_seqs <= 0 || num_seqs > MLA_MAX_PROMPT_SEQS) return MLA_ERR_INVALID_ARG;
+  if (num_kv_heads <= 0 || num_kv_heads > d->num_heads || d->num_heads % num_kv_heads != 0) return MLA_ERR_INVALID_ARG;
+  if ((long long)n_q * d->num_heads > kMaxQueryRows || (long long)n_k * num_kv_heads > kMaxQueryRows)
+    return MLA_ERR_INVALID_ARG;
+  if (!(softmax_scale > 0.f) || softmax_scale == INFINITY) return MLA_ERR_INVALID_ARG;
+  if (!cu_q || !cu_k || !aligned(cu_q, 4) || !aligned(cu_k, 4)) return MLA_ERR_INVALID_ARG;
+  if (n_q > 0 && (!q_nope || !q_pe || !out)) return MLA_ERR_INVALID_ARG;
+  if (n_q > 0 && n_k > 0 && (!k_nope || !k_pe || !v)) return MLA_ERR_INVALID_ARG;
+  if (!aligned(q_nope, 16) || !aligned(q_pe, 16) || !aligned(k_nope, 16) || !aligned(k_pe, 16) || !aligned(v, 16) ||
+      !aligned(out, 16) || (lse_out && !aligned(lse_out, 4)))
+    return MLA_ERR_INVALID_ARG;
+  const PromptLayout L = prompt_layout(num_seqs, n_q);
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < L.total) return MLA_ERR_WORKSPACE;
+  char* ws = static_cast<char*>(workspace);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (n_q == 0) return cudaMemsetAsync(ws + L.status, 0, sizeof(int), s) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  PromptParams p;
+  p.cu_q = cu_q;
+  p.cu_k = cu_k;
+  p.q_nope = static_cast<const __nv_bfloat16*>(q_nope);
+  p.q_pe = static_cast<const __nv_bfloat16*>(q_pe);
+  p.k_nope = static_cast<const __nv_bfloat16*>(k_nope);
+  p.k_pe = static_cast<const __nv_bfloat16*>(k_pe);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse_out = lse_out;
+  p.status = reinterpret_cast<int*>(ws + L.status);
+  p.block_start = reinterpret_cast<int*>(ws + L.block_start);
+  p.items = reinterpret_cast<PromptItem*>(ws + L.items);
+  p.n_q = n_q;
+  p.n_k = n_k;
+  p.num_seqs = num_seqs;
+  p.heads = d->num_heads;
+  p.kv_heads = num_kv_heads;
+  p.sm_count = sm_count();
+  p.scale = softmax_scale;
+  p.scale_log2 = softmax_scale * kLog2e;
+  if (p.sm_count <= 0) return MLA_ERR_CUDA;
+  if (launch_prompt_plan(p, s) != cudaSuccess) return MLA_ERR_CUDA;
+  return launch_prompt_attention(p, s) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
 int mla_combine(const mla_dims* d, const float* partial_o, const float* partial_lse, int32_t batch,

@@ -72,6 +72,55 @@ struct AppendParams {
   int n_tokens, num_seqs, max_pages, num_pages, page_size;
 };
 
+// Packed rows read back out of the cache (mla_cache_read).
+struct CacheReadParams {
+  const void* cache;         // bf16, int8 or e4m3 [num_pages, P, 576]
+  const float* scale_zero;   // [num_pages, P, 2] (INT8) or [num_pages, P] (FP8)
+  const int* block_table;    // [num_seqs, max_pages]
+  const int* starts;         // [num_seqs] first position, or null: 0
+  const int* cu_rows;        // [num_seqs + 1]
+  __nv_bfloat16* c_kv;       // [n_rows, 512]
+  __nv_bfloat16* k_pe;       // [n_rows, 64]
+  int* status;               // optional
+  int num_seqs, max_pages, num_pages, page_size, n_rows;
+};
+
+// Latents expanded to per-head keys and values (mla_expand_kv).
+struct ExpandParams {
+  const __nv_bfloat16* c_kv;  // [n_rows, 512]
+  const __nv_bfloat16* W_UK;  // [heads, 128, 512]
+  const __nv_bfloat16* W_UV;  // [heads, 128, 512]
+  __nv_bfloat16* k_nope;      // [n_rows, heads, 128]
+  __nv_bfloat16* v;           // [n_rows, heads, 128]
+  int* status;                // optional
+  int n_rows, heads;
+  int sm_count;               // sizes the grid
+};
+
+// Causal attention over packed prompts (mla_prompt_attention).  The plan
+// kernel lists the work, longest first: one item per block of up to 256 query
+// rows of a sequence; the attention kernel runs every item for every head.
+struct PromptItem {
+  int q_row0, rows;        // first packed query row and number of rows (1..256)
+  int k_row0;              // first packed key row of the sequence
+  int vis0;                // keys that row 0 sees (row i sees vis0 + i; none if that is <= 0)
+  int kv_begin, kv_end;    // key range of this item, relative to k_row0
+  int slot, pieces;        // split keys: first partial of the block and number of its pieces (1: not split)
+};
+struct PromptParams {
+  const int* cu_q;           // [num_seqs + 1]
+  const int* cu_k;           // [num_seqs + 1]
+  const __nv_bfloat16 *q_nope, *q_pe, *k_nope, *k_pe, *v;
+  __nv_bfloat16* out;        // [n_q, heads, 128]
+  float* lse_out;            // [n_q, heads] or null
+  int* status;               // workspace: status word, then the number of items
+  int* block_start;          // workspace: [num_seqs + 1] first block of each sequence
+  PromptItem* items;         // workspace: [n_q / 256 + num_seqs]
+  int n_q, n_k, num_seqs, heads, kv_heads, sm_count;
+  float scale_log2;          // softmax_scale * log2(e)
+  float scale;
+};
+
 struct CombineUVParams {
   const float* partial_o;     // [NSEG, H, 512]
   const float* partial_lse;   // [NSEG, H]
@@ -97,6 +146,10 @@ cudaError_t launch_absorb(const AbsorbParams& p, bool fp16_out, cudaStream_t str
 cudaError_t launch_append(const AppendParams& p, int code, cudaStream_t stream);
 cudaError_t launch_combine_uv(const CombineUVParams& p, cudaStream_t stream);
 cudaError_t launch_combine(const CombineParams& p, cudaStream_t stream);
+cudaError_t launch_cache_read(const CacheReadParams& p, int code, cudaStream_t stream);
+cudaError_t launch_expand(const ExpandParams& p, cudaStream_t stream);
+cudaError_t launch_prompt_plan(const PromptParams& p, cudaStream_t stream);
+cudaError_t launch_prompt_attention(const PromptParams& p, cudaStream_t stream);
 cudaError_t launch_gather(const GatherParams& p, int code, cudaStream_t stream);
 cudaError_t launch_decode_tc(const DecodeParams& p, int hc, int code, int grid, cudaStream_t stream);
 int decode_head_group(int heads, bool byte_cache);

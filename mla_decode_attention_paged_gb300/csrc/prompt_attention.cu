@@ -1,0 +1,551 @@
+// prompt_attention.cu -- causal attention over packed prompts in the
+// un-absorbed form: per-head keys [k_nope | k_pe] and values, grouped heads,
+// sequences of different lengths.
+//
+// For query row i of sequence b (cu_q[b] <= i < cu_q[b + 1], Lq and Lk its
+// query and key counts, t = i - cu_q[b]) and head h, with kv head g = h / (H /
+// H_kv), over the keys j < t + 1 + Lk - Lq:
+//     s_j = scale * (q_nope[i][h] . k_nope[j][g] + q_pe[i][h] . k_pe[j])
+//     out[i][h] = sum_j softmax(s)_j v[j][g],   lse[i][h] = ln sum_j exp(s_j)
+// ("Beyond the Attention Bottleneck", "Down-Projection and Up-Projection
+// Mechanics" and "The RoPE Compatibility Problem"; "The Architecture of
+// Memory", "The Prefill Phase": a prompt's tokens are processed together.)
+// 320 multiply-adds per (query, key, head), against the 1,088 of the absorbed
+// form: the tensor cores bound it.
+//
+// One CTA per SM takes items from the plan's list: a block of up to 256 query
+// rows of one sequence and one head, as two tiles of 128 rows (the MMA's M).
+// Keys come in tiles of 128.  Per key tile and query tile,
+//     S [128 x 128] = Q [128 x 192] K^T   12 MMAs, both operands in shared memory
+//     O [128 x 128] += P [128 x 128] V     8 MMAs, P (bf16) in tensor memory over S
+// The tensor pipe alternates between the two query tiles, so that one tile's
+// softmax runs while the other tile's products do.  Tensor memory: S x2, O x2,
+// all 512 columns.  Shared memory: Q of both tiles (96 KB) and a ring of eight
+// 16 KB boxes [128 keys x 64 columns] (three to a key tile, two to a value
+// tile).
+//
+// Softmax: one thread per query row, online in fp32 and base 2.  The running
+// maximum only has to bound the scores within 8 (log2 units); a tile that
+// breaks the bound raises it and rescales O and the sum.  P is rounded to bf16
+// for the MMA (2^-9 relative per weight, averaged over the keys); the sum
+// takes the unrounded fp32 weights.
+//
+// Warps: 0-3 softmax and epilogue of query tile 0, 4-7 of tile 1, 8 TMA
+// producer, 9 tensor memory and MMA issue.  Every wait is bounded: on timeout
+// the CTA records MLA_ERR_DEVICE_TIMEOUT, drains, frees its tensor memory and
+// returns.
+#include <atomic>
+
+#include "blackwell_ptx.cuh"
+#include "decode_common.cuh"
+#include "params.cuh"
+
+namespace mla {
+namespace {
+
+using namespace ptx;
+using namespace dc;
+
+constexpr int kBlockRows = 256;                    // query rows of an item
+constexpr int kKeys = 128;                         // keys of a tile
+constexpr uint32_t kBox = 128 * 128;               // [128 rows x 64 columns] bf16, SW128: 16 KB
+constexpr uint32_t kQTile = 3 * kBox;              // q_nope columns 0-63, 64-127, q_pe
+constexpr int kRing = 8;                           // boxes of the key / value ring
+constexpr uint32_t kOffRing = 2 * kQTile;
+constexpr uint32_t kOffMisc = kOffRing + kRing * kBox;
+constexpr uint32_t kSmem = kOffMisc + 512 + 1024;  // + barriers, alignment slack
+constexpr int kPromptThreads = 320;
+constexpr uint32_t kColS = 0, kColO = 256;         // tensor memory columns: S x2, O x2
+constexpr uint64_t kWaitNs = 2000000000ull;        // 2 s
+constexpr float kRescale = 8.f;                    // log2 units
+constexpr int kPlanThreads = 1024;
+constexpr int kBuckets = 1024;                     // cost classes of the plan's counting sort
+static_assert(kSmem <= 232448, "dynamic shared memory of one CTA");
+
+// ----- plan ----------------------------------------------------------------------
+// One CTA: checks cu_q and cu_k, cuts every sequence into blocks of 256 query
+// rows and lists them by falling number of key tiles (a counting sort), so
+// that dealing the list round-robin over the CTAs balances them.  A sequence
+// whose offsets decrease or pass the end, and every one after it, is skipped
+// and reported; this also bounds the list.
+__device__ __forceinline__ int key_tiles(int vis_last) { return vis_last > 0 ? (vis_last + kKeys - 1) / kKeys : 0; }
+
+__global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams p) {
+  __shared__ int scan_tmp[32];
+  __shared__ int hist[kBuckets];
+  __shared__ int carry, first_bad;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int tid = threadIdx.x;
+  if (tid == 0) {
+    carry = 0;
+    first_bad = p.num_seqs;
+    p.status[0] = MLA_OK;
+  }
+  for (int i = tid; i < kBuckets; i += kPlanThreads) hist[i] = 0;
+  __syncthreads();
+  for (int b = tid; b < p.num_seqs; b += kPlanThreads) {
+    const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1], k0 = p.cu_k[b], k1 = p.cu_k[b + 1];
+    if (q0 < 0 || q1 < q0 || q1 > p.n_q || k0 < 0 || k1 < k0 || k1 > p.n_k) atomicMin(&first_bad, b);
+  }
+  __syncthreads();
+  const int good = first_bad;
+  if (tid == 0 && good < p.num_seqs) set_status(p.status, MLA_ERR_DEVICE_BOUNDS);
+  for (int base = 0; base < good; base += kPlanThreads) {
+    const int b = base + tid;
+    const int blocks = b < good ? (p.cu_q[b + 1] - p.cu_q[b] + kBlockRows - 1) / kBlockRows : 0;
+    int total;
+    const int ex = block_exclusive_scan(blocks, scan_tmp, &total);
+    if (b < good) p.block_start[b] = carry + ex;
+    __syncthreads();
+    if (tid == 0) carry += total;
+    __syncthreads();
+  }
+  const int n = carry;
+  if (tid == 0) p.status[1] = n;
+  __syncthreads();  // block_start is read below by other threads of this CTA
+  auto block_item = [&](int i, int& bucket) {
+    int lo = 0, hi = good - 1;  // last sequence whose first block is <= i and that has blocks
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (p.block_start[mid] <= i) lo = mid; else hi = mid - 1;
+    }
+    const int b = lo, q0 = p.cu_q[b], lq = p.cu_q[b + 1] - q0, k0 = p.cu_k[b], lk = p.cu_k[b + 1] - k0;
+    const int r0 = (i - p.block_start[b]) * kBlockRows;
+    PromptItem it;
+    it.q_row0 = q0 + r0;
+    it.rows = min(kBlockRows, lq - r0);
+    it.k_row0 = k0;
+    it.vis0 = lk - lq + r0 + 1;
+    it.kv_begin = 0;
+    it.kv_end = max(0, it.vis0 + it.rows - 1);
+    it.slot = -1;
+    it.pieces = 1;
+    bucket = kBuckets - 1 - min(kBuckets - 1, key_tiles(it.kv_end));
+    return it;
+  };
+  for (int i = tid; i < n; i += kPlanThreads) {
+    int bucket;
+    block_item(i, bucket);
+    atomicAdd(&hist[bucket], 1);
+  }
+  __syncthreads();
+  int total;
+  const int ex = block_exclusive_scan(hist[tid], scan_tmp, &total);
+  hist[tid] = ex;
+  __syncthreads();
+  // the order inside a bucket is arbitrary: it decides which CTA runs an item, not its result
+  for (int i = tid; i < n; i += kPlanThreads) {
+    int bucket;
+    const PromptItem it = block_item(i, bucket);
+    p.items[atomicAdd(&hist[bucket], 1)] = it;
+  }
+}
+
+// ----- attention -------------------------------------------------------------------
+struct PromptBarriers {
+  uint64_t q_full[2], q_empty[2];  // query tile loaded / read by its last QK
+  uint64_t full[kRing];            // ring box landed
+  uint64_t k_empty[2], v_empty[2]; // boxes of even / odd key tiles read by their last MMA
+  uint64_t s_full[2];              // scores of a tile complete
+  uint64_t p_full[2];              // P written (and O rescaled where needed)
+  uint64_t o_full[2], o_free[2];   // output complete / read
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+};
+
+__device__ __forceinline__ void fail(PromptBarriers* B, int* status) {
+  B->abort = 1;
+  set_status(status, MLA_ERR_DEVICE_TIMEOUT);
+}
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ PromptItem load_item(const PromptItem* items, int i) {
+  const int4* src = reinterpret_cast<const int4*>(items + i);
+  const int4 a = src[0], b = src[1];
+  return {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+}
+
+// Key tiles of query tile t (0, 1) of an item.
+__device__ __forceinline__ int tiles_of(const PromptItem& it, int t) {
+  if (it.rows <= 128 * t) return 0;
+  const int last = min(it.rows, 128 * (t + 1)) - 1;
+  return key_tiles(min(it.kv_end, it.vis0 + last) - it.kv_begin);
+}
+
+// The CTA's n-th unit of work (item, head), dealt in a serpentine over the
+// sorted list: CTA c takes c, 2G - 1 - c, 2G + c, ...
+__device__ __forceinline__ long long unit_of(int n) {
+  const int G = gridDim.x, c = blockIdx.x;
+  return (long long)n * G + ((n & 1) ? G - 1 - c : c);
+}
+
+__global__ void __launch_bounds__(kPromptThreads, 1)
+    prompt_attention_kernel(const __grid_constant__ CUtensorMap map_qn, const __grid_constant__ CUtensorMap map_qp,
+                            const __grid_constant__ CUtensorMap map_kn, const __grid_constant__ CUtensorMap map_kp,
+                            const __grid_constant__ CUtensorMap map_v, PromptParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  PromptBarriers* B = reinterpret_cast<PromptBarriers*>(smem + kOffMisc);
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&B->q_full[t], 1);
+      mbar_init(&B->q_empty[t], 1);
+      mbar_init(&B->k_empty[t], 1);
+      mbar_init(&B->v_empty[t], 1);
+      mbar_init(&B->s_full[t], 1);
+      mbar_init(&B->p_full[t], 128);
+      mbar_init(&B->o_full[t], 1);
+      mbar_init(&B->o_free[t], 128);
+    }
+    for (int i = 0; i < kRing; ++i) mbar_init(&B->full[i], 1);
+    mbar_init(&B->drain, 1);
+    B->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(&B->tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = B->tmem_base;
+  griddep_wait();  // the plan's list
+  griddep_launch_dependents();
+  const volatile int* abort_flag = &B->abort;
+  const int H = p.heads, group = H / p.kv_heads;
+  const long long units = (long long)p.status[1] * H;
+
+  if (warp == 8 && lane == 0) {
+    // ------------------------------------------------------------ TMA producer
+    // Box i (0-2: K, 3-4: V) of key tile j sits at ring position (5 j + i) % 8,
+    // last used by box (5 j + i - 8): K_{j-2} for i = 0, V_{j-2} for i = 1, 2,
+    // K_{j-1} for i = 3, 4.  j counts the CTA's key tiles over all its items.
+    bool ok = true;
+    uint32_t j = 0, nq[2] = {0, 0};
+    for (int n = 0; ok; ++n) {
+      const long long u = unit_of(n);
+      if (u >= units) break;
+      const PromptItem it = load_item(p.items, int(u / H));
+      const int h = int(u % H), g = h / group;
+      const int nt0 = tiles_of(it, 0), nt1 = tiles_of(it, 1), nt = max(nt0, nt1);
+      for (int t = 0; t < 2 && ok; ++t) {
+        if (!(t ? nt1 : nt0)) continue;
+        if (nq[t] > 0 && !(ok = mbar_wait(&B->q_empty[t], (nq[t] - 1) & 1, abort_flag, kWaitNs))) break;
+        ++nq[t];
+        uint8_t* q = smem + t * kQTile;
+        const int row = it.q_row0 + 128 * t;
+        mbar_arrive_expect_tx(&B->q_full[t], kQTile);
+        tma_load_3d(q, &map_qn, 0, h, row, &B->q_full[t]);
+        tma_load_3d(q + kBox, &map_qn, 64, h, row, &B->q_full[t]);
+        tma_load_3d(q + 2 * kBox, &map_qp, 0, h, row, &B->q_full[t]);
+      }
+      for (int kt = 0; kt < nt && ok; ++kt, ++j) {
+        const int key = it.k_row0 + it.kv_begin + kt * kKeys;
+#pragma unroll 1
+        for (int i = 0; i < 5; ++i) {
+          if (i == 0 && j >= 2) ok = mbar_wait(&B->k_empty[j & 1], ((j - 2) >> 1) & 1, abort_flag, kWaitNs);
+          if (i == 1 && j >= 2) ok = mbar_wait(&B->v_empty[j & 1], ((j - 2) >> 1) & 1, abort_flag, kWaitNs);
+          if (i == 3 && j >= 1) ok = mbar_wait(&B->k_empty[(j - 1) & 1], ((j - 1) >> 1) & 1, abort_flag, kWaitNs);
+          if (!ok) break;
+          const uint32_t slot = (5 * j + i) % kRing;
+          uint8_t* dst = smem + kOffRing + slot * kBox;
+          mbar_arrive_expect_tx(&B->full[slot], kBox);
+          if (i == 2) tma_load_2d(dst, &map_kp, 0, key, &B->full[slot]);
+          else tma_load_3d(dst, i < 3 ? &map_kn : &map_v, (i == 1 || i == 4) ? 64 : 0, g, key, &B->full[slot]);
+        }
+      }
+    }
+    if (!ok) fail(B, p.status);
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ MMA issue
+    // Per key tile j: PV of tile 0, QK of tile 0 for j + 1, then both of tile
+    // 1.  MMAs of one thread run in order, so QK of j + 1 may overwrite the
+    // scores whose P the PV of j before it reads.
+    constexpr uint32_t id_qk = idesc_bf16_f32(128, 128, false, false);
+    constexpr uint32_t id_pv = idesc_bf16_f32(128, 128, false, true), id_pv64 = idesc_bf16_f32(128, 64, false, true);
+    constexpr uint64_t kDescK = smem_desc(0, 16, 1024, kSwizzle128B);    // K-major
+    constexpr uint64_t kDescMN = smem_desc(0, kBox, 1024, kSwizzle128B); // MN-major, 64-column blocks a box apart
+    bool ok = true;
+    uint32_t j = 0, nq[2] = {0, 0}, np[2] = {0, 0}, no[2] = {0, 0};
+    // phase of ring position x = 5 j + i: its use number x / 8
+    auto wait_box = [&](uint32_t x) { return mbar_wait(&B->full[x % kRing], (x / kRing) & 1, abort_flag, kWaitNs); };
+    auto qk = [&](int t, uint32_t jj) -> bool {
+#pragma unroll 1
+      for (uint32_t i = 0; i < 3; ++i) {
+        const uint32_t x = 5 * jj + i;
+        if (!wait_box(x)) return false;
+        tc_fence_after();
+        const uint32_t a = sbase + t * kQTile + i * kBox, b = sbase + kOffRing + (x % kRing) * kBox;
+        if (lane == 0) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_bf16(tmem + kColS + 128 * t, kDescK | desc_addr(a + 32 * kk), kDescK | desc_addr(b + 32 * kk), id_qk,
+                     i > 0 || kk > 0);
+        }
+      }
+      if (lane == 0) mma_commit(&B->s_full[t]);
+      __syncwarp();
+      return true;
+    };
+    for (int n = 0; ok; ++n) {
+      const long long u = unit_of(n);
+      if (u >= units) break;
+      const PromptItem it = load_item(p.items, int(u / H));
+      const int nts[2] = {tiles_of(it, 0), tiles_of(it, 1)}, nt = max(nts[0], nts[1]);
+      if (nt == 0) continue;
+      // tile 1 sees at least the key tiles that tile 0 sees: the last reader of
+      // every key tile, which releases it, is tile 1 where it exists
+      const int last = nts[1] > 0 ? 1 : 0;
+      for (int t = 0; t < 2 && ok; ++t) {
+        if (!nts[t]) continue;
+        ok = mbar_wait(&B->q_full[t], nq[t] & 1, abort_flag, kWaitNs) && qk(t, j);
+        ++nq[t];
+        if (ok && lane == 0 && nts[t] == 1) mma_commit(&B->q_empty[t]);
+      }
+      if (ok && lane == 0) mma_commit(&B->k_empty[j & 1]);
+      __syncwarp();
+      for (int kt = 0; kt < nt && ok; ++kt, ++j) {
+        const uint32_t xv = 5 * j + 3;
+        ok = wait_box(xv) && wait_box(xv + 1);
+        if (!ok) break;
+        // PV reads the rows of whole 16-key steps; rows at and past the last
+        // key meet zero weights but must be finite: they are cleared here
+        const int valid = min(kKeys, it.kv_end - it.kv_begin - kt * kKeys), steps = (valid + 15) >> 4;
+        if (16 * steps > valid) {
+          const int tail = 16 * steps - valid;
+          for (int i = lane; i < tail * 16; i += 32)
+            *reinterpret_cast<uint4*>(smem + kOffRing + ((xv + ((i >> 3) & 1)) % kRing) * kBox +
+                                      (valid + (i >> 4)) * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+#pragma unroll 1
+        for (int t = 0; t < 2 && ok; ++t) {
+          if (kt >= nts[t]) continue;
+          if (kt == 0 && no[t] > 0) ok = mbar_wait(&B->o_free[t], (no[t] - 1) & 1, abort_flag, kWaitNs);
+          ok = ok && mbar_wait(&B->p_full[t], np[t] & 1, abort_flag, kWaitNs);
+          if (!ok) break;
+          ++np[t];
+          tc_fence_after();
+          if (lane == 0) {
+            const uint32_t o = tmem + kColO + 128 * t, pa = tmem + kColS + 128 * t;
+            const uint32_t v0 = sbase + kOffRing + (xv % kRing) * kBox, v1 = sbase + kOffRing + ((xv + 1) % kRing) * kBox;
+            if (v1 > v0) {  // the two boxes are neighbours: one N = 128 product
+              for (int kk = 0; kk < steps; ++kk)
+                mma_f16_tmem_a(o, pa + 8 * kk, kDescMN | desc_addr(v0 + 2048 * kk), id_pv, kt > 0 || kk > 0);
+            } else {        // the second box wrapped to the ring's start: a product for each
+              for (int kk = 0; kk < steps; ++kk) {
+                mma_f16_tmem_a(o, pa + 8 * kk, kDescMN | desc_addr(v0 + 2048 * kk), id_pv64, kt > 0 || kk > 0);
+                mma_f16_tmem_a(o + 64, pa + 8 * kk, kDescMN | desc_addr(v1 + 2048 * kk), id_pv64, kt > 0 || kk > 0);
+              }
+            }
+            if (t == last) mma_commit(&B->v_empty[j & 1]);
+            if (kt == nts[t] - 1) mma_commit(&B->o_full[t]);
+          }
+          if (kt == nts[t] - 1) ++no[t];
+          __syncwarp();
+          if (kt + 1 < nts[t]) {
+            ok = qk(t, j + 1);
+            if (ok && lane == 0) {
+              if (t == last) mma_commit(&B->k_empty[(j + 1) & 1]);
+              if (kt + 2 == nts[t]) mma_commit(&B->q_empty[t]);
+            }
+            __syncwarp();
+          }
+        }
+      }
+    }
+    if (lane == 0) {
+      if (!ok) fail(B, p.status);
+      mma_commit(&B->drain);  // every MMA issued completes before teardown
+      mbar_wait(&B->drain, 0, abort_flag, kWaitNs);
+    }
+  } else if (warp < 8) {
+    // ------------------------------------------------------------ softmax, epilogue
+    const int t = warp >> 2, r = 32 * (warp & 3) + lane;  // query tile, row = tensor memory lane
+    const uint32_t lane_off = uint32_t(32 * (warp & 3)) << 16;
+    const uint32_t ts = tmem + lane_off + kColS + 128 * t, to = tmem + lane_off + kColO + 128 * t;
+    bool ok = true;
+    uint32_t ns = 0, no = 0;
+    for (int n = 0; ok; ++n) {
+      const long long u = unit_of(n);
+      if (u >= units) break;
+      const PromptItem it = load_item(p.items, int(u / H));
+      const int h = int(u % H), nt = tiles_of(it, t);
+      const int row = 128 * t + r;                  // row of the item
+      const int vis = it.vis0 + row - it.kv_begin;  // keys of this item's range that the row sees
+      const int vis_first = it.vis0 + 128 * t - it.kv_begin, keys = it.kv_end - it.kv_begin;
+      float m = -INFINITY, l = 0.f;
+      for (int kt = 0; kt < nt; ++kt) {
+        ok = mbar_wait(&B->s_full[t], ns & 1, abort_flag, kWaitNs);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        ++ns;
+        tc_fence_after();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, s[c]);
+        if (kKeys * (kt + 1) > min(vis_first, keys)) {  // some row does not see some key of this tile
+          const int lim = min(vis, keys) - kKeys * kt;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (32 * c + i >= lim) s[c][i] = 0xff800000u;  // -inf
+        }
+        float mt = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) mt = fmaxf(mt, __uint_as_float(s[c][i]));
+        float alpha = 1.f;
+        bool rescale = false;
+        if (kt == 0) {
+          m = mt;
+        } else if ((mt - m) * p.scale_log2 > kRescale) {
+          alpha = ex2_ftz((m - mt) * p.scale_log2);
+          m = mt;
+          l *= alpha;
+          rescale = true;
+        }
+        if (__any_sync(0xffffffffu, rescale)) {
+          // s_full of this tile follows the PV of the tile before: O is complete up to there
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t o[32];
+            tmem_ld32(to + 32 * c, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_st32(to + 32 * c, o);
+          }
+        }
+        const float shift = m == -INFINITY ? 0.f : m * p.scale_log2;  // a row without keys: all weights 0
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float a = ex2_ftz(fmaf(__uint_as_float(s[c][2 * i]), p.scale_log2, -shift));
+            const float b = ex2_ftz(fmaf(__uint_as_float(s[c][2 * i + 1]), p.scale_log2, -shift));
+            l += a + b;
+            const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+            w[i] = *reinterpret_cast<const uint32_t*>(&v);
+          }
+          tmem_st16u(ts + 16 * c, w);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&B->p_full[t]);
+      }
+      if (!ok) break;
+      const bool live = row < it.rows;
+      const size_t orow = size_t(it.q_row0 + row) * H + h;
+      uint4* dst = reinterpret_cast<uint4*>(p.out + orow * kVDim);
+      if (nt > 0) {
+        ok = mbar_wait(&B->o_full[t], no & 1, abort_flag, kWaitNs);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        ++no;
+        tc_fence_after();
+        const float inv = l > 0.f ? __frcp_rn(l) : (l == 0.f ? 0.f : l);  // a row without keys: 0; NaN stays NaN
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[32];
+          tmem_ld32(to + 32 * c, o);
+          if (live) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(o[8 * i + 2 * e]) * inv,
+                                                               __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
+                w[e] = *reinterpret_cast<const uint32_t*>(&v);
+              }
+              dst[4 * c + i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(&B->o_free[t]);
+      } else if (live) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dst[i] = make_uint4(0, 0, 0, 0);
+      }
+      if (live && p.lse_out)
+        p.lse_out[orow] = l == 0.f ? -INFINITY : m * p.scale + logf(l);
+    }
+    if (!ok) fail(B, p.status);
+  }
+  // ---------------------------------------------------------------- teardown
+  __syncthreads();
+  if (B->abort) {  // copies already issued land before the shared memory is released
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 20000) {
+    }
+  }
+  tc_fence_after();
+  if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+// 3-D map over a [rows, heads, width] bf16 tensor: boxes of 64 columns x 1 head x 128 rows.
+bool make_map_heads(CUtensorMap* m, const void* base, uint64_t width, uint64_t heads, uint64_t rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {width, heads, rows};
+  cuuint64_t strides[2] = {width * 2, width * heads * 2};
+  cuuint32_t box[3] = {64, 1, 128};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+cudaError_t launch_prompt_plan(const PromptParams& p, cudaStream_t stream) {
+  return launch_pdl(prompt_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, 1, p);
+}
+
+cudaError_t launch_prompt_attention(const PromptParams& p, cudaStream_t stream) {
+  CUtensorMap qn, qp, kn, kp, v;
+  if (!make_map_heads(&qn, p.q_nope, kNope, p.heads, p.n_q) || !make_map_heads(&qp, p.q_pe, kRope, p.heads, p.n_q))
+    return cudaErrorInvalidValue;
+  if (p.n_k > 0) {
+    if (!make_map_heads(&kn, p.k_nope, kNope, p.kv_heads, p.n_k) || !make_map_heads(&v, p.v, kVDim, p.kv_heads, p.n_k) ||
+        !make_map_2d(&kp, p.k_pe, 2, kRope, p.n_k, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorInvalidValue;
+  } else {
+    kn = kp = v = qn;  // no keys: no key tile is ever loaded
+  }
+  static std::atomic<bool> attr[128];  // per device: attributes set (zero-initialised)
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 128 || !attr[dev]) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(prompt_attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 128) attr[dev] = true;
+  }
+  const long long most = ((long long)p.n_q / kBlockRows + p.num_seqs) * p.heads;  // units at most
+  const unsigned grid = unsigned(most < p.sm_count ? most : p.sm_count);
+  return launch_pdl(prompt_attention_kernel, dim3(grid), dim3(kPromptThreads), kSmem, stream, 1, qn, qp, kn, kp, v, p);
+}
+
+}  // namespace mla
