@@ -18,8 +18,7 @@
 // Keys come in tiles of 128.  Per key tile and query tile,
 //     S [128 x 128] = Q [128 x 192] K^T   12 MMAs, both operands in shared memory
 //     O [128 x 128] += P [128 x 128] V     8 MMAs, P (bf16) in tensor memory over S
-// The tensor pipe alternates between the two query tiles, so that one tile's
-// softmax runs while the other tile's products do.  Tensor memory: S x2, O x2,
+// One tile's softmax runs while the tensor pipe works on the other tile.  Tensor memory: S x2, O x2,
 // all 512 columns.  Shared memory: Q of both tiles (96 KB) and a ring of eight
 // 16 KB boxes [128 keys x 64 columns] (three to a key tile, two to a value
 // tile).
@@ -31,7 +30,8 @@
 // takes the unrounded fp32 weights.
 //
 // Warps: 0-3 softmax and epilogue of query tile 0, 4-7 of tile 1, 8 TMA
-// producer, 9 tensor memory and MMA issue.  Every wait is bounded: on timeout
+// producer, 9 (which also owns tensor memory) and 10 MMA issue for tiles 0 and
+// 1, 11 clears the ragged ends of value tiles.  Every wait is bounded: on timeout
 // the CTA records MLA_ERR_DEVICE_TIMEOUT, drains, frees its tensor memory and
 // returns.
 #include <atomic>
@@ -54,7 +54,7 @@ constexpr int kRing = 8;                           // boxes of the key / value r
 constexpr uint32_t kOffRing = 2 * kQTile;
 constexpr uint32_t kOffMisc = kOffRing + kRing * kBox;
 constexpr uint32_t kSmem = kOffMisc + 512 + 1024;  // + barriers, alignment slack
-constexpr int kPromptThreads = 320;
+constexpr int kPromptThreads = 384;
 constexpr uint32_t kColS = 0, kColO = 256;         // tensor memory columns: S x2, O x2
 constexpr uint64_t kWaitNs = 2000000000ull;        // 2 s
 constexpr float kRescale = 8.f;                    // log2 units
@@ -146,11 +146,12 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
 struct PromptBarriers {
   uint64_t q_full[2], q_empty[2];  // query tile loaded / read by its last QK
   uint64_t full[kRing];            // ring box landed
-  uint64_t k_empty[2], v_empty[2]; // boxes of even / odd key tiles read by their last MMA
+  uint64_t k_empty[2], v_empty[2]; // boxes of even / odd key tiles read by both MMA threads
   uint64_t s_full[2];              // scores of a tile complete
   uint64_t p_full[2];              // P written (and O rescaled where needed)
   uint64_t o_full[2], o_free[2];   // output complete / read
-  uint64_t drain;
+  uint64_t v_clean[2];             // a ragged value tile's rows past the last key cleared
+  uint64_t drain[2];
   uint32_t tmem_base;
   int abort;
 };
@@ -166,6 +167,42 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
       "[%5];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
+}
+
+// 32 tensor memory columns without waiting for them; ld_wait() completes all
+// loads of the warp, and values are used only after tie() follows it.
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tie(uint32_t (&r)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// Two fp32 operations at once on a register pair.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  return uint64_t(__float_as_uint(a)) | (uint64_t(__float_as_uint(b)) << 32);
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  return make_float2(__uint_as_float(uint32_t(v)), __uint_as_float(uint32_t(v >> 32)));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 
 __device__ __forceinline__ PromptItem load_item(const PromptItem* items, int i) {
@@ -201,15 +238,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     for (int t = 0; t < 2; ++t) {
       mbar_init(&B->q_full[t], 1);
       mbar_init(&B->q_empty[t], 1);
-      mbar_init(&B->k_empty[t], 1);
-      mbar_init(&B->v_empty[t], 1);
+      mbar_init(&B->k_empty[t], 3);  // both MMA threads and the clearing warp
+      mbar_init(&B->v_empty[t], 3);
+      mbar_init(&B->v_clean[t], 1);
       mbar_init(&B->s_full[t], 1);
-      mbar_init(&B->p_full[t], 128);
+      mbar_init(&B->drain[t], 1);
+      mbar_init(&B->p_full[t], 4);  // one lane of each of the tile's softmax warps
       mbar_init(&B->o_full[t], 1);
-      mbar_init(&B->o_free[t], 128);
+      mbar_init(&B->o_free[t], 4);
     }
     for (int i = 0; i < kRing; ++i) mbar_init(&B->full[i], 1);
-    mbar_init(&B->drain, 1);
     B->abort = 0;
     fence_mbar_init();
   }
@@ -268,110 +306,149 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       }
     }
     if (!ok) fail(B, p.status);
-  } else if (warp == 9) {
+  } else if ((warp == 9 || warp == 10) && lane == 0) {
     // ------------------------------------------------------------ MMA issue
-    // Per key tile j: PV of tile 0, QK of tile 0 for j + 1, then both of tile
-    // 1.  MMAs of one thread run in order, so QK of j + 1 may overwrite the
-    // scores whose P the PV of j before it reads.
+    // One thread per query tile t, each with its own chain: QK of the first
+    // key tile, then PV of a key tile and QK of the next.  MMAs of one thread
+    // run in order, so the QK may overwrite the scores whose P the PV before
+    // it reads.  The pipe takes only a few MMAs ahead, so whatever a thread
+    // does between two of them shows unless the other thread's fill the gap.
+    // Both threads pass every key tile and release it together: a thread whose
+    // query tile does not see it arrives once it has landed (and not before,
+    // or it could stand in for the other thread's release two tiles earlier).
+    const int t = warp - 9;
     constexpr uint32_t id_qk = idesc_bf16_f32(128, 128, false, false);
     constexpr uint32_t id_pv = idesc_bf16_f32(128, 128, false, true), id_pv64 = idesc_bf16_f32(128, 64, false, true);
     constexpr uint64_t kDescK = smem_desc(0, 16, 1024, kSwizzle128B);    // K-major
     constexpr uint64_t kDescMN = smem_desc(0, kBox, 1024, kSwizzle128B); // MN-major, 64-column blocks a box apart
+    const uint32_t ds = tmem + kColS + 128 * t, dO = tmem + kColO + 128 * t;
+    const uint64_t q_desc = kDescK | desc_addr(sbase + t * kQTile);
     bool ok = true;
-    uint32_t j = 0, nq[2] = {0, 0}, np[2] = {0, 0}, no[2] = {0, 0};
-    // phase of ring position x = 5 j + i: its use number x / 8
+    uint32_t j = 0, nq = 0, np = 0, no = 0, nragged = 0;
+    // ring position x = 5 j + i: box x % 8, use number x / 8
     auto wait_box = [&](uint32_t x) { return mbar_wait(&B->full[x % kRing], (x / kRing) & 1, abort_flag, kWaitNs); };
-    auto qk = [&](int t, uint32_t jj) -> bool {
-#pragma unroll 1
+    auto qk = [&](uint32_t jj, bool sees) -> bool {
+#pragma unroll
       for (uint32_t i = 0; i < 3; ++i) {
         const uint32_t x = 5 * jj + i;
         if (!wait_box(x)) return false;
+        if (!sees) continue;
         tc_fence_after();
-        const uint32_t a = sbase + t * kQTile + i * kBox, b = sbase + kOffRing + (x % kRing) * kBox;
-        if (lane == 0) {
+        const uint64_t a = q_desc + i * (kBox >> 4), b = kDescK | desc_addr(sbase + kOffRing + (x % kRing) * kBox);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_bf16(tmem + kColS + 128 * t, kDescK | desc_addr(a + 32 * kk), kDescK | desc_addr(b + 32 * kk), id_qk,
-                     i > 0 || kk > 0);
-        }
+        for (int kk = 0; kk < 4; ++kk) mma_bf16(ds, a + 2 * kk, b + 2 * kk, id_qk, i > 0 || kk > 0);
       }
-      if (lane == 0) mma_commit(&B->s_full[t]);
-      __syncwarp();
+      if (sees) {
+        mma_commit(&B->s_full[t]);
+        mma_commit(&B->k_empty[jj & 1]);
+      } else {
+        mbar_arrive(&B->k_empty[jj & 1]);
+      }
       return true;
     };
     for (int n = 0; ok; ++n) {
       const long long u = unit_of(n);
       if (u >= units) break;
       const PromptItem it = load_item(p.items, int(u / H));
-      const int nts[2] = {tiles_of(it, 0), tiles_of(it, 1)}, nt = max(nts[0], nts[1]);
+      const int mine = tiles_of(it, t), nt = max(mine, tiles_of(it, t ^ 1));
       if (nt == 0) continue;
-      // tile 1 sees at least the key tiles that tile 0 sees: the last reader of
-      // every key tile, which releases it, is tile 1 where it exists
-      const int last = nts[1] > 0 ? 1 : 0;
-      for (int t = 0; t < 2 && ok; ++t) {
-        if (!nts[t]) continue;
-        ok = mbar_wait(&B->q_full[t], nq[t] & 1, abort_flag, kWaitNs) && qk(t, j);
-        ++nq[t];
-        if (ok && lane == 0 && nts[t] == 1) mma_commit(&B->q_empty[t]);
+      if (mine > 0) {
+        ok = mbar_wait(&B->q_full[t], nq & 1, abort_flag, kWaitNs);
+        ++nq;
       }
-      if (ok && lane == 0) mma_commit(&B->k_empty[j & 1]);
-      __syncwarp();
+      ok = ok && qk(j, mine > 0);
+      if (ok && mine == 1) mma_commit(&B->q_empty[t]);
       for (int kt = 0; kt < nt && ok; ++kt, ++j) {
         const uint32_t xv = 5 * j + 3;
         ok = wait_box(xv) && wait_box(xv + 1);
-        if (!ok) break;
-        // PV reads the rows of whole 16-key steps; rows at and past the last
-        // key meet zero weights but must be finite: they are cleared here
-        const int valid = min(kKeys, it.kv_end - it.kv_begin - kt * kKeys), steps = (valid + 15) >> 4;
-        if (16 * steps > valid) {
-          const int tail = 16 * steps - valid;
-          for (int i = lane; i < tail * 16; i += 32)
-            *reinterpret_cast<uint4*>(smem + kOffRing + ((xv + ((i >> 3) & 1)) % kRing) * kBox +
-                                      (valid + (i >> 4)) * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
-          fence_proxy_async_smem();
-          __syncwarp();
+        const int valid = it.kv_end - it.kv_begin - kt * kKeys;
+        if (valid < kKeys && (valid & 15)) {  // the last tile's rows past the keys are cleared first
+          ok = ok && mbar_wait(&B->v_clean[nragged & 1], (nragged >> 1) & 1, abort_flag, kWaitNs);
+          ++nragged;
         }
-#pragma unroll 1
-        for (int t = 0; t < 2 && ok; ++t) {
-          if (kt >= nts[t]) continue;
-          if (kt == 0 && no[t] > 0) ok = mbar_wait(&B->o_free[t], (no[t] - 1) & 1, abort_flag, kWaitNs);
-          ok = ok && mbar_wait(&B->p_full[t], np[t] & 1, abort_flag, kWaitNs);
+        if (!ok) break;
+        if (kt < mine) {
+          if (kt == 0 && no > 0) ok = mbar_wait(&B->o_free[t], (no - 1) & 1, abort_flag, kWaitNs);
+          ok = ok && mbar_wait(&B->p_full[t], np & 1, abort_flag, kWaitNs);
           if (!ok) break;
-          ++np[t];
+          ++np;
           tc_fence_after();
-          if (lane == 0) {
-            const uint32_t o = tmem + kColO + 128 * t, pa = tmem + kColS + 128 * t;
-            const uint32_t v0 = sbase + kOffRing + (xv % kRing) * kBox, v1 = sbase + kOffRing + ((xv + 1) % kRing) * kBox;
-            if (v1 > v0) {  // the two boxes are neighbours: one N = 128 product
-              for (int kk = 0; kk < steps; ++kk)
-                mma_f16_tmem_a(o, pa + 8 * kk, kDescMN | desc_addr(v0 + 2048 * kk), id_pv, kt > 0 || kk > 0);
-            } else {        // the second box wrapped to the ring's start: a product for each
+          const uint32_t s0 = xv % kRing;
+          const uint64_t v0 = kDescMN | desc_addr(sbase + kOffRing + s0 * kBox);
+          if (valid >= kKeys && s0 != kRing - 1) {
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) mma_f16_tmem_a(dO, ds + 8 * kk, v0 + 128 * kk, id_pv, kt > 0 || kk > 0);
+          } else {
+            const int steps = (min(valid, kKeys) + 15) >> 4;
+            if (s0 != kRing - 1) {
+              for (int kk = 0; kk < steps; ++kk) mma_f16_tmem_a(dO, ds + 8 * kk, v0 + 128 * kk, id_pv, kt > 0 || kk > 0);
+            } else {  // the second box wrapped to the ring's start: a product for each
+              const uint64_t v1 = kDescMN | desc_addr(sbase + kOffRing);
               for (int kk = 0; kk < steps; ++kk) {
-                mma_f16_tmem_a(o, pa + 8 * kk, kDescMN | desc_addr(v0 + 2048 * kk), id_pv64, kt > 0 || kk > 0);
-                mma_f16_tmem_a(o + 64, pa + 8 * kk, kDescMN | desc_addr(v1 + 2048 * kk), id_pv64, kt > 0 || kk > 0);
+                mma_f16_tmem_a(dO, ds + 8 * kk, v0 + 128 * kk, id_pv64, kt > 0 || kk > 0);
+                mma_f16_tmem_a(dO + 64, ds + 8 * kk, v1 + 128 * kk, id_pv64, kt > 0 || kk > 0);
               }
             }
-            if (t == last) mma_commit(&B->v_empty[j & 1]);
-            if (kt == nts[t] - 1) mma_commit(&B->o_full[t]);
           }
-          if (kt == nts[t] - 1) ++no[t];
-          __syncwarp();
-          if (kt + 1 < nts[t]) {
-            ok = qk(t, j + 1);
-            if (ok && lane == 0) {
-              if (t == last) mma_commit(&B->k_empty[(j + 1) & 1]);
-              if (kt + 2 == nts[t]) mma_commit(&B->q_empty[t]);
-            }
-            __syncwarp();
+          mma_commit(&B->v_empty[j & 1]);
+          if (kt == mine - 1) {
+            mma_commit(&B->o_full[t]);
+            ++no;
           }
+        } else {
+          mbar_arrive(&B->v_empty[j & 1]);
+        }
+        if (kt + 1 < nt) {
+          ok = qk(j + 1, kt + 1 < mine);
+          if (ok && kt + 2 == mine) mma_commit(&B->q_empty[t]);
         }
       }
     }
-    if (lane == 0) {
-      if (!ok) fail(B, p.status);
-      mma_commit(&B->drain);  // every MMA issued completes before teardown
-      mbar_wait(&B->drain, 0, abort_flag, kWaitNs);
+    if (!ok) fail(B, p.status);
+    mma_commit(&B->drain[t]);  // every MMA issued completes before teardown
+    mbar_wait(&B->drain[t], 0, abort_flag, kWaitNs);
+  } else if (warp == 11) {
+    // ------------------------------------------------------------ ragged ends
+    // PV reads whole 16-key steps; the rows of a range's last value tile past
+    // its last key meet zero weights but must be finite, so they are cleared.
+    // The warp follows every box and shares in its release: a parity wait is
+    // only right for the phase after the last one seen.
+    bool ok = true;
+    uint32_t j = 0, nragged = 0;
+    for (int n = 0; ok; ++n) {
+      const long long u = unit_of(n);
+      if (u >= units) break;
+      const PromptItem it = load_item(p.items, int(u / H));
+      const int nt = max(tiles_of(it, 0), tiles_of(it, 1));
+      const int valid = it.kv_end - it.kv_begin - (nt - 1) * kKeys;
+      const bool ragged = nt > 0 && valid < kKeys && (valid & 15);
+      for (int kt = 0; kt < nt && ok; ++kt, ++j) {
+        for (uint32_t i = 0; i < 5 && ok; ++i) {
+          const uint32_t x = 5 * j + i;
+          ok = mbar_wait(&B->full[x % kRing], (x / kRing) & 1, abort_flag, kWaitNs);
+          if (ok && lane == 0 && i == 2) mbar_arrive(&B->k_empty[j & 1]);
+          if (ok && lane == 0 && i == 4 && !(ragged && kt == nt - 1)) mbar_arrive(&B->v_empty[j & 1]);
+        }
+      }
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
+      if (!ragged) continue;
+      const uint32_t xv = 5 * (j - 1) + 3;
+      const int tail = 16 - (valid & 15);
+      for (int i = lane; i < tail * 16; i += 32)
+        *reinterpret_cast<uint4*>(smem + kOffRing + ((xv + ((i >> 3) & 1)) % kRing) * kBox + (valid + (i >> 4)) * 128 +
+                                  (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&B->v_clean[nragged & 1]);
+        mbar_arrive(&B->v_empty[(j - 1) & 1]);
+      }
+      ++nragged;
     }
+    if (!ok) fail(B, p.status);
   } else if (warp < 8) {
     // ------------------------------------------------------------ softmax, epilogue
     const int t = warp >> 2, r = 32 * (warp & 3) + lane;  // query tile, row = tensor memory lane
@@ -398,7 +475,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         tc_fence_after();
         uint32_t s[4][32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, s[c]);
+        for (int c = 0; c < 4; ++c) tmem_ld32_async(ts + 32 * c, s[c]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tie(s[c]);
         if (kKeys * (kt + 1) > min(vis_first, keys)) {  // some row does not see some key of this tile
           const int lim = min(vis, keys) - kKeys * kt;
 #pragma unroll
@@ -407,11 +487,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             for (int i = 0; i < 32; ++i)
               if (32 * c + i >= lim) s[c][i] = 0xff800000u;  // -inf
         }
-        float mt = -INFINITY;
+        float mx[4];  // four chains
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < 4; ++c) {
+          mx[c] = __uint_as_float(s[c][0]);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) mt = fmaxf(mt, __uint_as_float(s[c][i]));
+          for (int i = 1; i < 31; i += 2)
+            mx[c] = fmaxf(fmaxf(mx[c], __uint_as_float(s[c][i])), __uint_as_float(s[c][i + 1]));
+          mx[c] = fmaxf(mx[c], __uint_as_float(s[c][31]));
+        }
+        const float mt = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), -INFINITY);
         float alpha = 1.f;
         bool rescale = false;
         if (kt == 0) {
@@ -419,37 +504,43 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         } else if ((mt - m) * p.scale_log2 > kRescale) {
           alpha = ex2_ftz((m - mt) * p.scale_log2);
           m = mt;
-          l *= alpha;
           rescale = true;
         }
         if (__any_sync(0xffffffffu, rescale)) {
           // s_full of this tile follows the PV of the tile before: O is complete up to there
+          l *= alpha;
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t o[32];
-            tmem_ld32(to + 32 * c, o);
+          for (int c = 0; c < 8; ++c) {
+            float o[16];
+            tmem_ld16(to + 16 * c, o);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-            tmem_st32(to + 32 * c, o);
+            for (int i = 0; i < 16; ++i) o[i] *= alpha;
+            tmem_st16(to + 16 * c, o);
           }
         }
         const float shift = m == -INFINITY ? 0.f : m * p.scale_log2;  // a row without keys: all weights 0
+        const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2), shift2 = pack2(-shift, -shift);
+        uint64_t sum[2] = {0, 0};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t w[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float a = ex2_ftz(fmaf(__uint_as_float(s[c][2 * i]), p.scale_log2, -shift));
-            const float b = ex2_ftz(fmaf(__uint_as_float(s[c][2 * i + 1]), p.scale_log2, -shift));
-            l += a + b;
+            const float2 x = unpack2(
+                fma2(pack2(__uint_as_float(s[c][2 * i]), __uint_as_float(s[c][2 * i + 1])), scale2, shift2));
+            const float a = ex2_ftz(x.x), b = ex2_ftz(x.y);
+            sum[i & 1] = add2(sum[i & 1], pack2(a, b));
             const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
             w[i] = *reinterpret_cast<const uint32_t*>(&v);
           }
           tmem_st16u(ts + 16 * c, w);
         }
+        const float2 total = unpack2(add2(sum[0], sum[1]));
+        l += total.x + total.y;
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(&B->p_full[t]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&B->p_full[t]);
       }
       if (!ok) break;
       const bool live = row < it.rows;
@@ -483,7 +574,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           }
         }
         tc_fence_before();
-        mbar_arrive(&B->o_free[t]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&B->o_free[t]);
       } else if (live) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) dst[i] = make_uint4(0, 0, 0, 0);
