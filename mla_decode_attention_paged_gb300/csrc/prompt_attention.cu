@@ -145,12 +145,13 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
 // ----- attention -------------------------------------------------------------------
 struct PromptBarriers {
   uint64_t q_full[2], q_empty[2];  // query tile loaded / read by its last QK
-  uint64_t full[kRing];            // ring box landed
+  uint64_t k_full[2], v_full[2];   // boxes of even / odd key tiles landed
   uint64_t k_empty[2], v_empty[2]; // boxes of even / odd key tiles read by both MMA threads
   uint64_t s_full[2];              // scores of a tile complete
-  uint64_t p_full[2];              // P written (and O rescaled where needed)
+  uint64_t p_full[2], p_rest[2];   // P of the first 96 keys written (and O rescaled where needed); of the last 32
   uint64_t o_full[2], o_free[2];   // output complete / read
   uint64_t v_clean[2];             // a ragged value tile's rows past the last key cleared
+  uint64_t turn[2];                // the MMA threads' turns
   uint64_t drain[2];
   uint32_t tmem_base;
   int abort;
@@ -205,6 +206,18 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return d;
 }
 
+__device__ __forceinline__ float row_max(const uint32_t (&s)[4][32]) {  // four chains
+  float mx[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    mx[c] = fmaxf(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
+#pragma unroll
+    for (int i = 2; i < 32; i += 2)
+      mx[c] = fmaxf(fmaxf(mx[c], __uint_as_float(s[c][i])), __uint_as_float(s[c][i + 1]));
+  }
+  return fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), -INFINITY);  // NaN scores do not count
+}
+
 __device__ __forceinline__ PromptItem load_item(const PromptItem* items, int i) {
   const int4* src = reinterpret_cast<const int4*>(items + i);
   const int4 a = src[0], b = src[1];
@@ -238,16 +251,19 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     for (int t = 0; t < 2; ++t) {
       mbar_init(&B->q_full[t], 1);
       mbar_init(&B->q_empty[t], 1);
+      mbar_init(&B->k_full[t], 1);
+      mbar_init(&B->v_full[t], 1);
       mbar_init(&B->k_empty[t], 3);  // both MMA threads and the clearing warp
       mbar_init(&B->v_empty[t], 3);
       mbar_init(&B->v_clean[t], 1);
       mbar_init(&B->s_full[t], 1);
+      mbar_init(&B->turn[t], 1);
       mbar_init(&B->drain[t], 1);
+      mbar_init(&B->p_rest[t], 4);
       mbar_init(&B->p_full[t], 4);  // one lane of each of the tile's softmax warps
       mbar_init(&B->o_full[t], 1);
       mbar_init(&B->o_free[t], 4);
     }
-    for (int i = 0; i < kRing; ++i) mbar_init(&B->full[i], 1);
     B->abort = 0;
     fence_mbar_init();
   }
@@ -297,11 +313,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           if (i == 1 && j >= 2) ok = mbar_wait(&B->v_empty[j & 1], ((j - 2) >> 1) & 1, abort_flag, kWaitNs);
           if (i == 3 && j >= 1) ok = mbar_wait(&B->k_empty[(j - 1) & 1], ((j - 1) >> 1) & 1, abort_flag, kWaitNs);
           if (!ok) break;
-          const uint32_t slot = (5 * j + i) % kRing;
-          uint8_t* dst = smem + kOffRing + slot * kBox;
-          mbar_arrive_expect_tx(&B->full[slot], kBox);
-          if (i == 2) tma_load_2d(dst, &map_kp, 0, key, &B->full[slot]);
-          else tma_load_3d(dst, i < 3 ? &map_kn : &map_v, (i == 1 || i == 4) ? 64 : 0, g, key, &B->full[slot]);
+          uint8_t* dst = smem + kOffRing + ((5 * j + i) % kRing) * kBox;
+          uint64_t* bar = i < 3 ? &B->k_full[j & 1] : &B->v_full[j & 1];
+          if (i == 0) mbar_arrive_expect_tx(bar, 3 * kBox);
+          if (i == 3) mbar_arrive_expect_tx(bar, 2 * kBox);
+          if (i == 2) tma_load_2d(dst, &map_kp, 0, key, bar);
+          else tma_load_3d(dst, i < 3 ? &map_kn : &map_v, (i == 1 || i == 4) ? 64 : 0, g, key, bar);
         }
       }
     }
@@ -311,37 +328,49 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     // One thread per query tile t, each with its own chain: QK of the first
     // key tile, then PV of a key tile and QK of the next.  MMAs of one thread
     // run in order, so the QK may overwrite the scores whose P the PV before
-    // it reads.  The pipe takes only a few MMAs ahead, so whatever a thread
-    // does between two of them shows unless the other thread's fill the gap.
-    // Both threads pass every key tile and release it together: a thread whose
-    // query tile does not see it arrives once it has landed (and not before,
-    // or it could stand in for the other thread's release two tiles earlier).
+    // it reads.
+    //
+    // The threads take turns, a product pair (PV, next QK) at a time: left to
+    // themselves their MMAs interleave and both query tiles come to wait for
+    // their softmax at the same time.  The pipe takes only a few MMAs ahead,
+    // so whatever a turn does between two MMAs shows: the next turn starts
+    // before this one's last four MMAs, and only thread 0 waits for boxes
+    // (thread 1's turn follows on the same boxes).  Both threads pass every key
+    // tile, whether their query tile sees it or not.
     const int t = warp - 9;
     constexpr uint32_t id_qk = idesc_bf16_f32(128, 128, false, false);
     constexpr uint32_t id_pv = idesc_bf16_f32(128, 128, false, true), id_pv64 = idesc_bf16_f32(128, 64, false, true);
     constexpr uint64_t kDescK = smem_desc(0, 16, 1024, kSwizzle128B);    // K-major
     constexpr uint64_t kDescMN = smem_desc(0, kBox, 1024, kSwizzle128B); // MN-major, 64-column blocks a box apart
     const uint32_t ds = tmem + kColS + 128 * t, dO = tmem + kColO + 128 * t;
-    const uint64_t q_desc = kDescK | desc_addr(sbase + t * kQTile);
+    const uint64_t q_desc = kDescK | desc_addr(sbase + t * kQTile), ring_k = kDescK | desc_addr(sbase + kOffRing),
+                   ring_v = kDescMN | desc_addr(sbase + kOffRing);
     bool ok = true;
-    uint32_t j = 0, nq = 0, np = 0, no = 0, nragged = 0;
-    // ring position x = 5 j + i: box x % 8, use number x / 8
-    auto wait_box = [&](uint32_t x) { return mbar_wait(&B->full[x % kRing], (x / kRing) & 1, abort_flag, kWaitNs); };
-    auto qk = [&](uint32_t jj, bool sees) -> bool {
-#pragma unroll
-      for (uint32_t i = 0; i < 3; ++i) {
-        const uint32_t x = 5 * jj + i;
-        if (!wait_box(x)) return false;
-        if (!sees) continue;
+    uint32_t j = 0, nq = 0, np = 0, no = 0, nragged = 0, nturn = 0;
+    // turn k of thread 1 follows turn k of thread 0, which follows turn k - 1 of thread 1
+    auto take_turn = [&]() {
+      const bool w = mbar_wait(&B->turn[t], (nturn & 1) ^ (t ^ 1), abort_flag, kWaitNs);
+      ++nturn;
+      return w;
+    };
+    auto pass_turn = [&]() { mbar_arrive(&B->turn[t ^ 1]); };
+    auto qk = [&](uint32_t jj, bool sees) -> bool {  // ends the turn
+      if (t == 0) {
+        if (!mbar_wait(&B->k_full[jj & 1], (jj >> 1) & 1, abort_flag, kWaitNs)) return false;
         tc_fence_after();
-        const uint64_t a = q_desc + i * (kBox >> 4), b = kDescK | desc_addr(sbase + kOffRing + (x % kRing) * kBox);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) mma_bf16(ds, a + 2 * kk, b + 2 * kk, id_qk, i > 0 || kk > 0);
       }
       if (sees) {
+#pragma unroll
+        for (uint32_t i = 0; i < 3; ++i) {
+          const uint64_t a = q_desc + i * (kBox >> 4), b = ring_k + ((5 * jj + i) % kRing) * (kBox >> 4);
+          if (i == 2) pass_turn();
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) mma_bf16(ds, a + 2 * kk, b + 2 * kk, id_qk, i > 0 || kk > 0);
+        }
         mma_commit(&B->s_full[t]);
         mma_commit(&B->k_empty[jj & 1]);
       } else {
+        pass_turn();
         mbar_arrive(&B->k_empty[jj & 1]);
       }
       return true;
@@ -356,37 +385,45 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         ok = mbar_wait(&B->q_full[t], nq & 1, abort_flag, kWaitNs);
         ++nq;
       }
-      ok = ok && qk(j, mine > 0);
+      if (!(ok = ok && take_turn())) break;
+      tc_fence_after();
+      ok = qk(j, mine > 0);
       if (ok && mine == 1) mma_commit(&B->q_empty[t]);
       for (int kt = 0; kt < nt && ok; ++kt, ++j) {
         const uint32_t xv = 5 * j + 3;
-        ok = wait_box(xv) && wait_box(xv + 1);
+        ok = t == 1 || mbar_wait(&B->v_full[j & 1], (j >> 1) & 1, abort_flag, kWaitNs);
         const int valid = it.kv_end - it.kv_begin - kt * kKeys;
-        if (valid < kKeys && (valid & 15)) {  // the last tile's rows past the keys are cleared first
+        if (t == 0 && valid < kKeys && (valid & 15)) {  // the last tile's rows past the keys are cleared first
           ok = ok && mbar_wait(&B->v_clean[nragged & 1], (nragged >> 1) & 1, abort_flag, kWaitNs);
           ++nragged;
         }
-        if (!ok) break;
-        if (kt < mine) {
+        if (ok && kt < mine) {
           if (kt == 0 && no > 0) ok = mbar_wait(&B->o_free[t], (no - 1) & 1, abort_flag, kWaitNs);
           ok = ok && mbar_wait(&B->p_full[t], np & 1, abort_flag, kWaitNs);
-          if (!ok) break;
           ++np;
+        }
+        if (!(ok = ok && take_turn())) break;
+        if (kt < mine) {
           tc_fence_after();
           const uint32_t s0 = xv % kRing;
-          const uint64_t v0 = kDescMN | desc_addr(sbase + kOffRing + s0 * kBox);
+          const uint64_t v0 = ring_v + s0 * (kBox >> 4);
           if (valid >= kKeys && s0 != kRing - 1) {
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk) mma_f16_tmem_a(dO, ds + 8 * kk, v0 + 128 * kk, id_pv, kt > 0 || kk > 0);
+            for (int kk = 0; kk < 6; ++kk) mma_f16_tmem_a(dO, ds + 8 * kk, v0 + 128 * kk, id_pv, kt > 0 || kk > 0);
+            if (!(ok = mbar_wait(&B->p_rest[t], (np - 1) & 1, abort_flag, kWaitNs))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 6; kk < 8; ++kk) mma_f16_tmem_a(dO, ds + 8 * kk, v0 + 128 * kk, id_pv, 1);
           } else {
+            if (!(ok = mbar_wait(&B->p_rest[t], (np - 1) & 1, abort_flag, kWaitNs))) break;
+            tc_fence_after();
             const int steps = (min(valid, kKeys) + 15) >> 4;
             if (s0 != kRing - 1) {
               for (int kk = 0; kk < steps; ++kk) mma_f16_tmem_a(dO, ds + 8 * kk, v0 + 128 * kk, id_pv, kt > 0 || kk > 0);
             } else {  // the second box wrapped to the ring's start: a product for each
-              const uint64_t v1 = kDescMN | desc_addr(sbase + kOffRing);
               for (int kk = 0; kk < steps; ++kk) {
                 mma_f16_tmem_a(dO, ds + 8 * kk, v0 + 128 * kk, id_pv64, kt > 0 || kk > 0);
-                mma_f16_tmem_a(dO + 64, ds + 8 * kk, v1 + 128 * kk, id_pv64, kt > 0 || kk > 0);
+                mma_f16_tmem_a(dO + 64, ds + 8 * kk, ring_v + 128 * kk, id_pv64, kt > 0 || kk > 0);
               }
             }
           }
@@ -401,6 +438,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (kt + 1 < nt) {
           ok = qk(j + 1, kt + 1 < mine);
           if (ok && kt + 2 == mine) mma_commit(&B->q_empty[t]);
+        } else {
+          pass_turn();
         }
       }
     }
@@ -411,7 +450,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     // ------------------------------------------------------------ ragged ends
     // PV reads whole 16-key steps; the rows of a range's last value tile past
     // its last key meet zero weights but must be finite, so they are cleared.
-    // The warp follows every box and shares in its release: a parity wait is
+    // The warp follows every tile and shares in its release: a parity wait is
     // only right for the phase after the last one seen.
     bool ok = true;
     uint32_t j = 0, nragged = 0;
@@ -423,12 +462,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       const int valid = it.kv_end - it.kv_begin - (nt - 1) * kKeys;
       const bool ragged = nt > 0 && valid < kKeys && (valid & 15);
       for (int kt = 0; kt < nt && ok; ++kt, ++j) {
-        for (uint32_t i = 0; i < 5 && ok; ++i) {
-          const uint32_t x = 5 * j + i;
-          ok = mbar_wait(&B->full[x % kRing], (x / kRing) & 1, abort_flag, kWaitNs);
-          if (ok && lane == 0 && i == 2) mbar_arrive(&B->k_empty[j & 1]);
-          if (ok && lane == 0 && i == 4 && !(ragged && kt == nt - 1)) mbar_arrive(&B->v_empty[j & 1]);
-        }
+        ok = mbar_wait(&B->k_full[j & 1], (j >> 1) & 1, abort_flag, kWaitNs);
+        if (ok && lane == 0) mbar_arrive(&B->k_empty[j & 1]);
+        ok = ok && mbar_wait(&B->v_full[j & 1], (j >> 1) & 1, abort_flag, kWaitNs);
+        if (ok && lane == 0 && !(ragged && kt == nt - 1)) mbar_arrive(&B->v_empty[j & 1]);
       }
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
@@ -487,26 +524,17 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             for (int i = 0; i < 32; ++i)
               if (32 * c + i >= lim) s[c][i] = 0xff800000u;  // -inf
         }
-        float mx[4];  // four chains
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          mx[c] = __uint_as_float(s[c][0]);
-#pragma unroll
-          for (int i = 1; i < 31; i += 2)
-            mx[c] = fmaxf(fmaxf(mx[c], __uint_as_float(s[c][i])), __uint_as_float(s[c][i + 1]));
-          mx[c] = fmaxf(mx[c], __uint_as_float(s[c][31]));
-        }
-        const float mt = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), -INFINITY);
+        const float mt = row_max(s);
         float alpha = 1.f;
-        bool rescale = false;
+        bool up = false;
         if (kt == 0) {
           m = mt;
         } else if ((mt - m) * p.scale_log2 > kRescale) {
           alpha = ex2_ftz((m - mt) * p.scale_log2);
           m = mt;
-          rescale = true;
+          up = true;
         }
-        if (__any_sync(0xffffffffu, rescale)) {
+        if (__any_sync(0xffffffffu, up)) {
           // s_full of this tile follows the PV of the tile before: O is complete up to there
           l *= alpha;
 #pragma unroll 1
@@ -518,11 +546,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             tmem_st16(to + 16 * c, o);
           }
         }
+        // The MMA thread starts on the first 96 keys while the last 32 are computed.
         const float shift = m == -INFINITY ? 0.f : m * p.scale_log2;  // a row without keys: all weights 0
         const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2), shift2 = pack2(-shift, -shift);
         uint64_t sum[2] = {0, 0};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        auto weights = [&](int c) {
           uint32_t w[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
@@ -534,13 +562,20 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             w[i] = *reinterpret_cast<const uint32_t*>(&v);
           }
           tmem_st16u(ts + 16 * c, w);
-        }
+        };
+#pragma unroll
+        for (int c = 0; c < 3; ++c) weights(c);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&B->p_full[t]);
+        weights(3);
         const float2 total = unpack2(add2(sum[0], sum[1]));
         l += total.x + total.y;
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&B->p_full[t]);
+        if (lane == 0) mbar_arrive(&B->p_rest[t]);
       }
       if (!ok) break;
       const bool live = row < it.rows;
