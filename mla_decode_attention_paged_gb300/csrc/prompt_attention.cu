@@ -224,6 +224,26 @@ __device__ __forceinline__ PromptItem load_item(const PromptItem* items, int i) 
   return {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 }
 
+// The same for a whole warp, uniform in the eyes of the compiler.
+__device__ __forceinline__ PromptItem load_item_uniform(const PromptItem* items, int i) {
+  PromptItem it = load_item(items, i);
+  it.q_row0 = __shfl_sync(0xffffffffu, it.q_row0, 0);
+  it.rows = __shfl_sync(0xffffffffu, it.rows, 0);
+  it.vis0 = __shfl_sync(0xffffffffu, it.vis0, 0);
+  it.kv_begin = __shfl_sync(0xffffffffu, it.kv_begin, 0);
+  it.kv_end = __shfl_sync(0xffffffffu, it.kv_end, 0);
+  return it;
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
 // Key tiles of query tile t (0, 1) of an item.
 __device__ __forceinline__ int tiles_of(const PromptItem& it, int t) {
   if (it.rows <= 128 * t) return 0;
@@ -246,7 +266,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   PromptBarriers* B = reinterpret_cast<PromptBarriers*>(smem + kOffMisc);
   const uint32_t sbase = smem_u32(smem);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // uniform in the eyes of the compiler, so that the MMA warps' descriptors live in uniform registers
+  const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) {
       mbar_init(&B->q_full[t], 1);
@@ -323,20 +344,21 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       }
     }
     if (!ok) fail(B, p.status);
-  } else if ((warp == 9 || warp == 10) && lane == 0) {
+  } else if (warp == 9 || warp == 10) {
     // ------------------------------------------------------------ MMA issue
-    // One thread per query tile t, each with its own chain: QK of the first
-    // key tile, then PV of a key tile and QK of the next.  MMAs of one thread
-    // run in order, so the QK may overwrite the scores whose P the PV before
-    // it reads.
+    // One warp per query tile t, each with its own chain: QK of the first key
+    // tile, then PV of a key tile and QK of the next.  MMAs of one thread run
+    // in order, so the QK may overwrite the scores whose P the PV before it
+    // reads.
     //
-    // The threads take turns, a product pair (PV, next QK) at a time: left to
+    // The warps take turns, a product pair (PV, next QK) at a time: left to
     // themselves their MMAs interleave and both query tiles come to wait for
-    // their softmax at the same time.  The pipe takes only a few MMAs ahead,
-    // so whatever a turn does between two MMAs shows: the next turn starts
-    // before this one's last four MMAs, and only thread 0 waits for boxes
-    // (thread 1's turn follows on the same boxes).  Both threads pass every key
-    // tile, whether their query tile sees it or not.
+    // their softmax at the same time.  The pipe takes only a few MMAs ahead, so
+    // whatever a turn does between two MMAs shows: the MMAs are straight-line
+    // code on uniform registers, the next turn starts before this one's last
+    // four MMAs, and only warp 9 waits for boxes (the other's turn follows on
+    // the same boxes).  Both warps pass every key tile, whether their query
+    // tile sees it or not.
     const int t = warp - 9;
     constexpr uint32_t id_qk = idesc_bf16_f32(128, 128, false, false);
     constexpr uint32_t id_pv = idesc_bf16_f32(128, 128, false, true), id_pv64 = idesc_bf16_f32(128, 64, false, true);
@@ -345,40 +367,49 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const uint32_t ds = tmem + kColS + 128 * t, dO = tmem + kColO + 128 * t;
     const uint64_t q_desc = kDescK | desc_addr(sbase + t * kQTile), ring_k = kDescK | desc_addr(sbase + kOffRing),
                    ring_v = kDescMN | desc_addr(sbase + kOffRing);
+    const bool leader = elect_one();
     bool ok = true;
     uint32_t j = 0, nq = 0, np = 0, no = 0, nragged = 0, nturn = 0;
-    // turn k of thread 1 follows turn k of thread 0, which follows turn k - 1 of thread 1
+    // turn k of tile 1 follows turn k of tile 0, which follows turn k - 1 of tile 1
     auto take_turn = [&]() {
       const bool w = mbar_wait(&B->turn[t], (nturn & 1) ^ (t ^ 1), abort_flag, kWaitNs);
       ++nturn;
+      tc_fence_after();
       return w;
     };
     auto pass_turn = [&]() { mbar_arrive(&B->turn[t ^ 1]); };
-    auto qk = [&](uint32_t jj, bool sees) -> bool {  // ends the turn
+    // QK of key tile jj, `sees`: this query tile sees it, `last`: none after it.  Ends the turn.
+    auto qk = [&](uint32_t jj, bool sees, bool last) -> bool {
+      const uint64_t b0 = ring_k + ((5 * jj) % kRing) * (kBox >> 4), b1 = ring_k + ((5 * jj + 1) % kRing) * (kBox >> 4),
+                     b2 = ring_k + ((5 * jj + 2) % kRing) * (kBox >> 4);
       if (t == 0) {
         if (!mbar_wait(&B->k_full[jj & 1], (jj >> 1) & 1, abort_flag, kWaitNs)) return false;
         tc_fence_after();
       }
-      if (sees) {
+      if (leader) {
+        if (sees) {
 #pragma unroll
-        for (uint32_t i = 0; i < 3; ++i) {
-          const uint64_t a = q_desc + i * (kBox >> 4), b = ring_k + ((5 * jj + i) % kRing) * (kBox >> 4);
-          if (i == 2) pass_turn();
+          for (int kk = 0; kk < 4; ++kk) mma_bf16(ds, q_desc + 2 * kk, b0 + 2 * kk, id_qk, kk > 0);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) mma_bf16(ds, a + 2 * kk, b + 2 * kk, id_qk, i > 0 || kk > 0);
+          for (int kk = 0; kk < 4; ++kk) mma_bf16(ds, q_desc + (kBox >> 4) + 2 * kk, b1 + 2 * kk, id_qk, 1);
+          pass_turn();
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) mma_bf16(ds, q_desc + 2 * (kBox >> 4) + 2 * kk, b2 + 2 * kk, id_qk, 1);
+          mma_commit(&B->s_full[t]);
+          mma_commit(&B->k_empty[jj & 1]);
+          if (last) mma_commit(&B->q_empty[t]);
+        } else {
+          pass_turn();
+          mbar_arrive(&B->k_empty[jj & 1]);
         }
-        mma_commit(&B->s_full[t]);
-        mma_commit(&B->k_empty[jj & 1]);
-      } else {
-        pass_turn();
-        mbar_arrive(&B->k_empty[jj & 1]);
       }
+      __syncwarp();
       return true;
     };
     for (int n = 0; ok; ++n) {
       const long long u = unit_of(n);
       if (u >= units) break;
-      const PromptItem it = load_item(p.items, int(u / H));
+      const PromptItem it = load_item_uniform(p.items, int(u / H));
       const int mine = tiles_of(it, t), nt = max(mine, tiles_of(it, t ^ 1));
       if (nt == 0) continue;
       if (mine > 0) {
@@ -386,11 +417,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         ++nq;
       }
       if (!(ok = ok && take_turn())) break;
-      tc_fence_after();
-      ok = qk(j, mine > 0);
-      if (ok && mine == 1) mma_commit(&B->q_empty[t]);
+      ok = qk(j, mine > 0, mine == 1);
       for (int kt = 0; kt < nt && ok; ++kt, ++j) {
-        const uint32_t xv = 5 * j + 3;
+        const uint32_t s0 = (5 * j + 3) % kRing;
+        const uint64_t v0 = ring_v + s0 * (kBox >> 4);
         ok = t == 1 || mbar_wait(&B->v_full[j & 1], (j >> 1) & 1, abort_flag, kWaitNs);
         const int valid = it.kv_end - it.kv_begin - kt * kKeys;
         if (t == 0 && valid < kKeys && (valid & 15)) {  // the last tile's rows past the keys are cleared first
@@ -400,52 +430,51 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (ok && kt < mine) {
           if (kt == 0 && no > 0) ok = mbar_wait(&B->o_free[t], (no - 1) & 1, abort_flag, kWaitNs);
           ok = ok && mbar_wait(&B->p_full[t], np & 1, abort_flag, kWaitNs);
-          ++np;
         }
         if (!(ok = ok && take_turn())) break;
         if (kt < mine) {
+          const bool whole = valid >= kKeys && s0 != kRing - 1;
+          if (whole && leader) {
+#pragma unroll
+            for (int kk = 0; kk < 6; ++kk) mma_f16_tmem_a(dO, ds + 8 * kk, v0 + 128 * kk, id_pv, kk > 0 ? 1 : kt);
+          }
+          if (!(ok = mbar_wait(&B->p_rest[t], np & 1, abort_flag, kWaitNs))) break;
+          ++np;
           tc_fence_after();
-          const uint32_t s0 = xv % kRing;
-          const uint64_t v0 = ring_v + s0 * (kBox >> 4);
-          if (valid >= kKeys && s0 != kRing - 1) {
+          if (leader) {
+            if (whole) {
 #pragma unroll
-            for (int kk = 0; kk < 6; ++kk) mma_f16_tmem_a(dO, ds + 8 * kk, v0 + 128 * kk, id_pv, kt > 0 || kk > 0);
-            if (!(ok = mbar_wait(&B->p_rest[t], (np - 1) & 1, abort_flag, kWaitNs))) break;
-            tc_fence_after();
+              for (int kk = 6; kk < 8; ++kk) mma_f16_tmem_a(dO, ds + 8 * kk, v0 + 128 * kk, id_pv, 1);
+            } else {
+              const int steps = (min(valid, kKeys) + 15) >> 4;
+              if (s0 != kRing - 1) {
+                for (int kk = 0; kk < steps; ++kk) mma_f16_tmem_a(dO, ds + 8 * kk, v0 + 128 * kk, id_pv, kt | kk);
+              } else {  // the second box wrapped to the ring's start: a product for each
 #pragma unroll
-            for (int kk = 6; kk < 8; ++kk) mma_f16_tmem_a(dO, ds + 8 * kk, v0 + 128 * kk, id_pv, 1);
-          } else {
-            if (!(ok = mbar_wait(&B->p_rest[t], (np - 1) & 1, abort_flag, kWaitNs))) break;
-            tc_fence_after();
-            const int steps = (min(valid, kKeys) + 15) >> 4;
-            if (s0 != kRing - 1) {
-              for (int kk = 0; kk < steps; ++kk) mma_f16_tmem_a(dO, ds + 8 * kk, v0 + 128 * kk, id_pv, kt > 0 || kk > 0);
-            } else {  // the second box wrapped to the ring's start: a product for each
-              for (int kk = 0; kk < steps; ++kk) {
-                mma_f16_tmem_a(dO, ds + 8 * kk, v0 + 128 * kk, id_pv64, kt > 0 || kk > 0);
-                mma_f16_tmem_a(dO + 64, ds + 8 * kk, ring_v + 128 * kk, id_pv64, kt > 0 || kk > 0);
+                for (int kk = 0; kk < 8; ++kk) {
+                  if (kk >= steps) break;
+                  mma_f16_tmem_a(dO, ds + 8 * kk, v0 + 128 * kk, id_pv64, kk > 0 ? 1 : kt);
+                  mma_f16_tmem_a(dO + 64, ds + 8 * kk, ring_v + 128 * kk, id_pv64, kk > 0 ? 1 : kt);
+                }
               }
             }
+            mma_commit(&B->v_empty[j & 1]);
+            if (kt == mine - 1) mma_commit(&B->o_full[t]);
           }
-          mma_commit(&B->v_empty[j & 1]);
-          if (kt == mine - 1) {
-            mma_commit(&B->o_full[t]);
-            ++no;
-          }
-        } else {
+          if (kt == mine - 1) ++no;
+        } else if (leader) {
           mbar_arrive(&B->v_empty[j & 1]);
         }
-        if (kt + 1 < nt) {
-          ok = qk(j + 1, kt + 1 < mine);
-          if (ok && kt + 2 == mine) mma_commit(&B->q_empty[t]);
-        } else {
-          pass_turn();
-        }
+        if (kt + 1 < nt) ok = qk(j + 1, kt + 1 < mine, kt + 2 == mine);
+        else if (leader) pass_turn();
       }
     }
-    if (!ok) fail(B, p.status);
-    mma_commit(&B->drain[t]);  // every MMA issued completes before teardown
-    mbar_wait(&B->drain[t], 0, abort_flag, kWaitNs);
+    if (leader) {
+      if (!ok) fail(B, p.status);
+      mma_commit(&B->drain[t]);  // every MMA issued completes before teardown
+      mbar_wait(&B->drain[t], 0, abort_flag, kWaitNs);
+    }
+    __syncwarp();
   } else if (warp == 11) {
     // ------------------------------------------------------------ ragged ends
     // PV reads whole 16-key steps; the rows of a range's last value tile past
