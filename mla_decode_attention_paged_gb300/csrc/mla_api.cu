@@ -406,17 +406,23 @@ SparseLayout sparse_layout(const mla_dims* d, int batch, int top_k, size_t decod
 
 // Workspace of mla_prompt_attention: the status word and item count, the
 // first block of every sequence, the list of items (a sequence of n rows has
-// at most n / 256 + 1 blocks).
+// at most n / 256 + 1 blocks), and the partial results of split blocks.
 struct PromptLayout {
-  size_t status, block_start, items, total;
+  size_t status, block_start, items, arrived, partial_ml, partial_o, total;
+  int partial_rows;
 };
 
-PromptLayout prompt_layout(int num_seqs, int n_q) {
+PromptLayout prompt_layout(int num_seqs, int n_q, int heads) {
   PromptLayout L;
   size_t off = 0;
+  const long long most = (long long)n_q * heads * kPromptMaxPieces;
+  L.partial_rows = most < kPromptPartialRows ? int(most) : kPromptPartialRows;
   L.status = off;       off = align256(off + 8);
   L.block_start = off;  off = align256(off + 4 * (size_t(num_seqs) + 1));
-  L.items = off;        off = align256(off + sizeof(PromptItem) * (size_t(n_q) / 256 + num_seqs));
+  L.items = off;        off = align256(off + sizeof(PromptItem) * (size_t(n_q) / kPromptRows + num_seqs + kPromptExtraItems));
+  L.arrived = off;      off = align256(off + size_t(4) * kPromptMaxSplit * heads * 8);
+  L.partial_ml = off;   off = align256(off + sizeof(float2) * L.partial_rows);
+  L.partial_o = off;    off = align256(off + size_t(4) * kVDim * L.partial_rows);
   L.total = off;
   return L;
 }
@@ -544,7 +550,7 @@ int mla_expand_kv(const mla_dims* d, const void* c_kv, int32_t n_rows, const voi
 size_t mla_prompt_attention_workspace_size(const mla_dims* d, int32_t num_seqs, int32_t n_q) {
   if (mla_check_dims(d) != MLA_OK || num_seqs <= 0 || num_seqs > MLA_MAX_PROMPT_SEQS || n_q < 0) return 0;
   if ((long long)n_q * d->num_heads > kMaxQueryRows) return 0;
-  return prompt_layout(num_seqs, n_q).total;
+  return prompt_layout(num_seqs, n_q, d->num_heads).total;
 }
 
 int mla_prompt_attention(const mla_dims* d, const void* q_nope, const void* q_pe, int32_t n_q, const void* k_nope,
@@ -564,7 +570,7 @@ int mla_prompt_attention(const mla_dims* d, const void* q_nope, const void* q_pe
   if (!aligned(q_nope, 16) || !aligned(q_pe, 16) || !aligned(k_nope, 16) || !aligned(k_pe, 16) || !aligned(v, 16) ||
       !aligned(out, 16) || (lse_out && !aligned(lse_out, 4)))
     return MLA_ERR_INVALID_ARG;
-  const PromptLayout L = prompt_layout(num_seqs, n_q);
+  const PromptLayout L = prompt_layout(num_seqs, n_q, d->num_heads);
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < L.total) return MLA_ERR_WORKSPACE;
   char* ws = static_cast<char*>(workspace);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -582,6 +588,10 @@ int mla_prompt_attention(const mla_dims* d, const void* q_nope, const void* q_pe
   p.status = reinterpret_cast<int*>(ws + L.status);
   p.block_start = reinterpret_cast<int*>(ws + L.block_start);
   p.items = reinterpret_cast<PromptItem*>(ws + L.items);
+  p.arrived = reinterpret_cast<int*>(ws + L.arrived);
+  p.partial_o = reinterpret_cast<float*>(ws + L.partial_o);
+  p.partial_ml = reinterpret_cast<float2*>(ws + L.partial_ml);
+  p.partial_rows = L.partial_rows;
   p.n_q = n_q;
   p.n_k = n_k;
   p.num_seqs = num_seqs;

@@ -99,14 +99,24 @@ struct ExpandParams {
 
 // Causal attention over packed prompts (mla_prompt_attention).  The plan
 // kernel lists the work, longest first: one item per block of up to 256 query
-// rows of a sequence; the attention kernel runs every item for every head.
-struct PromptItem {
-  int q_row0, rows;        // first packed query row and number of rows (1..256)
-  int k_row0;              // first packed key row of the sequence
-  int vis0;                // keys that row 0 sees (row i sees vis0 + i; none if that is <= 0)
-  int kv_begin, kv_end;    // key range of this item, relative to k_row0
-  int slot, pieces;        // split keys: first partial of the block and number of its pieces (1: not split)
+// rows of a sequence, or several over parts of its keys where there are few
+// blocks; the attention kernel runs every item for every head.
+struct alignas(16) PromptItem {
+  int q_row0, rows;      // first packed query row and number of rows (1..256)
+  int k_row0;            // first packed key row of the sequence
+  int vis0;              // keys that row 0 sees (row i sees vis0 + i; none if that is <= 0)
+  int kv_begin, kv_end;  // key range of this item, relative to k_row0
+  int pieces, piece;     // items that share the block's keys, and which one this is
+  int split;             // pieces > 1: number of the block among the split ones
+  int partial;           // pieces > 1: first partial row of the block
+  int pad[2];
 };
+constexpr int kPromptRows = 256;         // query rows of a block
+constexpr int kPromptMaxPieces = 32;     // pieces of one block
+constexpr int kPromptMaxSplit = 64;      // split blocks of one call
+constexpr int kPromptExtraItems = 512;   // items beyond one per block
+// partial rows of one call: two rounds of blocks on 152 SMs
+constexpr int kPromptPartialRows = 2 * 152 * kPromptRows;
 struct PromptParams {
   const int* cu_q;           // [num_seqs + 1]
   const int* cu_k;           // [num_seqs + 1]
@@ -115,8 +125,11 @@ struct PromptParams {
   float* lse_out;            // [n_q, heads] or null
   int* status;               // workspace: status word, then the number of items
   int* block_start;          // workspace: [num_seqs + 1] first block of each sequence
-  PromptItem* items;         // workspace: [n_q / 256 + num_seqs]
-  int n_q, n_k, num_seqs, heads, kv_heads, sm_count;
+  PromptItem* items;         // workspace: [n_q / 256 + num_seqs + kPromptExtraItems]
+  int* arrived;              // workspace: [kPromptMaxSplit][heads][8] pieces done, per 32 rows
+  float* partial_o;          // workspace: [partial_rows][128] unnormalised outputs
+  float2* partial_ml;        // workspace: [partial_rows] reference maximum (unscaled) and sum
+  int n_q, n_k, num_seqs, heads, kv_heads, sm_count, partial_rows;
   float scale_log2;          // softmax_scale * log2(e)
   float scale;
 };

@@ -46,7 +46,6 @@ namespace {
 using namespace ptx;
 using namespace dc;
 
-constexpr int kBlockRows = 256;                    // query rows of an item
 constexpr int kKeys = 128;                         // keys of a tile
 constexpr uint32_t kBox = 128 * 128;               // [128 rows x 64 columns] bf16, SW128: 16 KB
 constexpr uint32_t kQTile = 3 * kBox;              // q_nope columns 0-63, 64-127, q_pe
@@ -64,21 +63,35 @@ static_assert(kSmem <= 232448, "dynamic shared memory of one CTA");
 
 // ----- plan ----------------------------------------------------------------------
 // One CTA: checks cu_q and cu_k, cuts every sequence into blocks of 256 query
-// rows and lists them by falling number of key tiles (a counting sort), so
-// that dealing the list round-robin over the CTAs balances them.  A sequence
-// whose offsets decrease or pass the end, and every one after it, is skipped
-// and reported; this also bounds the list.
+// rows, splits the keys of long blocks where there are too few blocks to fill
+// the SMs, and lists the items by falling number of key tiles (a counting
+// sort), so that dealing the list round-robin over the CTAs balances them.  A
+// sequence whose offsets decrease or pass the end, and every one after it, is
+// skipped and reported; this also bounds the list.
+//
+// Split: candidate k (one warp each) cuts the longest block into k + 1 pieces
+// and every block into pieces of at most that length.  Its estimate, in key
+// tiles: the longest piece where every unit (item, head) has its own CTA, else
+// the mean load and a share of the longest piece for the uneven end, plus
+// three tiles for a unit's start and end and two for the merge.  The pieces of
+// a block depend on the lengths and the SM count alone, and are merged in
+// order, so results repeat bit for bit.
 __device__ __forceinline__ int key_tiles(int vis_last) { return vis_last > 0 ? (vis_last + kKeys - 1) / kKeys : 0; }
+__device__ __forceinline__ int pieces_of(int tiles, int longest) { return tiles > longest ? (tiles + longest - 1) / longest : 1; }
 
 __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams p) {
   __shared__ int scan_tmp[32];
   __shared__ int hist[kBuckets];
-  __shared__ int carry, first_bad;
+  __shared__ int carry, first_bad, longest, piece_tiles, split_count, partial_count;
+  __shared__ float estimate[kPlanThreads / 32];
   griddep_wait();
   griddep_launch_dependents();
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     carry = 0;
+    longest = 0;
+    split_count = 0;
+    partial_count = 0;
     first_bad = p.num_seqs;
     p.status[0] = MLA_OK;
   }
@@ -93,7 +106,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
   if (tid == 0 && good < p.num_seqs) set_status(p.status, MLA_ERR_DEVICE_BOUNDS);
   for (int base = 0; base < good; base += kPlanThreads) {
     const int b = base + tid;
-    const int blocks = b < good ? (p.cu_q[b + 1] - p.cu_q[b] + kBlockRows - 1) / kBlockRows : 0;
+    const int blocks = b < good ? (p.cu_q[b + 1] - p.cu_q[b] + kPromptRows - 1) / kPromptRows : 0;
     int total;
     const int ex = block_exclusive_scan(blocks, scan_tmp, &total);
     if (b < good) p.block_start[b] = carry + ex;
@@ -101,44 +114,104 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
     if (tid == 0) carry += total;
     __syncthreads();
   }
-  const int n = carry;
-  if (tid == 0) p.status[1] = n;
-  __syncthreads();  // block_start is read below by other threads of this CTA
-  auto block_item = [&](int i, int& bucket) {
-    int lo = 0, hi = good - 1;  // last sequence whose first block is <= i and that has blocks
+  const int n = carry;  // block_start is read below by other threads: the barriers above order it
+  auto block_item = [&](int i) {
+    int lo = 0, hi = good - 1;  // last sequence whose first block is <= i
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (p.block_start[mid] <= i) lo = mid; else hi = mid - 1;
     }
     const int b = lo, q0 = p.cu_q[b], lq = p.cu_q[b + 1] - q0, k0 = p.cu_k[b], lk = p.cu_k[b + 1] - k0;
-    const int r0 = (i - p.block_start[b]) * kBlockRows;
+    const int r0 = (i - p.block_start[b]) * kPromptRows;
     PromptItem it;
     it.q_row0 = q0 + r0;
-    it.rows = min(kBlockRows, lq - r0);
+    it.rows = min(kPromptRows, lq - r0);
     it.k_row0 = k0;
     it.vis0 = lk - lq + r0 + 1;
     it.kv_begin = 0;
     it.kv_end = max(0, it.vis0 + it.rows - 1);
-    it.slot = -1;
     it.pieces = 1;
-    bucket = kBuckets - 1 - min(kBuckets - 1, key_tiles(it.kv_end));
+    it.piece = 0;
+    it.split = -1;
+    it.partial = 0;
+    it.pad[0] = it.pad[1] = 0;
     return it;
   };
+  // more units than two rounds are never split (below): their blocks need no estimate
+  const int G = p.sm_count;
+  const bool few = (long long)n * p.heads <= 2 * G;
+  if (few) {
+    for (int i = tid; i < n; i += kPlanThreads) atomicMax(&longest, key_tiles(block_item(i).kv_end));
+    __syncthreads();
+    const int T = (longest + warp) / (warp + 1);  // ceil(longest / (warp + 1))
+    int pieces = 0, top = 0, rows = 0, splits = 0;
+    long long tiles = 0;
+    for (int i = lane; i < n && T > 0; i += 32) {
+      const PromptItem it = block_item(i);
+      const int t = key_tiles(it.kv_end), c = pieces_of(t, T);
+      pieces += c;
+      tiles += t;
+      top = max(top, (t + c - 1) / c);
+      if (c > 1) {
+        rows += c * it.rows;
+        ++splits;
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      pieces += __shfl_xor_sync(0xffffffffu, pieces, o);
+      tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      rows += __shfl_xor_sync(0xffffffffu, rows, o);
+      splits += __shfl_xor_sync(0xffffffffu, splits, o);
+    }
+    const float units = float(pieces) * p.heads, load = float(tiles) * p.heads + 3.f * units;
+    float e = fmaxf(top + 3.f, load / G + (units > G ? 0.35f * top : 0.f));
+    if (warp > 0) e = 1.1f * (e + 2.f);  // only where it clearly pays
+    if (T == 0 || units > 2 * G || splits > kPromptMaxSplit || pieces > n + kPromptExtraItems ||
+        (long long)rows * p.heads > p.partial_rows)
+      e = warp > 0 ? 1e30f : 1e29f;
+    if (lane == 0) estimate[warp] = e;
+    __syncthreads();
+    if (tid == 0) {
+      int best = 0;
+      for (int k = 1; k < kPromptMaxPieces; ++k)
+        if (estimate[k] < estimate[best]) best = k;
+      piece_tiles = best == 0 ? 0x7fffffff : (longest + best) / (best + 1);
+    }
+  } else if (tid == 0) {
+    piece_tiles = 0x7fffffff;
+  }
+  __syncthreads();
+  const int T = piece_tiles;
   for (int i = tid; i < n; i += kPlanThreads) {
-    int bucket;
-    block_item(i, bucket);
-    atomicAdd(&hist[bucket], 1);
+    const int t = key_tiles(block_item(i).kv_end), c = pieces_of(t, T);
+    for (int q = 0; q < c; ++q)
+      atomicAdd(&hist[kBuckets - 1 - min(kBuckets - 1, (q + 1) * t / c - q * t / c)], 1);
   }
   __syncthreads();
   int total;
   const int ex = block_exclusive_scan(hist[tid], scan_tmp, &total);
   hist[tid] = ex;
+  if (tid == 0) p.status[1] = total;
   __syncthreads();
   // the order inside a bucket is arbitrary: it decides which CTA runs an item, not its result
   for (int i = tid; i < n; i += kPlanThreads) {
-    int bucket;
-    const PromptItem it = block_item(i, bucket);
-    p.items[atomicAdd(&hist[bucket], 1)] = it;
+    PromptItem it = block_item(i);
+    const int keys = it.kv_end, t = key_tiles(keys), c = pieces_of(t, T);
+    it.pieces = c;
+    if (c > 1) {
+      it.split = atomicAdd(&split_count, 1);
+      it.partial = atomicAdd(&partial_count, c * it.rows * p.heads);
+      for (int e = 0; e < p.heads * 8; ++e) p.arrived[size_t(it.split) * p.heads * 8 + e] = 0;
+    }
+    for (int q = 0; q < c; ++q) {
+      const int t0 = q * t / c, t1 = (q + 1) * t / c;
+      it.piece = q;
+      it.kv_begin = t0 * kKeys;
+      it.kv_end = min(keys, t1 * kKeys);
+      p.items[atomicAdd(&hist[kBuckets - 1 - min(kBuckets - 1, t1 - t0)], 1)] = it;
+    }
   }
 }
 
@@ -218,10 +291,17 @@ __device__ __forceinline__ float row_max(const uint32_t (&s)[4][32]) {  // four 
   return fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), -INFINITY);  // NaN scores do not count
 }
 
+// Volatile: the softmax warps load an item once more for their epilogue rather
+// than hold its fields in registers through the key loop.
+__device__ __forceinline__ int4 load_int4(const int4* src) {
+  int4 v;
+  asm volatile("ld.global.v4.s32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(src));
+  return v;
+}
 __device__ __forceinline__ PromptItem load_item(const PromptItem* items, int i) {
   const int4* src = reinterpret_cast<const int4*>(items + i);
-  const int4 a = src[0], b = src[1];
-  return {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  const int4 a = load_int4(src), b = load_int4(src + 1), c = load_int4(src + 2);
+  return {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, {0, 0}};
 }
 
 // The same for a whole warp, uniform in the eyes of the compiler.
@@ -244,6 +324,69 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
+// 1 / l; 0 for a row without keys (l = 0); NaN stays NaN.
+__device__ __forceinline__ float inverse_sum(float l) { return l > 0.f ? __frcp_rn(l) : (l == 0.f ? 0.f : l); }
+
+// Eight outputs, scaled and rounded to bf16.
+__device__ __forceinline__ uint4 pack_out(const uint32_t* o, float inv) {
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+    w[e] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// One row of a split block per lane: out = sum_i w_i O_i / sum_i w_i l_i with
+// w_i = 2^((m_i - max m) scale_log2) over its pieces; pieces without keys for
+// the row (l = 0) carry weight 0 and no output.  The partials are read past L1:
+// other SMs wrote them during this kernel.
+static __device__ __noinline__ void merge_rows(const PromptParams& p, const PromptItem& it, size_t prow0, size_t orow,
+                                               bool live) {
+  if (!live) return;
+  float top = -INFINITY;
+  for (int i = 0; i < it.pieces; ++i) {
+    const float2 ml = __ldcg(p.partial_ml + prow0 + size_t(i) * it.rows);
+    if (ml.y != 0.f) top = fmaxf(top, ml.x);
+  }
+  const float base = top == -INFINITY ? 0.f : top;
+  float l = 0.f;
+  for (int i = 0; i < it.pieces; ++i) {
+    const float2 ml = __ldcg(p.partial_ml + prow0 + size_t(i) * it.rows);
+    if (ml.y != 0.f) l = fmaf(ml.y, ex2_ftz((ml.x - base) * p.scale_log2), l);
+  }
+  const float inv = inverse_sum(l);
+  uint4* dst = reinterpret_cast<uint4*>(p.out + orow * kVDim);
+#pragma unroll 1
+  for (int c = 0; c < kVDim; c += 32) {
+    float acc[32];
+#pragma unroll
+    for (int e = 0; e < 32; ++e) acc[e] = 0.f;
+    for (int i = 0; i < it.pieces; ++i) {
+      const size_t prow = prow0 + size_t(i) * it.rows;
+      const float2 ml = __ldcg(p.partial_ml + prow);
+      if (ml.y == 0.f) continue;
+      const float w = ex2_ftz((ml.x - base) * p.scale_log2);
+      const float4* src = reinterpret_cast<const float4*>(p.partial_o + prow * kVDim + c);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float4 x = __ldcg(src + e);
+        acc[4 * e] = fmaf(x.x, w, acc[4 * e]);
+        acc[4 * e + 1] = fmaf(x.y, w, acc[4 * e + 1]);
+        acc[4 * e + 2] = fmaf(x.z, w, acc[4 * e + 2]);
+        acc[4 * e + 3] = fmaf(x.w, w, acc[4 * e + 3]);
+      }
+    }
+    uint32_t o[32];
+#pragma unroll
+    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(acc[e]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) dst[c / 8 + e] = pack_out(&o[8 * e], inv);
+  }
+  if (p.lse_out) p.lse_out[orow] = l == 0.f ? -INFINITY : base * p.scale + logf(l);
+}
+
 // Key tiles of query tile t (0, 1) of an item.
 __device__ __forceinline__ int tiles_of(const PromptItem& it, int t) {
   if (it.rows <= 128 * t) return 0;
@@ -253,9 +396,9 @@ __device__ __forceinline__ int tiles_of(const PromptItem& it, int t) {
 
 // The CTA's n-th unit of work (item, head), dealt in a serpentine over the
 // sorted list: CTA c takes c, 2G - 1 - c, 2G + c, ...
-__device__ __forceinline__ long long unit_of(int n) {
+__device__ __forceinline__ int unit_of(int n) {  // units: at most 2^26 and two rounds
   const int G = gridDim.x, c = blockIdx.x;
-  return (long long)n * G + ((n & 1) ? G - 1 - c : c);
+  return n * G + ((n & 1) ? G - 1 - c : c);
 }
 
 __global__ void __launch_bounds__(kPromptThreads, 1)
@@ -300,7 +443,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   griddep_launch_dependents();
   const volatile int* abort_flag = &B->abort;
   const int H = p.heads, group = H / p.kv_heads;
-  const long long units = (long long)p.status[1] * H;
+  const int units = p.status[1] * H;
 
   if (warp == 8 && lane == 0) {
     // ------------------------------------------------------------ TMA producer
@@ -310,10 +453,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     bool ok = true;
     uint32_t j = 0, nq[2] = {0, 0};
     for (int n = 0; ok; ++n) {
-      const long long u = unit_of(n);
+      const int u = unit_of(n);
       if (u >= units) break;
-      const PromptItem it = load_item(p.items, int(u / H));
-      const int h = int(u % H), g = h / group;
+      const PromptItem it = load_item(p.items, u / H);
+      const int h = u % H, g = h / group;
       const int nt0 = tiles_of(it, 0), nt1 = tiles_of(it, 1), nt = max(nt0, nt1);
       for (int t = 0; t < 2 && ok; ++t) {
         if (!(t ? nt1 : nt0)) continue;
@@ -407,9 +550,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       return true;
     };
     for (int n = 0; ok; ++n) {
-      const long long u = unit_of(n);
+      const int u = unit_of(n);
       if (u >= units) break;
-      const PromptItem it = load_item_uniform(p.items, int(u / H));
+      const PromptItem it = load_item_uniform(p.items, u / H);
       const int mine = tiles_of(it, t), nt = max(mine, tiles_of(it, t ^ 1));
       if (nt == 0) continue;
       if (mine > 0) {
@@ -484,9 +627,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     bool ok = true;
     uint32_t j = 0, nragged = 0;
     for (int n = 0; ok; ++n) {
-      const long long u = unit_of(n);
+      const int u = unit_of(n);
       if (u >= units) break;
-      const PromptItem it = load_item(p.items, int(u / H));
+      const PromptItem it = load_item(p.items, u / H);
       const int nt = max(tiles_of(it, 0), tiles_of(it, 1));
       const int valid = it.kv_end - it.kv_begin - (nt - 1) * kKeys;
       const bool ragged = nt > 0 && valid < kKeys && (valid & 15);
@@ -523,13 +666,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     bool ok = true;
     uint32_t ns = 0, no = 0;
     for (int n = 0; ok; ++n) {
-      const long long u = unit_of(n);
+      const int u = unit_of(n);
       if (u >= units) break;
-      const PromptItem it = load_item(p.items, int(u / H));
-      const int h = int(u % H), nt = tiles_of(it, t);
-      const int row = 128 * t + r;                  // row of the item
-      const int vis = it.vis0 + row - it.kv_begin;  // keys of this item's range that the row sees
-      const int vis_first = it.vis0 + 128 * t - it.kv_begin, keys = it.kv_end - it.kv_begin;
+      int nt, vis, vis_first, keys;
+      {
+        const PromptItem it = load_item(p.items, u / H);
+        nt = tiles_of(it, t);
+        vis = it.vis0 + 128 * t + r - it.kv_begin;  // keys of this item's range that the row sees
+        vis_first = it.vis0 + 128 * t - it.kv_begin;
+        keys = it.kv_end - it.kv_begin;
+      }
       float m = -INFINITY, l = 0.f;
       for (int kt = 0; kt < nt; ++kt) {
         ok = mbar_wait(&B->s_full[t], ns & 1, abort_flag, kWaitNs);
@@ -607,9 +753,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (lane == 0) mbar_arrive(&B->p_rest[t]);
       }
       if (!ok) break;
+      const PromptItem it = load_item(p.items, u / H);
+      const int h = u % H, row = 128 * t + r;  // row of the item
       const bool live = row < it.rows;
       const size_t orow = size_t(it.q_row0 + row) * H + h;
-      uint4* dst = reinterpret_cast<uint4*>(p.out + orow * kVDim);
       if (nt > 0) {
         ok = mbar_wait(&B->o_full[t], no & 1, abort_flag, kWaitNs);
         if (!__all_sync(0xffffffffu, ok)) {
@@ -618,34 +765,60 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         ++no;
         tc_fence_after();
-        const float inv = l > 0.f ? __frcp_rn(l) : (l == 0.f ? 0.f : l);  // a row without keys: 0; NaN stays NaN
+      }
+      if (it.pieces == 1) {
+        uint4* dst = reinterpret_cast<uint4*>(p.out + orow * kVDim);
+        if (nt > 0) {
+          const float inv = inverse_sum(l);
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t o[32];
-          tmem_ld32(to + 32 * c, o);
-          if (live) {
+          for (int c = 0; c < 4; ++c) {
+            uint32_t o[32];
+            tmem_ld32(to + 32 * c, o);
+            if (live) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t w[4];
+              for (int i = 0; i < 4; ++i) dst[4 * c + i] = pack_out(&o[8 * i], inv);
+            }
+          }
+        } else if (live) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(o[8 * i + 2 * e]) * inv,
-                                                               __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
-                w[e] = *reinterpret_cast<const uint32_t*>(&v);
-              }
-              dst[4 * c + i] = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int i = 0; i < 16; ++i) dst[i] = make_uint4(0, 0, 0, 0);
+        }
+        if (live && p.lse_out) p.lse_out[orow] = l == 0.f ? -INFINITY : m * p.scale + logf(l);
+      } else if (__any_sync(0xffffffffu, live)) {
+        // A piece of a split block: its unnormalised output, reference maximum
+        // and sum go to the workspace; the warp that brings the last piece of
+        // these 32 rows merges all of them, in order.
+        const size_t prow0 = size_t(it.partial) + size_t(h) * it.pieces * it.rows + row;  // piece 0 of this row
+        float4* dst = reinterpret_cast<float4*>(p.partial_o + (prow0 + size_t(it.piece) * it.rows) * kVDim);
+        if (nt > 0) {
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t o[32];
+            tmem_ld32(to + 32 * c, o);
+            if (live) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                dst[8 * c + i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                             __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
             }
           }
         }
+        if (live) p.partial_ml[prow0 + size_t(it.piece) * it.rows] = make_float2(m, l);
+        __threadfence();
+        __syncwarp();
+        int before = 0;
+        if (lane == 0) before = atomicAdd(&p.arrived[(size_t(it.split) * H + h) * 8 + (row >> 5)], 1);
+        before = __shfl_sync(0xffffffffu, before, 0);
+        if (before == it.pieces - 1) {
+          __threadfence();
+          merge_rows(p, it, prow0, orow, live);
+        }
+      }
+      if (nt > 0) {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&B->o_free[t]);
-      } else if (live) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) dst[i] = make_uint4(0, 0, 0, 0);
       }
-      if (live && p.lse_out)
-        p.lse_out[orow] = l == 0.f ? -INFINITY : m * p.scale + logf(l);
     }
     if (!ok) fail(B, p.status);
   }
@@ -699,7 +872,8 @@ cudaError_t launch_prompt_attention(const PromptParams& p, cudaStream_t stream) 
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 128) attr[dev] = true;
   }
-  const long long most = ((long long)p.n_q / kBlockRows + p.num_seqs) * p.heads;  // units at most
+  // units at most: every block, split or not
+  const long long most = ((long long)p.n_q / kPromptRows + p.num_seqs) * kPromptMaxPieces * p.heads;
   const unsigned grid = unsigned(most < p.sm_count ? most : p.sm_count);
   return launch_pdl(prompt_attention_kernel, dim3(grid), dim3(kPromptThreads), kSmem, stream, 1, qn, qp, kn, kp, v, p);
 }

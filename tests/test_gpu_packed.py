@@ -287,6 +287,21 @@ def test_prompt_no_keys_no_lse(cuda_lib):
     assert lse is None and torch.equal(out, out0)
 
 
+@pytest.mark.parametrize("q_lens,k_lens,H,kv", [
+    ((1,), (5000,), 16, 16),                  # one token: keys split over the SMs
+    ((19, 7), (9000, 5011), 16, 16),
+    ((300,), (300,), 16, 4),                  # short: split or not, the same result within the bounds
+    ((2048,), (2048,), 16, 2),                # the longest blocks of one prompt
+    ((129, 40), (3000, 17), 16, 16),          # a split block beside one with rows that see no key
+    ((1, 1, 1), (4097, 128, 2600), 32, 1),
+])
+def test_prompt_split_keys(cuda_lib, q_lens, k_lens, H, kv):
+    x = _prompt(q_lens, k_lens, H=H, kv=kv, seed=12)
+    _check(x)
+    a, b = _gpu(x), _gpu(x)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 def test_prompt_many_sequences(cuda_lib):
     """More sequences than the plan's CTA has threads, mostly empty."""
     g = torch.Generator().manual_seed(5)
