@@ -2,11 +2,22 @@
 // K_t = W^UK c_t and V_t = W^UV c_t ("Beyond the Attention Bottleneck",
 // "Down-Projection and Up-Projection Mechanics").
 //
-// Two products of the same latents, [n x 512] x [512 x H*128] each: a CTA
-// computes 128 rows x one head of one of them, [128 x 512] x [512 x 128], on
-// the tensor cores (both operands K-major, TMA into 128-byte-swizzled shared
-// memory in blocks of 64 latent dims, fp32 accumulation in tensor memory) and
-// rounds once to bf16.
+// Two products of the same latents, [n x 512] x [512 x H*128] each, 262,144
+// multiply-adds per row and head: the tensor cores bound it from some hundred
+// rows on, and with only 512 latent dims to a product the operands' way from
+// L2 is next.  So a pair of CTAs (one MMA over both SMs, M = 256 rows, N = 256
+// columns = two heads) keeps its weights in shared memory -- each CTA the
+// [128 x 512] of one head, 128 KB -- and streams only latents: 16 KB boxes of
+// its own 128 rows x 64 latent dims, 256 FLOP to a byte.  The pair walks a
+// contiguous range of the (column block, row tile) list, so it reloads weights
+// once or twice.  Accumulators (256 columns) alternate between the two halves
+// of tensor memory, so that rounding and storing a tile overlaps the next
+// tile's MMAs; outputs leave through shared memory by TMA, which also drops
+// the rows past n.
+//
+// Warps: 0 TMA producer, 1 tensor memory and (in the leading CTA) MMA issue,
+// 2-5 epilogue.  Every wait is bounded: on timeout the CTA records
+// MLA_ERR_DEVICE_TIMEOUT, drains, frees its tensor memory and returns.
 #include <atomic>
 
 #include "blackwell_ptx.cuh"
@@ -18,136 +29,297 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kExpThreads = 128;
-constexpr int kExpStages = 4;
-constexpr uint32_t kExpBox = 128 * 128;               // [128 rows x 64 latent dims] bf16, SW128
-constexpr uint32_t kExpStage = 2 * kExpBox;           // rows, weights
-constexpr uint32_t kExpOffMisc = kExpStages * kExpStage;
-constexpr uint32_t kExpSmem = kExpOffMisc + 256 + 1024;
-constexpr uint64_t kExpWaitNs = 2000000000ull;
+constexpr int kExpThreads = 192;
+constexpr int kStages = 4;
 constexpr int kKBlocks = kLatent / 64;
+constexpr uint32_t kBox = 128 * 128;                  // [128 rows x 64 columns] bf16, SW128: 16 KB
+constexpr uint32_t kOffA = kKBlocks * kBox;           // after the weights
+constexpr uint32_t kOffOut = kOffA + kStages * kBox;  // two output boxes
+constexpr uint32_t kOffMisc = kOffOut + 2 * kBox;
+constexpr uint32_t kSmem = kOffMisc + 256 + 1024;
+constexpr uint64_t kWaitNs = 2000000000ull;
+static_assert(kSmem <= 232448, "dynamic shared memory of one CTA");
 
 struct ExpandBarriers {
-  uint64_t full[kExpStages], empty[kExpStages], done;
+  uint64_t a_full[kStages];   // leading CTA: both CTAs' latent boxes landed
+  uint64_t a_empty[kStages];  // each CTA: read by their MMAs
+  uint64_t b_full, b_empty;   // weights landed (leading CTA) / read by their last MMA (each CTA)
+  uint64_t acc_full[2];       // each CTA: accumulator complete
+  uint64_t acc_empty[2];      // leading CTA: read by both CTAs' epilogues
+  uint64_t drain;
   uint32_t tmem_base;
   int abort;
 };
 
-__global__ void __launch_bounds__(kExpThreads) expand_kernel(const __grid_constant__ CUtensorMap map_c,
-                                                             const __grid_constant__ CUtensorMap map_uk,
-                                                             const __grid_constant__ CUtensorMap map_uv,
-                                                             ExpandParams p) {
+__device__ __forceinline__ void fail(ExpandBarriers* B, int* status) {
+  B->abort = 1;
+  set_status(status, MLA_ERR_DEVICE_TIMEOUT);
+}
+
+// ----- two-CTA forms ------------------------------------------------------------
+__device__ __forceinline__ void tmem_alloc2(uint32_t* dst, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(ncols)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish2() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// D (+)= A B over both CTAs of the pair: each CTA's shared memory holds its 128
+// rows of A and its half of B's rows, its tensor memory its 128 rows of D.
+__device__ __forceinline__ void mma2_bf16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrives on the barrier at this offset in both CTAs when this thread's MMAs are complete.
+__device__ __forceinline__ void mma2_commit(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"(uint16_t(3))
+      : "memory");
+}
+// Box at (x, y) into this CTA's shared memory, its bytes counted on a barrier
+// of either CTA of the pair (cluster address).
+__device__ __forceinline__ void tma2_load_2d(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+      "%3}], [%4];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(smem_u32(src))
+               : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+__global__ void __launch_bounds__(kExpThreads, 1)
+    expand_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ CUtensorMap map_uk,
+                  const __grid_constant__ CUtensorMap map_uv, const __grid_constant__ CUtensorMap map_k,
+                  const __grid_constant__ CUtensorMap map_v, ExpandParams p) {
   extern __shared__ uint8_t smem_raw[];
+  // the same offset in both CTAs: barriers are addressed across the pair
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  ExpandBarriers* B = reinterpret_cast<ExpandBarriers*>(smem + kExpOffMisc);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) {
-    for (int i = 0; i < kExpStages; ++i) {
-      mbar_init(&B->full[i], 1);
-      mbar_init(&B->empty[i], 1);
+  ExpandBarriers* B = reinterpret_cast<ExpandBarriers*>(smem + kOffMisc);
+  const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const int rank = int(cluster_ctarank());
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&B->a_full[i], 1);
+      mbar_init(&B->a_empty[i], 1);
     }
-    mbar_init(&B->done, 1);
+    mbar_init(&B->b_full, 1);
+    mbar_init(&B->b_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&B->acc_full[i], 1);
+      mbar_init(&B->acc_empty[i], 8);  // one lane of each epilogue warp of both CTAs
+    }
+    mbar_init(&B->drain, 1);
     B->abort = 0;
     fence_mbar_init();
   }
-  if (warp == 0) {
-    tmem_alloc(&B->tmem_base, 128);
-    tmem_relinquish();
+  if (warp == 1) {
+    tmem_alloc2(&B->tmem_base, 512);
+    tmem_relinquish2();
   }
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();
   tc_fence_after();
   const uint32_t tmem = B->tmem_base, sbase = smem_u32(smem);
   griddep_wait();
   griddep_launch_dependents();
-  const int unit = blockIdx.x % (2 * p.heads), m0 = (blockIdx.x / (2 * p.heads)) * 128;
-  const int head = unit % p.heads;
-  const bool is_v = unit >= p.heads;
-  bool ok = true;
-  if (tid == 0) {
-    const CUtensorMap* map_w = is_v ? &map_uv : &map_uk;
-    auto load = [&](int kb) {
-      const int s = kb % kExpStages;
-      mbar_arrive_expect_tx(&B->full[s], kExpStage);
-      tma_load_2d(smem + s * kExpStage, &map_c, 64 * kb, m0, &B->full[s]);
-      tma_load_2d(smem + s * kExpStage + kExpBox, map_w, 64 * kb, head * 128, &B->full[s]);
-    };
-    constexpr uint32_t idesc = idesc_bf16_f32(128, 128, false, false);
-    constexpr uint64_t kDesc = smem_desc(0, 16, 1024, kSwizzle128B);
-    for (int kb = 0; kb < kExpStages; ++kb) load(kb);
-    for (int kb = 0; kb < kKBlocks && ok; ++kb) {
-      const int s = kb % kExpStages;
-      ok = mbar_wait(&B->full[s], (kb / kExpStages) & 1, &B->abort, kExpWaitNs);
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t a = sbase + s * kExpStage;
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-        mma_bf16(tmem, kDesc | desc_addr(a + 32 * kk), kDesc | desc_addr(a + kExpBox + 32 * kk), idesc, kb + kk > 0);
-      mma_commit(&B->empty[s]);
-      if (kb + kExpStages < kKBlocks) {
-        ok = mbar_wait(&B->empty[s], (kb / kExpStages) & 1, &B->abort, kExpWaitNs);
-        if (ok) load(kb + kExpStages);
+  const volatile int* abort_flag = &B->abort;
+  // units (column block, row tile), column blocks outermost: first W^UK's, then W^UV's
+  const int tiles = (p.n_rows + 255) / 256, P = gridDim.x / 2, pair = blockIdx.x / 2;
+  const long long total = (long long)tiles * p.heads;
+  const int u0 = int(total * pair / P), u1 = int(total * (pair + 1) / P);
+
+  if (warp == 0 && lane == 0) {
+    // ------------------------------------------------------------ TMA producer
+    bool ok = true;
+    uint32_t k = 0, nb = 0;
+    const uint32_t b_full = mapa_shared(smem_u32(&B->b_full), 0);
+    int block = -1;
+    for (int u = u0; u < u1 && ok; ++u) {
+      const int cb = u / tiles, row = (u % tiles) * 256 + 128 * rank;
+      if (cb != block) {
+        if (nb > 0 && !(ok = mbar_wait(&B->b_empty, (nb - 1) & 1, abort_flag, kWaitNs))) break;
+        ++nb;
+        block = cb;
+        const bool is_v = cb >= p.heads / 2;
+        const int wrow = (is_v ? cb - p.heads / 2 : cb) * 256 + 128 * rank;
+        if (rank == 0) mbar_arrive_expect_tx(&B->b_full, 2 * kKBlocks * kBox);
+        for (int i = 0; i < kKBlocks; ++i)
+          tma2_load_2d(smem + i * kBox, is_v ? &map_uv : &map_uk, 64 * i, wrow, b_full);
+      }
+      for (int i = 0; i < kKBlocks; ++i, ++k) {
+        const uint32_t s = k % kStages;
+        if (k >= kStages && !(ok = mbar_wait(&B->a_empty[s], ((k / kStages) - 1) & 1, abort_flag, kWaitNs))) break;
+        if (rank == 0) mbar_arrive_expect_tx(&B->a_full[s], 2 * kBox);
+        tma2_load_2d(smem + kOffA + s * kBox, &map_c, 64 * i, row, mapa_shared(smem_u32(&B->a_full[s]), 0));
       }
     }
-    if (!ok) B->abort = 1;
-    mma_commit(&B->done);
-  }
-  __syncwarp();
-  ok = mbar_wait(&B->done, 0, &B->abort, kExpWaitNs) && ok;
-  tc_fence_after();
-  __syncthreads();
-  if (!B->abort) {
-    const int r = m0 + 32 * warp + lane;
-    uint4* dst = reinterpret_cast<uint4*>((is_v ? p.v : p.k_nope) + (size_t(r) * p.heads + head) * 128);
+    if (!ok) fail(B, p.status);
+  } else if (warp == 1 && rank == 0) {
+    // ------------------------------------------------------------ MMA issue
+    constexpr uint32_t idesc = idesc_bf16_f32(256, 256, false, false);
+    constexpr uint64_t kDesc = smem_desc(0, 16, 1024, kSwizzle128B);
+    const uint64_t a0 = kDesc | desc_addr(sbase + kOffA), b0 = kDesc | desc_addr(sbase);
+    const bool leader = elect_one();
+    bool ok = true;
+    uint32_t k = 0, nb = 0, t = 0;
+    int block = -1;
+    for (int u = u0; u < u1 && ok; ++u, ++t) {
+      const int cb = u / tiles;
+      if (cb != block) {
+        if (!(ok = mbar_wait_cluster(&B->b_full, nb & 1, abort_flag, kWaitNs))) break;
+        ++nb;
+        block = cb;
+      }
+      const uint32_t d = tmem + 256 * (t & 1);
+      if (t >= 2 && !(ok = mbar_wait_cluster(&B->acc_empty[t & 1], ((t >> 1) - 1) & 1, abort_flag, kWaitNs))) break;
+      for (int i = 0; i < kKBlocks; ++i, ++k) {
+        const uint32_t s = k % kStages;
+        if (!(ok = mbar_wait_cluster(&B->a_full[s], (k / kStages) & 1, abort_flag, kWaitNs))) break;
+        tc_fence_after();
+        if (leader) {
+          const uint64_t a = a0 + s * (kBox >> 4), b = b0 + i * (kBox >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) mma2_bf16(d, a + 2 * kk, b + 2 * kk, idesc, kk > 0 ? 1 : i);
+          mma2_commit(&B->a_empty[s]);
+        }
+        __syncwarp();
+      }
+      if (ok && leader) {
+        mma2_commit(&B->acc_full[t & 1]);
+        if (u + 1 == u1 || (u + 1) / tiles != cb) mma2_commit(&B->b_empty);
+      }
+      __syncwarp();
+    }
+    if (leader) {
+      if (!ok) fail(B, p.status);
+      mma2_commit(&B->drain);  // every MMA issued completes before teardown
+    }
+    __syncwarp();
+  } else if (warp >= 2) {
+    // ------------------------------------------------------------ epilogue
+    // Tensor memory lane = row of this CTA's 128; four boxes of 64 columns per
+    // tile, alternating between two shared-memory buffers.
+    const int q4 = warp & 3, r = 32 * q4 + lane;
+    const bool issuer = threadIdx.x == 64;
+    bool ok = true;
+    uint32_t t = 0;
+    for (int u = u0; u < u1; ++u, ++t) {
+      const int cb = u / tiles, row = (u % tiles) * 256 + 128 * rank;
+      const bool is_v = cb >= p.heads / 2;
+      const int col = (is_v ? cb - p.heads / 2 : cb) * 256;
+      ok = mbar_wait_cluster(&B->acc_full[t & 1], (t >> 1) & 1, abort_flag, kWaitNs);
+      if (!ok) fail(B, p.status);  // the loop goes on to the barrier below, where all four warps leave together
+      tc_fence_after();
+      const uint32_t acc = tmem + (uint32_t(32 * q4) << 16) + 256 * (t & 1);
 #pragma unroll 1
-    for (int c = 0; c < 128; c += 32) {
-      uint32_t v[32];
-      tmem_ld32(tmem + (uint32_t(32 * warp) << 16) + c, v);
-      if (r < p.n_rows) {
+      for (int c = 0; c < 4; ++c) {
+        uint8_t* out = smem + kOffOut + (c & 1) * kBox;
+        uint32_t w[32];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t o[4];
+        for (int e = 0; e < 2; ++e) {
+          uint32_t v[32];
+          tmem_ld32(acc + 64 * c + 32 * e, v);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const __nv_bfloat162 b =
-                __floats2bfloat162_rn(__uint_as_float(v[8 * i + 2 * j]), __uint_as_float(v[8 * i + 2 * j + 1]));
-            o[j] = *reinterpret_cast<const uint32_t*>(&b);
+          for (int i = 0; i < 16; ++i) {
+            const __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+            w[16 * e + i] = *reinterpret_cast<const uint32_t*>(&x);
           }
-          dst[c / 8 + i] = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        if (c == 3) {  // the accumulator is read
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_cluster(mapa_shared(smem_u32(&B->acc_empty[t & 1]), 0));
+        }
+        // the buffer's store of two boxes ago has read it
+        if (issuer) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+        epilogue_sync();
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<uint4*>(out + r * 128 + ((i ^ (r & 7)) << 4)) =
+              make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        fence_proxy_async_smem();
+        epilogue_sync();
+        if (issuer && !*abort_flag) {
+          if (row < p.n_rows) tma_store_2d(is_v ? &map_v : &map_k, out, col + 64 * c, row);
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
         }
       }
+      if (*abort_flag) ok = false;
+      // every warp of the epilogue sees the same decision
+      uint32_t any;
+      asm volatile(
+          "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+          : "=r"(any)
+          : "r"(uint32_t(!ok))
+          : "memory");
+      if (any) break;
     }
-  } else if (tid == 0) {
-    set_status(p.status, MLA_ERR_DEVICE_TIMEOUT);
-    const uint64_t t0 = global_timer_ns();  // copies already issued land before the shared memory is released
+    if (issuer) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  }
+  // ---------------------------------------------------------------- teardown
+  __syncthreads();
+  if (warp == 1) mbar_wait(&B->drain, 0, abort_flag, kWaitNs);  // both CTAs: the commits arrive in both
+  if (B->abort) {  // copies already issued land before the shared memory is released
+    const uint64_t t0 = global_timer_ns();
     while (global_timer_ns() - t0 < 20000) {
     }
   }
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();  // the peer's copies, MMAs and arrivals into this CTA are done
   tc_fence_after();
-  if (warp == 0) tmem_dealloc(tmem, 128);
+  if (warp == 1) tmem_dealloc2(tmem, 512);
 }
 
 }  // namespace
 
 cudaError_t launch_expand(const ExpandParams& p, cudaStream_t stream) {
-  CUtensorMap mc, mk, mv;
+  CUtensorMap mc, muk, muv, mk, mv;
+  const uint64_t cols = uint64_t(p.heads) * 128;
   if (!dc::make_map_2d(&mc, p.c_kv, 2, kLatent, p.n_rows, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !dc::make_map_2d(&mk, p.W_UK, 2, kLatent, uint64_t(p.heads) * 128, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !dc::make_map_2d(&mv, p.W_UV, 2, kLatent, uint64_t(p.heads) * 128, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B))
+      !dc::make_map_2d(&muk, p.W_UK, 2, kLatent, cols, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !dc::make_map_2d(&muv, p.W_UV, 2, kLatent, cols, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !dc::make_map_2d(&mk, p.k_nope, 2, cols, p.n_rows, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !dc::make_map_2d(&mv, p.v, 2, cols, p.n_rows, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   static std::atomic<bool> attr[128];  // per device: attributes set (zero-initialised)
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 128 || !attr[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(expand_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kExpSmem));
+    const cudaError_t e = cudaFuncSetAttribute(expand_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 128) attr[dev] = true;
   }
-  const unsigned grid = unsigned((p.n_rows + 127) / 128) * 2u * unsigned(p.heads);
-  return launch_pdl(expand_kernel, dim3(grid), dim3(kExpThreads), kExpSmem, stream, 1, mc, mk, mv, p);
+  const long long units = (long long)((p.n_rows + 255) / 256) * p.heads, pairs = p.sm_count / 2;
+  return launch_pdl(expand_kernel, dim3(unsigned(2 * (units < pairs ? units : pairs))), dim3(kExpThreads), kSmem, stream,
+                    2, mc, muk, muv, mk, mv, p);
 }
 
 }  // namespace mla
