@@ -363,11 +363,11 @@ int mla_cache_read(const mla_dims* dims, const void* cache, const float* cache_s
  *
  *   c_kv        bf16 [n_rows, 512] (new latents, or mla_cache_read's)
  *   W_UK, W_UV  bf16 [H, 128, 512]
- *   k_nope, v   bf16 [n_rows, H, 128]
+ *   k_nope, v   bf16 [n_rows, H, 128], 32-byte aligned
  *   n_rows      n_rows * H <= MLA_MAX_QUERY_ROWS; 0 is a no-op
  *   device_status  optional int32 (device): MLA_ERR_DEVICE_TIMEOUT is stored
  *               here if a bounded wait runs out
- * All pointers to tensors 16-byte aligned.
+ * c_kv, W_UK and W_UV are 16-byte aligned.
  */
 int mla_expand_kv(const mla_dims* dims, const void* c_kv, int32_t n_rows, const void* W_UK, const void* W_UV,
                   void* k_nope, void* v, int32_t* device_status, mla_stream_t stream);

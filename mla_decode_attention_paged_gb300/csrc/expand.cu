@@ -12,8 +12,7 @@
 // contiguous range of the (column block, row tile) list, so it reloads weights
 // once or twice.  Accumulators (256 columns) alternate between the two halves
 // of tensor memory, so that rounding and storing a tile overlaps the next
-// tile's MMAs; outputs leave through shared memory by TMA, which also drops
-// the rows past n.
+// tile's MMAs; each thread stores its row in whole 32-byte sectors.
 //
 // Warps: 0 TMA producer, 1 tensor memory and (in the leading CTA) MMA issue,
 // 2-5 epilogue.  Every wait is bounded: on timeout the CTA records
@@ -30,12 +29,11 @@ namespace {
 using namespace ptx;
 
 constexpr int kExpThreads = 192;
-constexpr int kStages = 4;
+constexpr int kStages = 6;
 constexpr int kKBlocks = kLatent / 64;
 constexpr uint32_t kBox = 128 * 128;                  // [128 rows x 64 columns] bf16, SW128: 16 KB
 constexpr uint32_t kOffA = kKBlocks * kBox;           // after the weights
-constexpr uint32_t kOffOut = kOffA + kStages * kBox;  // two output boxes
-constexpr uint32_t kOffMisc = kOffOut + 2 * kBox;
+constexpr uint32_t kOffMisc = kOffA + kStages * kBox;
 constexpr uint32_t kSmem = kOffMisc + 256 + 1024;
 constexpr uint64_t kWaitNs = 2000000000ull;
 static_assert(kSmem <= 232448, "dynamic shared memory of one CTA");
@@ -98,27 +96,16 @@ __device__ __forceinline__ void tma2_load_2d(void* dst, const CUtensorMap* map, 
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int x, int y) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(x), "r"(y), "r"(smem_u32(src))
+// 32 bytes at a 32-byte-aligned address: a whole sector per lane.
+__device__ __forceinline__ void st_global_32(void* dst, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                : "memory");
 }
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(r));
-  return r != 0;
-}
-__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 __global__ void __launch_bounds__(kExpThreads, 1)
     expand_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ CUtensorMap map_uk,
-                  const __grid_constant__ CUtensorMap map_uv, const __grid_constant__ CUtensorMap map_k,
-                  const __grid_constant__ CUtensorMap map_v, ExpandParams p) {
+                  const __grid_constant__ CUtensorMap map_uv, ExpandParams p) {
   extern __shared__ uint8_t smem_raw[];
   // the same offset in both CTAs: barriers are addressed across the pair
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -225,64 +212,50 @@ __global__ void __launch_bounds__(kExpThreads, 1)
     __syncwarp();
   } else if (warp >= 2) {
     // ------------------------------------------------------------ epilogue
-    // Tensor memory lane = row of this CTA's 128; four boxes of 64 columns per
-    // tile, alternating between two shared-memory buffers.
+    // Tensor memory lane = row of this CTA's 128; a thread stores its row's 512
+    // contiguous bytes (two heads) as whole 32-byte sectors.
     const int q4 = warp & 3, r = 32 * q4 + lane;
-    const bool issuer = threadIdx.x == 64;
-    bool ok = true;
     uint32_t t = 0;
     for (int u = u0; u < u1; ++u, ++t) {
-      const int cb = u / tiles, row = (u % tiles) * 256 + 128 * rank;
+      const int cb = u / tiles, row = (u % tiles) * 256 + 128 * rank + r;
       const bool is_v = cb >= p.heads / 2;
-      const int col = (is_v ? cb - p.heads / 2 : cb) * 256;
-      ok = mbar_wait_cluster(&B->acc_full[t & 1], (t >> 1) & 1, abort_flag, kWaitNs);
-      if (!ok) fail(B, p.status);  // the loop goes on to the barrier below, where all four warps leave together
+      const int head = (is_v ? cb - p.heads / 2 : cb) * 2;
+      __nv_bfloat16* dst = (is_v ? p.v : p.k_nope) + (size_t(row) * p.heads + head) * 128;
+      const bool ok = mbar_wait_cluster(&B->acc_full[t & 1], (t >> 1) & 1, abort_flag, kWaitNs);
+      if (!__all_sync(0xffffffffu, ok)) {
+        fail(B, p.status);
+        break;
+      }
       tc_fence_after();
       const uint32_t acc = tmem + (uint32_t(32 * q4) << 16) + 256 * (t & 1);
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        uint8_t* out = smem + kOffOut + (c & 1) * kBox;
-        uint32_t w[32];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          uint32_t v[32];
-          tmem_ld32(acc + 64 * c + 32 * e, v);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-            w[16 * e + i] = *reinterpret_cast<const uint32_t*>(&x);
-          }
-        }
-        if (c == 3) {  // the accumulator is read
+      for (int c = 0; c < 256; c += 64) {
+        uint32_t v[2][32];
+        tmem_ld32_async(acc + c, v[0]);
+        tmem_ld32_async(acc + c + 32, v[1]);
+        tmem_ld_wait();
+        tie(v[0]);
+        tie(v[1]);
+        if (c == 192) {  // the accumulator is read
           tc_fence_before();
           __syncwarp();
           if (lane == 0) arrive_cluster(mapa_shared(smem_u32(&B->acc_empty[t & 1]), 0));
         }
-        // the buffer's store of two boxes ago has read it
-        if (issuer) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-        epilogue_sync();
+        if (row < p.n_rows) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          *reinterpret_cast<uint4*>(out + r * 128 + ((i ^ (r & 7)) << 4)) =
-              make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-        fence_proxy_async_smem();
-        epilogue_sync();
-        if (issuer && !*abort_flag) {
-          if (row < p.n_rows) tma_store_2d(is_v ? &map_v : &map_k, out, col + 64 * c, row);
-          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          for (int i = 0; i < 4; ++i) {
+            uint32_t w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const uint32_t* x = &v[i >> 1][16 * (i & 1) + 2 * e];
+              const __nv_bfloat162 y = __floats2bfloat162_rn(__uint_as_float(x[0]), __uint_as_float(x[1]));
+              w[e] = *reinterpret_cast<const uint32_t*>(&y);
+            }
+            st_global_32(dst + c + 16 * i, w);
+          }
         }
       }
-      if (*abort_flag) ok = false;
-      // every warp of the epilogue sees the same decision
-      uint32_t any;
-      asm volatile(
-          "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-          : "=r"(any)
-          : "r"(uint32_t(!ok))
-          : "memory");
-      if (any) break;
     }
-    if (issuer) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   // ---------------------------------------------------------------- teardown
   __syncthreads();
@@ -301,13 +274,11 @@ __global__ void __launch_bounds__(kExpThreads, 1)
 }  // namespace
 
 cudaError_t launch_expand(const ExpandParams& p, cudaStream_t stream) {
-  CUtensorMap mc, muk, muv, mk, mv;
+  CUtensorMap mc, muk, muv;
   const uint64_t cols = uint64_t(p.heads) * 128;
   if (!dc::make_map_2d(&mc, p.c_kv, 2, kLatent, p.n_rows, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !dc::make_map_2d(&muk, p.W_UK, 2, kLatent, cols, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !dc::make_map_2d(&muv, p.W_UV, 2, kLatent, cols, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !dc::make_map_2d(&mk, p.k_nope, 2, cols, p.n_rows, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !dc::make_map_2d(&mv, p.v, 2, cols, p.n_rows, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B))
+      !dc::make_map_2d(&muv, p.W_UV, 2, kLatent, cols, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   static std::atomic<bool> attr[128];  // per device: attributes set (zero-initialised)
   int dev = 0;
@@ -319,7 +290,7 @@ cudaError_t launch_expand(const ExpandParams& p, cudaStream_t stream) {
   }
   const long long units = (long long)((p.n_rows + 255) / 256) * p.heads, pairs = p.sm_count / 2;
   return launch_pdl(expand_kernel, dim3(unsigned(2 * (units < pairs ? units : pairs))), dim3(kExpThreads), kSmem, stream,
-                    2, mc, muk, muv, mk, mv, p);
+                    2, mc, muk, muv, p);
 }
 
 }  // namespace mla

@@ -530,7 +530,7 @@ int mla_expand_kv(const mla_dims* d, const void* c_kv, int32_t n_rows, const voi
   if (n_rows == 0) return MLA_OK;
   if ((long long)n_rows * d->num_heads > kMaxQueryRows) return MLA_ERR_INVALID_ARG;
   if (!c_kv || !W_UK || !W_UV || !k_nope || !v) return MLA_ERR_INVALID_ARG;
-  if (!aligned(c_kv, 16) || !aligned(W_UK, 16) || !aligned(W_UV, 16) || !aligned(k_nope, 16) || !aligned(v, 16) ||
+  if (!aligned(c_kv, 16) || !aligned(W_UK, 16) || !aligned(W_UV, 16) || !aligned(k_nope, 32) || !aligned(v, 32) ||
       (device_status && !aligned(device_status, 4)))
     return MLA_ERR_INVALID_ARG;
   ExpandParams p;
