@@ -6,13 +6,18 @@
 // multiply-adds per row and head: the tensor cores bound it from some hundred
 // rows on, and with only 512 latent dims to a product the operands' way from
 // L2 is next.  So a pair of CTAs (one MMA over both SMs, M = 256 rows, N = 256
-// columns = two heads) keeps its weights in shared memory -- each CTA the
-// [128 x 512] of one head, 128 KB -- and streams only latents: 16 KB boxes of
-// its own 128 rows x 64 latent dims, 256 FLOP to a byte.  The pair walks a
-// contiguous range of the (column block, row tile) list, so it reloads weights
-// once or twice.  Accumulators (256 columns) alternate between the two halves
-// of tensor memory, so that rounding and storing a tile overlaps the next
-// tile's MMAs; each thread stores its row in whole 32-byte sectors.
+// columns = two heads) keeps one operand's [256 x 512] in shared memory, 128 KB
+// in each CTA, and streams the other in 16 KB boxes of 128 rows x 64 latent dims
+// to each CTA: 256 FLOP to a byte.  It walks a contiguous range of the (resident
+// block, streamed block) list.  The smaller operand is streamed, as it is read
+// once per resident block and should stay in L2: weights (4 MB at 16 heads)
+// where there are more rows than weight rows (256 to a head), else latents.  34,816 rows
+// at 16 heads: 112 us with the weights streamed, 120 with the latents; 5,003
+// rows at 128 heads: 137 and 127 us.  Accumulators (256 columns) alternate
+// between the two halves of tensor memory, so that rounding and storing a tile
+// overlaps the next tile's MMAs; each thread stores its row in whole 32-byte
+// sectors.  What bounds both sizes now is the outputs' way to memory: without
+// the stores they take 72 and 81 us, and filling as many bytes takes 74 and 84.
 //
 // Warps: 0 TMA producer, 1 tensor memory and (in the leading CTA) MMA issue,
 // 2-5 epilogue.  Every wait is bounded: on timeout the CTA records
@@ -32,16 +37,16 @@ constexpr int kExpThreads = 192;
 constexpr int kStages = 6;
 constexpr int kKBlocks = kLatent / 64;
 constexpr uint32_t kBox = 128 * 128;                  // [128 rows x 64 columns] bf16, SW128: 16 KB
-constexpr uint32_t kOffA = kKBlocks * kBox;           // after the weights
-constexpr uint32_t kOffMisc = kOffA + kStages * kBox;
+constexpr uint32_t kOffRing = kKBlocks * kBox;        // after the resident operand
+constexpr uint32_t kOffMisc = kOffRing + kStages * kBox;
 constexpr uint32_t kSmem = kOffMisc + 256 + 1024;
 constexpr uint64_t kWaitNs = 2000000000ull;
 static_assert(kSmem <= 232448, "dynamic shared memory of one CTA");
 
 struct ExpandBarriers {
-  uint64_t a_full[kStages];   // leading CTA: both CTAs' latent boxes landed
-  uint64_t a_empty[kStages];  // each CTA: read by their MMAs
-  uint64_t b_full, b_empty;   // weights landed (leading CTA) / read by their last MMA (each CTA)
+  uint64_t full[kStages];        // leading CTA: both CTAs' streamed boxes landed
+  uint64_t empty[kStages];       // each CTA: read by their MMAs
+  uint64_t res_full, res_empty;  // resident operand landed (leading CTA) / read by its last MMA (each CTA)
   uint64_t acc_full[2];       // each CTA: accumulator complete
   uint64_t acc_empty[2];      // leading CTA: read by both CTAs' epilogues
   uint64_t drain;
@@ -103,6 +108,8 @@ __device__ __forceinline__ void st_global_32(void* dst, const uint32_t (&w)[8]) 
                : "memory");
 }
 
+// kRowsResident: latents resident, weights streamed; else the other way round.
+template <bool kRowsResident>
 __global__ void __launch_bounds__(kExpThreads, 1)
     expand_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ CUtensorMap map_uk,
                   const __grid_constant__ CUtensorMap map_uv, ExpandParams p) {
@@ -114,11 +121,11 @@ __global__ void __launch_bounds__(kExpThreads, 1)
   const int rank = int(cluster_ctarank());
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&B->a_full[i], 1);
-      mbar_init(&B->a_empty[i], 1);
+      mbar_init(&B->full[i], 1);
+      mbar_init(&B->empty[i], 1);
     }
-    mbar_init(&B->b_full, 1);
-    mbar_init(&B->b_empty, 1);
+    mbar_init(&B->res_full, 1);
+    mbar_init(&B->res_empty, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&B->acc_full[i], 1);
       mbar_init(&B->acc_empty[i], 8);  // one lane of each epilogue warp of both CTAs
@@ -138,34 +145,39 @@ __global__ void __launch_bounds__(kExpThreads, 1)
   griddep_wait();
   griddep_launch_dependents();
   const volatile int* abort_flag = &B->abort;
-  // units (column block, row tile), column blocks outermost: first W^UK's, then W^UV's
-  const int tiles = (p.n_rows + 255) / 256, P = gridDim.x / 2, pair = blockIdx.x / 2;
-  const long long total = (long long)tiles * p.heads;
+  // units (resident block, streamed block), the resident ones outermost; column
+  // blocks are W^UK's, then W^UV's
+  const int blocks = p.heads, tiles = (p.n_rows + 255) / 256, inner = kRowsResident ? blocks : tiles;
+  const int P = gridDim.x / 2, pair = blockIdx.x / 2;
+  const long long total = (long long)tiles * blocks;
   const int u0 = int(total * pair / P), u1 = int(total * (pair + 1) / P);
+  const uint32_t row_box = kRowsResident ? 0 : kOffRing, col_box = kRowsResident ? kOffRing : 0;
 
   if (warp == 0 && lane == 0) {
     // ------------------------------------------------------------ TMA producer
     bool ok = true;
-    uint32_t k = 0, nb = 0;
-    const uint32_t b_full = mapa_shared(smem_u32(&B->b_full), 0);
-    int block = -1;
+    uint32_t k = 0, nr = 0;
+    const uint32_t res_full = mapa_shared(smem_u32(&B->res_full), 0);
+    // box i (64 latent dims) of this CTA's half of row tile / column block x
+    auto load = [&](bool rows, int x, int i, uint8_t* dst, uint32_t bar) {
+      const bool is_v = !rows && x >= blocks / 2;
+      tma2_load_2d(dst, rows ? &map_c : is_v ? &map_uv : &map_uk, 64 * i, (is_v ? x - blocks / 2 : x) * 256 + 128 * rank,
+                   bar);
+    };
+    int resident = -1;
     for (int u = u0; u < u1 && ok; ++u) {
-      const int cb = u / tiles, row = (u % tiles) * 256 + 128 * rank;
-      if (cb != block) {
-        if (nb > 0 && !(ok = mbar_wait(&B->b_empty, (nb - 1) & 1, abort_flag, kWaitNs))) break;
-        ++nb;
-        block = cb;
-        const bool is_v = cb >= p.heads / 2;
-        const int wrow = (is_v ? cb - p.heads / 2 : cb) * 256 + 128 * rank;
-        if (rank == 0) mbar_arrive_expect_tx(&B->b_full, 2 * kKBlocks * kBox);
-        for (int i = 0; i < kKBlocks; ++i)
-          tma2_load_2d(smem + i * kBox, is_v ? &map_uv : &map_uk, 64 * i, wrow, b_full);
+      if (u / inner != resident) {
+        if (nr > 0 && !(ok = mbar_wait(&B->res_empty, (nr - 1) & 1, abort_flag, kWaitNs))) break;
+        ++nr;
+        resident = u / inner;
+        if (rank == 0) mbar_arrive_expect_tx(&B->res_full, 2 * kKBlocks * kBox);
+        for (int i = 0; i < kKBlocks; ++i) load(kRowsResident, resident, i, smem + i * kBox, res_full);
       }
       for (int i = 0; i < kKBlocks; ++i, ++k) {
         const uint32_t s = k % kStages;
-        if (k >= kStages && !(ok = mbar_wait(&B->a_empty[s], ((k / kStages) - 1) & 1, abort_flag, kWaitNs))) break;
-        if (rank == 0) mbar_arrive_expect_tx(&B->a_full[s], 2 * kBox);
-        tma2_load_2d(smem + kOffA + s * kBox, &map_c, 64 * i, row, mapa_shared(smem_u32(&B->a_full[s]), 0));
+        if (k >= kStages && !(ok = mbar_wait(&B->empty[s], ((k / kStages) - 1) & 1, abort_flag, kWaitNs))) break;
+        if (rank == 0) mbar_arrive_expect_tx(&B->full[s], 2 * kBox);
+        load(!kRowsResident, u % inner, i, smem + kOffRing + s * kBox, mapa_shared(smem_u32(&B->full[s]), 0));
       }
     }
     if (!ok) fail(B, p.status);
@@ -173,35 +185,34 @@ __global__ void __launch_bounds__(kExpThreads, 1)
     // ------------------------------------------------------------ MMA issue
     constexpr uint32_t idesc = idesc_bf16_f32(256, 256, false, false);
     constexpr uint64_t kDesc = smem_desc(0, 16, 1024, kSwizzle128B);
-    const uint64_t a0 = kDesc | desc_addr(sbase + kOffA), b0 = kDesc | desc_addr(sbase);
+    const uint64_t a0 = kDesc | desc_addr(sbase + row_box), b0 = kDesc | desc_addr(sbase + col_box);
     const bool leader = elect_one();
     bool ok = true;
-    uint32_t k = 0, nb = 0, t = 0;
-    int block = -1;
+    uint32_t k = 0, nr = 0, t = 0;
+    int resident = -1;
     for (int u = u0; u < u1 && ok; ++u, ++t) {
-      const int cb = u / tiles;
-      if (cb != block) {
-        if (!(ok = mbar_wait_cluster(&B->b_full, nb & 1, abort_flag, kWaitNs))) break;
-        ++nb;
-        block = cb;
+      if (u / inner != resident) {
+        if (!(ok = mbar_wait_cluster(&B->res_full, nr & 1, abort_flag, kWaitNs))) break;
+        ++nr;
+        resident = u / inner;
       }
       const uint32_t d = tmem + 256 * (t & 1);
       if (t >= 2 && !(ok = mbar_wait_cluster(&B->acc_empty[t & 1], ((t >> 1) - 1) & 1, abort_flag, kWaitNs))) break;
       for (int i = 0; i < kKBlocks; ++i, ++k) {
         const uint32_t s = k % kStages;
-        if (!(ok = mbar_wait_cluster(&B->a_full[s], (k / kStages) & 1, abort_flag, kWaitNs))) break;
+        if (!(ok = mbar_wait_cluster(&B->full[s], (k / kStages) & 1, abort_flag, kWaitNs))) break;
         tc_fence_after();
         if (leader) {
-          const uint64_t a = a0 + s * (kBox >> 4), b = b0 + i * (kBox >> 4);
+          const uint64_t a = a0 + (kRowsResident ? i : s) * (kBox >> 4), b = b0 + (kRowsResident ? s : i) * (kBox >> 4);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) mma2_bf16(d, a + 2 * kk, b + 2 * kk, idesc, kk > 0 ? 1 : i);
-          mma2_commit(&B->a_empty[s]);
+          mma2_commit(&B->empty[s]);
         }
         __syncwarp();
       }
       if (ok && leader) {
         mma2_commit(&B->acc_full[t & 1]);
-        if (u + 1 == u1 || (u + 1) / tiles != cb) mma2_commit(&B->b_empty);
+        if (u + 1 == u1 || (u + 1) / inner != resident) mma2_commit(&B->res_empty);
       }
       __syncwarp();
     }
@@ -217,9 +228,10 @@ __global__ void __launch_bounds__(kExpThreads, 1)
     const int q4 = warp & 3, r = 32 * q4 + lane;
     uint32_t t = 0;
     for (int u = u0; u < u1; ++u, ++t) {
-      const int cb = u / tiles, row = (u % tiles) * 256 + 128 * rank + r;
-      const bool is_v = cb >= p.heads / 2;
-      const int head = (is_v ? cb - p.heads / 2 : cb) * 2;
+      const int cb = kRowsResident ? u % inner : u / inner;
+      const int row = (kRowsResident ? u / inner : u % inner) * 256 + 128 * rank + r;
+      const bool is_v = cb >= blocks / 2;
+      const int head = (is_v ? cb - blocks / 2 : cb) * 2;
       __nv_bfloat16* dst = (is_v ? p.v : p.k_nope) + (size_t(row) * p.heads + head) * 128;
       const bool ok = mbar_wait_cluster(&B->acc_full[t & 1], (t >> 1) & 1, abort_flag, kWaitNs);
       if (!__all_sync(0xffffffffu, ok)) {
@@ -284,12 +296,16 @@ cudaError_t launch_expand(const ExpandParams& p, cudaStream_t stream) {
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 128 || !attr[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(expand_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
-    if (e != cudaSuccess) return e;
+    for (auto* k : {expand_kernel<false>, expand_kernel<true>}) {
+      const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
+      if (e != cudaSuccess) return e;
+    }
     if (dev >= 0 && dev < 128) attr[dev] = true;
   }
   const long long units = (long long)((p.n_rows + 255) / 256) * p.heads, pairs = p.sm_count / 2;
-  return launch_pdl(expand_kernel, dim3(unsigned(2 * (units < pairs ? units : pairs))), dim3(kExpThreads), kSmem, stream,
+  // columns: 256 to a head (k_nope and v)
+  auto* kernel = p.n_rows > 256ll * p.heads ? expand_kernel<true> : expand_kernel<false>;
+  return launch_pdl(kernel, dim3(unsigned(2 * (units < pairs ? units : pairs))), dim3(kExpThreads), kSmem, stream,
                     2, mc, muk, muv, p);
 }
 
