@@ -353,23 +353,36 @@ def decode_sparse(d: Dims, q_nope, q_pe, cache, scale_zero, block_table, seq_len
     return out, lse_out
 
 
-def _rows(t: torch.Tensor, shape: tuple, name: str):
-    """Check a tensor's shape; None in ``shape`` matches any size."""
+def _arg(t: torch.Tensor, name: str, dtype, shape: tuple, dev: torch.device) -> int:
+    """Pointer of a contiguous tensor of this type, shape and device."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev
+            and t.is_contiguous()):
+        return t.data_ptr()
+    p = _ptr(t, dtype, name, dev)  # raises what is wrong, unless it is the shape
+    if t is None:
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    return p
+
+
+def _dims_of(t: torch.Tensor, name: str, n: int):
+    """Shape of an ``n``-dimensional CUDA tensor (the sizes the other arguments are checked against)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() != len(shape) or any(want is not None and have != want for have, want in zip(t.shape, shape)):
-        want = ", ".join("*" if n is None else str(n) for n in shape)
-        raise ValueError(f"{name} must have shape [{want}], got {list(t.shape)}")
+    if t.dim() != n:
+        raise ValueError(f"{name} must have {n} dimensions, got {list(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.shape
 
 
-def _call_on(dev: torch.device, stream, call) -> int:
-    """call(stream pointer) with ``dev`` current, on ``stream`` or dev's current stream."""
-    if dev.type != "cuda":
-        raise ValueError(f"tensors must be CUDA tensors, got {dev}")
-    if dev.index == torch.cuda.current_device():
-        return call(_stream(stream))
-    with torch.cuda.device(dev):
-        return call(_stream(stream))
+def _call_on(dev: torch.device, stream, fn, *args) -> int:
+    """fn(*args, stream) with ``dev`` current, on ``stream`` or dev's current stream."""
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return fn(*args, _stream(stream))
+    return fn(*args, torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else _stream(stream))
 
 
 def cache_read(d: Dims, cache: torch.Tensor, scale_zero: torch.Tensor | None, block_table: torch.Tensor,
@@ -381,31 +394,34 @@ def cache_read(d: Dims, cache: torch.Tensor, scale_zero: torch.Tensor | None, bl
     from position starts[b] (0 without ``starts``) on.  Returns (c_kv bf16
     [n_rows, 512], k_pe bf16 [n_rows, 64]); ``n_rows`` may be left out where
     an output is given."""
-    dev = cache.device
-    B = block_table.shape[0]
-    _rows(cu_rows, (B + 1,), "cu_rows")
-    if starts is not None:
-        _rows(starts, (B,), "starts")
+    pages = _dims_of(cache, "cache", 3)[0]
+    B, max_pages = _dims_of(block_table, "block_table", 2)
+    dev, P = cache.device, d.page_size
     if n_rows is None:
         given = c_kv if c_kv is not None else k_pe
         if given is None:
             raise ValueError("n_rows is needed where neither c_kv nor k_pe is given")
-        n_rows = given.shape[0]
-    _rows(cache, (None, d.page_size, d.kv_lora_rank + d.rope_dim), "cache")
-    if scale_zero is not None and d.cache_dtype != MLA_CACHE_BF16:
-        _rows(scale_zero, tuple(cache.shape[:2]) + ((2,) if d.cache_dtype == MLA_CACHE_INT8 else ()), "scale_zero")
+        n_rows = _dims_of(given, "c_kv" if c_kv is not None else "k_pe", 2)[0]
     if c_kv is None:
         c_kv = torch.empty((n_rows, d.kv_lora_rank), dtype=torch.bfloat16, device=dev)
     if k_pe is None:
         k_pe = torch.empty((n_rows, d.rope_dim), dtype=torch.bfloat16, device=dev)
-    _rows(c_kv, (n_rows, d.kv_lora_rank), "c_kv")
-    _rows(k_pe, (n_rows, d.rope_dim), "k_pe")
-    args = (ctypes.byref(d), *_cache_ptrs(d, cache, scale_zero, dev), cache.shape[0],
-            _ptr(block_table, torch.int32, "block_table", dev), B, block_table.shape[1],
-            _ptr(starts, torch.int32, "starts", dev), _ptr(cu_rows, torch.int32, "cu_rows", dev), int(n_rows),
-            _ptr(c_kv, torch.bfloat16, "c_kv", dev), _ptr(k_pe, torch.bfloat16, "k_pe", dev),
-            _ptr(device_status, torch.int32, "device_status", dev))
-    _check(_call_on(dev, stream, lambda s: _L().mla_cache_read(*args, s)), "mla_cache_read")
+    code = d.cache_dtype
+    if code == MLA_CACHE_FP8 and cache.dtype == torch.float8_e4m3fn:
+        cache = cache.view(torch.uint8)
+    want = (torch.bfloat16, torch.int8, torch.uint8)[code] if 0 <= code <= 2 else torch.bfloat16
+    st = _call_on(
+        dev, stream, _L().mla_cache_read, ctypes.byref(d),
+        _arg(cache, "cache", want, (pages, P, d.kv_lora_rank + d.rope_dim), dev),
+        None if code == MLA_CACHE_BF16 else
+        _arg(scale_zero, "scale_zero", torch.float32, (pages, P, 2) if code == MLA_CACHE_INT8 else (pages, P), dev),
+        pages, _arg(block_table, "block_table", torch.int32, (B, max_pages), dev), B, max_pages,
+        None if starts is None else _arg(starts, "starts", torch.int32, (B,), dev),
+        _arg(cu_rows, "cu_rows", torch.int32, (B + 1,), dev), int(n_rows),
+        _arg(c_kv, "c_kv", torch.bfloat16, (n_rows, d.kv_lora_rank), dev),
+        _arg(k_pe, "k_pe", torch.bfloat16, (n_rows, d.rope_dim), dev),
+        None if device_status is None else _ptr(device_status, torch.int32, "device_status", dev))
+    _check(st, "mla_cache_read")
     return c_kv, k_pe
 
 
@@ -413,22 +429,19 @@ def expand_kv(d: Dims, c_kv: torch.Tensor, W_UK: torch.Tensor, W_UV: torch.Tenso
               v: torch.Tensor | None = None, device_status: torch.Tensor | None = None, stream=None):
     """mla_expand_kv: latents c_kv bf16 [n, 512] to per-head keys and values.
     Returns (k_nope bf16 [n, H, 128], v bf16 [n, H, 128])."""
-    dev = c_kv.device
-    H = d.num_heads
-    _rows(c_kv, (None, d.kv_lora_rank), "c_kv")
-    _rows(W_UK, (H, d.qk_nope_dim, d.kv_lora_rank), "W_UK")
-    _rows(W_UV, (H, d.v_head_dim, d.kv_lora_rank), "W_UV")
-    n = c_kv.shape[0]
+    n = _dims_of(c_kv, "c_kv", 2)[0]
+    dev, H, R, bf16 = c_kv.device, d.num_heads, d.kv_lora_rank, torch.bfloat16
     if k_nope is None:
-        k_nope = torch.empty((n, H, d.qk_nope_dim), dtype=torch.bfloat16, device=dev)
+        k_nope = torch.empty((n, H, d.qk_nope_dim), dtype=bf16, device=dev)
     if v is None:
-        v = torch.empty((n, H, d.v_head_dim), dtype=torch.bfloat16, device=dev)
-    _rows(k_nope, (n, H, d.qk_nope_dim), "k_nope")
-    _rows(v, (n, H, d.v_head_dim), "v")
-    args = (ctypes.byref(d), _ptr(c_kv, torch.bfloat16, "c_kv"), n, _ptr(W_UK, torch.bfloat16, "W_UK", dev),
-            _ptr(W_UV, torch.bfloat16, "W_UV", dev), _ptr(k_nope, torch.bfloat16, "k_nope", dev),
-            _ptr(v, torch.bfloat16, "v", dev), _ptr(device_status, torch.int32, "device_status", dev))
-    _check(_call_on(dev, stream, lambda s: _L().mla_expand_kv(*args, s)), "mla_expand_kv")
+        v = torch.empty((n, H, d.v_head_dim), dtype=bf16, device=dev)
+    st = _call_on(dev, stream, _L().mla_expand_kv, ctypes.byref(d), _arg(c_kv, "c_kv", bf16, (n, R), dev), n,
+                  _arg(W_UK, "W_UK", bf16, (H, d.qk_nope_dim, R), dev),
+                  _arg(W_UV, "W_UV", bf16, (H, d.v_head_dim, R), dev),
+                  _arg(k_nope, "k_nope", bf16, (n, H, d.qk_nope_dim), dev),
+                  _arg(v, "v", bf16, (n, H, d.v_head_dim), dev),
+                  None if device_status is None else _ptr(device_status, torch.int32, "device_status", dev))
+    _check(st, "mla_expand_kv")
     return k_nope, v
 
 
@@ -449,33 +462,27 @@ def prompt_attention(d: Dims, q_nope: torch.Tensor, q_pe: torch.Tensor, k_nope: 
     query rows cu_q[b] .. cu_q[b + 1] - 1 and the key rows cu_k[b] ..
     cu_k[b + 1] - 1, its queries being its last positions.  Returns (out bf16
     [n_q, H, 128], lse fp32 [n_q, H] or None)."""
-    dev = q_nope.device
-    H = d.num_heads
-    _rows(q_nope, (None, H, d.qk_nope_dim), "q_nope")
-    _rows(k_nope, (None, None, d.qk_nope_dim), "k_nope")
-    n_q, n_k, kv_heads = q_nope.shape[0], k_nope.shape[0], k_nope.shape[1]
-    _rows(q_pe, (n_q, H, d.rope_dim), "q_pe")
-    _rows(k_pe, (n_k, d.rope_dim), "k_pe")
-    _rows(v, (n_k, kv_heads, d.v_head_dim), "v")
-    B = cu_q.shape[0] - 1
-    _rows(cu_q, (B + 1,), "cu_q")
-    _rows(cu_k, (B + 1,), "cu_k")
+    n_q = _dims_of(q_nope, "q_nope", 3)[0]
+    n_k, kv_heads, _ = _dims_of(k_nope, "k_nope", 3)
+    B = _dims_of(cu_q, "cu_q", 1)[0] - 1
+    dev, H, bf16 = q_nope.device, d.num_heads, torch.bfloat16
     if workspace is None:
         workspace = torch.empty(prompt_attention_workspace_size(d, B, n_q), dtype=torch.uint8, device=dev)
     if out is None:
-        out = torch.empty((n_q, H, d.v_head_dim), dtype=torch.bfloat16, device=dev)
+        out = torch.empty((n_q, H, d.v_head_dim), dtype=bf16, device=dev)
     if lse_out is None and want_lse:
         lse_out = torch.empty((n_q, H), dtype=torch.float32, device=dev)
-    _rows(out, (n_q, H, d.v_head_dim), "out")
-    if lse_out is not None:
-        _rows(lse_out, (n_q, H), "lse_out")
-    args = (ctypes.byref(d), _ptr(q_nope, torch.bfloat16, "q_nope"), _ptr(q_pe, torch.bfloat16, "q_pe", dev), n_q,
-            _ptr(k_nope, torch.bfloat16, "k_nope", dev), _ptr(k_pe, torch.bfloat16, "k_pe", dev),
-            _ptr(v, torch.bfloat16, "v", dev), n_k, kv_heads, _ptr(cu_q, torch.int32, "cu_q", dev),
-            _ptr(cu_k, torch.int32, "cu_k", dev), B, float(softmax_scale), _ptr(workspace, None, "workspace", dev),
-            workspace.numel() * workspace.element_size(), _ptr(out, torch.bfloat16, "out", dev),
-            _ptr(lse_out, torch.float32, "lse_out", dev))
-    _check(_call_on(dev, stream, lambda s: _L().mla_prompt_attention(*args, s)), "mla_prompt_attention")
+    st = _call_on(
+        dev, stream, _L().mla_prompt_attention, ctypes.byref(d),
+        _arg(q_nope, "q_nope", bf16, (n_q, H, d.qk_nope_dim), dev),
+        _arg(q_pe, "q_pe", bf16, (n_q, H, d.rope_dim), dev), n_q,
+        _arg(k_nope, "k_nope", bf16, (n_k, kv_heads, d.qk_nope_dim), dev),
+        _arg(k_pe, "k_pe", bf16, (n_k, d.rope_dim), dev), _arg(v, "v", bf16, (n_k, kv_heads, d.v_head_dim), dev), n_k,
+        kv_heads, _arg(cu_q, "cu_q", torch.int32, (B + 1,), dev), _arg(cu_k, "cu_k", torch.int32, (B + 1,), dev), B,
+        float(softmax_scale), _ptr(workspace, None, "workspace", dev), workspace.numel() * workspace.element_size(),
+        _arg(out, "out", bf16, (n_q, H, d.v_head_dim), dev),
+        None if lse_out is None else _arg(lse_out, "lse_out", torch.float32, (n_q, H), dev))
+    _check(st, "mla_prompt_attention")
     return out, lse_out
 
 
