@@ -58,6 +58,7 @@ constexpr uint32_t kColS = 0, kColO = 256;         // tensor memory columns: S x
 constexpr uint64_t kWaitNs = 2000000000ull;        // 2 s
 constexpr float kRescale = 8.f;                    // log2 units
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanSeqs = 1024;                    // sequences whose offsets the plan holds in shared memory
 constexpr int kBuckets = 1024;                     // cost classes of the plan's counting sort
 static_assert(kSmem <= 232448, "dynamic shared memory of one CTA");
 
@@ -84,9 +85,23 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
   __shared__ int hist[kBuckets];
   __shared__ int carry, first_bad, longest, piece_tiles, split_count, partial_count;
   __shared__ float estimate[kPlanThreads / 32];
+  // offsets and block starts, here where they fit: the loops below read them over and over
+  __shared__ int offsets[3][kPlanSeqs + 1];
   griddep_wait();
   griddep_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const bool fits = p.num_seqs <= kPlanSeqs;
+  const int *cu_q = p.cu_q, *cu_k = p.cu_k;
+  int* block_start = p.block_start;
+  if (fits) {
+    for (int b = tid; b <= p.num_seqs; b += kPlanThreads) {
+      offsets[0][b] = p.cu_q[b];
+      offsets[1][b] = p.cu_k[b];
+    }
+    cu_q = offsets[0];
+    cu_k = offsets[1];
+    block_start = offsets[2];
+  }
   if (tid == 0) {
     carry = 0;
     longest = 0;
@@ -98,7 +113,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
   for (int i = tid; i < kBuckets; i += kPlanThreads) hist[i] = 0;
   __syncthreads();
   for (int b = tid; b < p.num_seqs; b += kPlanThreads) {
-    const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1], k0 = p.cu_k[b], k1 = p.cu_k[b + 1];
+    const int q0 = cu_q[b], q1 = cu_q[b + 1], k0 = cu_k[b], k1 = cu_k[b + 1];
     if (q0 < 0 || q1 < q0 || q1 > p.n_q || k0 < 0 || k1 < k0 || k1 > p.n_k) atomicMin(&first_bad, b);
   }
   __syncthreads();
@@ -106,10 +121,10 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
   if (tid == 0 && good < p.num_seqs) set_status(p.status, MLA_ERR_DEVICE_BOUNDS);
   for (int base = 0; base < good; base += kPlanThreads) {
     const int b = base + tid;
-    const int blocks = b < good ? (p.cu_q[b + 1] - p.cu_q[b] + kPromptRows - 1) / kPromptRows : 0;
+    const int blocks = b < good ? (cu_q[b + 1] - cu_q[b] + kPromptRows - 1) / kPromptRows : 0;
     int total;
     const int ex = block_exclusive_scan(blocks, scan_tmp, &total);
-    if (b < good) p.block_start[b] = carry + ex;
+    if (b < good) block_start[b] = carry + ex;
     __syncthreads();
     if (tid == 0) carry += total;
     __syncthreads();
@@ -119,10 +134,10 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
     int lo = 0, hi = good - 1;  // last sequence whose first block is <= i
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (p.block_start[mid] <= i) lo = mid; else hi = mid - 1;
+      if (block_start[mid] <= i) lo = mid; else hi = mid - 1;
     }
-    const int b = lo, q0 = p.cu_q[b], lq = p.cu_q[b + 1] - q0, k0 = p.cu_k[b], lk = p.cu_k[b + 1] - k0;
-    const int r0 = (i - p.block_start[b]) * kPromptRows;
+    const int b = lo, q0 = cu_q[b], lq = cu_q[b + 1] - q0, k0 = cu_k[b], lk = cu_k[b + 1] - k0;
+    const int r0 = (i - block_start[b]) * kPromptRows;
     PromptItem it;
     it.q_row0 = q0 + r0;
     it.rows = min(kPromptRows, lq - r0);
@@ -203,7 +218,6 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
     if (c > 1) {
       it.split = atomicAdd(&split_count, 1);
       it.partial = atomicAdd(&partial_count, c * it.rows * p.heads);
-      for (int e = 0; e < p.heads * 8; ++e) p.arrived[size_t(it.split) * p.heads * 8 + e] = 0;
     }
     for (int q = 0; q < c; ++q) {
       const int t0 = q * t / c, t1 = (q + 1) * t / c;
@@ -213,6 +227,8 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
       p.items[atomicAdd(&hist[kBuckets - 1 - min(kBuckets - 1, t1 - t0)], 1)] = it;
     }
   }
+  __syncthreads();
+  for (int e = tid; e < split_count * p.heads * 8; e += kPlanThreads) p.arrived[e] = 0;
 }
 
 // ----- attention -------------------------------------------------------------------
