@@ -414,7 +414,8 @@ size_t mla_prompt_attention_workspace_size(const mla_dims* dims, int32_t num_seq
  * left as they were, and no row of another sequence or of none ever reaches a
  * result, whatever it holds.  Within a sequence a NaN or infinity in a key
  * reaches only the queries that see it; one in a value may also reach the
- * queries up to 127 positions before it.  Tensors are 16-byte aligned.
+ * queries up to 127 positions before it.  The bf16 inputs are 16-byte aligned,
+ * out 32-byte aligned.
  * Results are bit-identical between runs; calls sharing one workspace must not
  * overlap on the device.  dims' page_size and cache_dtype are not used.
  */

@@ -375,6 +375,12 @@ __device__ __forceinline__ void tie(uint32_t (&r)[32]) {
   for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
 }
 
+// 32 bytes at a 32-byte-aligned address: a whole sector per lane.
+__device__ __forceinline__ void st_global_32(void* dst, uint4 a, uint4 b) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(a.x), "r"(a.y), "r"(a.z),
+               "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
 // One lane of the (converged) warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;

@@ -101,13 +101,6 @@ __device__ __forceinline__ void tma2_load_2d(void* dst, const CUtensorMap* map, 
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// 32 bytes at a 32-byte-aligned address: a whole sector per lane.
-__device__ __forceinline__ void st_global_32(void* dst, const uint32_t (&w)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
-}
-
 // kRowsResident: latents resident, weights streamed; else the other way round.
 template <bool kRowsResident>
 __global__ void __launch_bounds__(kExpThreads, 1)
@@ -263,7 +256,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
               const __nv_bfloat162 y = __floats2bfloat162_rn(__uint_as_float(x[0]), __uint_as_float(x[1]));
               w[e] = *reinterpret_cast<const uint32_t*>(&y);
             }
-            st_global_32(dst + c + 16 * i, w);
+            st_global_32(dst + c + 16 * i, make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]));
           }
         }
       }

@@ -568,7 +568,7 @@ int mla_prompt_attention(const mla_dims* d, const void* q_nope, const void* q_pe
   if (n_q > 0 && (!q_nope || !q_pe || !out)) return MLA_ERR_INVALID_ARG;
   if (n_q > 0 && n_k > 0 && (!k_nope || !k_pe || !v)) return MLA_ERR_INVALID_ARG;
   if (!aligned(q_nope, 16) || !aligned(q_pe, 16) || !aligned(k_nope, 16) || !aligned(k_pe, 16) || !aligned(v, 16) ||
-      !aligned(out, 16) || (lse_out && !aligned(lse_out, 4)))
+      !aligned(out, 32) || (lse_out && !aligned(lse_out, 4)))
     return MLA_ERR_INVALID_ARG;
   const PromptLayout L = prompt_layout(num_seqs, n_q, d->num_heads);
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < L.total) return MLA_ERR_WORKSPACE;

@@ -52,7 +52,7 @@ constexpr uint32_t kQTile = 3 * kBox;              // q_nope columns 0-63, 64-12
 constexpr int kRing = 8;                           // boxes of the key / value ring
 constexpr uint32_t kOffRing = 2 * kQTile;
 constexpr uint32_t kOffMisc = kOffRing + kRing * kBox;
-constexpr uint32_t kSmem = kOffMisc + 512 + 1024;  // + barriers, alignment slack
+constexpr uint32_t kSmem = kOffMisc + 1024 + 1024;  // + barriers, alignment slack
 constexpr int kPromptThreads = 384;
 constexpr uint32_t kColS = 0, kColO = 256;         // tensor memory columns: S x2, O x2
 constexpr uint64_t kWaitNs = 2000000000ull;        // 2 s
@@ -232,6 +232,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
 }
 
 // ----- attention -------------------------------------------------------------------
+constexpr int kItemRing = 4;
 struct PromptBarriers {
   uint64_t q_full[2], q_empty[2];  // query tile loaded / read by its last QK
   uint64_t k_full[2], v_full[2];   // boxes of even / odd key tiles landed
@@ -242,6 +243,8 @@ struct PromptBarriers {
   uint64_t v_clean[2];             // a ragged value tile's rows past the last key cleared
   uint64_t turn[2];                // the MMA threads' turns
   uint64_t drain[2];
+  uint64_t item_full[kItemRing], item_empty[kItemRing];
+  PromptItem items[kItemRing];     // the CTA's units, read ahead by the producer (head in pad[0]; rows = 0: no more)
   uint32_t tmem_base;
   int abort;
 };
@@ -289,29 +292,12 @@ __device__ __forceinline__ float row_max(const uint32_t (&s)[4][32]) {  // four 
   return fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), -INFINITY);  // NaN scores do not count
 }
 
-// Volatile: the softmax warps load an item once more for their epilogue rather
-// than hold its fields in registers through the key loop.
-__device__ __forceinline__ int4 load_int4(const int4* src) {
-  int4 v;
-  asm volatile("ld.global.v4.s32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(src));
-  return v;
-}
-__device__ __forceinline__ PromptItem load_item(const PromptItem* items, int i) {
-  const int4* src = reinterpret_cast<const int4*>(items + i);
-  const int4 a = load_int4(src), b = load_int4(src + 1), c = load_int4(src + 2);
-  return {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, {0, 0}};
+__device__ __forceinline__ PromptItem load_item(const PromptItem* src) {  // 16-byte loads, global or shared
+  const int4* v = reinterpret_cast<const int4*>(src);
+  const int4 a = v[0], b = v[1], c = v[2];
+  return {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, {c.z, c.w}};
 }
 
-// The same for a whole warp, uniform in the eyes of the compiler.
-__device__ __forceinline__ PromptItem load_item_uniform(const PromptItem* items, int i) {
-  PromptItem it = load_item(items, i);
-  it.q_row0 = __shfl_sync(0xffffffffu, it.q_row0, 0);
-  it.rows = __shfl_sync(0xffffffffu, it.rows, 0);
-  it.vis0 = __shfl_sync(0xffffffffu, it.vis0, 0);
-  it.kv_begin = __shfl_sync(0xffffffffu, it.kv_begin, 0);
-  it.kv_end = __shfl_sync(0xffffffffu, it.kv_end, 0);
-  return it;
-}
 // 1 / l; 0 for a row without keys (l = 0); NaN stays NaN.
 __device__ __forceinline__ float inverse_sum(float l) { return l > 0.f ? __frcp_rn(l) : (l == 0.f ? 0.f : l); }
 
@@ -375,6 +361,13 @@ static __device__ __noinline__ void merge_rows(const PromptParams& p, const Prom
   if (p.lse_out) p.lse_out[orow] = l == 0.f ? -INFINITY : base * p.scale + logf(l);
 }
 
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int x, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+
 // Key tiles of query tile t (0, 1) of an item.
 __device__ __forceinline__ int tiles_of(const PromptItem& it, int t) {
   if (it.rows <= 128 * t) return 0;
@@ -400,6 +393,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   // uniform in the eyes of the compiler, so that the MMA warps' descriptors live in uniform registers
   const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
+    for (int i = 0; i < kItemRing; ++i) {
+      mbar_init(&B->item_full[i], 1);
+      mbar_init(&B->item_empty[i], 11);  // 8 softmax warps, 2 MMA warps, the clearing warp
+    }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&B->q_full[t], 1);
       mbar_init(&B->q_empty[t], 1);
@@ -431,32 +428,52 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   griddep_launch_dependents();
   const volatile int* abort_flag = &B->abort;
   const int H = p.heads, group = H / p.kv_heads;
-  const int units = p.status[1] * H;
+  // waits for the CTA's n-th unit; false: a wait failed
+  auto item_ready = [&](int n) {
+    return mbar_wait(&B->item_full[n % kItemRing], (n / kItemRing) & 1, abort_flag, kWaitNs);
+  };
 
   if (warp == 8 && lane == 0) {
     // ------------------------------------------------------------ TMA producer
     // Box i (0-2: K, 3-4: V) of key tile j sits at ring position (5 j + i) % 8,
     // last used by box (5 j + i - 8): K_{j-2} for i = 0, V_{j-2} for i = 1, 2,
     // K_{j-1} for i = 3, 4.  j counts the CTA's key tiles over all its items.
+    // Units are published two ahead of their loads' end: the MMA warps fetch
+    // their next query tile as soon as the last QK of a unit is done.
     bool ok = true;
-    uint32_t j = 0, nq[2] = {0, 0};
-    for (int n = 0; ok; ++n) {
+    uint32_t j = 0;
+    const int units = p.status[1] * H;
+    PromptItem it, next;
+    auto fetch = [&](int n, PromptItem& x) {
       const int u = unit_of(n);
-      if (u >= units) break;
-      const PromptItem it = load_item(p.items, u / H);
-      const int h = u % H, g = h / group;
-      const int nt0 = tiles_of(it, 0), nt1 = tiles_of(it, 1), nt = max(nt0, nt1);
-      for (int t = 0; t < 2 && ok; ++t) {
-        if (!(t ? nt1 : nt0)) continue;
-        if (nq[t] > 0 && !(ok = mbar_wait(&B->q_empty[t], (nq[t] - 1) & 1, abort_flag, kWaitNs))) break;
-        ++nq[t];
-        uint8_t* q = smem + t * kQTile;
-        const int row = it.q_row0 + 128 * t;
-        mbar_arrive_expect_tx(&B->q_full[t], kQTile);
-        tma_load_3d(q, &map_qn, 0, h, row, &B->q_full[t]);
-        tma_load_3d(q + kBox, &map_qn, 64, h, row, &B->q_full[t]);
-        tma_load_3d(q + 2 * kBox, &map_qp, 0, h, row, &B->q_full[t]);
+      if (u < units) {
+        x = load_item(p.items + u / H);
+        x.pad[0] = u % H;
+      } else {
+        x.rows = 0;
       }
+    };
+    auto publish = [&](int n, const PromptItem& x) {
+      const int slot = n % kItemRing;
+      if (n >= kItemRing && !mbar_wait(&B->item_empty[slot], ((n / kItemRing) - 1) & 1, abort_flag, kWaitNs)) return false;
+      B->items[slot] = x;
+      mbar_arrive(&B->item_full[slot]);
+      return true;
+    };
+    fetch(0, it);
+    fetch(1, next);
+    ok = publish(0, it);
+    for (int n = 0; ok && it.rows > 0; ++n, it = next, fetch(n + 1, next)) {
+      if (!(ok = publish(n + 1, next))) break;
+      if (next.rows > 0) {  // the next unit's queries on their way to L2
+        for (int t = 0; 128 * t < next.rows; ++t) {
+          tma_prefetch_3d(&map_qn, 0, next.pad[0], next.q_row0 + 128 * t);
+          tma_prefetch_3d(&map_qn, 64, next.pad[0], next.q_row0 + 128 * t);
+          tma_prefetch_3d(&map_qp, 0, next.pad[0], next.q_row0 + 128 * t);
+        }
+      }
+      const int g = it.pad[0] / group;
+      const int nt = max(tiles_of(it, 0), tiles_of(it, 1));
       for (int kt = 0; kt < nt && ok; ++kt, ++j) {
         const int key = it.k_row0 + it.kv_begin + kt * kKeys;
 #pragma unroll 1
@@ -500,7 +517,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                    ring_v = kDescMN | desc_addr(sbase + kOffRing);
     const bool leader = elect_one();
     bool ok = true;
-    uint32_t j = 0, nq = 0, np = 0, no = 0, nragged = 0, nturn = 0;
+    uint32_t j = 0, nload = 0, nq = 0, np = 0, no = 0, nragged = 0, nturn = 0;
     // turn k of tile 1 follows turn k of tile 0, which follows turn k - 1 of tile 1
     auto take_turn = [&]() {
       const bool w = mbar_wait(&B->turn[t], (nturn & 1) ^ (t ^ 1), abort_flag, kWaitNs);
@@ -537,12 +554,36 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       __syncwarp();
       return true;
     };
+    // this warp's query tile of unit n, once the last QK before it has read the buffer
+    auto load_q = [&](int n) -> bool {
+      if (!item_ready(n)) return false;
+      const PromptItem it = load_item(&B->items[n % kItemRing]);
+      if (tiles_of(it, t) == 0) return true;
+      if (nload > 0 && !mbar_wait(&B->q_empty[t], (nload - 1) & 1, abort_flag, kWaitNs)) return false;
+      ++nload;
+      if (leader) {
+        uint8_t* q = smem + t * kQTile;
+        const int row = it.q_row0 + 128 * t;
+        mbar_arrive_expect_tx(&B->q_full[t], kQTile);
+        tma_load_3d(q, &map_qn, 0, it.pad[0], row, &B->q_full[t]);
+        tma_load_3d(q + kBox, &map_qn, 64, it.pad[0], row, &B->q_full[t]);
+        tma_load_3d(q + 2 * kBox, &map_qp, 0, it.pad[0], row, &B->q_full[t]);
+      }
+      __syncwarp();
+      return true;
+    };
+    ok = load_q(0);
     for (int n = 0; ok; ++n) {
-      const int u = unit_of(n);
-      if (u >= units) break;
-      const PromptItem it = load_item_uniform(p.items, u / H);
-      const int mine = tiles_of(it, t), nt = max(mine, tiles_of(it, t ^ 1));
-      if (nt == 0) continue;
+      if (!(ok = item_ready(n))) break;
+      const PromptItem it = load_item(&B->items[n % kItemRing]);
+      __syncwarp();
+      if (leader) mbar_arrive(&B->item_empty[n % kItemRing]);
+      if (it.rows == 0) break;
+      const int mine = __shfl_sync(0xffffffffu, tiles_of(it, t), 0);
+      const int nt = __shfl_sync(0xffffffffu, max(mine, tiles_of(it, t ^ 1)), 0);
+      const int keys = __shfl_sync(0xffffffffu, it.kv_end - it.kv_begin, 0);
+      if (mine == 0) ok = load_q(n + 1);
+      if (nt == 0 || !ok) continue;
       if (mine > 0) {
         ok = mbar_wait(&B->q_full[t], nq & 1, abort_flag, kWaitNs);
         ++nq;
@@ -553,11 +594,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const uint32_t s0 = (5 * j + 3) % kRing;
         const uint64_t v0 = ring_v + s0 * (kBox >> 4);
         ok = t == 1 || mbar_wait(&B->v_full[j & 1], (j >> 1) & 1, abort_flag, kWaitNs);
-        const int valid = it.kv_end - it.kv_begin - kt * kKeys;
+        const int valid = keys - kt * kKeys;
         if (t == 0 && valid < kKeys && (valid & 15)) {  // the last tile's rows past the keys are cleared first
           ok = ok && mbar_wait(&B->v_clean[nragged & 1], (nragged >> 1) & 1, abort_flag, kWaitNs);
           ++nragged;
         }
+        if (ok && kt == mine - 1) ok = load_q(n + 1);  // while the last weights are computed
         if (ok && kt < mine) {
           if (kt == 0 && no > 0) ok = mbar_wait(&B->o_free[t], (no - 1) & 1, abort_flag, kWaitNs);
           ok = ok && mbar_wait(&B->p_full[t], np & 1, abort_flag, kWaitNs);
@@ -615,9 +657,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     bool ok = true;
     uint32_t j = 0, nragged = 0;
     for (int n = 0; ok; ++n) {
-      const int u = unit_of(n);
-      if (u >= units) break;
-      const PromptItem it = load_item(p.items, u / H);
+      if (!(ok = item_ready(n))) break;
+      const PromptItem it = load_item(&B->items[n % kItemRing]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&B->item_empty[n % kItemRing]);
+      if (it.rows == 0) break;
       const int nt = max(tiles_of(it, 0), tiles_of(it, 1));
       const int valid = it.kv_end - it.kv_begin - (nt - 1) * kKeys;
       const bool ragged = nt > 0 && valid < kKeys && (valid & 15);
@@ -654,11 +698,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     bool ok = true;
     uint32_t ns = 0, no = 0;
     for (int n = 0; ok; ++n) {
-      const int u = unit_of(n);
-      if (u >= units) break;
+      ok = item_ready(n);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
       int nt, vis, vis_first, keys;
       {
-        const PromptItem it = load_item(p.items, u / H);
+        const PromptItem it = load_item(&B->items[n % kItemRing]);
+        if (it.rows == 0) break;
         nt = tiles_of(it, t);
         vis = it.vis0 + 128 * t + r - it.kv_begin;  // keys of this item's range that the row sees
         vis_first = it.vis0 + 128 * t - it.kv_begin;
@@ -741,8 +789,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (lane == 0) mbar_arrive(&B->p_rest[t]);
       }
       if (!ok) break;
-      const PromptItem it = load_item(p.items, u / H);
-      const int h = u % H, row = 128 * t + r;  // row of the item
+      const PromptItem it = load_item(&B->items[n % kItemRing]);  // not held in registers through the key loop
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&B->item_empty[n % kItemRing]);
+      const int h = it.pad[0], row = 128 * t + r;  // row of the item
       const bool live = row < it.rows;
       const size_t orow = size_t(it.q_row0 + row) * H + h;
       if (nt > 0) {
@@ -758,13 +808,24 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         uint4* dst = reinterpret_cast<uint4*>(p.out + orow * kVDim);
         if (nt > 0) {
           const float inv = inverse_sum(l);
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t o[32];
-            tmem_ld32(to + 32 * c, o);
+#pragma unroll
+          for (int c = 0; c < 4; c += 2) {
+            uint32_t o[2][32];
+            tmem_ld32_async(to + 32 * c, o[0]);
+            tmem_ld32_async(to + 32 * c + 32, o[1]);
+            tmem_ld_wait();
+            tie(o[0]);
+            tie(o[1]);
+            if (c == 2) {  // the output is read: the next unit's products may overwrite it
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&B->o_free[t]);
+            }
             if (live) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) dst[4 * c + i] = pack_out(&o[8 * i], inv);
+              for (int i = 0; i < 4; ++i)
+                st_global_32(dst + 4 * c + 2 * i, pack_out(&o[i >> 1][16 * (i & 1)], inv),
+                             pack_out(&o[i >> 1][16 * (i & 1) + 8], inv));
             }
           }
         } else if (live) {
@@ -802,7 +863,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           merge_rows(p, it, prow0, orow, live);
         }
       }
-      if (nt > 0) {
+      if (nt > 0 && it.pieces > 1) {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&B->o_free[t]);
