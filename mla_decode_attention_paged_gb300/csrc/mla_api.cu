@@ -404,11 +404,11 @@ SparseLayout sparse_layout(const mla_dims* d, int batch, int top_k, size_t decod
   return L;
 }
 
-// Workspace of mla_prompt_attention: the status word and item count, the
-// first block of every sequence, the list of items (a sequence of n rows has
+// Workspace of mla_prompt_attention: the status word, item count and unit
+// counter, the first block and first item of every sequence, the list of items (a sequence of n rows has
 // at most n / 256 + 1 blocks), and the partial results of split blocks.
 struct PromptLayout {
-  size_t status, block_start, items, arrived, partial_ml, partial_o, total;
+  size_t status, block_start, seq_first, items, arrived, partial_ml, partial_o, total;
   int partial_rows;
 };
 
@@ -417,8 +417,9 @@ PromptLayout prompt_layout(int num_seqs, int n_q, int heads) {
   size_t off = 0;
   const long long most = (long long)n_q * heads * kPromptMaxPieces;
   L.partial_rows = most < kPromptPartialRows ? int(most) : kPromptPartialRows;
-  L.status = off;       off = align256(off + 8);
+  L.status = off;       off = align256(off + 12);
   L.block_start = off;  off = align256(off + 4 * (size_t(num_seqs) + 1));
+  L.seq_first = off;    off = align256(off + 4 * size_t(num_seqs));
   L.items = off;        off = align256(off + sizeof(PromptItem) * (size_t(n_q) / kPromptRows + num_seqs + kPromptExtraItems));
   L.arrived = off;      off = align256(off + size_t(4) * kPromptMaxSplit * heads * 8);
   L.partial_ml = off;   off = align256(off + sizeof(float2) * L.partial_rows);
@@ -587,6 +588,7 @@ int mla_prompt_attention(const mla_dims* d, const void* q_nope, const void* q_pe
   p.lse_out = lse_out;
   p.status = reinterpret_cast<int*>(ws + L.status);
   p.block_start = reinterpret_cast<int*>(ws + L.block_start);
+  p.seq_first = reinterpret_cast<int*>(ws + L.seq_first);
   p.items = reinterpret_cast<PromptItem*>(ws + L.items);
   p.arrived = reinterpret_cast<int*>(ws + L.arrived);
   p.partial_o = reinterpret_cast<float*>(ws + L.partial_o);

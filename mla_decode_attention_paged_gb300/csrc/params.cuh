@@ -109,7 +109,8 @@ struct alignas(16) PromptItem {
   int pieces, piece;     // items that share the block's keys, and which one this is
   int split;             // pieces > 1: number of the block among the split ones
   int partial;           // pieces > 1: first partial row of the block
-  int pad[2];
+  int head;              // the unit's head (in the attention kernel's copy)
+  int pad;
 };
 constexpr int kPromptRows = 256;         // query rows of a block
 constexpr int kPromptMaxPieces = 32;     // pieces of one block
@@ -123,7 +124,8 @@ struct PromptParams {
   const __nv_bfloat16 *q_nope, *q_pe, *k_nope, *k_pe, *v;
   __nv_bfloat16* out;        // [n_q, heads, 128]
   float* lse_out;            // [n_q, heads] or null
-  int* status;               // workspace: status word, then the number of items
+  int* status;               // workspace: status word, number of items, units taken
+  int* seq_first;            // workspace: [num_seqs] first item of each sequence
   int* block_start;          // workspace: [num_seqs + 1] first block of each sequence
   PromptItem* items;         // workspace: [n_q / 256 + num_seqs + kPromptExtraItems]
   int* arrived;              // workspace: [kPromptMaxSplit][heads][8] pieces done, per 32 rows
