@@ -29,9 +29,9 @@
 // for the MMA (2^-9 relative per weight, averaged over the keys); the sum
 // takes the unrounded fp32 weights.
 //
-// Warps: 0-3 softmax and epilogue of query tile 0, 4-7 of tile 1, 8 TMA
-// producer, 9 (which also owns tensor memory) and 10 MMA issue for tiles 0 and
-// 1, 11 clears the ragged ends of value tiles.  Every wait is bounded: on timeout
+// Warps: 0-3 softmax and epilogue of query tile 0, 4-7 of tile 1, 8 units and
+// key copies, 9 (which also owns tensor memory) and 10 query copies and MMA
+// issue for tiles 0 and 1, 11 value copies.  Every wait is bounded: on timeout
 // the CTA records MLA_ERR_DEVICE_TIMEOUT, drains, frees its tensor memory and
 // returns.
 #include <atomic>
@@ -267,7 +267,6 @@ struct PromptBarriers {
   uint64_t s_full[2];              // scores of a tile complete
   uint64_t p_full[2], p_rest[2];   // P of the first 96 keys written (and O rescaled where needed); of the last 32
   uint64_t o_full[2], o_free[2];   // output complete / read
-  uint64_t v_clean[2];             // a ragged value tile's rows past the last key cleared
   uint64_t turn[2];                // the MMA threads' turns
   uint64_t drain[2];
   uint64_t item_full[kItemRing], item_empty[kItemRing];
@@ -415,16 +414,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kItemRing; ++i) {
       mbar_init(&B->item_full[i], 1);
-      mbar_init(&B->item_empty[i], 11);  // 8 softmax warps, 2 MMA warps, the clearing warp
+      mbar_init(&B->item_empty[i], 11);  // 8 softmax warps, 2 MMA warps, the value producer
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&B->q_full[t], 1);
       mbar_init(&B->q_empty[t], 1);
       mbar_init(&B->k_full[t], 1);
       mbar_init(&B->v_full[t], 1);
-      mbar_init(&B->k_empty[t], 3);  // both MMA threads and the clearing warp
-      mbar_init(&B->v_empty[t], 3);
-      mbar_init(&B->v_clean[t], 1);
+      mbar_init(&B->k_empty[t], 2);  // both MMA warps
+      mbar_init(&B->v_empty[t], 2);
       mbar_init(&B->s_full[t], 1);
       mbar_init(&B->turn[t], 1);
       mbar_init(&B->drain[t], 1);
@@ -454,10 +452,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   };
 
   if (warp == 8 && lane == 0) {
-    // ------------------------------------------------------------ TMA producer
+    // ------------------------------------------------------------ units, key copies
     // Box i (0-2: K, 3-4: V) of key tile j sits at ring position (5 j + i) % 8,
     // last used by box (5 j + i - 8): K_{j-2} for i = 0, V_{j-2} for i = 1, 2,
     // K_{j-1} for i = 3, 4.  j counts the CTA's key tiles over all its items.
+    // One thread takes about 650 cycles to issue a box, five boxes as long as a
+    // key tile's products, so the values have their own (warp 11).
     // Units are published two ahead of their loads' end: the MMA warps fetch
     // their next query tile as soon as the last QK of a unit is done.
     bool ok = true;
@@ -465,15 +465,19 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     // Unit u is item u / H for head u % H.  Each CTA's first is its own number,
     // the others come from a counter: which CTA runs a unit does not change it.
     const int units = p.status[1] * H;
-    PromptItem it, next;
-    auto fetch = [&](int n, PromptItem& x) {
-      const int u = n == 0 ? int(blockIdx.x) : int(gridDim.x) + atomicAdd(&p.status[2], 1);
+    // The counter's answer and the item it leads to are each waited for a key
+    // tile later: this thread issues in order, and a wait here holds back the
+    // copies.
+    PromptItem it, next, after;
+    auto take = [&]() { return int(gridDim.x) + atomicAdd(&p.status[2], 1); };
+    auto fetch = [&](int u) {
+      PromptItem x;
+      x.rows = 0;
       if (u < units) {
         x = load_item(p.items + u / H);
         x.head = u % H;
-      } else {
-        x.rows = 0;
       }
+      return x;
     };
     auto publish = [&](int n, const PromptItem& x) {
       const int slot = n % kItemRing;
@@ -482,11 +486,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       mbar_arrive(&B->item_full[slot]);
       return true;
     };
-    fetch(0, it);
-    fetch(1, next);  // the counter stops at most two past the units for each CTA
+    it = fetch(blockIdx.x);
     ok = publish(0, it);
-    for (int n = 0; ok && it.rows > 0; ++n, it = next, fetch(n + 1, next)) {
+    int u_after = it.rows > 0 ? take() : units;
+    next = fetch(u_after);  // the counter stops at most two past the units for each CTA
+    for (int n = 0; ok && it.rows > 0; ++n, it = next, next = after) {
       if (!(ok = publish(n + 1, next))) break;
+      u_after = take();
+      bool fetched = false;
       if (next.rows > 0) {  // the next unit's queries on their way to L2
         for (int t = 0; 128 * t < next.rows; ++t) {
           tma_prefetch_3d(&map_qn, 0, next.head, next.q_row0 + 128 * t);
@@ -498,20 +505,19 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       const int nt = max(tiles_of(it, 0), tiles_of(it, 1));
       for (int kt = 0; kt < nt && ok; ++kt, ++j) {
         const int key = it.k_row0 + it.kv_begin + kt * kKeys;
-#pragma unroll 1
-        for (int i = 0; i < 5; ++i) {
-          if (i == 0 && j >= 2) ok = mbar_wait(&B->k_empty[j & 1], ((j - 2) >> 1) & 1, abort_flag, kWaitNs);
-          if (i == 1 && j >= 2) ok = mbar_wait(&B->v_empty[j & 1], ((j - 2) >> 1) & 1, abort_flag, kWaitNs);
-          if (i == 3 && j >= 1) ok = mbar_wait(&B->k_empty[(j - 1) & 1], ((j - 1) >> 1) & 1, abort_flag, kWaitNs);
-          if (!ok) break;
-          uint8_t* dst = smem + kOffRing + ((5 * j + i) % kRing) * kBox;
-          uint64_t* bar = i < 3 ? &B->k_full[j & 1] : &B->v_full[j & 1];
-          if (i == 0) mbar_arrive_expect_tx(bar, 3 * kBox);
-          if (i == 3) mbar_arrive_expect_tx(bar, 2 * kBox);
-          if (i == 2) tma_load_2d(dst, &map_kp, 0, key, bar);
-          else tma_load_3d(dst, i < 3 ? &map_kn : &map_v, (i == 1 || i == 4) ? 64 : 0, g, key, bar);
+        uint64_t* bar = &B->k_full[j & 1];
+        if (j >= 2 && !(ok = mbar_wait(&B->k_empty[j & 1], ((j - 2) >> 1) & 1, abort_flag, kWaitNs))) break;
+        mbar_arrive_expect_tx(bar, 3 * kBox);
+        tma_load_3d(smem + kOffRing + (5 * j % kRing) * kBox, &map_kn, 0, g, key, bar);
+        if (j >= 2 && !(ok = mbar_wait(&B->v_empty[j & 1], ((j - 2) >> 1) & 1, abort_flag, kWaitNs))) break;
+        tma_load_3d(smem + kOffRing + ((5 * j + 1) % kRing) * kBox, &map_kn, 64, g, key, bar);
+        tma_load_2d(smem + kOffRing + ((5 * j + 2) % kRing) * kBox, &map_kp, 0, key, bar);
+        if (!fetched) {
+          after = fetch(u_after);
+          fetched = true;
         }
       }
+      if (!fetched) after = fetch(u_after);
     }
     if (!ok) fail(B, p.status);
   } else if (warp == 9 || warp == 10) {
@@ -539,7 +545,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                    ring_v = kDescMN | desc_addr(sbase + kOffRing);
     const bool leader = elect_one();
     bool ok = true;
-    uint32_t j = 0, nload = 0, nq = 0, np = 0, no = 0, nragged = 0, nturn = 0;
+    uint32_t j = 0, nload = 0, nq = 0, np = 0, no = 0, nturn = 0;
     // turn k of tile 1 follows turn k of tile 0, which follows turn k - 1 of tile 1
     auto take_turn = [&]() {
       const bool w = mbar_wait(&B->turn[t], (nturn & 1) ^ (t ^ 1), abort_flag, kWaitNs);
@@ -617,9 +623,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const uint64_t v0 = ring_v + s0 * (kBox >> 4);
         ok = t == 1 || mbar_wait(&B->v_full[j & 1], (j >> 1) & 1, abort_flag, kWaitNs);
         const int valid = keys - kt * kKeys;
-        if (t == 0 && valid < kKeys && (valid & 15)) {  // the last tile's rows past the keys are cleared first
-          ok = ok && mbar_wait(&B->v_clean[nragged & 1], (nragged >> 1) & 1, abort_flag, kWaitNs);
-          ++nragged;
+        if (t == 0 && ok && valid < kKeys && (valid & 15)) {
+          // PV reads whole 16-key steps; the rows of the last tile past its
+          // last key meet zero weights but must be finite: they are cleared
+          // (for the other warp too, whose turn comes later)
+          const int tail = 16 - (valid & 15);
+          for (int i = lane; i < tail * 16; i += 32)
+            *reinterpret_cast<uint4*>(smem + kOffRing + ((s0 + ((i >> 3) & 1)) % kRing) * kBox + (valid + (i >> 4)) * 128 +
+                                      (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
         }
         if (ok && kt == mine - 1) ok = load_q(n + 1);  // while the last weights are computed
         if (ok && kt < mine) {
@@ -670,46 +683,25 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       mbar_wait(&B->drain[t], 0, abort_flag, kWaitNs);
     }
     __syncwarp();
-  } else if (warp == 11) {
-    // ------------------------------------------------------------ ragged ends
-    // PV reads whole 16-key steps; the rows of a range's last value tile past
-    // its last key meet zero weights but must be finite, so they are cleared.
-    // The warp follows every tile and shares in its release: a parity wait is
-    // only right for the phase after the last one seen.
+  } else if (warp == 11 && lane == 0) {
+    // ------------------------------------------------------------ value copies
     bool ok = true;
-    uint32_t j = 0, nragged = 0;
+    uint32_t j = 0;
     for (int n = 0; ok; ++n) {
       if (!(ok = item_ready(n))) break;
       const PromptItem it = load_item(&B->items[n % kItemRing]);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&B->item_empty[n % kItemRing]);
+      mbar_arrive(&B->item_empty[n % kItemRing]);
       if (it.rows == 0) break;
+      const int g = it.head / group;
       const int nt = max(tiles_of(it, 0), tiles_of(it, 1));
-      const int valid = it.kv_end - it.kv_begin - (nt - 1) * kKeys;
-      const bool ragged = nt > 0 && valid < kKeys && (valid & 15);
       for (int kt = 0; kt < nt && ok; ++kt, ++j) {
-        ok = mbar_wait(&B->k_full[j & 1], (j >> 1) & 1, abort_flag, kWaitNs);
-        if (ok && lane == 0) mbar_arrive(&B->k_empty[j & 1]);
-        ok = ok && mbar_wait(&B->v_full[j & 1], (j >> 1) & 1, abort_flag, kWaitNs);
-        if (ok && lane == 0 && !(ragged && kt == nt - 1)) mbar_arrive(&B->v_empty[j & 1]);
+        const int key = it.k_row0 + it.kv_begin + kt * kKeys;
+        uint64_t* bar = &B->v_full[j & 1];
+        if (j >= 1 && !(ok = mbar_wait(&B->k_empty[(j - 1) & 1], ((j - 1) >> 1) & 1, abort_flag, kWaitNs))) break;
+        mbar_arrive_expect_tx(bar, 2 * kBox);
+        tma_load_3d(smem + kOffRing + ((5 * j + 3) % kRing) * kBox, &map_v, 0, g, key, bar);
+        tma_load_3d(smem + kOffRing + ((5 * j + 4) % kRing) * kBox, &map_v, 64, g, key, bar);
       }
-      if (!__all_sync(0xffffffffu, ok)) {
-        ok = false;
-        break;
-      }
-      if (!ragged) continue;
-      const uint32_t xv = 5 * (j - 1) + 3;
-      const int tail = 16 - (valid & 15);
-      for (int i = lane; i < tail * 16; i += 32)
-        *reinterpret_cast<uint4*>(smem + kOffRing + ((xv + ((i >> 3) & 1)) % kRing) * kBox + (valid + (i >> 4)) * 128 +
-                                  (i & 7) * 16) = make_uint4(0, 0, 0, 0);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&B->v_clean[nragged & 1]);
-        mbar_arrive(&B->v_empty[(j - 1) & 1]);
-      }
-      ++nragged;
     }
     if (!ok) fail(B, p.status);
   } else if (warp < 8) {
