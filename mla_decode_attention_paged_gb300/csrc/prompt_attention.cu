@@ -579,7 +579,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           mbar_arrive(&B->k_empty[jj & 1]);
         }
       }
-      __syncwarp();
       return true;
     };
     // this warp's query tile of unit n, once the last QK before it has read the buffer
@@ -597,12 +596,19 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         tma_load_3d(q + kBox, &map_qn, 64, it.head, row, &B->q_full[t]);
         tma_load_3d(q + 2 * kBox, &map_qp, 0, it.head, row, &B->q_full[t]);
       }
-      __syncwarp();
       return true;
     };
     ok = load_q(0);
-    for (int n = 0; ok; ++n) {
-      if (!(ok = item_ready(n))) break;
+    for (int n = 0;; ++n) {
+      // Lanes may disagree on a wait that runs out.  They meet here once a unit
+      // (and nowhere else, so that none waits for one that left): a lane that
+      // gave up has raised the abort flag, which ends the others' waits.
+      ok = ok && item_ready(n);
+      if (!ok) fail(B, p.status);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
       const PromptItem it = load_item(&B->items[n % kItemRing]);
       __syncwarp();
       if (leader) mbar_arrive(&B->item_empty[n % kItemRing]);
@@ -616,23 +622,24 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         ok = mbar_wait(&B->q_full[t], nq & 1, abort_flag, kWaitNs);
         ++nq;
       }
-      if (!(ok = ok && take_turn())) break;
+      if (!(ok = ok && take_turn())) continue;
       ok = qk(j, mine > 0, mine == 1);
       for (int kt = 0; kt < nt && ok; ++kt, ++j) {
         const uint32_t s0 = (5 * j + 3) % kRing;
         const uint64_t v0 = ring_v + s0 * (kBox >> 4);
         ok = t == 1 || mbar_wait(&B->v_full[j & 1], (j >> 1) & 1, abort_flag, kWaitNs);
         const int valid = keys - kt * kKeys;
-        if (t == 0 && ok && valid < kKeys && (valid & 15)) {
+        if (t == 0 && ok && valid < kKeys && (valid & 15) && leader) {
           // PV reads whole 16-key steps; the rows of the last tile past its
           // last key meet zero weights but must be finite: they are cleared
           // (for the other warp too, whose turn comes later)
-          const int tail = 16 - (valid & 15);
-          for (int i = lane; i < tail * 16; i += 32)
-            *reinterpret_cast<uint4*>(smem + kOffRing + ((s0 + ((i >> 3) & 1)) % kRing) * kBox + (valid + (i >> 4)) * 128 +
-                                      (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+          uint8_t* box[2] = {smem + kOffRing + s0 * kBox, smem + kOffRing + ((s0 + 1) % kRing) * kBox};
+          for (int row = valid; row < ((valid + 15) & ~15); ++row) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              *reinterpret_cast<uint4*>(box[i >> 3] + row * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
           fence_proxy_async_smem();
-          __syncwarp();
         }
         if (ok && kt == mine - 1) ok = load_q(n + 1);  // while the last weights are computed
         if (ok && kt < mine) {
