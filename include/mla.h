@@ -494,7 +494,8 @@ int mla_set_timing_events(mla_event_t start, mla_event_t stop);
  * than its copies deliver: that wait cannot complete, runs into its time
  * limit (about 2 s), and the kernel records MLA_ERR_DEVICE_TIMEOUT in the
  * workspace status word, releases its resources and returns; the device and
- * the context stay usable.  Nothing faults, traps or hangs.  Process-wide; 0
+ * the context stay usable.  mla_expand_kv (its first weight or latent copy) and
+ * mla_prompt_attention (its first key tile) take part the same way.  Nothing faults, traps or hangs.  Process-wide; 0
  * (the default) disables it.  Returns MLA_OK. */
 int mla_test_inject_wait_timeout(int32_t enable);
 

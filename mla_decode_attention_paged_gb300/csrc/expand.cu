@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
       for (int i = 0; i < kKBlocks; ++i, ++k) {
         const uint32_t s = k % kStages;
         if (k >= kStages && !(ok = mbar_wait(&B->empty[s], ((k / kStages) - 1) & 1, abort_flag, kWaitNs))) break;
-        if (rank == 0) mbar_arrive_expect_tx(&B->full[s], 2 * kBox);
+        if (rank == 0) mbar_arrive_expect_tx(&B->full[s], 2 * kBox + (p.inject_wait_timeout && k == 0 ? 16 : 0));
         load(!kRowsResident, u % inner, i, smem + kOffRing + s * kBox, mapa_shared(smem_u32(&B->full[s]), 0));
       }
     }

@@ -544,6 +544,7 @@ int mla_expand_kv(const mla_dims* d, const void* c_kv, int32_t n_rows, const voi
   p.n_rows = n_rows;
   p.heads = d->num_heads;
   p.sm_count = sm_count();
+  p.inject_wait_timeout = g_inject_wait_timeout.load();
   if (p.sm_count <= 0) return MLA_ERR_CUDA;
   return launch_expand(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
@@ -602,6 +603,7 @@ int mla_prompt_attention(const mla_dims* d, const void* q_nope, const void* q_pe
   p.sm_count = sm_count();
   p.scale = softmax_scale;
   p.scale_log2 = softmax_scale * kLog2e;
+  p.inject_wait_timeout = g_inject_wait_timeout.load();
   if (p.sm_count <= 0) return MLA_ERR_CUDA;
   if (launch_prompt_plan(p, s) != cudaSuccess) return MLA_ERR_CUDA;
   return launch_prompt_attention(p, s) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;

@@ -95,6 +95,7 @@ struct ExpandParams {
   int* status;                // optional
   int n_rows, heads;
   int sm_count;               // sizes the grid
+  int inject_wait_timeout;    // test hook: 16 bytes of the first streamed box never delivered
 };
 
 // Causal attention over packed prompts (mla_prompt_attention).  The plan
@@ -134,6 +135,7 @@ struct PromptParams {
   int n_q, n_k, num_seqs, heads, kv_heads, sm_count, partial_rows;
   float scale_log2;          // softmax_scale * log2(e)
   float scale;
+  int inject_wait_timeout;   // test hook: 16 bytes of the first key tile never delivered
 };
 
 struct CombineUVParams {

@@ -507,7 +507,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const int key = it.k_row0 + it.kv_begin + kt * kKeys;
         uint64_t* bar = &B->k_full[j & 1];
         if (j >= 2 && !(ok = mbar_wait(&B->k_empty[j & 1], ((j - 2) >> 1) & 1, abort_flag, kWaitNs))) break;
-        mbar_arrive_expect_tx(bar, 3 * kBox);
+        mbar_arrive_expect_tx(bar, 3 * kBox + (p.inject_wait_timeout && j == 0 ? 16 : 0));
         tma_load_3d(smem + kOffRing + (5 * j % kRing) * kBox, &map_kn, 0, g, key, bar);
         if (j >= 2 && !(ok = mbar_wait(&B->v_empty[j & 1], ((j - 2) >> 1) & 1, abort_flag, kWaitNs))) break;
         tma_load_3d(smem + kOffRing + ((5 * j + 1) % kRing) * kBox, &map_kn, 64, g, key, bar);
