@@ -59,6 +59,7 @@ constexpr uint64_t kWaitNs = 2000000000ull;        // 2 s
 constexpr float kRescale = 8.f;                    // log2 units
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanSeqs = 1024;                    // sequences whose offsets the plan holds in shared memory
+constexpr int kMinSplit = 6;                       // key tiles of a block that is never split
 constexpr int kBuckets = 1024;                     // cost classes of the plan's counting sort
 static_assert(kSmem <= 232448, "dynamic shared memory of one CTA");
 
@@ -166,10 +167,14 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
   };
   // more units than two rounds are never split (below): their blocks need no estimate
   const int G = p.sm_count;
-  const bool few = (long long)n * p.heads <= 2 * G;
+  // (nor are short ones: a piece would be little more than its start and merge)
+  bool few = (long long)n * p.heads <= 2 * G && p.n_k > kMinSplit * kKeys;
   if (few) {
     for (int i = tid; i < n; i += kPlanThreads) atomicMax(&longest, key_tiles(block_item(i, sequence_of(i)).kv_end));
     __syncthreads();
+    few = longest > kMinSplit;
+  }
+  if (few) {
     const int T = (longest + warp) / (warp + 1);  // ceil(longest / (warp + 1))
     int pieces = 0, top = 0, rows = 0, splits = 0;
     long long tiles = 0;
@@ -200,11 +205,19 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
       e = warp > 0 ? 1e30f : 1e29f;
     if (lane == 0) estimate[warp] = e;
     __syncthreads();
-    if (tid == 0) {
-      int best = 0;
-      for (int k = 1; k < kPromptMaxPieces; ++k)
-        if (estimate[k] < estimate[best]) best = k;
-      piece_tiles = best == 0 ? 0x7fffffff : (longest + best) / (best + 1);
+    if (warp == 0) {  // the lowest estimate, of equal ones the first
+      float low = estimate[lane];
+      int best = lane;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const float e2 = __shfl_xor_sync(0xffffffffu, low, o);
+        const int b2 = __shfl_xor_sync(0xffffffffu, best, o);
+        if (e2 < low || (e2 == low && b2 < best)) {
+          low = e2;
+          best = b2;
+        }
+      }
+      if (lane == 0) piece_tiles = best == 0 ? 0x7fffffff : (longest + best) / (best + 1);
     }
   } else if (tid == 0) {
     piece_tiles = 0x7fffffff;
@@ -486,7 +499,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       mbar_arrive(&B->item_full[slot]);
       return true;
     };
-    it = fetch(blockIdx.x);
+    it = load_item(p.items + blockIdx.x / H);  // in the list's bounds, if maybe not written: beside the count's load
+    it.head = blockIdx.x % H;
+    if (int(blockIdx.x) >= units) it.rows = 0;
     ok = publish(0, it);
     int u_after = it.rows > 0 ? take() : units;
     next = fetch(u_after);  // the counter stops at most two past the units for each CTA
