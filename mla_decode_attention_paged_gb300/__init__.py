@@ -355,12 +355,14 @@ def decode_sparse(d: Dims, q_nope, q_pe, cache, scale_zero, block_table, seq_len
 
 def _arg(t: torch.Tensor, name: str, dtype, shape: tuple, dev: torch.device) -> int:
     """Pointer of a contiguous tensor of this type, shape and device."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev
-            and t.is_contiguous()):
-        return t.data_ptr()
-    p = _ptr(t, dtype, name, dev)  # raises what is wrong, unless it is the shape
+    try:  # the common case first: these checks are most of a small call's host time
+        if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if t is None:
         raise TypeError(f"{name} must be a torch.Tensor")
+    p = _ptr(t, dtype, name, dev)  # raises what is wrong, unless it is the shape
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
     return p
@@ -368,18 +370,21 @@ def _arg(t: torch.Tensor, name: str, dtype, shape: tuple, dev: torch.device) -> 
 
 def _dims_of(t: torch.Tensor, name: str, n: int):
     """Shape of an ``n``-dimensional CUDA tensor (the sizes the other arguments are checked against)."""
+    try:
+        if t.is_cuda and len(t.shape) == n:
+            return t.shape
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dim() != n:
         raise ValueError(f"{name} must have {n} dimensions, got {list(t.shape)}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return t.shape
+    raise ValueError(f"{name} must be a CUDA tensor")
 
 
 def _call_on(dev: torch.device, stream, fn, *args) -> int:
     """fn(*args, stream) with ``dev`` current, on ``stream`` or dev's current stream."""
-    if dev.index != torch.cuda.current_device():
+    if dev.index != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
             return fn(*args, _stream(stream))
     return fn(*args, torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else _stream(stream))
@@ -479,7 +484,7 @@ def prompt_attention(d: Dims, q_nope: torch.Tensor, q_pe: torch.Tensor, k_nope: 
         _arg(k_nope, "k_nope", bf16, (n_k, kv_heads, d.qk_nope_dim), dev),
         _arg(k_pe, "k_pe", bf16, (n_k, d.rope_dim), dev), _arg(v, "v", bf16, (n_k, kv_heads, d.v_head_dim), dev), n_k,
         kv_heads, _arg(cu_q, "cu_q", torch.int32, (B + 1,), dev), _arg(cu_k, "cu_k", torch.int32, (B + 1,), dev), B,
-        float(softmax_scale), _ptr(workspace, None, "workspace", dev), workspace.numel() * workspace.element_size(),
+        float(softmax_scale), _ptr(workspace, None, "workspace", dev), workspace.nbytes,
         _arg(out, "out", bf16, (n_q, H, d.v_head_dim), dev),
         None if lse_out is None else _arg(lse_out, "lse_out", torch.float32, (n_q, H), dev))
     _check(st, "mla_prompt_attention")
