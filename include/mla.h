@@ -340,7 +340,7 @@ int mla_decode_sparse(const mla_dims* dims, const void* q_nope, const void* q_pe
  *               sequence
  *   n_rows      rows of the outputs; 0 is a no-op
  *   c_kv        bf16 [n_rows, 512] latents;  k_pe bf16 [n_rows, 64] RoPE keys
- *               (rotated, as the append stored them); both 16-byte aligned.
+ *               (rotated, as the append stored them); both 32-byte aligned.
  *               bf16 caches are copied bit for bit; 1-byte caches are
  *               dequantised in fp32 and rounded once to bf16.
  *   device_status  optional int32 (device); a row whose position or page-table

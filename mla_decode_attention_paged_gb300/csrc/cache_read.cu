@@ -124,8 +124,7 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(CacheReadParam
       dequant_codes<kCode>(v[u], scale[u], kCode == kCodeInt8 ? zp[u] : 0.f, lo, hi);
       uint4* dst = q < 32 ? reinterpret_cast<uint4*>(p.c_kv + r * kLatent) + 2 * q
                           : reinterpret_cast<uint4*>(p.k_pe + r * kRope) + 2 * (q - 32);
-      dst[0] = lo;
-      dst[1] = hi;
+      ptx::st_global_32(dst, lo, hi);
     } else {
       uint4* dst = q < 64 ? reinterpret_cast<uint4*>(p.c_kv + r * kLatent) + q
                           : reinterpret_cast<uint4*>(p.k_pe + r * kRope) + (q - 64);

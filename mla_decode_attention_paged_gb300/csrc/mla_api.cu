@@ -502,7 +502,7 @@ int mla_cache_read(const mla_dims* d, const void* cache, const float* cache_scal
   const int code = cache_code(d);
   const bool byte = code != kCodeBf16;
   if (!cache || !block_table || !cu_rows || !c_kv || !k_pe || (byte && !cache_scale_zero)) return MLA_ERR_INVALID_ARG;
-  if (!aligned(cache, 16) || !aligned(c_kv, 16) || !aligned(k_pe, 16) || !aligned(block_table, 4) ||
+  if (!aligned(cache, 16) || !aligned(c_kv, 32) || !aligned(k_pe, 32) || !aligned(block_table, 4) ||
       !aligned(cu_rows, 4) || (starts && !aligned(starts, 4)) || (device_status && !aligned(device_status, 4)) ||
       (byte && !aligned(cache_scale_zero, 8)))
     return MLA_ERR_INVALID_ARG;
