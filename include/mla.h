@@ -1,6 +1,7 @@
 /*
  * mla.h -- C ABI of libmla_gb300: single-token Multi-Head Latent Attention
- * (MLA) decode over a paged, compressed KV cache, for one GB300 (sm_103a).
+ * (MLA) decode over a paged, compressed KV cache, for one GB300 (sm_103a),
+ * and prompts over it (absorbed chunks, and packed prompts un-absorbed).
  *
  * Sources of the operations (page title, then section):
  *   "Beyond the Attention Bottleneck" (micrologics.org), sections
@@ -413,9 +414,9 @@ size_t mla_prompt_attention_workspace_size(const mla_dims* dims, int32_t num_seq
  * Rows of no sequence (before cu_q[0], from cu_q[num_seqs] on, or skipped) are
  * left as they were, and no row of another sequence or of none ever reaches a
  * result, whatever it holds.  Within a sequence a NaN or infinity in a key
- * reaches only the queries that see it; one in a value may also reach the
- * queries up to 127 positions before it.  The bf16 inputs are 16-byte aligned,
- * out 32-byte aligned.
+ * reaches only the queries that see it; one in a value may also reach queries
+ * less than 256 positions before it (as weight 0 times the value).  The bf16
+ * inputs are 16-byte aligned, out 32-byte aligned.
  * Results are bit-identical between runs; calls sharing one workspace must not
  * overlap on the device.  dims' page_size and cache_dtype are not used.
  */

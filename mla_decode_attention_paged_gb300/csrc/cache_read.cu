@@ -11,8 +11,12 @@
 //
 // Bound by memory: 1,152 / 584 / 580 bytes read and 1,152 written per row.  A
 // CTA resolves its rows first (one thread per row: binary search in cu_rows,
-// then the page-table entry), then all threads move 16-byte pieces with every
-// load of the CTA issued before its first store.
+// then the page-table entry), then all threads move 16-byte source pieces with
+// every load of the CTA issued before its first store.  A 1-byte piece becomes
+// 32 bytes, stored at once: as two 16-byte stores, each half of its sectors,
+// 129,000 INT8 rows took 40.6 us, as whole sectors 33.4 us (5.9 TB/s, 88% of
+// the measured copy peak); 194,000 FP8 rows 66 and 53 us (6.4 TB/s, 94%).  32
+// rows to a CTA; 16 took 36.5 us on the INT8 rows.
 #include "blackwell_ptx.cuh"
 #include "decode_common.cuh"
 #include "params.cuh"

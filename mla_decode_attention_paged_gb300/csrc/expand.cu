@@ -11,13 +11,15 @@
 // to each CTA: 256 FLOP to a byte.  It walks a contiguous range of the (resident
 // block, streamed block) list.  The smaller operand is streamed, as it is read
 // once per resident block and should stay in L2: weights (4 MB at 16 heads)
-// where there are more rows than weight rows (256 to a head), else latents.  34,816 rows
-// at 16 heads: 112 us with the weights streamed, 120 with the latents; 5,003
-// rows at 128 heads: 137 and 127 us.  Accumulators (256 columns) alternate
-// between the two halves of tensor memory, so that rounding and storing a tile
-// overlaps the next tile's MMAs; each thread stores its row in whole 32-byte
-// sectors.  What bounds both sizes now is the outputs' way to memory: without
-// the stores they take 72 and 81 us, and filling as many bytes takes 74 and 84.
+// where there are more rows than weight rows (256 to a head), else latents.
+// 34,816 rows at 16 heads: 110 us with the weights streamed, 120 with the
+// latents; 5,003 rows at 128 heads: 137 and 128 us.  Accumulators (256 columns)
+// alternate between the two halves of tensor memory, so that rounding and
+// storing a tile overlaps the next tile's MMAs; each thread stores its row in
+// whole 32-byte sectors.  What bounds both sizes now is products and outputs
+// together: without the stores they take 72 and 82 us (1.9 and 2.0 PFLOP/s),
+// without the streamed copies 92 and 106, and filling as many bytes takes 74 and
+// 84 us.
 //
 // Warps: 0 TMA producer, 1 tensor memory and (in the leading CTA) MMA issue,
 // 2-5 epilogue.  Every wait is bounded: on timeout the CTA records
