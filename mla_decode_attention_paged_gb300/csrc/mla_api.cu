@@ -405,12 +405,20 @@ SparseLayout sparse_layout(const mla_dims* d, int batch, int top_k, size_t decod
 }
 
 // Workspace of mla_prompt_attention: the status word, item count and unit
-// counter, the first block and first item of every sequence, the list of items (a sequence of n rows has
-// at most n / 256 + 1 blocks), and the partial results of split blocks.
+// counter, the first block and first item of every sequence, the list of
+// items (a sequence of n rows, heads packed into them, has at most n / 256 + 1
+// blocks), and the partial results of split blocks.
 struct PromptLayout {
   size_t status, block_start, seq_first, items, arrived, partial_ml, partial_o, total;
   int partial_rows;
 };
+
+// log2 of the largest power of two (at most 128) that divides n.
+int pack_of(int n) {
+  int f = 0;
+  while (f < 7 && n % (2 << f) == 0) ++f;
+  return f;
+}
 
 PromptLayout prompt_layout(int num_seqs, int n_q, int heads) {
   PromptLayout L;
@@ -420,8 +428,8 @@ PromptLayout prompt_layout(int num_seqs, int n_q, int heads) {
   L.status = off;       off = align256(off + 12);
   L.block_start = off;  off = align256(off + 4 * (size_t(num_seqs) + 1));
   L.seq_first = off;    off = align256(off + 4 * size_t(num_seqs));
-  L.items = off;        off = align256(off + sizeof(PromptItem) * (size_t(n_q) / kPromptRows + num_seqs + kPromptExtraItems));
-  L.arrived = off;      off = align256(off + size_t(4) * kPromptMaxSplit * heads * 8);
+  L.items = off;        off = align256(off + sizeof(PromptItem) * ((size_t(n_q) << pack_of(heads)) / kPromptRows + num_seqs + kPromptExtraItems));
+  L.arrived = off;      off = align256(off + size_t(4) * kPromptMaxSplit * 8);
   L.partial_ml = off;   off = align256(off + sizeof(float2) * L.partial_rows);
   L.partial_o = off;    off = align256(off + size_t(4) * kVDim * L.partial_rows);
   L.total = off;
@@ -600,6 +608,8 @@ int mla_prompt_attention(const mla_dims* d, const void* q_nope, const void* q_pe
   p.num_seqs = num_seqs;
   p.heads = d->num_heads;
   p.kv_heads = num_kv_heads;
+  p.pack = pack_of(d->num_heads / num_kv_heads);
+  p.heads_v = d->num_heads >> p.pack;
   p.sm_count = sm_count();
   p.scale = softmax_scale;
   p.scale_log2 = softmax_scale * kLog2e;

@@ -103,9 +103,9 @@ struct ExpandParams {
 // rows of a sequence, or several over parts of its keys where there are few
 // blocks; the attention kernel runs every item for every head.
 struct alignas(16) PromptItem {
-  int q_row0, rows;      // first packed query row and number of rows (1..256)
+  int q_row0, rows;      // first packed token and number of rows (1..256): row i is token i >> pack, head i mod 2^pack
   int k_row0;            // first packed key row of the sequence
-  int vis0;              // keys that row 0 sees (row i sees vis0 + i; none if that is <= 0)
+  int vis0;              // keys that row 0 sees (row i sees vis0 + (i >> pack); none if that is <= 0)
   int kv_begin, kv_end;  // key range of this item, relative to k_row0
   int pieces, piece;     // items that share the block's keys, and which one this is
   int split;             // pieces > 1: number of the block among the split ones
@@ -115,7 +115,7 @@ struct alignas(16) PromptItem {
 };
 constexpr int kPromptRows = 256;         // query rows of a block
 constexpr int kPromptMaxPieces = 32;     // pieces of one block
-constexpr int kPromptMaxSplit = 64;      // split blocks of one call
+constexpr int kPromptMaxSplit = 1024;    // split units (block, head) of one call
 constexpr int kPromptExtraItems = 512;   // items beyond one per block
 // partial rows of one call: two rounds of blocks on 152 SMs
 constexpr int kPromptPartialRows = 2 * 152 * kPromptRows;
@@ -128,11 +128,12 @@ struct PromptParams {
   int* status;               // workspace: status word, number of items, units taken
   int* seq_first;            // workspace: [num_seqs] first item of each sequence
   int* block_start;          // workspace: [num_seqs + 1] first block of each sequence
-  PromptItem* items;         // workspace: [n_q / 256 + num_seqs + kPromptExtraItems]
-  int* arrived;              // workspace: [kPromptMaxSplit][heads][8] pieces done, per 32 rows
+  PromptItem* items;         // workspace: [(n_q << pack) / 256 + num_seqs + kPromptExtraItems]
+  int* arrived;              // workspace: [kPromptMaxSplit][8] pieces done, per 32 rows
   float* partial_o;          // workspace: [partial_rows][128] unnormalised outputs
   float2* partial_ml;        // workspace: [partial_rows] reference maximum (unscaled) and sum
   int n_q, n_k, num_seqs, heads, kv_heads, sm_count, partial_rows;
+  int pack, heads_v;         // log2 of the heads packed into rows, and heads >> pack
   float scale_log2;          // softmax_scale * log2(e)
   float scale;
   int inject_wait_timeout;   // test hook: 16 bytes of the first key tile never delivered

@@ -15,7 +15,10 @@
 //
 // One CTA per SM takes units of work from the plan's list: a block of up to 256
 // query rows of one sequence and one head, as two tiles of 128 rows (the MMA's
-// M).  Keys come in tiles of 128.  Per key tile and query tile,
+// M).  Heads that share a key/value head are packed into the rows, row = token *
+// F + head, F the largest power of two that divides the group (at most 128): a
+// block then spans 256 / F tokens, so less of its diagonal tiles is masked and
+// few tokens fill it, and the copy of a query tile is one box of F heads.  Keys come in tiles of 128.  Per key tile and query tile,
 //     S [128 x 128] = Q [128 x 192] K^T   12 MMAs, both operands in shared memory
 //     O [128 x 128] += P [128 x 128] V     8 MMAs, P (bf16) in tensor memory over S
 // of 65 cycles each, so a key tile takes the pipe 2,600 cycles; one query tile's
@@ -140,7 +143,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
   if (tid == 0 && good < p.num_seqs) set_status(p.status, MLA_ERR_DEVICE_BOUNDS);
   for (int base = 0; base < good; base += kPlanThreads) {
     const int b = base + tid;
-    const int blocks = b < good ? (cu_q[b + 1] - cu_q[b] + kPromptRows - 1) / kPromptRows : 0;
+    const int blocks = b < good ? (((cu_q[b + 1] - cu_q[b]) << p.pack) + kPromptRows - 1) / kPromptRows : 0;
     int total;
     const int ex = block_exclusive_scan(blocks, scan_tmp, &total);
     if (b < good) block_start[b] = carry + ex;
@@ -149,7 +152,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
     __syncthreads();
   }
   const int n = carry;  // block_start is read below by other threads: the barriers above order it
-  auto blocks_of = [&](int b) { return (cu_q[b + 1] - cu_q[b] + kPromptRows - 1) / kPromptRows; };
+  auto blocks_of = [&](int b) { return (((cu_q[b + 1] - cu_q[b]) << p.pack) + kPromptRows - 1) / kPromptRows; };
   auto sequence_of = [&](int i) {
     int lo = 0, hi = good - 1;  // last sequence whose first block is <= i
     while (lo < hi) {
@@ -160,14 +163,14 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
   };
   auto block_item = [&](int i, int b) {
     const int q0 = cu_q[b], lq = cu_q[b + 1] - q0, k0 = cu_k[b], lk = cu_k[b + 1] - k0;
-    const int r0 = (i - block_start[b]) * kPromptRows;
+    const int r0 = (i - block_start[b]) * kPromptRows, t0 = r0 >> p.pack;
     PromptItem it;
-    it.q_row0 = q0 + r0;
-    it.rows = min(kPromptRows, lq - r0);
+    it.q_row0 = q0 + t0;
+    it.rows = min(kPromptRows, (lq << p.pack) - r0);
     it.k_row0 = k0;
-    it.vis0 = lk - lq + r0 + 1;
+    it.vis0 = lk - lq + t0 + 1;
     it.kv_begin = 0;
-    it.kv_end = max(0, it.vis0 + it.rows - 1);
+    it.kv_end = max(0, it.vis0 + ((it.rows - 1) >> p.pack));
     it.pieces = 1;
     it.piece = 0;
     it.split = -1;
@@ -178,7 +181,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
   // more units than two rounds are never split (below): their blocks need no estimate
   const int G = p.sm_count;
   // (nor are short ones: a piece would be little more than its start and merge)
-  bool few = (long long)n * p.heads <= 2 * G && p.n_k > kMinSplit * kKeys;
+  bool few = (long long)n * p.heads_v <= 2 * G && p.n_k > kMinSplit * kKeys;
   if (few) {
     for (int i = tid; i < n; i += kPlanThreads) atomicMax(&longest, key_tiles(block_item(i, sequence_of(i)).kv_end));
     __syncthreads();
@@ -207,11 +210,11 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
       rows += __shfl_xor_sync(0xffffffffu, rows, o);
       splits += __shfl_xor_sync(0xffffffffu, splits, o);
     }
-    const float units = float(pieces) * p.heads, load = float(tiles) * p.heads + 3.f * units;
+    const float units = float(pieces) * p.heads_v, load = float(tiles) * p.heads_v + 3.f * units;
     float e = fmaxf(top + 3.f, load / G + (units > G ? 0.35f * top : 0.f));
     if (warp > 0) e = 1.1f * (e + 2.f);  // only where it clearly pays
-    if (T == 0 || units > 2 * G || splits > kPromptMaxSplit || pieces > n + kPromptExtraItems ||
-        (long long)rows * p.heads > p.partial_rows)
+    if (T == 0 || units > 2 * G || splits * p.heads_v > kPromptMaxSplit || pieces > n + kPromptExtraItems ||
+        (long long)rows * p.heads_v > p.partial_rows)
       e = warp > 0 ? 1e30f : 1e29f;
     if (lane == 0) estimate[warp] = e;
     __syncthreads();
@@ -266,7 +269,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
     it.pieces = c;
     if (c > 1) {
       it.split = atomicAdd(&split_count, 1);
-      it.partial = atomicAdd(&partial_count, c * it.rows * p.heads);
+      it.partial = atomicAdd(&partial_count, c * it.rows * p.heads_v);
     }
     const int at = seq_first[b] + items_of(b, local + 1, blocks);
     for (int q = 0; q < c; ++q) {
@@ -278,7 +281,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
     }
   }
   __syncthreads();
-  for (int e = tid; e < split_count * p.heads * 8; e += kPlanThreads) p.arrived[e] = 0;
+  for (int e = tid; e < split_count * p.heads_v * 8; e += kPlanThreads) p.arrived[e] = 0;
 }
 
 // ----- attention -------------------------------------------------------------------
@@ -418,9 +421,9 @@ __device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int x, i
 }
 
 // Key tiles of query tile t (0, 1) of an item.
-__device__ __forceinline__ int tiles_of(const PromptItem& it, int t) {
+__device__ __forceinline__ int tiles_of(const PromptItem& it, int t, int pack) {
   if (it.rows <= 128 * t) return 0;
-  const int last = min(it.rows, 128 * (t + 1)) - 1;
+  const int last = (min(it.rows, 128 * (t + 1)) - 1) >> pack;
   return key_tiles(min(it.kv_end, it.vis0 + last) - it.kv_begin);
 }
 
@@ -468,7 +471,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   griddep_wait();  // the plan's list
   griddep_launch_dependents();
   const volatile int* abort_flag = &B->abort;
-  const int H = p.heads, group = H / p.kv_heads;
+  const int H = p.heads_v, group = (p.heads / p.kv_heads) >> p.pack;  // (packed) heads, and those of a kv head
   // waits for the CTA's n-th unit; false: a wait failed
   auto item_ready = [&](int n) {
     return mbar_wait(&B->item_full[n % kItemRing], (n / kItemRing) & 1, abort_flag, kWaitNs);
@@ -521,13 +524,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       bool fetched = false;
       if (next.rows > 0) {  // the next unit's queries on their way to L2
         for (int t = 0; 128 * t < next.rows; ++t) {
-          tma_prefetch_3d(&map_qn, 0, next.head, next.q_row0 + 128 * t);
-          tma_prefetch_3d(&map_qn, 64, next.head, next.q_row0 + 128 * t);
-          tma_prefetch_3d(&map_qp, 0, next.head, next.q_row0 + 128 * t);
+          tma_prefetch_3d(&map_qn, 0, next.head << p.pack, next.q_row0 + (128 * t >> p.pack));
+          tma_prefetch_3d(&map_qn, 64, next.head << p.pack, next.q_row0 + (128 * t >> p.pack));
+          tma_prefetch_3d(&map_qp, 0, next.head << p.pack, next.q_row0 + (128 * t >> p.pack));
         }
       }
       const int g = it.head / group;
-      const int nt = max(tiles_of(it, 0), tiles_of(it, 1));
+      const int nt = max(tiles_of(it, 0, p.pack), tiles_of(it, 1, p.pack));
       for (int kt = 0; kt < nt && ok; ++kt, ++j) {
         const int key = it.k_row0 + it.kv_begin + kt * kKeys;
         uint64_t* bar = &B->k_full[j & 1];
@@ -610,16 +613,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     auto load_q = [&](int n) -> bool {
       if (!item_ready(n)) return false;
       const PromptItem it = load_item(&B->items[n % kItemRing]);
-      if (tiles_of(it, t) == 0) return true;
+      if (tiles_of(it, t, p.pack) == 0) return true;
       if (nload > 0 && !mbar_wait(&B->q_empty[t], (nload - 1) & 1, abort_flag, kWaitNs)) return false;
       ++nload;
       if (leader) {
         uint8_t* q = smem + t * kQTile;
-        const int row = it.q_row0 + 128 * t;
+        const int row = it.q_row0 + (128 * t >> p.pack), head = it.head << p.pack;
         mbar_arrive_expect_tx(&B->q_full[t], kQTile);
-        tma_load_3d(q, &map_qn, 0, it.head, row, &B->q_full[t]);
-        tma_load_3d(q + kBox, &map_qn, 64, it.head, row, &B->q_full[t]);
-        tma_load_3d(q + 2 * kBox, &map_qp, 0, it.head, row, &B->q_full[t]);
+        tma_load_3d(q, &map_qn, 0, head, row, &B->q_full[t]);
+        tma_load_3d(q + kBox, &map_qn, 64, head, row, &B->q_full[t]);
+        tma_load_3d(q + 2 * kBox, &map_qp, 0, head, row, &B->q_full[t]);
       }
       return true;
     };
@@ -638,8 +641,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       __syncwarp();
       if (leader) mbar_arrive(&B->item_empty[n % kItemRing]);
       if (it.rows == 0) break;
-      const int mine = __shfl_sync(0xffffffffu, tiles_of(it, t), 0);
-      const int nt = __shfl_sync(0xffffffffu, max(mine, tiles_of(it, t ^ 1)), 0);
+      const int mine = __shfl_sync(0xffffffffu, tiles_of(it, t, p.pack), 0);
+      const int nt = __shfl_sync(0xffffffffu, max(mine, tiles_of(it, t ^ 1, p.pack)), 0);
       const int keys = __shfl_sync(0xffffffffu, it.kv_end - it.kv_begin, 0);
       if (mine == 0) ok = load_q(n + 1);
       if (nt == 0 || !ok) continue;
@@ -725,7 +728,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       mbar_arrive(&B->item_empty[n % kItemRing]);
       if (it.rows == 0) break;
       const int g = it.head / group;
-      const int nt = max(tiles_of(it, 0), tiles_of(it, 1));
+      const int nt = max(tiles_of(it, 0, p.pack), tiles_of(it, 1, p.pack));
       for (int kt = 0; kt < nt && ok; ++kt, ++j) {
         const int key = it.k_row0 + it.kv_begin + kt * kKeys;
         uint64_t* bar = &B->v_full[j & 1];
@@ -753,9 +756,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       {
         const PromptItem it = load_item(&B->items[n % kItemRing]);
         if (it.rows == 0) break;
-        nt = tiles_of(it, t);
-        vis = it.vis0 + 128 * t + r - it.kv_begin;  // keys of this item's range that the row sees
-        vis_first = it.vis0 + 128 * t - it.kv_begin;
+        nt = tiles_of(it, t, p.pack);
+        vis = it.vis0 + ((128 * t + r) >> p.pack) - it.kv_begin;  // keys of this item's range that the row sees
+        vis_first = it.vis0 + (128 * t >> p.pack) - it.kv_begin;
         keys = it.kv_end - it.kv_begin;
       }
       float m = -INFINITY, l = 0.f;
@@ -840,7 +843,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       if (lane == 0) mbar_arrive(&B->item_empty[n % kItemRing]);
       const int h = it.head, row = 128 * t + r;  // row of the item
       const bool live = row < it.rows;
-      const size_t orow = size_t(it.q_row0 + row) * H + h;
+      const size_t orow = size_t(it.q_row0 + (row >> p.pack)) * p.heads + (h << p.pack) + (row & ((1 << p.pack) - 1));
       if (nt > 0) {
         ok = mbar_wait(&B->o_full[t], no & 1, abort_flag, kWaitNs);
         if (!__all_sync(0xffffffffu, ok)) {
@@ -928,13 +931,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   if (warp == 9) tmem_dealloc(tmem, 512);
 }
 
-// 3-D map over a [rows, heads, width] bf16 tensor: boxes of 64 columns x 1 head x 128 rows.
-bool make_map_heads(CUtensorMap* m, const void* base, uint64_t width, uint64_t heads, uint64_t rows) {
+// 3-D map over a [rows, heads, width] bf16 tensor: boxes of 64 columns x `box_heads` heads x as many rows as make 128.
+bool make_map_heads(CUtensorMap* m, const void* base, uint64_t width, uint64_t heads, uint64_t rows, uint32_t box_heads) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[3] = {width, heads, rows};
   cuuint64_t strides[2] = {width * 2, width * heads * 2};
-  cuuint32_t box[3] = {64, 1, 128};
+  cuuint32_t box[3] = {64, box_heads, 128 / box_heads};
   cuuint32_t estr[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -949,10 +952,12 @@ cudaError_t launch_prompt_plan(const PromptParams& p, cudaStream_t stream) {
 
 cudaError_t launch_prompt_attention(const PromptParams& p, cudaStream_t stream) {
   CUtensorMap qn, qp, kn, kp, v;
-  if (!make_map_heads(&qn, p.q_nope, kNope, p.heads, p.n_q) || !make_map_heads(&qp, p.q_pe, kRope, p.heads, p.n_q))
+  if (!make_map_heads(&qn, p.q_nope, kNope, p.heads, p.n_q, 1u << p.pack) ||
+      !make_map_heads(&qp, p.q_pe, kRope, p.heads, p.n_q, 1u << p.pack))
     return cudaErrorInvalidValue;
   if (p.n_k > 0) {
-    if (!make_map_heads(&kn, p.k_nope, kNope, p.kv_heads, p.n_k) || !make_map_heads(&v, p.v, kVDim, p.kv_heads, p.n_k) ||
+    if (!make_map_heads(&kn, p.k_nope, kNope, p.kv_heads, p.n_k, 1) ||
+        !make_map_heads(&v, p.v, kVDim, p.kv_heads, p.n_k, 1) ||
         !make_map_2d(&kp, p.k_pe, 2, kRope, p.n_k, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;
   } else {
@@ -967,8 +972,7 @@ cudaError_t launch_prompt_attention(const PromptParams& p, cudaStream_t stream) 
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 128) attr[dev] = true;
   }
-  // units at most: every block, split or not
-  const long long most = ((long long)p.n_q / kPromptRows + p.num_seqs) * kPromptMaxPieces * p.heads;
+  const long long most = (((long long)p.n_q << p.pack) / kPromptRows + p.num_seqs) * kPromptMaxPieces * p.heads_v;  // units
   const unsigned grid = unsigned(most < p.sm_count ? most : p.sm_count);
   return launch_pdl(prompt_attention_kernel, dim3(grid), dim3(kPromptThreads), kSmem, stream, 1, qn, qp, kn, kp, v, p);
 }

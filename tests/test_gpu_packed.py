@@ -208,6 +208,19 @@ def test_prompt_grouped_heads(cuda_lib, H, kv):
     _check(_prompt((150, 33, 270), (150, 200, 270), H=H, kv=kv, seed=3))
 
 
+@pytest.mark.parametrize("H,kv,q_lens,k_lens", [
+    (96, 3, (5, 130), (77, 130)),                 # 32 heads of a group in the rows
+    (96, 32, (100, 9), (100, 300)),               # groups of 3: none
+    (96, 16, (100, 9), (100, 300)),               # groups of 6: two at a time
+    (128, 1, (1, 2, 3, 17), (1, 500, 3, 40)),     # 128: a block of two tokens
+    (128, 1, (9,), (2100,)),                      # packed and split
+    (16, 2, (1, 1, 0, 1, 33), (3000, 1, 5, 129, 33)),
+    (32, 4, (300, 5, 200), (100, 0, 199)),        # rows that see no key
+])
+def test_prompt_packed_heads(cuda_lib, H, kv, q_lens, k_lens):
+    _check(_prompt(q_lens, k_lens, H=H, kv=kv, seed=13))
+
+
 @pytest.mark.parametrize("q_std,scale", [(0.01, SCALE), (20.0, SCALE), (1.0, 1.0), (1.0, 1e-3)])
 def test_prompt_flat_and_peaked_scores(cuda_lib, q_std, scale):
     _check(_prompt((520,), (520,), q_std=q_std, seed=4), scale=scale)
