@@ -65,9 +65,10 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(CacheReadParam
   __shared__ long long src_row[kRows];                 // cache row, or -1: not written
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
-  const int tid = threadIdx.x, r0 = blockIdx.x * kRows;
+  const int tid = threadIdx.x;
+  const long long r0 = (long long)blockIdx.x * kRows;
   if (tid < kRows) {
-    const int r = r0 + tid;
+    const long long r = r0 + tid;
     long long row = -1;
     if (r < p.n_rows) {
       // b = (number of entries <= r) - 1
@@ -141,8 +142,8 @@ template <int kCode>
 cudaError_t launch_read(const CacheReadParams& p, cudaStream_t stream) {
   // few rows: eight to a CTA, so that they spread over the SMs
   if (p.n_rows <= 8 * 512)
-    return launch_pdl(cache_read_kernel<kCode, 8>, dim3((p.n_rows + 7) / 8), dim3(kReadThreads), 0, stream, 1, p);
-  return launch_pdl(cache_read_kernel<kCode, 32>, dim3((p.n_rows + 31) / 32), dim3(kReadThreads), 0, stream, 1, p);
+    return launch_pdl(cache_read_kernel<kCode, 8>, dim3((unsigned(p.n_rows) + 7) / 8), dim3(kReadThreads), 0, stream, 1, p);
+  return launch_pdl(cache_read_kernel<kCode, 32>, dim3((unsigned(p.n_rows) + 31) / 32), dim3(kReadThreads), 0, stream, 1, p);
 }
 
 }  // namespace

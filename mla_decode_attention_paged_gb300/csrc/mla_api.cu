@@ -615,7 +615,6 @@ int mla_prompt_attention(const mla_dims* d, const void* q_nope, const void* q_pe
   p.scale_log2 = softmax_scale * kLog2e;
   p.inject_wait_timeout = g_inject_wait_timeout.load();
   if (p.sm_count <= 0) return MLA_ERR_CUDA;
-  if (launch_prompt_plan(p, s) != cudaSuccess) return MLA_ERR_CUDA;
   return launch_prompt_attention(p, s) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 

@@ -166,7 +166,6 @@ cudaError_t launch_combine_uv(const CombineUVParams& p, cudaStream_t stream);
 cudaError_t launch_combine(const CombineParams& p, cudaStream_t stream);
 cudaError_t launch_cache_read(const CacheReadParams& p, int code, cudaStream_t stream);
 cudaError_t launch_expand(const ExpandParams& p, cudaStream_t stream);
-cudaError_t launch_prompt_plan(const PromptParams& p, cudaStream_t stream);
 cudaError_t launch_prompt_attention(const PromptParams& p, cudaStream_t stream);
 cudaError_t launch_gather(const GatherParams& p, int code, cudaStream_t stream);
 cudaError_t launch_decode_tc(const DecodeParams& p, int hc, int code, int grid, cudaStream_t stream);

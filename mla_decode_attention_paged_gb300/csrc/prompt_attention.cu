@@ -100,6 +100,30 @@ static_assert(kSmem <= 232448, "dynamic shared memory of one CTA");
 __device__ __forceinline__ int key_tiles(int vis_last) { return vis_last > 0 ? (vis_last + kKeys - 1) / kKeys : 0; }
 __device__ __forceinline__ int pieces_of(int tiles, int longest) { return tiles > longest ? (tiles + longest - 1) / longest : 1; }
 
+__device__ __forceinline__ bool bad_offsets(const PromptParams& p, int q0, int q1, int k0, int k1) {
+  return q0 < 0 || q1 < q0 || q1 > p.n_q || k0 < 0 || k1 < k0 || k1 > p.n_k;
+}
+__device__ __forceinline__ int blocks_of(const PromptParams& p, int tokens) {
+  return ((tokens << p.pack) + kPromptRows - 1) / kPromptRows;
+}
+// The whole item of block i of the sequence with query rows [q0, q1) and key rows [k0, k1).
+__device__ __forceinline__ PromptItem make_item(const PromptParams& p, int q0, int q1, int k0, int k1, int i) {
+  const int r0 = i * kPromptRows, t0 = r0 >> p.pack;
+  PromptItem it;
+  it.q_row0 = q0 + t0;
+  it.rows = min(kPromptRows, ((q1 - q0) << p.pack) - r0);
+  it.k_row0 = k0;
+  it.vis0 = (k1 - k0) - (q1 - q0) + t0 + 1;
+  it.kv_begin = 0;
+  it.kv_end = max(0, it.vis0 + ((it.rows - 1) >> p.pack));
+  it.pieces = 1;
+  it.piece = 0;
+  it.split = -1;
+  it.partial = 0;
+  it.head = it.pad = 0;
+  return it;
+}
+
 __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams p) {
   __shared__ int scan_tmp[32];
   __shared__ int hist[kBuckets];
@@ -136,14 +160,14 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
   __syncthreads();
   for (int b = tid; b < p.num_seqs; b += kPlanThreads) {
     const int q0 = cu_q[b], q1 = cu_q[b + 1], k0 = cu_k[b], k1 = cu_k[b + 1];
-    if (q0 < 0 || q1 < q0 || q1 > p.n_q || k0 < 0 || k1 < k0 || k1 > p.n_k) atomicMin(&first_bad, b);
+    if (bad_offsets(p, q0, q1, k0, k1)) atomicMin(&first_bad, b);
   }
   __syncthreads();
   const int good = first_bad;
   if (tid == 0 && good < p.num_seqs) set_status(p.status, MLA_ERR_DEVICE_BOUNDS);
   for (int base = 0; base < good; base += kPlanThreads) {
     const int b = base + tid;
-    const int blocks = b < good ? (((cu_q[b + 1] - cu_q[b]) << p.pack) + kPromptRows - 1) / kPromptRows : 0;
+    const int blocks = b < good ? blocks_of(p, cu_q[b + 1] - cu_q[b]) : 0;
     int total;
     const int ex = block_exclusive_scan(blocks, scan_tmp, &total);
     if (b < good) block_start[b] = carry + ex;
@@ -152,7 +176,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
     __syncthreads();
   }
   const int n = carry;  // block_start is read below by other threads: the barriers above order it
-  auto blocks_of = [&](int b) { return (((cu_q[b + 1] - cu_q[b]) << p.pack) + kPromptRows - 1) / kPromptRows; };
+  auto blocks_in = [&](int b) { return blocks_of(p, cu_q[b + 1] - cu_q[b]); };
   auto sequence_of = [&](int i) {
     int lo = 0, hi = good - 1;  // last sequence whose first block is <= i
     while (lo < hi) {
@@ -162,21 +186,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
     return lo;
   };
   auto block_item = [&](int i, int b) {
-    const int q0 = cu_q[b], lq = cu_q[b + 1] - q0, k0 = cu_k[b], lk = cu_k[b + 1] - k0;
-    const int r0 = (i - block_start[b]) * kPromptRows, t0 = r0 >> p.pack;
-    PromptItem it;
-    it.q_row0 = q0 + t0;
-    it.rows = min(kPromptRows, (lq << p.pack) - r0);
-    it.k_row0 = k0;
-    it.vis0 = lk - lq + t0 + 1;
-    it.kv_begin = 0;
-    it.kv_end = max(0, it.vis0 + ((it.rows - 1) >> p.pack));
-    it.pieces = 1;
-    it.piece = 0;
-    it.split = -1;
-    it.partial = 0;
-    it.head = it.pad = 0;
-    return it;
+    return make_item(p, cu_q[b], cu_q[b + 1], cu_k[b], cu_k[b + 1], i - block_start[b]);
   };
   // more units than two rounds are never split (below): their blocks need no estimate
   const int G = p.sm_count;
@@ -247,7 +257,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
   };
   auto bucket_of = [&](int b) { return kBuckets - 1 - min(kBuckets - 1, key_tiles(cu_k[b + 1] - cu_k[b])); };
   for (int b = tid; b < good; b += kPlanThreads) {
-    const int c = items_of(b, 0, blocks_of(b));
+    const int c = items_of(b, 0, blocks_in(b));
     if (c > 0) atomicAdd(&hist[bucket_of(b)], c);
   }
   __syncthreads();
@@ -258,12 +268,12 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
   __syncthreads();
   // the order of equally long sequences is arbitrary: it decides which CTA runs an item, not its result
   for (int b = tid; b < good; b += kPlanThreads) {
-    const int c = items_of(b, 0, blocks_of(b));
+    const int c = items_of(b, 0, blocks_in(b));
     if (c > 0) seq_first[b] = atomicAdd(&hist[bucket_of(b)], c);
   }
   __syncthreads();
   for (int i = tid; i < n; i += kPlanThreads) {
-    const int b = sequence_of(i), local = i - block_start[b], blocks = blocks_of(b);
+    const int b = sequence_of(i), local = i - block_start[b], blocks = blocks_in(b);
     PromptItem it = block_item(i, b);
     const int keys = it.kv_end, t = key_tiles(keys), c = pieces_of(t, T);
     it.pieces = c;
@@ -427,6 +437,8 @@ __device__ __forceinline__ int tiles_of(const PromptItem& it, int t, int pack) {
   return key_tiles(min(it.kv_end, it.vis0 + last) - it.kv_begin);
 }
 
+// kDirect: few sequences, blocks and keys; the CTAs list the work themselves.
+template <bool kDirect>
 __global__ void __launch_bounds__(kPromptThreads, 1)
     prompt_attention_kernel(const __grid_constant__ CUtensorMap map_qn, const __grid_constant__ CUtensorMap map_qp,
                             const __grid_constant__ CUtensorMap map_kn, const __grid_constant__ CUtensorMap map_kp,
@@ -477,6 +489,27 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     return mbar_wait(&B->item_full[n % kItemRing], (n / kItemRing) & 1, abort_flag, kWaitNs);
   };
 
+  int direct_items = 0;
+  if (kDirect && warp == 8) {
+    // No plan: this warp lists the blocks of the at most 32 sequences, in
+    // order.  Every CTA writes the same list and reads what it wrote.
+    const bool in = lane < p.num_seqs;
+    const int q0 = in ? p.cu_q[lane] : 0, q1 = in ? p.cu_q[lane + 1] : 0;
+    const int k0 = in ? p.cu_k[lane] : 0, k1 = in ? p.cu_k[lane + 1] : 0;
+    const unsigned bad = __ballot_sync(0xffffffffu, in && bad_offsets(p, q0, q1, k0, k1));
+    const int good = bad ? __ffs(bad) - 1 : p.num_seqs;  // sequences from the first bad one on are skipped
+    if (blockIdx.x == 0 && lane == 0) *p.status = bad ? MLA_ERR_DEVICE_BOUNDS : MLA_OK;
+    const int blocks = lane < good ? blocks_of(p, q1 - q0) : 0;
+    int end = blocks;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, end, o);
+      if (lane >= o) end += x;
+    }
+    for (int i = 0; i < blocks; ++i) p.items[end - blocks + i] = make_item(p, q0, q1, k0, k1, i);
+    direct_items = __shfl_sync(0xffffffffu, end, 31);
+    __syncwarp();
+  }
   if (warp == 8 && lane == 0) {
     // ------------------------------------------------------------ units, key copies
     // Box i (0-2: K, 3-4: V) of key tile j sits at ring position (5 j + i) % 8,
@@ -490,12 +523,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     uint32_t j = 0;
     // Unit u is item u / H for head u % H.  Each CTA's first is its own number,
     // the others come from a counter: which CTA runs a unit does not change it.
-    const int units = p.status[1] * H;
+    const int units = (kDirect ? direct_items : p.status[1]) * H;
     // The counter's answer and the item it leads to are each waited for a key
     // tile later: this thread issues in order, and a wait here holds back the
     // copies.
     PromptItem it, next, after;
-    auto take = [&]() { return int(gridDim.x) + atomicAdd(&p.status[2], 1); };
+    int dealt = blockIdx.x;
+    auto take = [&]() { return kDirect ? dealt += gridDim.x : int(gridDim.x) + atomicAdd(&p.status[2], 1); };
     auto fetch = [&](int u) {
       PromptItem x;
       x.rows = 0;
@@ -946,10 +980,6 @@ bool make_map_heads(CUtensorMap* m, const void* base, uint64_t width, uint64_t h
 
 }  // namespace
 
-cudaError_t launch_prompt_plan(const PromptParams& p, cudaStream_t stream) {
-  return launch_pdl(prompt_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, 1, p);
-}
-
 cudaError_t launch_prompt_attention(const PromptParams& p, cudaStream_t stream) {
   CUtensorMap qn, qp, kn, kp, v;
   if (!make_map_heads(&qn, p.q_nope, kNope, p.heads, p.n_q, 1u << p.pack) ||
@@ -967,14 +997,25 @@ cudaError_t launch_prompt_attention(const PromptParams& p, cudaStream_t stream) 
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 128 || !attr[dev]) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(prompt_attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
-    if (e != cudaSuccess) return e;
+    for (auto* k : {prompt_attention_kernel<false>, prompt_attention_kernel<true>}) {
+      const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
+      if (e != cudaSuccess) return e;
+    }
     if (dev >= 0 && dev < 128) attr[dev] = true;
   }
-  const long long most = (((long long)p.n_q << p.pack) / kPromptRows + p.num_seqs) * kPromptMaxPieces * p.heads_v;  // units
+  const long long blocks = ((long long)p.n_q << p.pack) / kPromptRows + p.num_seqs;  // at most
+  const long long most = blocks * kPromptMaxPieces * p.heads_v;                      // units
   const unsigned grid = unsigned(most < p.sm_count ? most : p.sm_count);
-  return launch_pdl(prompt_attention_kernel, dim3(grid), dim3(kPromptThreads), kSmem, stream, 1, qn, qp, kn, kp, v, p);
+  // Two rounds of whole units at most, none with keys to split: a plan would
+  // cost more than it can save (93 tokens at 16 heads: 9.5 us with one on the
+  // device, 2.6 us of a second launch on the host).
+  if (p.num_seqs <= 32 && blocks * p.heads_v <= 2 * p.sm_count && p.n_k <= kMinSplit * kKeys)
+    return launch_pdl(prompt_attention_kernel<true>, dim3(grid), dim3(kPromptThreads), kSmem, stream, 1, qn, qp, kn, kp,
+                      v, p);
+  const cudaError_t e = launch_pdl(prompt_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, 1, p);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(prompt_attention_kernel<false>, dim3(grid), dim3(kPromptThreads), kSmem, stream, 1, qn, qp, kn, kp, v,
+                    p);
 }
 
 }  // namespace mla
