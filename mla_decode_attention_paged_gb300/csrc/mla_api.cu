@@ -409,7 +409,7 @@ SparseLayout sparse_layout(const mla_dims* d, int batch, int top_k, size_t decod
 // items (a sequence of n rows, heads packed into them, has at most n / 256 + 1
 // blocks), and the partial results of split blocks.
 struct PromptLayout {
-  size_t status, block_start, seq_first, items, arrived, partial_ml, partial_o, total;
+  size_t status, block_start, seq_first, items, splits, partial_ml, partial_o, total;
   int partial_rows;
 };
 
@@ -425,11 +425,11 @@ PromptLayout prompt_layout(int num_seqs, int n_q, int heads) {
   size_t off = 0;
   const long long most = (long long)n_q * heads * kPromptMaxPieces;
   L.partial_rows = most < kPromptPartialRows ? int(most) : kPromptPartialRows;
-  L.status = off;       off = align256(off + 12);
+  L.status = off;       off = align256(off + 20);
   L.block_start = off;  off = align256(off + 4 * (size_t(num_seqs) + 1));
   L.seq_first = off;    off = align256(off + 4 * size_t(num_seqs));
   L.items = off;        off = align256(off + sizeof(PromptItem) * ((size_t(n_q) << pack_of(heads)) / kPromptRows + num_seqs + kPromptExtraItems));
-  L.arrived = off;      off = align256(off + size_t(4) * kPromptMaxSplit * 8);
+  L.splits = off;       off = align256(off + sizeof(PromptSplit) * kPromptMaxSplit);
   L.partial_ml = off;   off = align256(off + sizeof(float2) * L.partial_rows);
   L.partial_o = off;    off = align256(off + size_t(4) * kVDim * L.partial_rows);
   L.total = off;
@@ -599,7 +599,7 @@ int mla_prompt_attention(const mla_dims* d, const void* q_nope, const void* q_pe
   p.block_start = reinterpret_cast<int*>(ws + L.block_start);
   p.seq_first = reinterpret_cast<int*>(ws + L.seq_first);
   p.items = reinterpret_cast<PromptItem*>(ws + L.items);
-  p.arrived = reinterpret_cast<int*>(ws + L.arrived);
+  p.splits = reinterpret_cast<PromptSplit*>(ws + L.splits);
   p.partial_o = reinterpret_cast<float*>(ws + L.partial_o);
   p.partial_ml = reinterpret_cast<float2*>(ws + L.partial_ml);
   p.partial_rows = L.partial_rows;

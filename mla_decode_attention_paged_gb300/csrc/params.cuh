@@ -108,14 +108,17 @@ struct alignas(16) PromptItem {
   int vis0;              // keys that row 0 sees (row i sees vis0 + (i >> pack); none if that is <= 0)
   int kv_begin, kv_end;  // key range of this item, relative to k_row0
   int pieces, piece;     // items that share the block's keys, and which one this is
-  int split;             // pieces > 1: number of the block among the split ones
   int partial;           // pieces > 1: first partial row of the block
   int head;              // the unit's head (in the attention kernel's copy)
-  int pad;
+  int pad[2];
+};
+struct PromptSplit {     // a block whose keys are split, for the merge
+  int q_row0, rows, pieces, partial;
+  int row_start;         // rows of the split blocks before
 };
 constexpr int kPromptRows = 256;         // query rows of a block
 constexpr int kPromptMaxPieces = 32;     // pieces of one block
-constexpr int kPromptMaxSplit = 1024;    // split units (block, head) of one call
+constexpr int kPromptMaxSplit = 512;     // blocks of a call that may be split
 constexpr int kPromptExtraItems = 512;   // items beyond one per block
 // partial rows of one call: two rounds of blocks on 152 SMs
 constexpr int kPromptPartialRows = 2 * 152 * kPromptRows;
@@ -125,14 +128,15 @@ struct PromptParams {
   const __nv_bfloat16 *q_nope, *q_pe, *k_nope, *k_pe, *v;
   __nv_bfloat16* out;        // [n_q, heads, 128]
   float* lse_out;            // [n_q, heads] or null
-  int* status;               // workspace: status word, number of items, units taken
+  int* status;               // workspace: status word, items, units taken, split blocks and their rows
   int* seq_first;            // workspace: [num_seqs] first item of each sequence
   int* block_start;          // workspace: [num_seqs + 1] first block of each sequence
   PromptItem* items;         // workspace: [(n_q << pack) / 256 + num_seqs + kPromptExtraItems]
-  int* arrived;              // workspace: [kPromptMaxSplit][8] pieces done, per 32 rows
+  PromptSplit* splits;       // workspace: [kPromptMaxSplit]
   float* partial_o;          // workspace: [partial_rows][128] unnormalised outputs
   float2* partial_ml;        // workspace: [partial_rows] reference maximum (unscaled) and sum
   int n_q, n_k, num_seqs, heads, kv_heads, sm_count, partial_rows;
+  int may_split;             // keys may be split (set by the launch)
   int pack, heads_v;         // log2 of the heads packed into rows, and heads >> pack
   float scale_log2;          // softmax_scale * log2(e)
   float scale;
@@ -166,7 +170,7 @@ cudaError_t launch_combine_uv(const CombineUVParams& p, cudaStream_t stream);
 cudaError_t launch_combine(const CombineParams& p, cudaStream_t stream);
 cudaError_t launch_cache_read(const CacheReadParams& p, int code, cudaStream_t stream);
 cudaError_t launch_expand(const ExpandParams& p, cudaStream_t stream);
-cudaError_t launch_prompt_attention(const PromptParams& p, cudaStream_t stream);
+cudaError_t launch_prompt_attention(PromptParams p, cudaStream_t stream);
 cudaError_t launch_gather(const GatherParams& p, int code, cudaStream_t stream);
 cudaError_t launch_decode_tc(const DecodeParams& p, int hc, int code, int grid, cudaStream_t stream);
 int decode_head_group(int heads, bool byte_cache);

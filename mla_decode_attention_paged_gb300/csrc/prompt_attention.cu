@@ -94,9 +94,9 @@ static_assert(kSmem <= 232448, "dynamic shared memory of one CTA");
 // and every block into pieces of at most that length.  Its estimate, in key
 // tiles: the longest piece where every unit (item, head) has its own CTA, else
 // the mean load and a share of the longest piece for the uneven end, plus
-// three tiles for a unit's start and end and two for the merge.  The pieces of
-// a block depend on the lengths and the SM count alone, and are merged in
-// order, so results repeat bit for bit.
+// three tiles for a unit's start and end and two for the merge, a kernel of its
+// own.  The pieces of a block depend on the lengths and the SM count alone, and
+// are merged in order, so results repeat bit for bit.
 __device__ __forceinline__ int key_tiles(int vis_last) { return vis_last > 0 ? (vis_last + kKeys - 1) / kKeys : 0; }
 __device__ __forceinline__ int pieces_of(int tiles, int longest) { return tiles > longest ? (tiles + longest - 1) / longest : 1; }
 
@@ -118,16 +118,15 @@ __device__ __forceinline__ PromptItem make_item(const PromptParams& p, int q0, i
   it.kv_end = max(0, it.vis0 + ((it.rows - 1) >> p.pack));
   it.pieces = 1;
   it.piece = 0;
-  it.split = -1;
   it.partial = 0;
-  it.head = it.pad = 0;
+  it.head = it.pad[0] = it.pad[1] = 0;
   return it;
 }
 
 __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams p) {
   __shared__ int scan_tmp[32];
   __shared__ int hist[kBuckets];
-  __shared__ int carry, first_bad, longest, piece_tiles, split_count, partial_count;
+  __shared__ int carry, first_bad, longest, piece_tiles;
   __shared__ float estimate[kPlanThreads / 32];
   // offsets and block starts, here where they fit: the loops below read them over and over
   __shared__ int offsets[4][kPlanSeqs + 1];
@@ -150,11 +149,10 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
   if (tid == 0) {
     carry = 0;
     longest = 0;
-    split_count = 0;
-    partial_count = 0;
     first_bad = p.num_seqs;
     p.status[0] = MLA_OK;
     p.status[2] = 0;  // units taken
+    p.status[3] = 0;  // split blocks
   }
   for (int i = tid; i < kBuckets; i += kPlanThreads) hist[i] = 0;
   __syncthreads();
@@ -191,7 +189,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
   // more units than two rounds are never split (below): their blocks need no estimate
   const int G = p.sm_count;
   // (nor are short ones: a piece would be little more than its start and merge)
-  bool few = (long long)n * p.heads_v <= 2 * G && p.n_k > kMinSplit * kKeys;
+  bool few = p.may_split && (long long)n * p.heads_v <= 2 * G && n <= kPromptMaxSplit;
   if (few) {
     for (int i = tid; i < n; i += kPlanThreads) atomicMax(&longest, key_tiles(block_item(i, sequence_of(i)).kv_end));
     __syncthreads();
@@ -223,7 +221,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
     const float units = float(pieces) * p.heads_v, load = float(tiles) * p.heads_v + 3.f * units;
     float e = fmaxf(top + 3.f, load / G + (units > G ? 0.35f * top : 0.f));
     if (warp > 0) e = 1.1f * (e + 2.f);  // only where it clearly pays
-    if (T == 0 || units > 2 * G || splits * p.heads_v > kPromptMaxSplit || pieces > n + kPromptExtraItems ||
+    if (T == 0 || units > 2 * G ||  pieces > n + kPromptExtraItems ||
         (long long)rows * p.heads_v > p.partial_rows)
       e = warp > 0 ? 1e30f : 1e29f;
     if (lane == 0) estimate[warp] = e;
@@ -272,15 +270,31 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
     if (c > 0) seq_first[b] = atomicAdd(&hist[bucket_of(b)], c);
   }
   __syncthreads();
+  int partial0 = 0;
+  if (split) {  // n <= kPromptMaxSplit <= the threads: block `tid`'s place among the split ones, their partial and output rows
+    int pieces = 1, rows = 0;
+    PromptItem it;
+    if (tid < n) {
+      it = block_item(tid, sequence_of(tid));
+      pieces = pieces_of(key_tiles(it.kv_end), T);
+      rows = pieces > 1 ? it.rows : 0;
+    }
+    int splits, partials, out_rows;
+    const int number = block_exclusive_scan(rows > 0, scan_tmp, &splits);
+    partial0 = block_exclusive_scan(pieces * rows * p.heads_v, scan_tmp, &partials);
+    const int row_start = block_exclusive_scan(rows, scan_tmp, &out_rows);
+    if (rows > 0) p.splits[number] = {it.q_row0, rows, pieces, partial0, row_start};
+    if (tid == 0) {
+      p.status[3] = splits;
+      p.status[4] = out_rows;
+    }
+  }
   for (int i = tid; i < n; i += kPlanThreads) {
     const int b = sequence_of(i), local = i - block_start[b], blocks = blocks_in(b);
     PromptItem it = block_item(i, b);
     const int keys = it.kv_end, t = key_tiles(keys), c = pieces_of(t, T);
     it.pieces = c;
-    if (c > 1) {
-      it.split = atomicAdd(&split_count, 1);
-      it.partial = atomicAdd(&partial_count, c * it.rows * p.heads_v);
-    }
+    it.partial = partial0;
     const int at = seq_first[b] + items_of(b, local + 1, blocks);
     for (int q = 0; q < c; ++q) {
       const int t0 = q * t / c, t1 = (q + 1) * t / c;
@@ -290,8 +304,6 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
       p.items[at + q] = it;
     }
   }
-  __syncthreads();
-  for (int e = tid; e < split_count * p.heads_v * 8; e += kPlanThreads) p.arrived[e] = 0;
 }
 
 // ----- attention -------------------------------------------------------------------
@@ -357,7 +369,7 @@ __device__ __forceinline__ float row_max(const uint32_t (&s)[4][32]) {  // four 
 __device__ __forceinline__ PromptItem load_item(const PromptItem* src) {  // 16-byte loads, global or shared
   const int4* v = reinterpret_cast<const int4*>(src);
   const int4 a = v[0], b = v[1], c = v[2];
-  return {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
+  return {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, {c.z, c.w}};
 }
 
 // 1 / l; 0 for a row without keys (l = 0); NaN stays NaN.
@@ -372,55 +384,6 @@ __device__ __forceinline__ uint4 pack_out(const uint32_t* o, float inv) {
     w[e] = *reinterpret_cast<const uint32_t*>(&v);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// One row of a split block per lane: out = sum_i w_i O_i / sum_i w_i l_i with
-// w_i = 2^((m_i - max m) scale_log2) over its pieces; pieces without keys for
-// the row (l = 0) carry weight 0 and no output.  The partials are read past L1:
-// other SMs wrote them during this kernel.
-static __device__ __noinline__ void merge_rows(const PromptParams& p, const PromptItem& it, size_t prow0, size_t orow,
-                                               bool live) {
-  if (!live) return;
-  float top = -INFINITY;
-  for (int i = 0; i < it.pieces; ++i) {
-    const float2 ml = __ldcg(p.partial_ml + prow0 + size_t(i) * it.rows);
-    if (ml.y != 0.f) top = fmaxf(top, ml.x);
-  }
-  const float base = top == -INFINITY ? 0.f : top;
-  float l = 0.f;
-  for (int i = 0; i < it.pieces; ++i) {
-    const float2 ml = __ldcg(p.partial_ml + prow0 + size_t(i) * it.rows);
-    if (ml.y != 0.f) l = fmaf(ml.y, ex2_ftz((ml.x - base) * p.scale_log2), l);
-  }
-  const float inv = inverse_sum(l);
-  uint4* dst = reinterpret_cast<uint4*>(p.out + orow * kVDim);
-#pragma unroll 1
-  for (int c = 0; c < kVDim; c += 32) {
-    float acc[32];
-#pragma unroll
-    for (int e = 0; e < 32; ++e) acc[e] = 0.f;
-    for (int i = 0; i < it.pieces; ++i) {
-      const size_t prow = prow0 + size_t(i) * it.rows;
-      const float2 ml = __ldcg(p.partial_ml + prow);
-      if (ml.y == 0.f) continue;
-      const float w = ex2_ftz((ml.x - base) * p.scale_log2);
-      const float4* src = reinterpret_cast<const float4*>(p.partial_o + prow * kVDim + c);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float4 x = __ldcg(src + e);
-        acc[4 * e] = fmaf(x.x, w, acc[4 * e]);
-        acc[4 * e + 1] = fmaf(x.y, w, acc[4 * e + 1]);
-        acc[4 * e + 2] = fmaf(x.z, w, acc[4 * e + 2]);
-        acc[4 * e + 3] = fmaf(x.w, w, acc[4 * e + 3]);
-      }
-    }
-    uint32_t o[32];
-#pragma unroll
-    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(acc[e]);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) dst[c / 8 + e] = pack_out(&o[8 * e], inv);
-  }
-  if (p.lse_out) p.lse_out[orow] = l == 0.f ? -INFINITY : base * p.scale + logf(l);
 }
 
 __device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int x, int y, int z) {
@@ -916,12 +879,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           for (int i = 0; i < 16; ++i) dst[i] = make_uint4(0, 0, 0, 0);
         }
         if (live && p.lse_out) p.lse_out[orow] = l == 0.f ? -INFINITY : m * p.scale + logf(l);
-      } else if (__any_sync(0xffffffffu, live)) {
+      } else {
         // A piece of a split block: its unnormalised output, reference maximum
-        // and sum go to the workspace; the warp that brings the last piece of
-        // these 32 rows merges all of them, in order.
-        const size_t prow0 = size_t(it.partial) + size_t(h) * it.pieces * it.rows + row;  // piece 0 of this row
-        float4* dst = reinterpret_cast<float4*>(p.partial_o + (prow0 + size_t(it.piece) * it.rows) * kVDim);
+        // and sum go to the workspace, for the merge.
+        const size_t prow = size_t(it.partial) + (size_t(h) * it.pieces + it.piece) * it.rows + row;
+        float* dst = p.partial_o + prow * kVDim;
         if (nt > 0) {
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
@@ -929,22 +891,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             tmem_ld32(to + 32 * c, o);
             if (live) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                dst[8 * c + i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                             __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+              for (int i = 0; i < 4; ++i)
+                st_global_32(dst + 32 * c + 8 * i, make_uint4(o[8 * i], o[8 * i + 1], o[8 * i + 2], o[8 * i + 3]),
+                             make_uint4(o[8 * i + 4], o[8 * i + 5], o[8 * i + 6], o[8 * i + 7]));
             }
           }
         }
-        if (live) p.partial_ml[prow0 + size_t(it.piece) * it.rows] = make_float2(m, l);
-        __threadfence();
-        __syncwarp();
-        int before = 0;
-        if (lane == 0) before = atomicAdd(&p.arrived[(size_t(it.split) * H + h) * 8 + (row >> 5)], 1);
-        before = __shfl_sync(0xffffffffu, before, 0);
-        if (before == it.pieces - 1) {
-          __threadfence();
-          merge_rows(p, it, prow0, orow, live);
-        }
+        if (live) p.partial_ml[prow] = make_float2(m, l);
       }
       if (nt > 0 && it.pieces > 1) {
         tc_fence_before();
@@ -978,9 +931,64 @@ bool make_map_heads(CUtensorMap* m, const void* base, uint64_t width, uint64_t h
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// ----- merge -----------------------------------------------------------------------
+// One warp per (row of a split block, head): out = sum_i w_i O_i / sum_i w_i l_i
+// with w_i = 2^((m_i - max m) scale_log2) over the block's pieces, lane i holding
+// piece i's m and l, every lane four of the 128 columns.  Pieces without keys for
+// the row (l = 0) carry weight 0 and no output.  A merge by the CTA that brought
+// the last piece, a row to a thread, took 60 us and more of blocks of 256 rows
+// (256 rows behind 8,192 keys at 16 heads: 128 us in all).
+constexpr int kMergeThreads = 256;
+__global__ void __launch_bounds__(kMergeThreads) prompt_merge_kernel(PromptParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int splits = p.status[3];
+  if (splits == 0) return;
+  const int rows = p.status[4], lane = threadIdx.x & 31, warps = gridDim.x * (kMergeThreads / 32);
+  for (int task = blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5); task < rows * p.heads_v; task += warps) {
+    const int h = task / rows, r = task % rows;
+    int lo = 0, hi = splits - 1;  // last split block that starts at or before row r
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (p.splits[mid].row_start <= r) lo = mid; else hi = mid - 1;
+    }
+    const PromptSplit sp = p.splits[lo];
+    const int row = r - sp.row_start;
+    const size_t prow0 = size_t(sp.partial) + size_t(h) * sp.pieces * sp.rows + row;
+    const float2 ml = lane < sp.pieces ? p.partial_ml[prow0 + size_t(lane) * sp.rows] : make_float2(-INFINITY, 0.f);
+    float top = ml.y != 0.f ? ml.x : -INFINITY;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float base = top == -INFINITY ? 0.f : top;
+    const float w = ml.y != 0.f ? ex2_ftz((ml.x - base) * p.scale_log2) : 0.f;
+    float l = ml.y != 0.f ? w * ml.y : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    const unsigned has = __ballot_sync(0xffffffffu, ml.y != 0.f);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = 0; i < sp.pieces; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      if (!(has >> i & 1)) continue;
+      const float4 x = reinterpret_cast<const float4*>(p.partial_o + (prow0 + size_t(i) * sp.rows) * kVDim)[lane];
+      acc.x = fmaf(x.x, wi, acc.x);
+      acc.y = fmaf(x.y, wi, acc.y);
+      acc.z = fmaf(x.z, wi, acc.z);
+      acc.w = fmaf(x.w, wi, acc.w);
+    }
+    const float inv = inverse_sum(l);
+    const size_t orow =
+        size_t(sp.q_row0 + (row >> p.pack)) * p.heads + (h << p.pack) + (row & ((1 << p.pack) - 1));
+    const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), b = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+    reinterpret_cast<uint2*>(p.out + orow * kVDim)[lane] =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    if (lane == 0 && p.lse_out) p.lse_out[orow] = l == 0.f ? -INFINITY : base * p.scale + logf(l);
+  }
+}
+
 }  // namespace
 
-cudaError_t launch_prompt_attention(const PromptParams& p, cudaStream_t stream) {
+cudaError_t launch_prompt_attention(PromptParams p, cudaStream_t stream) {
   CUtensorMap qn, qp, kn, kp, v;
   if (!make_map_heads(&qn, p.q_nope, kNope, p.heads, p.n_q, 1u << p.pack) ||
       !make_map_heads(&qp, p.q_pe, kRope, p.heads, p.n_q, 1u << p.pack))
@@ -1012,10 +1020,15 @@ cudaError_t launch_prompt_attention(const PromptParams& p, cudaStream_t stream) 
   if (p.num_seqs <= 32 && blocks * p.heads_v <= 2 * p.sm_count && p.n_k <= kMinSplit * kKeys)
     return launch_pdl(prompt_attention_kernel<true>, dim3(grid), dim3(kPromptThreads), kSmem, stream, 1, qn, qp, kn, kp,
                       v, p);
-  const cudaError_t e = launch_pdl(prompt_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, 1, p);
+  // Splitting keys is for calls whose query rows make two rounds at most, and
+  // with keys to split (rows that cu_q leaves out count, too: the lengths are on
+  // the device); only they launch the merge.
+  p.may_split = (((long long)p.n_q << p.pack) / kPromptRows) * p.heads_v <= 2 * p.sm_count && p.n_k > kMinSplit * kKeys;
+  cudaError_t e = launch_pdl(prompt_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, 1, p);
   if (e != cudaSuccess) return e;
-  return launch_pdl(prompt_attention_kernel<false>, dim3(grid), dim3(kPromptThreads), kSmem, stream, 1, qn, qp, kn, kp, v,
-                    p);
+  e = launch_pdl(prompt_attention_kernel<false>, dim3(grid), dim3(kPromptThreads), kSmem, stream, 1, qn, qp, kn, kp, v, p);
+  if (e != cudaSuccess || !p.may_split) return e;
+  return launch_pdl(prompt_merge_kernel, dim3(4 * p.sm_count), dim3(kMergeThreads), 0, stream, 1, p);
 }
 
 }  // namespace mla
