@@ -72,7 +72,8 @@ constexpr uint64_t kWaitNs = 2000000000ull;        // 2 s
 constexpr float kRescale = 8.f;                    // log2 units
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanSeqs = 1024;                    // sequences whose offsets the plan holds in shared memory
-constexpr int kMinSplit = 6;                       // key tiles of a block that is never split
+constexpr float kMergeTiles = 5.f;                 // the merge, in key tiles' time
+constexpr int kMinSplit = 10;                      // key tiles of a block that is never split
 constexpr int kBuckets = 1024;                     // cost classes of the plan's counting sort
 static_assert(kSmem <= 232448, "dynamic shared memory of one CTA");
 
@@ -94,7 +95,7 @@ static_assert(kSmem <= 232448, "dynamic shared memory of one CTA");
 // and every block into pieces of at most that length.  Its estimate, in key
 // tiles: the longest piece where every unit (item, head) has its own CTA, else
 // the mean load and a share of the longest piece for the uneven end, plus
-// three tiles for a unit's start and end and two for the merge, a kernel of its
+// three tiles for a unit's start and end and five for the merge, a kernel of its
 // own.  The pieces of a block depend on the lengths and the SM count alone, and
 // are merged in order, so results repeat bit for bit.
 __device__ __forceinline__ int key_tiles(int vis_last) { return vis_last > 0 ? (vis_last + kKeys - 1) / kKeys : 0; }
@@ -220,7 +221,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
     }
     const float units = float(pieces) * p.heads_v, load = float(tiles) * p.heads_v + 3.f * units;
     float e = fmaxf(top + 3.f, load / G + (units > G ? 0.35f * top : 0.f));
-    if (warp > 0) e = 1.1f * (e + 2.f);  // only where it clearly pays
+    if (warp > 0) e = 1.1f * (e + kMergeTiles);  // only where it clearly pays
     if (T == 0 || units > 2 * G ||  pieces > n + kPromptExtraItems ||
         (long long)rows * p.heads_v > p.partial_rows)
       e = warp > 0 ? 1e30f : 1e29f;
@@ -1014,10 +1015,14 @@ cudaError_t launch_prompt_attention(PromptParams p, cudaStream_t stream) {
   const long long blocks = ((long long)p.n_q << p.pack) / kPromptRows + p.num_seqs;  // at most
   const long long most = blocks * kPromptMaxPieces * p.heads_v;                      // units
   const unsigned grid = unsigned(most < p.sm_count ? most : p.sm_count);
-  // Two rounds of whole units at most, none with keys to split: a plan would
-  // cost more than it can save (93 tokens at 16 heads: 9.5 us with one on the
-  // device, 2.6 us of a second launch on the host).
-  if (p.num_seqs <= 32 && blocks * p.heads_v <= 2 * p.sm_count && p.n_k <= kMinSplit * kKeys)
+  // No plan where it would cost more than it can save: two rounds of units at
+  // most with no block long enough to split, or one round that fills more than
+  // two thirds of the SMs (half a unit more to each SM would be a second round).
+  // 93 tokens at 16 heads: 11.4 us without, 12.7 with one; 2,048 tokens: 36 and
+  // 42 us.
+  const long long whole = blocks * p.heads_v;
+  if (p.num_seqs <= 32 && ((whole <= 2 * p.sm_count && p.n_k <= kMinSplit * kKeys) ||
+                           (whole <= p.sm_count && 3 * whole > 2 * p.sm_count)))
     return launch_pdl(prompt_attention_kernel<true>, dim3(grid), dim3(kPromptThreads), kSmem, stream, 1, qn, qp, kn, kp,
                       v, p);
   // Splitting keys is for calls whose query rows make two rounds at most, and
@@ -1028,7 +1033,7 @@ cudaError_t launch_prompt_attention(PromptParams p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   e = launch_pdl(prompt_attention_kernel<false>, dim3(grid), dim3(kPromptThreads), kSmem, stream, 1, qn, qp, kn, kp, v, p);
   if (e != cudaSuccess || !p.may_split) return e;
-  return launch_pdl(prompt_merge_kernel, dim3(4 * p.sm_count), dim3(kMergeThreads), 0, stream, 1, p);
+  return launch_pdl(prompt_merge_kernel, dim3(8 * p.sm_count), dim3(kMergeThreads), 0, stream, 1, p);
 }
 
 }  // namespace mla
