@@ -65,7 +65,7 @@ constexpr uint32_t kQTile = 3 * kBox;              // q_nope columns 0-63, 64-12
 constexpr int kRing = 8;                           // boxes of the key / value ring
 constexpr uint32_t kOffRing = 2 * kQTile;
 constexpr uint32_t kOffMisc = kOffRing + kRing * kBox;
-constexpr uint32_t kSmem = kOffMisc + 1024 + 1024;  // + barriers, alignment slack
+constexpr uint32_t kSmem = kOffMisc + 2048 + 1024;  // + barriers, alignment slack
 constexpr int kPromptThreads = 384;
 constexpr uint32_t kColS = 0, kColO = 256;         // tensor memory columns: S x2, O x2
 constexpr uint64_t kWaitNs = 2000000000ull;        // 2 s
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
 }
 
 // ----- attention -------------------------------------------------------------------
-constexpr int kItemRing = 4;
+constexpr int kItemRing = 4, kDirectSeqs = 32;
 struct PromptBarriers {
   uint64_t q_full[2], q_empty[2];  // query tile loaded / read by its last QK
   uint64_t k_full[2], v_full[2];   // boxes of even / odd key tiles landed
@@ -320,9 +320,13 @@ struct PromptBarriers {
   uint64_t drain[2];
   uint64_t item_full[kItemRing], item_empty[kItemRing];
   PromptItem items[kItemRing];     // the CTA's units, read ahead by the producer (rows = 0: no more)
+  // without a plan: the sequences' offsets (q0, q1, k0, k1) and the blocks up to and with each
+  int4 seqs[kDirectSeqs];
+  int seq_end[kDirectSeqs];
   uint32_t tmem_base;
   int abort;
 };
+static_assert(sizeof(PromptBarriers) <= 2048, "shared memory behind the ring");
 
 __device__ __forceinline__ void fail(PromptBarriers* B, int* status) {
   B->abort = 1;
@@ -455,22 +459,21 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 
   int direct_items = 0;
   if (kDirect && warp == 8) {
-    // No plan: this warp lists the blocks of the at most 32 sequences, in
-    // order.  Every CTA writes the same list and reads what it wrote.
+    // No plan: this warp lists the sequences, at most 32, in shared memory.
     const bool in = lane < p.num_seqs;
     const int q0 = in ? p.cu_q[lane] : 0, q1 = in ? p.cu_q[lane + 1] : 0;
     const int k0 = in ? p.cu_k[lane] : 0, k1 = in ? p.cu_k[lane + 1] : 0;
     const unsigned bad = __ballot_sync(0xffffffffu, in && bad_offsets(p, q0, q1, k0, k1));
     const int good = bad ? __ffs(bad) - 1 : p.num_seqs;  // sequences from the first bad one on are skipped
     if (blockIdx.x == 0 && lane == 0) *p.status = bad ? MLA_ERR_DEVICE_BOUNDS : MLA_OK;
-    const int blocks = lane < good ? blocks_of(p, q1 - q0) : 0;
-    int end = blocks;
+    int end = lane < good ? blocks_of(p, q1 - q0) : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int x = __shfl_up_sync(0xffffffffu, end, o);
       if (lane >= o) end += x;
     }
-    for (int i = 0; i < blocks; ++i) p.items[end - blocks + i] = make_item(p, q0, q1, k0, k1, i);
+    B->seqs[lane] = make_int4(q0, q1, k0, k1);
+    B->seq_end[lane] = end;
     direct_items = __shfl_sync(0xffffffffu, end, 31);
     __syncwarp();
   }
@@ -498,7 +501,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       PromptItem x;
       x.rows = 0;
       if (u < units) {
-        x = load_item(p.items + u / H);
+        const int i = u / H;
+        if (kDirect) {
+          int b = 0;  // the first sequence whose blocks end past i
+          while (B->seq_end[b] <= i) ++b;
+          const int4 q = B->seqs[b];
+          x = make_item(p, q.x, q.y, q.z, q.w, b > 0 ? i - B->seq_end[b - 1] : i);
+        } else {
+          x = load_item(p.items + i);
+        }
         x.head = u % H;
       }
       return x;
@@ -510,9 +521,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       mbar_arrive(&B->item_full[slot]);
       return true;
     };
-    it = load_item(p.items + blockIdx.x / H);  // in the list's bounds, if maybe not written: beside the count's load
-    it.head = blockIdx.x % H;
-    if (int(blockIdx.x) >= units) it.rows = 0;
+    if (kDirect) {
+      it = fetch(blockIdx.x);
+    } else {
+      it = load_item(p.items + blockIdx.x / H);  // in the list's bounds, if maybe not written: beside the count's load
+      it.head = blockIdx.x % H;
+      if (int(blockIdx.x) >= units) it.rows = 0;
+    }
     ok = publish(0, it);
     int u_after = it.rows > 0 ? take() : units;
     next = fetch(u_after);  // the counter stops at most two past the units for each CTA
@@ -1021,7 +1036,7 @@ cudaError_t launch_prompt_attention(PromptParams p, cudaStream_t stream) {
   // 93 tokens at 16 heads: 11.4 us without, 12.7 with one; 2,048 tokens: 36 and
   // 42 us.
   const long long whole = blocks * p.heads_v;
-  if (p.num_seqs <= 32 && ((whole <= 2 * p.sm_count && p.n_k <= kMinSplit * kKeys) ||
+  if (p.num_seqs <= kDirectSeqs && ((whole <= 2 * p.sm_count && p.n_k <= kMinSplit * kKeys) ||
                            (whole <= p.sm_count && 3 * whole > 2 * p.sm_count)))
     return launch_pdl(prompt_attention_kernel<true>, dim3(grid), dim3(kPromptThreads), kSmem, stream, 1, qn, qp, kn, kp,
                       v, p);
