@@ -390,6 +390,18 @@ def _call_on(dev: torch.device, stream, fn, *args) -> int:
     return fn(*args, torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else _stream(stream))
 
 
+def _new(shape, dtype, dev: torch.device, stream) -> torch.Tensor:
+    """torch.empty in the memory of the stream that the call runs on: a tensor
+    of another stream's memory could still be in use there, or be handed out
+    again there while the call runs."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream), device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
 def cache_read(d: Dims, cache: torch.Tensor, scale_zero: torch.Tensor | None, block_table: torch.Tensor,
                cu_rows: torch.Tensor, starts: torch.Tensor | None = None, n_rows: int | None = None,
                c_kv: torch.Tensor | None = None, k_pe: torch.Tensor | None = None,
@@ -408,9 +420,9 @@ def cache_read(d: Dims, cache: torch.Tensor, scale_zero: torch.Tensor | None, bl
             raise ValueError("n_rows is needed where neither c_kv nor k_pe is given")
         n_rows = _dims_of(given, "c_kv" if c_kv is not None else "k_pe", 2)[0]
     if c_kv is None:
-        c_kv = torch.empty((n_rows, d.kv_lora_rank), dtype=torch.bfloat16, device=dev)
+        c_kv = _new((n_rows, d.kv_lora_rank), torch.bfloat16, dev, stream)
     if k_pe is None:
-        k_pe = torch.empty((n_rows, d.rope_dim), dtype=torch.bfloat16, device=dev)
+        k_pe = _new((n_rows, d.rope_dim), torch.bfloat16, dev, stream)
     code = d.cache_dtype
     if code == MLA_CACHE_FP8 and cache.dtype == torch.float8_e4m3fn:
         cache = cache.view(torch.uint8)
@@ -437,9 +449,9 @@ def expand_kv(d: Dims, c_kv: torch.Tensor, W_UK: torch.Tensor, W_UV: torch.Tenso
     n = _dims_of(c_kv, "c_kv", 2)[0]
     dev, H, R, bf16 = c_kv.device, d.num_heads, d.kv_lora_rank, torch.bfloat16
     if k_nope is None:
-        k_nope = torch.empty((n, H, d.qk_nope_dim), dtype=bf16, device=dev)
+        k_nope = _new((n, H, d.qk_nope_dim), bf16, dev, stream)
     if v is None:
-        v = torch.empty((n, H, d.v_head_dim), dtype=bf16, device=dev)
+        v = _new((n, H, d.v_head_dim), bf16, dev, stream)
     st = _call_on(dev, stream, _L().mla_expand_kv, ctypes.byref(d), _arg(c_kv, "c_kv", bf16, (n, R), dev), n,
                   _arg(W_UK, "W_UK", bf16, (H, d.qk_nope_dim, R), dev),
                   _arg(W_UV, "W_UV", bf16, (H, d.v_head_dim, R), dev),
@@ -472,11 +484,11 @@ def prompt_attention(d: Dims, q_nope: torch.Tensor, q_pe: torch.Tensor, k_nope: 
     B = _dims_of(cu_q, "cu_q", 1)[0] - 1
     dev, H, bf16 = q_nope.device, d.num_heads, torch.bfloat16
     if workspace is None:
-        workspace = torch.empty(prompt_attention_workspace_size(d, B, n_q), dtype=torch.uint8, device=dev)
+        workspace = _new(prompt_attention_workspace_size(d, B, n_q), torch.uint8, dev, stream)
     if out is None:
-        out = torch.empty((n_q, H, d.v_head_dim), dtype=bf16, device=dev)
+        out = _new((n_q, H, d.v_head_dim), bf16, dev, stream)
     if lse_out is None and want_lse:
-        lse_out = torch.empty((n_q, H), dtype=torch.float32, device=dev)
+        lse_out = _new((n_q, H), torch.float32, dev, stream)
     st = _call_on(
         dev, stream, _L().mla_prompt_attention, ctypes.byref(d),
         _arg(q_nope, "q_nope", bf16, (n_q, H, d.qk_nope_dim), dev),

@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(CacheReadParam
       // b = (number of entries <= r) - 1
       int lo = 0, hi = p.num_seqs + 1;
       while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
+        const int mid = lo + ((hi - lo) >> 1);
         if (p.cu_rows[mid] <= r) lo = mid + 1; else hi = mid;
       }
       const int b = lo - 1;

@@ -87,9 +87,9 @@ static_assert(kSmem <= 232448, "dynamic shared memory of one CTA");
 // them from L2 (a list sorted by block length alone read the keys and values of
 // many equal prompts from memory once per block), and short units come last
 // (heads before blocks left the last head's longest blocks for the end: 1,000
-// instead of 893 us for 16,384 tokens at 16 heads).  A
-// sequence whose offsets decrease or pass the end, and every one after it, is
-// skipped and reported; this also bounds the list.
+// instead of 893 us for 16,384 tokens at 16 heads).  A sequence whose offsets
+// decrease or pass the end, and every one after it, is skipped and reported;
+// this also bounds the list.
 //
 // Split: candidate k (one warp each) cuts the longest block into k + 1 pieces
 // and every block into pieces of at most that length.  Its estimate, in key
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
   }
   if (few) {
     const int T = (longest + warp) / (warp + 1);  // ceil(longest / (warp + 1))
-    int pieces = 0, top = 0, rows = 0, splits = 0;
+    int pieces = 0, top = 0, rows = 0;
     long long tiles = 0;
     for (int i = lane; i < n && T > 0; i += 32) {
       const PromptItem it = block_item(i, sequence_of(i));
@@ -206,10 +206,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
       pieces += c;
       tiles += t;
       top = max(top, (t + c - 1) / c);
-      if (c > 1) {
-        rows += c * it.rows;
-        ++splits;
-      }
+      if (c > 1) rows += c * it.rows;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -217,12 +214,11 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
       tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
       top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
       rows += __shfl_xor_sync(0xffffffffu, rows, o);
-      splits += __shfl_xor_sync(0xffffffffu, splits, o);
     }
     const float units = float(pieces) * p.heads_v, load = float(tiles) * p.heads_v + 3.f * units;
     float e = fmaxf(top + 3.f, load / G + (units > G ? 0.35f * top : 0.f));
     if (warp > 0) e = 1.1f * (e + kMergeTiles);  // only where it clearly pays
-    if (T == 0 || units > 2 * G ||  pieces > n + kPromptExtraItems ||
+    if (T == 0 || units > 2 * G || pieces > n + kPromptExtraItems ||
         (long long)rows * p.heads_v > p.partial_rows)
       e = warp > 0 ? 1e30f : 1e29f;
     if (lane == 0) estimate[warp] = e;

@@ -290,6 +290,60 @@ def test_prompt_bad_offsets(cuda_lib):
     assert st == mla.MLA_ERR_DEVICE_BOUNDS and torch.all(out == 7.0)
 
 
+@pytest.mark.parametrize("good,last", [
+    ((50,), 2000),                    # keys to split
+    (tuple(range(40)), 40),           # more sequences than are listed without a plan
+    ((3000,), 40),                    # more units than are split
+])
+def test_prompt_bad_offsets_in_a_plan(cuda_lib, good, last):
+    """As test_prompt_bad_offsets, for calls whose work a plan lists: the good sequences before are computed."""
+    q = list(good) + [60, 40]
+    k = list(good) + [60, last]
+    x = _prompt(q, k, seed=18)
+    out0, lse0, st = _gpu(x)
+    assert st == mla.MLA_OK
+    cu_q, cu_k = _cu(q), _cu(k)
+    n, m = len(good) + 1, sum(good)  # the offset to break, and the rows before it
+    for name, at, value in (("q", n, m - 1), ("k", n, m - 1), ("q", n, sum(q) + 1), ("k", n, sum(k) + 1),
+                            ("q", n, 2**31 - 1), ("k", n, -(2**31))):
+        bad_q, bad_k = cu_q.clone(), cu_k.clone()
+        (bad_q if name == "q" else bad_k)[at] = value
+        out = torch.full_like(out0, 7.0)
+        lse = torch.full_like(lse0, 7.0)
+        _, _, st = _gpu(x, cu_q=bad_q, cu_k=bad_k, out=out, lse_out=lse)
+        assert st == mla.MLA_ERR_DEVICE_BOUNDS
+        # which pieces a block is cut into may differ without the last sequences: compare to the formula's bounds
+        y = {**x, "q_lens": list(good), "k_lens": list(good)}
+        ref, lref, tol, ltol = R.attention(x["q_nope"], x["q_pe"], x["k_nope"], x["k_pe"], x["v"], y["q_lens"],
+                                           y["k_lens"], SCALE)
+        assert R.worst(out[:m].cpu(), ref, tol) <= 1.0 and R.worst(lse[:m].cpu(), lref, ltol) <= 1.0
+        assert torch.all(out[m:] == 7.0) and torch.all(lse[m:] == 7.0)
+
+
+@pytest.mark.parametrize("q_lens,k_lens", [
+    ((100, 70, 30), (1500, 1900, 30)),                     # split keys
+    ((3000, 70, 600), (3000, 1900, 700)),                  # whole blocks
+    (tuple(range(1, 40)), tuple(range(3, 42))),            # many sequences
+])
+def test_prompt_rows_of_no_sequence_in_a_plan(cuda_lib, q_lens, k_lens):
+    """As test_prompt_rows_of_no_sequence, for calls whose work a plan lists."""
+    x = _prompt(q_lens, k_lens, seed=19, pad=40)
+    out0, lse0, st = _gpu(x)
+    assert st == mla.MLA_OK
+    y = {k: (v.clone() if torch.is_tensor(v) else v) for k, v in x.items()}
+    for name, lens in (("q_nope", q_lens), ("q_pe", q_lens), ("k_nope", k_lens), ("k_pe", k_lens), ("v", k_lens)):
+        y[name][lens[0]:lens[0] + lens[1]] = float("nan")  # the second sequence
+        y[name][sum(lens):] = float("inf")                 # the rows behind the last
+    n = sum(q_lens)
+    out, lse = torch.full_like(out0, 7.0), torch.full_like(lse0, 7.0)
+    _, _, st = _gpu(y, out=out, lse_out=lse)
+    assert st == mla.MLA_OK
+    keep = torch.cat([torch.arange(q_lens[0]), torch.arange(q_lens[0] + q_lens[1], n)])
+    assert torch.equal(out[keep], out0[keep]) and torch.equal(lse[keep], lse0[keep])
+    assert torch.all(out[n:] == 7.0) and torch.all(lse[n:] == 7.0)
+    assert torch.isnan(out[q_lens[0]:q_lens[0] + q_lens[1]]).all()
+
+
 def test_prompt_no_keys_no_lse(cuda_lib):
     x = _prompt((5, 7), (0, 0), seed=9)
     out, lse, st = _gpu(x)

@@ -131,6 +131,32 @@ def test_streams_side_by_side(cuda_lib):
     assert torch.equal(steps[0][1][4], refs[0][4])
 
 
+@pytest.mark.parametrize("as_handle", [False, True])
+def test_tensors_made_for_another_stream(cuda_lib, as_handle):
+    """Workspace and outputs that the binding allocates belong to the stream of
+    the call: what the current stream allocates meanwhile does not meet them."""
+    run, outs, _, x = _step(30)
+    run()
+    torch.cuda.synchronize()
+    ref = [t.clone() for t in outs]
+    d = mla.dims(H, P, fp8=True)
+    s = torch.cuda.Stream()
+    on = s.cuda_stream if as_handle else s
+    nk = x["cu_k"][-1].item()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)  # the calls below wait for about 10 ms
+    c, pe = mla.cache_read(d, x["cache"], x["sc"], x["table"], x["cu_k"], n_rows=nk, stream=on)
+    k, v = mla.expand_kv(d, c, x["uk"], x["uv"], stream=on)
+    out, lse = mla.prompt_attention(d, x["qn"], x["qp"], k, pe, v, x["cu_q"], x["cu_k"], SCALE, stream=on)
+    size = mla.prompt_attention_workspace_size(d, 3, x["qn"].shape[0])
+    for _ in range(4):
+        torch.empty(size, dtype=torch.uint8, device="cuda").fill_(1)
+    torch.cuda.synchronize()
+    for t, r in zip((c, pe, k, v, out, lse), ref):
+        assert torch.equal(t, r)
+
+
 def test_offsets_past_32_bits(cuda_lib):
     """Query, key and output rows whose element offsets do not fit 31 bits."""
     heads, big = 128, 140000  # 140,000 x 128 heads x 128 = 2.3e9 elements
