@@ -91,13 +91,16 @@ static_assert(kSmem <= 232448, "dynamic shared memory of one CTA");
 // decrease or pass the end, and every one after it, is skipped and reported;
 // this also bounds the list.
 //
-// Split: candidate k (one warp each) cuts the longest block into k + 1 pieces
-// and every block into pieces of at most that length.  Its estimate, in key
-// tiles: the longest piece where every unit (item, head) has its own CTA, else
-// the mean load and a share of the longest piece for the uneven end, plus
-// three tiles for a unit's start and end and five for the merge, a kernel of its
-// own.  The pieces of a block depend on the lengths and the SM count alone, and
-// are merged in order, so results repeat bit for bit.
+// Split: candidate k cuts the longest block into k + 1 pieces and every block
+// into pieces of at most that length.  Its estimate, in key tiles: the longest
+// piece where every unit (item, head) has its own CTA, else the mean load and a
+// share of the longest piece for the uneven end, plus three tiles for a unit's
+// start and end and five for the merge, a kernel of its own.  The pieces of a
+// block depend on the lengths and the SM count alone, and are merged in order,
+// so results repeat bit for bit.  This path is a dozen microseconds of latency
+// if written without care, most of it instructions fetched for the first time:
+// it has few of them (a candidate to a lane, sums by shared-memory atomics, the
+// place in the list by counting), not few operations.
 __device__ __forceinline__ int key_tiles(int vis_last) { return vis_last > 0 ? (vis_last + kKeys - 1) / kKeys : 0; }
 __device__ __forceinline__ int pieces_of(int tiles, int longest) { return tiles > longest ? (tiles + longest - 1) / longest : 1; }
 
@@ -127,8 +130,10 @@ __device__ __forceinline__ PromptItem make_item(const PromptParams& p, int q0, i
 __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams p) {
   __shared__ int scan_tmp[32];
   __shared__ int hist[kBuckets];
-  __shared__ int carry, first_bad, longest, piece_tiles;
-  __shared__ float estimate[kPlanThreads / 32];
+  __shared__ int carry, first_bad, longest, total_tiles, piece_tiles;
+  __shared__ int few_tiles[kPromptMaxSplit], few_rows[kPromptMaxSplit], few_key[kPromptMaxSplit], few_pieces[kPromptMaxSplit];
+  __shared__ int cand_pieces[32], cand_top[32], cand_rows[32];  // sums over the blocks, of each candidate
+  __shared__ unsigned long long taken;  // split blocks, their rows << 10, their partial rows << 32
   // offsets and block starts, here where they fit: the loops below read them over and over
   __shared__ int offsets[4][kPlanSeqs + 1];
   griddep_wait();
@@ -149,13 +154,15 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
   }
   if (tid == 0) {
     carry = 0;
-    longest = 0;
+    longest = total_tiles = 0;
+    taken = 0;
     first_bad = p.num_seqs;
     p.status[0] = MLA_OK;
     p.status[2] = 0;  // units taken
     p.status[3] = 0;  // split blocks
   }
   for (int i = tid; i < kBuckets; i += kPlanThreads) hist[i] = 0;
+  if (tid < 32) cand_pieces[tid] = cand_top[tid] = cand_rows[tid] = 0;
   __syncthreads();
   for (int b = tid; b < p.num_seqs; b += kPlanThreads) {
     const int q0 = cu_q[b], q1 = cu_q[b + 1], k0 = cu_k[b], k1 = cu_k[b + 1];
@@ -187,45 +194,43 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
   auto block_item = [&](int i, int b) {
     return make_item(p, cu_q[b], cu_q[b + 1], cu_k[b], cu_k[b + 1], i - block_start[b]);
   };
-  // more units than two rounds are never split (below): their blocks need no estimate
+  // more units than two rounds are never split, nor are short blocks: a piece
+  // would be little more than its start and merge
   const int G = p.sm_count;
-  // (nor are short ones: a piece would be little more than its start and merge)
-  bool few = p.may_split && (long long)n * p.heads_v <= 2 * G && n <= kPromptMaxSplit;
-  if (few) {
-    for (int i = tid; i < n; i += kPlanThreads) atomicMax(&longest, key_tiles(block_item(i, sequence_of(i)).kv_end));
-    __syncthreads();
-    few = longest > kMinSplit;
-  }
-  if (few) {
-    const int T = (longest + warp) / (warp + 1);  // ceil(longest / (warp + 1))
-    int pieces = 0, top = 0, rows = 0;
-    long long tiles = 0;
-    for (int i = lane; i < n && T > 0; i += 32) {
-      const PromptItem it = block_item(i, sequence_of(i));
-      const int t = key_tiles(it.kv_end), c = pieces_of(t, T);
-      pieces += c;
-      tiles += t;
-      top = max(top, (t + c - 1) / c);
-      if (c > 1) rows += c * it.rows;
+  if (p.may_split && (long long)n * p.heads_v <= 2 * G && n <= kPromptMaxSplit) {
+    PromptItem it;
+    int t = 0, key = 0;
+    if (tid < n) {
+      const int b = sequence_of(tid);
+      it = block_item(tid, b);
+      t = key_tiles(it.kv_end);
+      key = key_tiles(cu_k[b + 1] - cu_k[b]);
+      few_tiles[tid] = t;
+      few_rows[tid] = it.rows;
+      few_key[tid] = key;
+      atomicMax(&longest, t);
+      atomicAdd(&total_tiles, t);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      pieces += __shfl_xor_sync(0xffffffffu, pieces, o);
-      tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      rows += __shfl_xor_sync(0xffffffffu, rows, o);
-    }
-    const float units = float(pieces) * p.heads_v, load = float(tiles) * p.heads_v + 3.f * units;
-    float e = fmaxf(top + 3.f, load / G + (units > G ? 0.35f * top : 0.f));
-    if (warp > 0) e = 1.1f * (e + kMergeTiles);  // only where it clearly pays
-    if (T == 0 || units > 2 * G || pieces > n + kPromptExtraItems ||
-        (long long)rows * p.heads_v > p.partial_rows)
-      e = warp > 0 ? 1e30f : 1e29f;
-    if (lane == 0) estimate[warp] = e;
     __syncthreads();
-    if (warp == 0) {  // the lowest estimate, of equal ones the first
-      float low = estimate[lane];
-      int best = lane;
+    const bool split = longest > kMinSplit;
+    if (split) {
+      const int T = (longest + lane) / (lane + 1);  // lane: candidate
+      for (int i = warp; i < n; i += 32) {
+        const int ti = few_tiles[i], c = pieces_of(ti, T);
+        atomicAdd(&cand_pieces[lane], c);
+        atomicMax(&cand_top[lane], (ti + c - 1) / c);
+        if (c > 1) atomicAdd(&cand_rows[lane], c * few_rows[i]);
+      }
+    }
+    __syncthreads();
+    if (warp == 0) {
+      const int pieces = cand_pieces[lane], top = cand_top[lane];
+      const float units = float(pieces) * p.heads_v, load = float(total_tiles) * p.heads_v + 3.f * units;
+      float low = fmaxf(top + 3.f, load / G + (units > G ? 0.35f * top : 0.f));
+      if (lane > 0) low = 1.1f * (low + kMergeTiles);  // only where it clearly pays
+      if (units > 2 * G || pieces > n + kPromptExtraItems || (long long)cand_rows[lane] * p.heads_v > p.partial_rows)
+        low = lane > 0 ? 1e30f : 1e29f;
+      int best = lane;  // the lowest estimate, of equal ones the first
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
         const float e2 = __shfl_xor_sync(0xffffffffu, low, o);
@@ -235,24 +240,44 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
           best = b2;
         }
       }
-      if (lane == 0) piece_tiles = best == 0 ? 0x7fffffff : (longest + best) / (best + 1);
+      if (lane == 0) {
+        piece_tiles = split && best > 0 ? (longest + best) / (best + 1) : 0x7fffffff;
+        p.status[1] = split && best > 0 ? cand_pieces[best] : n;
+      }
     }
-  } else if (tid == 0) {
-    piece_tiles = 0x7fffffff;
+    __syncthreads();
+    const int c = pieces_of(t, piece_tiles);
+    if (tid < n) few_pieces[tid] = c;
+    __syncthreads();
+    if (tid < n) {
+      int at = 0;  // pieces of the blocks listed before: of longer sequences, and the later ones of its own
+      for (int j = 0; j < n; ++j)
+        if (few_key[j] > key || (few_key[j] == key && j > tid)) at += few_pieces[j];
+      const int keys = it.kv_end;
+      it.pieces = c;
+      if (c > 1) {
+        const unsigned long long old =
+            atomicAdd(&taken, 1ull | (unsigned long long)it.rows << 10 | (unsigned long long)(c * it.rows * p.heads_v) << 32);
+        it.partial = int(old >> 32);
+        p.splits[int(old & 1023)] = {it.q_row0, it.rows, c, it.partial, int(uint32_t(old) >> 10)};
+      }
+      for (int q = 0; q < c; ++q) {
+        it.piece = q;
+        it.kv_begin = q * t / c * kKeys;
+        it.kv_end = min(keys, (q + 1) * t / c * kKeys);
+        p.items[at + q] = it;
+      }
+    }
+    __syncthreads();
+    if (tid == 0) {
+      p.status[3] = int(taken & 1023);
+      p.status[4] = int(uint32_t(taken) >> 10);
+    }
+    return;
   }
-  __syncthreads();
-  const int T = piece_tiles;
-  const bool split = T != 0x7fffffff;
-  // items of blocks [first, last) of sequence b
-  auto items_of = [&](int b, int first, int last) {
-    if (!split) return last - first;
-    int c = 0;
-    for (int i = first; i < last; ++i) c += pieces_of(key_tiles(block_item(block_start[b] + i, b).kv_end), T);
-    return c;
-  };
   auto bucket_of = [&](int b) { return kBuckets - 1 - min(kBuckets - 1, key_tiles(cu_k[b + 1] - cu_k[b])); };
   for (int b = tid; b < good; b += kPlanThreads) {
-    const int c = items_of(b, 0, blocks_in(b));
+    const int c = blocks_in(b);
     if (c > 0) atomicAdd(&hist[bucket_of(b)], c);
   }
   __syncthreads();
@@ -263,43 +288,13 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
   __syncthreads();
   // the order of equally long sequences is arbitrary: it decides which CTA runs an item, not its result
   for (int b = tid; b < good; b += kPlanThreads) {
-    const int c = items_of(b, 0, blocks_in(b));
+    const int c = blocks_in(b);
     if (c > 0) seq_first[b] = atomicAdd(&hist[bucket_of(b)], c);
   }
   __syncthreads();
-  int partial0 = 0;
-  if (split) {  // n <= kPromptMaxSplit <= the threads: block `tid`'s place among the split ones, their partial and output rows
-    int pieces = 1, rows = 0;
-    PromptItem it;
-    if (tid < n) {
-      it = block_item(tid, sequence_of(tid));
-      pieces = pieces_of(key_tiles(it.kv_end), T);
-      rows = pieces > 1 ? it.rows : 0;
-    }
-    int splits, partials, out_rows;
-    const int number = block_exclusive_scan(rows > 0, scan_tmp, &splits);
-    partial0 = block_exclusive_scan(pieces * rows * p.heads_v, scan_tmp, &partials);
-    const int row_start = block_exclusive_scan(rows, scan_tmp, &out_rows);
-    if (rows > 0) p.splits[number] = {it.q_row0, rows, pieces, partial0, row_start};
-    if (tid == 0) {
-      p.status[3] = splits;
-      p.status[4] = out_rows;
-    }
-  }
   for (int i = tid; i < n; i += kPlanThreads) {
-    const int b = sequence_of(i), local = i - block_start[b], blocks = blocks_in(b);
-    PromptItem it = block_item(i, b);
-    const int keys = it.kv_end, t = key_tiles(keys), c = pieces_of(t, T);
-    it.pieces = c;
-    it.partial = partial0;
-    const int at = seq_first[b] + items_of(b, local + 1, blocks);
-    for (int q = 0; q < c; ++q) {
-      const int t0 = q * t / c, t1 = (q + 1) * t / c;
-      it.piece = q;
-      it.kv_begin = t0 * kKeys;
-      it.kv_end = min(keys, t1 * kKeys);
-      p.items[at + q] = it;
-    }
+    const int b = sequence_of(i);
+    p.items[seq_first[b] + blocks_in(b) - 1 - (i - block_start[b])] = block_item(i, b);
   }
 }
 
