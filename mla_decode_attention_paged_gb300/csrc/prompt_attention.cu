@@ -97,10 +97,10 @@ static_assert(kSmem <= 232448, "dynamic shared memory of one CTA");
 // share of the longest piece for the uneven end, plus three tiles for a unit's
 // start and end and five for the merge, a kernel of its own.  The pieces of a
 // block depend on the lengths and the SM count alone, and are merged in order,
-// so results repeat bit for bit.  This path is a dozen microseconds of latency
-// if written without care, most of it instructions fetched for the first time:
-// it has few of them (a candidate to a lane, sums by shared-memory atomics, the
-// place in the list by counting), not few operations.
+// so results repeat bit for bit.  A plan is all latency, and was 2.5 us more with a
+// warp to each candidate, shuffles for the sums, and sorts and scans for the
+// list: here a candidate is a lane, the sums are atomics in shared memory and a
+// block counts the pieces ahead of it.
 __device__ __forceinline__ int key_tiles(int vis_last) { return vis_last > 0 ? (vis_last + kKeys - 1) / kKeys : 0; }
 __device__ __forceinline__ int pieces_of(int tiles, int longest) { return tiles > longest ? (tiles + longest - 1) / longest : 1; }
 
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
   __shared__ int hist[kBuckets];
   __shared__ int carry, first_bad, longest, total_tiles, piece_tiles;
   __shared__ int few_tiles[kPromptMaxSplit], few_rows[kPromptMaxSplit], few_key[kPromptMaxSplit], few_pieces[kPromptMaxSplit];
-  __shared__ int cand_pieces[32], cand_top[32], cand_rows[32];  // sums over the blocks, of each candidate
+  __shared__ int cand_pieces[32], cand_rows[32];  // sums over the blocks, of each candidate
   __shared__ unsigned long long taken;  // split blocks, their rows << 10, their partial rows << 32
   // offsets and block starts, here where they fit: the loops below read them over and over
   __shared__ int offsets[4][kPlanSeqs + 1];
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
     p.status[3] = 0;  // split blocks
   }
   for (int i = tid; i < kBuckets; i += kPlanThreads) hist[i] = 0;
-  if (tid < 32) cand_pieces[tid] = cand_top[tid] = cand_rows[tid] = 0;
+  if (tid < 32) cand_pieces[tid] = cand_rows[tid] = 0;
   __syncthreads();
   for (int b = tid; b < p.num_seqs; b += kPlanThreads) {
     const int q0 = cu_q[b], q1 = cu_q[b + 1], k0 = cu_k[b], k1 = cu_k[b + 1];
@@ -213,20 +213,19 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
     }
     __syncthreads();
     const bool split = longest > kMinSplit;
+    const int T = (longest + lane) / (lane + 1);  // lane: candidate
     if (split) {
-      const int T = (longest + lane) / (lane + 1);  // lane: candidate
       for (int i = warp; i < n; i += 32) {
         const int ti = few_tiles[i], c = pieces_of(ti, T);
         atomicAdd(&cand_pieces[lane], c);
-        atomicMax(&cand_top[lane], (ti + c - 1) / c);
         if (c > 1) atomicAdd(&cand_rows[lane], c * few_rows[i]);
       }
     }
     __syncthreads();
     if (warp == 0) {
-      const int pieces = cand_pieces[lane], top = cand_top[lane];
+      const int pieces = cand_pieces[lane];
       const float units = float(pieces) * p.heads_v, load = float(total_tiles) * p.heads_v + 3.f * units;
-      float low = fmaxf(top + 3.f, load / G + (units > G ? 0.35f * top : 0.f));
+      float low = fmaxf(T + 3.f, load * __frcp_rn(float(G)) + (units > G ? 0.35f * T : 0.f));
       if (lane > 0) low = 1.1f * (low + kMergeTiles);  // only where it clearly pays
       if (units > 2 * G || pieces > n + kPromptExtraItems || (long long)cand_rows[lane] * p.heads_v > p.partial_rows)
         low = lane > 0 ? 1e30f : 1e29f;
@@ -240,9 +239,9 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
           best = b2;
         }
       }
-      if (lane == 0) {
-        piece_tiles = split && best > 0 ? (longest + best) / (best + 1) : 0x7fffffff;
-        p.status[1] = split && best > 0 ? cand_pieces[best] : n;
+      if (lane == best) {
+        piece_tiles = split && best > 0 ? T : 0x7fffffff;
+        p.status[1] = split && best > 0 ? pieces : n;
       }
     }
     __syncthreads();
