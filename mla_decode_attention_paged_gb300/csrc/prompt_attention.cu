@@ -70,11 +70,11 @@ constexpr int kPromptThreads = 384;
 constexpr uint32_t kColS = 0, kColO = 256;         // tensor memory columns: S x2, O x2
 constexpr uint64_t kWaitNs = 2000000000ull;        // 2 s
 constexpr float kRescale = 8.f;                    // log2 units
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 1024, kFewPlan = 128;
 constexpr int kPlanSeqs = 1024;                    // sequences whose offsets the plan holds in shared memory
 constexpr float kMergeTiles = 5.f;                 // the merge, in key tiles' time
 constexpr int kMinSplit = 10;                      // key tiles of a block that is never split
-constexpr int kBuckets = 1024;                     // cost classes of the plan's counting sort
+constexpr int kBuckets = kPlanThreads;             // cost classes of the plan's counting sort
 static_assert(kSmem <= 232448, "dynamic shared memory of one CTA");
 
 // ----- plan ----------------------------------------------------------------------
@@ -127,9 +127,14 @@ __device__ __forceinline__ PromptItem make_item(const PromptParams& p, int q0, i
   return it;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams p) {
+// kThreads = kFewPlan: the call has at most that many blocks, no more units than
+// two rounds, and may split keys (fewer warps to meet at barriers: with the
+// merge's grid cut to its rows, 34.3 -> 33.4 us for 256 rows behind 8,192 keys).
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads) prompt_plan_kernel(PromptParams p) {
+  constexpr bool kFew = kThreads == kFewPlan;
   __shared__ int scan_tmp[32];
-  __shared__ int hist[kBuckets];
+  __shared__ int hist[kFew ? 1 : kBuckets];
   __shared__ int carry, first_bad, longest, total_tiles, piece_tiles;
   __shared__ int few_tiles[kPromptMaxSplit], few_rows[kPromptMaxSplit], few_key[kPromptMaxSplit], few_pieces[kPromptMaxSplit];
   __shared__ int cand_pieces[32], cand_rows[32];  // sums over the blocks, of each candidate
@@ -143,7 +148,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
   const int *cu_q = p.cu_q, *cu_k = p.cu_k;
   int *block_start = p.block_start, *seq_first = p.seq_first;
   if (fits) {
-    for (int b = tid; b <= p.num_seqs; b += kPlanThreads) {
+    for (int b = tid; b <= p.num_seqs; b += kThreads) {
       offsets[0][b] = p.cu_q[b];
       offsets[1][b] = p.cu_k[b];
     }
@@ -161,17 +166,17 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
     p.status[2] = 0;  // units taken
     p.status[3] = 0;  // split blocks
   }
-  for (int i = tid; i < kBuckets; i += kPlanThreads) hist[i] = 0;
+  if (!kFew) hist[tid] = 0;
   if (tid < 32) cand_pieces[tid] = cand_rows[tid] = 0;
   __syncthreads();
-  for (int b = tid; b < p.num_seqs; b += kPlanThreads) {
+  for (int b = tid; b < p.num_seqs; b += kThreads) {
     const int q0 = cu_q[b], q1 = cu_q[b + 1], k0 = cu_k[b], k1 = cu_k[b + 1];
     if (bad_offsets(p, q0, q1, k0, k1)) atomicMin(&first_bad, b);
   }
   __syncthreads();
   const int good = first_bad;
   if (tid == 0 && good < p.num_seqs) set_status(p.status, MLA_ERR_DEVICE_BOUNDS);
-  for (int base = 0; base < good; base += kPlanThreads) {
+  for (int base = 0; base < good; base += kThreads) {
     const int b = base + tid;
     const int blocks = b < good ? blocks_of(p, cu_q[b + 1] - cu_q[b]) : 0;
     int total;
@@ -197,7 +202,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
   // more units than two rounds are never split, nor are short blocks: a piece
   // would be little more than its start and merge
   const int G = p.sm_count;
-  if (p.may_split && (long long)n * p.heads_v <= 2 * G && n <= kPromptMaxSplit) {
+  if (kFew || (p.may_split && (long long)n * p.heads_v <= 2 * G && n <= kPromptMaxSplit)) {
     PromptItem it;
     int t = 0, key = 0;
     if (tid < n) {
@@ -215,7 +220,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
     const bool split = longest > kMinSplit;
     const int T = (longest + lane) / (lane + 1);  // lane: candidate
     if (split) {
-      for (int i = warp; i < n; i += 32) {
+      for (int i = warp; i < n; i += kThreads / 32) {
         const int ti = few_tiles[i], c = pieces_of(ti, T);
         atomicAdd(&cand_pieces[lane], c);
         if (c > 1) atomicAdd(&cand_rows[lane], c * few_rows[i]);
@@ -274,26 +279,28 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
     }
     return;
   }
-  auto bucket_of = [&](int b) { return kBuckets - 1 - min(kBuckets - 1, key_tiles(cu_k[b + 1] - cu_k[b])); };
-  for (int b = tid; b < good; b += kPlanThreads) {
-    const int c = blocks_in(b);
-    if (c > 0) atomicAdd(&hist[bucket_of(b)], c);
-  }
-  __syncthreads();
-  int total;
-  const int ex = block_exclusive_scan(hist[tid], scan_tmp, &total);
-  hist[tid] = ex;
-  if (tid == 0) p.status[1] = total;
-  __syncthreads();
-  // the order of equally long sequences is arbitrary: it decides which CTA runs an item, not its result
-  for (int b = tid; b < good; b += kPlanThreads) {
-    const int c = blocks_in(b);
-    if (c > 0) seq_first[b] = atomicAdd(&hist[bucket_of(b)], c);
-  }
-  __syncthreads();
-  for (int i = tid; i < n; i += kPlanThreads) {
-    const int b = sequence_of(i);
-    p.items[seq_first[b] + blocks_in(b) - 1 - (i - block_start[b])] = block_item(i, b);
+  if constexpr (!kFew) {
+    auto bucket_of = [&](int b) { return kBuckets - 1 - min(kBuckets - 1, key_tiles(cu_k[b + 1] - cu_k[b])); };
+    for (int b = tid; b < good; b += kThreads) {
+      const int c = blocks_in(b);
+      if (c > 0) atomicAdd(&hist[bucket_of(b)], c);
+    }
+    __syncthreads();
+    int total;
+    const int ex = block_exclusive_scan(hist[tid], scan_tmp, &total);
+    hist[tid] = ex;
+    if (tid == 0) p.status[1] = total;
+    __syncthreads();
+    // the order of equally long sequences is arbitrary: it decides which CTA runs an item, not its result
+    for (int b = tid; b < good; b += kThreads) {
+      const int c = blocks_in(b);
+      if (c > 0) seq_first[b] = atomicAdd(&hist[bucket_of(b)], c);
+    }
+    __syncthreads();
+    for (int i = tid; i < n; i += kThreads) {
+      const int b = sequence_of(i);
+      p.items[seq_first[b] + blocks_in(b) - 1 - (i - block_start[b])] = block_item(i, b);
+    }
   }
 }
 
@@ -1034,11 +1041,15 @@ cudaError_t launch_prompt_attention(PromptParams p, cudaStream_t stream) {
   // with keys to split (rows that cu_q leaves out count, too: the lengths are on
   // the device); only they launch the merge.
   p.may_split = (((long long)p.n_q << p.pack) / kPromptRows) * p.heads_v <= 2 * p.sm_count && p.n_k > kMinSplit * kKeys;
-  cudaError_t e = launch_pdl(prompt_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, 1, p);
+  const bool few = p.may_split && whole <= 2 * p.sm_count && blocks <= kFewPlan;
+  cudaError_t e = few ? launch_pdl(prompt_plan_kernel<kFewPlan>, dim3(1), dim3(kFewPlan), 0, stream, 1, p)
+                      : launch_pdl(prompt_plan_kernel<kPlanThreads>, dim3(1), dim3(kPlanThreads), 0, stream, 1, p);
   if (e != cudaSuccess) return e;
   e = launch_pdl(prompt_attention_kernel<false>, dim3(grid), dim3(kPromptThreads), kSmem, stream, 1, qn, qp, kn, kp, v, p);
   if (e != cudaSuccess || !p.may_split) return e;
-  return launch_pdl(prompt_merge_kernel, dim3(8 * p.sm_count), dim3(kMergeThreads), 0, stream, 1, p);
+  const long long merges = ((long long)p.n_q * p.heads + kMergeThreads / 32 - 1) / (kMergeThreads / 32);  // at most
+  return launch_pdl(prompt_merge_kernel, dim3(unsigned(merges < 8 * p.sm_count ? merges : 8 * p.sm_count)),
+                    dim3(kMergeThreads), 0, stream, 1, p);
 }
 
 }  // namespace mla
