@@ -41,6 +41,9 @@
 // warps 0.86.  Short units leave the pipe idle while the next unit's first keys
 // land and its first softmax runs: 24 ragged prompts of 1 to 2,048 tokens run at
 // 130 us (955 TFLOP/s), 14% of it the masked halves of the diagonal tiles.
+// Few rows behind long contexts (26 behind 32,768 and 20,011 keys) take 94 us,
+// 4.6 TB/s: one query tile at work, and a key tile's chain QK, softmax, PV takes
+// 2,930 cycles where its copies take 2,800.
 //
 // Warps: 0-3 softmax and epilogue of query tile 0, 4-7 of tile 1, 8 units and
 // key copies, 9 (which also owns tensor memory) and 10 query copies and MMA
@@ -1030,8 +1033,8 @@ cudaError_t launch_prompt_attention(PromptParams p, cudaStream_t stream) {
   // No plan where it would cost more than it can save: two rounds of units at
   // most with no block long enough to split, or one round that fills more than
   // two thirds of the SMs (half a unit more to each SM would be a second round).
-  // 93 tokens at 16 heads: 11.4 us without, 12.7 with one; 2,048 tokens: 36 and
-  // 42 us.
+  // 93 tokens at 16 heads: 11 us without, 12.7 with one; 2,048 tokens: 35 and
+  // 41 us.
   const long long whole = blocks * p.heads_v;
   if (p.num_seqs <= kDirectSeqs && ((whole <= 2 * p.sm_count && p.n_k <= kMinSplit * kKeys) ||
                            (whole <= p.sm_count && 3 * whole > 2 * p.sm_count)))
