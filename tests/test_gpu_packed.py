@@ -369,6 +369,23 @@ def test_prompt_split_keys(cuda_lib, q_lens, k_lens, H, kv):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("H,kv,n", [(16, 1, 200), (64, 1, 128), (32, 2, 129)])
+def test_prompt_many_single_tokens(cuda_lib, H, kv, n):
+    """Single tokens behind contexts of which a few are long enough to split; one
+    block to a sequence, in plans of either size, with and without a bad end."""
+    k_lens = [(37 * i) % 300 for i in range(n)]
+    k_lens[n // 3], k_lens[n - 2], k_lens[5] = 3001, 2048, 1409
+    x = _prompt([1] * n, k_lens, H=H, kv=kv, seed=21)
+    _check(x)
+    a, b = _gpu(x), _gpu(x)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    cu_k = _cu(k_lens)
+    cu_k[-1] = sum(k_lens) + 1
+    out = torch.full_like(a[0], 7.0)
+    _, _, st = _gpu(x, cu_k=cu_k, out=out)
+    assert st == mla.MLA_ERR_DEVICE_BOUNDS and torch.all(out[n - 1:] == 7.0) and not torch.any(out[:n - 1] == 7.0)
+
+
 def test_prompt_many_sequences(cuda_lib):
     """More sequences than the plan's CTA has threads, mostly empty."""
     g = torch.Generator().manual_seed(5)
