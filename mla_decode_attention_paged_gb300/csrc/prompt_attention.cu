@@ -572,9 +572,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     // themselves their MMAs interleave and both query tiles come to wait for
     // their softmax at the same time.  The pipe takes only a few MMAs ahead, so
     // whatever a turn does between two MMAs shows: the MMAs are straight-line
-    // code on uniform registers, the next turn starts before this one's last
-    // four MMAs, and only warp 9 waits for boxes (the other's turn follows on
-    // the same boxes).  Both warps pass every key tile, whether their query
+    // code on uniform registers, and only warp 9 waits for boxes (the other's
+    // turn follows on the same boxes).  The next turn starts when this one's
+    // MMAs and commits are issued: four MMAs before that, some of them run behind
+    // the next turn's and the tiles' softmaxes come to run at the same time (128
+    // heads over 8: 689 us, now 669); once the MMAs are complete, the pipe idles
+    // (686).  Both warps pass every key tile, whether their query
     // tile sees it or not.
     const int t = warp - 9;
     constexpr uint32_t id_qk = idesc_bf16_f32(128, 128, false, false);
@@ -609,11 +612,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           for (int kk = 0; kk < 4; ++kk) mma_bf16(ds, q_desc + 2 * kk, b0 + 2 * kk, id_qk, kk > 0);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) mma_bf16(ds, q_desc + (kBox >> 4) + 2 * kk, b1 + 2 * kk, id_qk, 1);
-          pass_turn();
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) mma_bf16(ds, q_desc + 2 * (kBox >> 4) + 2 * kk, b2 + 2 * kk, id_qk, 1);
           mma_commit(&B->s_full[t]);
           mma_commit(&B->k_empty[jj & 1]);
+          pass_turn();
           if (last) mma_commit(&B->q_empty[t]);
         } else {
           pass_turn();
