@@ -182,20 +182,23 @@ __global__ void __launch_bounds__(kExpThreads, 1)
     constexpr uint64_t kDesc = smem_desc(0, 16, 1024, kSwizzle128B);
     const uint64_t a0 = kDesc | desc_addr(sbase + row_box), b0 = kDesc | desc_addr(sbase + col_box);
     const bool leader = elect_one();
-    bool ok = true;
+    bool ok = true;  // of all lanes: they leave together
     uint32_t k = 0, nr = 0, t = 0;
     int resident = -1;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      return ok = __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, abort_flag, kWaitNs));
+    };
     for (int u = u0; u < u1 && ok; ++u, ++t) {
       if (u / inner != resident) {
-        if (!(ok = mbar_wait_cluster(&B->res_full, nr & 1, abort_flag, kWaitNs))) break;
+        if (!wait(&B->res_full, nr & 1)) break;
         ++nr;
         resident = u / inner;
       }
       const uint32_t d = tmem + 256 * (t & 1);
-      if (t >= 2 && !(ok = mbar_wait_cluster(&B->acc_empty[t & 1], ((t >> 1) - 1) & 1, abort_flag, kWaitNs))) break;
+      if (t >= 2 && !wait(&B->acc_empty[t & 1], ((t >> 1) - 1) & 1)) break;
       for (int i = 0; i < kKBlocks; ++i, ++k) {
         const uint32_t s = k % kStages;
-        if (!(ok = mbar_wait_cluster(&B->full[s], (k / kStages) & 1, abort_flag, kWaitNs))) break;
+        if (!wait(&B->full[s], (k / kStages) & 1)) break;
         tc_fence_after();
         if (leader) {
           const uint64_t a = a0 + (kRowsResident ? i : s) * (kBox >> 4), b = b0 + (kRowsResident ? s : i) * (kBox >> 4);
