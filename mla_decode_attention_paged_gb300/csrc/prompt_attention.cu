@@ -561,7 +561,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       if (!fetched) after = fetch(u_after);
     }
     if (!ok) fail(B, p.status);
-  } else if (warp == 9 || warp == 10) {
+  } else if ((warp == 9 || warp == 10) && elect_one()) {
     // ------------------------------------------------------------ MMA issue
     // One warp per query tile t, each with its own chain: QK of the first key
     // tile, then PV of a key tile and QK of the next.  MMAs of one thread run
@@ -572,13 +572,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     // themselves their MMAs interleave and both query tiles come to wait for
     // their softmax at the same time.  The pipe takes only a few MMAs ahead, so
     // whatever a turn does between two MMAs shows: the MMAs are straight-line
-    // code on uniform registers, and only warp 9 waits for boxes (the other's
-    // turn follows on the same boxes).  The next turn starts when this one's
+    // code, and only warp 9 waits for boxes (the other's turn follows on the same
+    // boxes).  The next turn starts when this one's
     // MMAs and commits are issued: four MMAs before that, some of them run behind
     // the next turn's and the tiles' softmaxes come to run at the same time (128
     // heads over 8: 689 us, now 669); once the MMAs are complete, the pipe idles
-    // (686).  Both warps pass every key tile, whether their query
-    // tile sees it or not.
+    // (686).  Both warps pass every key tile, whether their query tile sees it or
+    // not.
+    //
+    // One lane does all of it: a barrier tells a phase's end only until the next
+    // phase ends, so a lane that only waited could come too late to see it.  All
+    // lanes, meeting before the products of each turn, took 911 us for 16,384
+    // tokens where one takes 865.
     const int t = warp - 9;
     constexpr uint32_t id_qk = idesc_bf16_f32(128, 128, false, false);
     constexpr uint32_t id_pv = idesc_bf16_f32(128, 128, false, true), id_pv64 = idesc_bf16_f32(128, 64, false, true);
@@ -587,7 +592,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const uint32_t ds = tmem + kColS + 128 * t, dO = tmem + kColO + 128 * t;
     const uint64_t q_desc = kDescK | desc_addr(sbase + t * kQTile), ring_k = kDescK | desc_addr(sbase + kOffRing),
                    ring_v = kDescMN | desc_addr(sbase + kOffRing);
-    const bool leader = elect_one();
     bool ok = true;
     uint32_t j = 0, nload = 0, nq = 0, np = 0, no = 0, nturn = 0;
     // turn k of tile 1 follows turn k of tile 0, which follows turn k - 1 of tile 1
@@ -606,22 +610,20 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (!mbar_wait(&B->k_full[jj & 1], (jj >> 1) & 1, abort_flag, kWaitNs)) return false;
         tc_fence_after();
       }
-      if (leader) {
-        if (sees) {
+      if (sees) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) mma_bf16(ds, q_desc + 2 * kk, b0 + 2 * kk, id_qk, kk > 0);
+        for (int kk = 0; kk < 4; ++kk) mma_bf16(ds, q_desc + 2 * kk, b0 + 2 * kk, id_qk, kk > 0);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) mma_bf16(ds, q_desc + (kBox >> 4) + 2 * kk, b1 + 2 * kk, id_qk, 1);
+        for (int kk = 0; kk < 4; ++kk) mma_bf16(ds, q_desc + (kBox >> 4) + 2 * kk, b1 + 2 * kk, id_qk, 1);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) mma_bf16(ds, q_desc + 2 * (kBox >> 4) + 2 * kk, b2 + 2 * kk, id_qk, 1);
-          mma_commit(&B->s_full[t]);
-          mma_commit(&B->k_empty[jj & 1]);
-          pass_turn();
-          if (last) mma_commit(&B->q_empty[t]);
-        } else {
-          pass_turn();
-          mbar_arrive(&B->k_empty[jj & 1]);
-        }
+        for (int kk = 0; kk < 4; ++kk) mma_bf16(ds, q_desc + 2 * (kBox >> 4) + 2 * kk, b2 + 2 * kk, id_qk, 1);
+        mma_commit(&B->s_full[t]);
+        mma_commit(&B->k_empty[jj & 1]);
+        pass_turn();
+        if (last) mma_commit(&B->q_empty[t]);
+      } else {
+        pass_turn();
+        mbar_arrive(&B->k_empty[jj & 1]);
       }
       return true;
     };
@@ -632,34 +634,23 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       if (tiles_of(it, t, p.pack) == 0) return true;
       if (nload > 0 && !mbar_wait(&B->q_empty[t], (nload - 1) & 1, abort_flag, kWaitNs)) return false;
       ++nload;
-      if (leader) {
-        uint8_t* q = smem + t * kQTile;
-        const int row = it.q_row0 + (128 * t >> p.pack), head = it.head << p.pack;
-        mbar_arrive_expect_tx(&B->q_full[t], kQTile);
-        tma_load_3d(q, &map_qn, 0, head, row, &B->q_full[t]);
-        tma_load_3d(q + kBox, &map_qn, 64, head, row, &B->q_full[t]);
-        tma_load_3d(q + 2 * kBox, &map_qp, 0, head, row, &B->q_full[t]);
-      }
+      uint8_t* q = smem + t * kQTile;
+      const int row = it.q_row0 + (128 * t >> p.pack), head = it.head << p.pack;
+      mbar_arrive_expect_tx(&B->q_full[t], kQTile);
+      tma_load_3d(q, &map_qn, 0, head, row, &B->q_full[t]);
+      tma_load_3d(q + kBox, &map_qn, 64, head, row, &B->q_full[t]);
+      tma_load_3d(q + 2 * kBox, &map_qp, 0, head, row, &B->q_full[t]);
       return true;
     };
     ok = load_q(0);
     for (int n = 0;; ++n) {
-      // Lanes may disagree on a wait that runs out.  They meet here once a unit
-      // (and nowhere else, so that none waits for one that left): a lane that
-      // gave up has raised the abort flag, which ends the others' waits.
-      ok = ok && item_ready(n);
-      if (!ok) fail(B, p.status);
-      if (!__all_sync(0xffffffffu, ok)) {
-        ok = false;
-        break;
-      }
+      if (!(ok = ok && item_ready(n))) break;
       const PromptItem it = load_item(&B->items[n % kItemRing]);
-      __syncwarp();
-      if (leader) mbar_arrive(&B->item_empty[n % kItemRing]);
+      mbar_arrive(&B->item_empty[n % kItemRing]);
       if (it.rows == 0) break;
-      const int mine = __shfl_sync(0xffffffffu, tiles_of(it, t, p.pack), 0);
-      const int nt = __shfl_sync(0xffffffffu, max(mine, tiles_of(it, t ^ 1, p.pack)), 0);
-      const int keys = __shfl_sync(0xffffffffu, it.kv_end - it.kv_begin, 0);
+      const int mine = tiles_of(it, t, p.pack);
+      const int nt = max(mine, tiles_of(it, t ^ 1, p.pack));
+      const int keys = it.kv_end - it.kv_begin;
       if (mine == 0) ok = load_q(n + 1);
       if (nt == 0 || !ok) continue;
       if (mine > 0) {
@@ -673,7 +664,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const uint64_t v0 = ring_v + s0 * (kBox >> 4);
         ok = t == 1 || mbar_wait(&B->v_full[j & 1], (j >> 1) & 1, abort_flag, kWaitNs);
         const int valid = keys - kt * kKeys;
-        if (t == 0 && ok && valid < kKeys && (valid & 15) && leader) {
+        if (t == 0 && ok && valid < kKeys && (valid & 15)) {
           // PV reads whole 16-key steps; the rows of the last tile past its
           // last key meet zero weights but must be finite: they are cleared
           // (for the other warp too, whose turn comes later)
@@ -693,47 +684,42 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (!(ok = ok && take_turn())) break;
         if (kt < mine) {
           const bool whole = valid >= kKeys && s0 != kRing - 1;
-          if (whole && leader) {
+          if (whole) {
 #pragma unroll
             for (int kk = 0; kk < 6; ++kk) mma_f16_tmem_a(dO, ds + 8 * kk, v0 + 128 * kk, id_pv, kk > 0 ? 1 : kt);
           }
           if (!(ok = mbar_wait(&B->p_rest[t], np & 1, abort_flag, kWaitNs))) break;
           ++np;
           tc_fence_after();
-          if (leader) {
-            if (whole) {
+          if (whole) {
 #pragma unroll
-              for (int kk = 6; kk < 8; ++kk) mma_f16_tmem_a(dO, ds + 8 * kk, v0 + 128 * kk, id_pv, 1);
-            } else {
-              const int steps = (min(valid, kKeys) + 15) >> 4;
-              if (s0 != kRing - 1) {
-                for (int kk = 0; kk < steps; ++kk) mma_f16_tmem_a(dO, ds + 8 * kk, v0 + 128 * kk, id_pv, kt | kk);
-              } else {  // the second box wrapped to the ring's start: a product for each
+            for (int kk = 6; kk < 8; ++kk) mma_f16_tmem_a(dO, ds + 8 * kk, v0 + 128 * kk, id_pv, 1);
+          } else {
+            const int steps = (min(valid, kKeys) + 15) >> 4;
+            if (s0 != kRing - 1) {
+              for (int kk = 0; kk < steps; ++kk) mma_f16_tmem_a(dO, ds + 8 * kk, v0 + 128 * kk, id_pv, kt | kk);
+            } else {  // the second box wrapped to the ring's start: a product for each
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk) {
-                  if (kk >= steps) break;
-                  mma_f16_tmem_a(dO, ds + 8 * kk, v0 + 128 * kk, id_pv64, kk > 0 ? 1 : kt);
-                  mma_f16_tmem_a(dO + 64, ds + 8 * kk, ring_v + 128 * kk, id_pv64, kk > 0 ? 1 : kt);
-                }
+              for (int kk = 0; kk < 8; ++kk) {
+                if (kk >= steps) break;
+                mma_f16_tmem_a(dO, ds + 8 * kk, v0 + 128 * kk, id_pv64, kk > 0 ? 1 : kt);
+                mma_f16_tmem_a(dO + 64, ds + 8 * kk, ring_v + 128 * kk, id_pv64, kk > 0 ? 1 : kt);
               }
             }
-            mma_commit(&B->v_empty[j & 1]);
-            if (kt == mine - 1) mma_commit(&B->o_full[t]);
           }
+          mma_commit(&B->v_empty[j & 1]);
+          if (kt == mine - 1) mma_commit(&B->o_full[t]);
           if (kt == mine - 1) ++no;
-        } else if (leader) {
+        } else {
           mbar_arrive(&B->v_empty[j & 1]);
         }
         if (kt + 1 < nt) ok = qk(j + 1, kt + 1 < mine, kt + 2 == mine);
-        else if (leader) pass_turn();
+        else pass_turn();
       }
     }
-    if (leader) {
-      if (!ok) fail(B, p.status);
-      mma_commit(&B->drain[t]);  // every MMA issued completes before teardown
-      mbar_wait(&B->drain[t], 0, abort_flag, kWaitNs);
-    }
-    __syncwarp();
+    if (!ok) fail(B, p.status);
+    mma_commit(&B->drain[t]);  // every MMA issued completes before teardown
+    mbar_wait(&B->drain[t], 0, abort_flag, kWaitNs);
   } else if (warp == 11 && lane == 0) {
     // ------------------------------------------------------------ value copies
     bool ok = true;
@@ -926,6 +912,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     }
     if (!ok) fail(B, p.status);
   }
+  __syncwarp();
   // ---------------------------------------------------------------- teardown
   __syncthreads();
   if (B->abort) {  // copies already issued land before the shared memory is released
