@@ -33,16 +33,16 @@
 // for the MMA (at most 2^-8 relative per weight, averaged over the keys); the
 // sum takes the unrounded fp32 weights.
 //
-// Measured (16,384 tokens, 16 heads: 1.37 TFLOP): 860 us, 1,590 TFLOP/s, 84% of
+// Measured (16,384 tokens, 16 heads: 1.37 TFLOP): 864 us, 1,590 TFLOP/s, 84% of
 // the measured bf16 peak (from 1,582 us).  What each step gave: one MMA warp per
 // query tile instead of one for both 1.58 -> 1.08 ms; turns, one barrier per
 // tile's boxes and PV from the first 96 weights on 0.98; MMA issue as
-// straight-line code on uniform registers 0.90; key and value copies from two
-// warps 0.86.  Short units leave the pipe idle while the next unit's first keys
-// land and its first softmax runs: 24 ragged prompts of 1 to 2,048 tokens run at
-// 130 us (955 TFLOP/s), 14% of it the masked halves of the diagonal tiles.
-// Few rows behind long contexts (26 behind 32,768 and 20,011 keys) take 94 us,
-// 4.6 TB/s: one query tile at work, and a key tile's chain QK, softmax, PV takes
+// straight-line code 0.90; key and value copies from two warps 0.86.  Short units
+// leave the pipe idle while the next unit's first keys land and its first softmax
+// runs: 24 ragged prompts of 1 to 2,048 tokens run at 128 us (970 TFLOP/s), 14%
+// of it the masked halves of the diagonal tiles.
+// Few rows behind long contexts (26 behind 32,768 and 20,011 keys) take 98 us,
+// 4.5 TB/s: one query tile at work, and a key tile's chain QK, softmax, PV takes
 // 2,930 cycles where its copies take 2,800.
 //
 // Warps: 0-3 softmax and epilogue of query tile 0, 4-7 of tile 1, 8 units and
@@ -415,7 +415,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   PromptBarriers* B = reinterpret_cast<PromptBarriers*>(smem + kOffMisc);
   const uint32_t sbase = smem_u32(smem);
-  // uniform in the eyes of the compiler, so that the MMA warps' descriptors live in uniform registers
   const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kItemRing; ++i) {
@@ -482,8 +481,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     // Box i (0-2: K, 3-4: V) of key tile j sits at ring position (5 j + i) % 8,
     // last used by box (5 j + i - 8): K_{j-2} for i = 0, V_{j-2} for i = 1, 2,
     // K_{j-1} for i = 3, 4.  j counts the CTA's key tiles over all its items.
-    // One thread takes about 650 cycles to issue a box, five boxes as long as a
-    // key tile's products, so the values have their own (warp 11).
+    // A thread issues in order and its waits hold back what follows, so the
+    // values have their own (warp 11): 0.90 -> 0.86 ms for 16,384 tokens.
     // Units are published two ahead of their loads' end: the MMA warps fetch
     // their next query tile as soon as the last QK of a unit is done.
     bool ok = true;
