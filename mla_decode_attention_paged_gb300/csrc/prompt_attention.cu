@@ -871,14 +871,17 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
               __syncwarp();
               if (lane == 0) mbar_arrive(&B->o_free[t]);
             }
-            if (live) {
+            if (live && l != 0.f) {
 #pragma unroll
               for (int i = 0; i < 4; ++i)
                 st_global_32(dst + 4 * c + 2 * i, pack_out(&o[i >> 1][16 * (i & 1)], inv),
                              pack_out(&o[i >> 1][16 * (i & 1) + 8], inv));
             }
           }
-        } else if (live) {
+        }
+        // A row without keys: its products are 0 times values that other rows
+        // see, NaN where those are not finite, so they are not stored.
+        if (live && l == 0.f) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) dst[i] = make_uint4(0, 0, 0, 0);
         }

@@ -1,0 +1,61 @@
+"""Edges of the packed-prompt operators: rows that see no key beside values that
+are not finite."""
+import numpy as np
+import pytest
+import torch
+
+import mla_decode_attention_paged_gb300 as mla
+from mla_decode_attention_paged_gb300 import workloads as W
+import packed_reference as R
+
+pytestmark = pytest.mark.gpu
+
+SCALE = 1.0 / np.sqrt(192.0)
+NAMES = ("q_nope", "q_pe", "k_nope", "k_pe", "v")
+
+
+def _cu(lens):
+    return torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32).cuda()
+
+
+def _prompt(q_lens, k_lens, H=16, kv=16, seed=0, extra_q=0):
+    """Random inputs; ``extra_q`` query rows of no sequence behind the last."""
+    g = W.generator(seed + sum(q_lens) + sum(k_lens) + H)
+    nq, nk = sum(q_lens) + extra_q, sum(k_lens)
+    return dict(q_nope=W.draw_bf16((nq, H, 128), 1.5, g), q_pe=W.draw_bf16((nq, H, 64), 1.5, g),
+                k_nope=W.draw_bf16((nk, kv, 128), 1.0, g), k_pe=W.draw_bf16((nk, 64), 1.0, g),
+                v=W.draw_bf16((nk, kv, 128), 1.0, g), q_lens=list(q_lens), k_lens=list(k_lens), H=H)
+
+
+def _attend(x):
+    """(out, lse, the workspace's first five words): status, then, where a plan
+    ran, its items, the units taken, the split blocks and their rows (else -1)."""
+    d = mla.dims(x["H"], 64)
+    ws = torch.full((mla.prompt_attention_workspace_size(d, len(x["q_lens"]), x["q_nope"].shape[0]),), 255,
+                    dtype=torch.uint8, device="cuda")
+    out, lse = mla.prompt_attention(d, *(x[n].cuda() for n in NAMES), _cu(x["q_lens"]), _cu(x["k_lens"]), SCALE,
+                                    workspace=ws)
+    torch.cuda.synchronize()
+    return out, lse, ws[:20].view(torch.int32).tolist()
+
+
+# ----- rows that see no key ---------------------------------------------------------
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("H,kv,q_lens,k_lens", [
+    (16, 16, (300,), (100,)),            # the blocks listed without a plan
+    (16, 1, (296,), (100,)),             # 16 heads of a token in the rows
+    (16, 16, (300, 1), (100, 3000)),     # planned, beside a block whose keys are split
+    (16, 16, (300, 4000), (100, 4000)),  # planned, whole blocks
+])
+def test_rows_without_keys_beside_bad_values(cuda_lib, H, kv, q_lens, k_lens, bad):
+    """A row that sees no key gives 0 and -inf, whatever the values that other
+    rows of its tile see hold."""
+    x = _prompt(q_lens, k_lens, H=H, kv=kv, seed=1)
+    out0, lse0, _ = _attend(x)
+    none = q_lens[0] - k_lens[0]  # rows of the first sequence that see no key
+    x["v"][3] = bad  # query none + 3 is the first to see it, and its tile has rows that see nothing
+    out, lse, words = _attend(x)
+    assert words[0] == mla.MLA_OK
+    assert torch.all(out[:none] == 0) and torch.all(torch.isneginf(lse[:none]))
+    assert not torch.isfinite(out[none + 3:q_lens[0]]).any()
+    assert torch.equal(out[q_lens[0]:], out0[q_lens[0]:]) and torch.equal(lse, lse0)
