@@ -396,8 +396,9 @@ def _new(shape, dtype, dev: torch.device, stream) -> torch.Tensor:
     again there while the call runs."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=dev)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_stream(stream), device=dev)
+    if not isinstance(stream, torch.cuda.Stream):  # handle 0 is the default stream: ExternalStream(0) is another
+        handle = _stream(stream)
+        stream = torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=dev)
 

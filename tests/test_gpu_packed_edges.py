@@ -1,5 +1,5 @@
 """Edges of the packed-prompt operators: rows that see no key beside values that
-are not finite."""
+are not finite, and default-stream handles."""
 import numpy as np
 import pytest
 import torch
@@ -59,3 +59,24 @@ def test_rows_without_keys_beside_bad_values(cuda_lib, H, kv, q_lens, k_lens, ba
     assert torch.all(out[:none] == 0) and torch.all(torch.isneginf(lse[:none]))
     assert not torch.isfinite(out[none + 3:q_lens[0]]).any()
     assert torch.equal(out[q_lens[0]:], out0[q_lens[0]:]) and torch.equal(lse, lse0)
+
+
+# ----- streams --------------------------------------------------------------------------
+def _stream_of(t):
+    """Handle of the stream whose memory the allocator took a tensor from."""
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+    raise AssertionError("not the allocator's")
+
+
+def test_default_stream_by_handle(cuda_lib):
+    """Handle 0 is the default stream: what the binding allocates for such a call
+    is that stream's memory, also while another stream is current."""
+    g = W.generator(5)
+    c, w = W.draw_bf16((40, 512), 1.0, g).cuda(), W.draw_bf16((16, 128, 512), 0.02, g).cuda()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        k, v = mla.expand_kv(mla.dims(16, 64), c, w, w, stream=0)
+    torch.cuda.synchronize()
+    assert _stream_of(k) == 0 and _stream_of(v) == 0
