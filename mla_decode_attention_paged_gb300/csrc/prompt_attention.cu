@@ -77,6 +77,7 @@ constexpr int kPlanThreads = 1024, kFewPlan = 128;
 constexpr int kPlanSeqs = 1024;                    // sequences whose offsets the plan holds in shared memory
 constexpr float kMergeTiles = 5.f;                 // the merge, in key tiles' time
 constexpr int kMinSplit = 10;                      // key tiles of a block that is never split
+constexpr int kDirectTiles = 18;                   // key tiles of a call that one round of units runs without a plan
 constexpr int kBuckets = kPlanThreads;             // cost classes of the plan's counting sort
 static_assert(kSmem <= 232448, "dynamic shared memory of one CTA");
 
@@ -1024,12 +1025,17 @@ cudaError_t launch_prompt_attention(PromptParams p, cudaStream_t stream) {
   const unsigned grid = unsigned(most < p.sm_count ? most : p.sm_count);
   // No plan where it would cost more than it can save: two rounds of units at
   // most with no block long enough to split, or one round that fills more than
-  // two thirds of the SMs (half a unit more to each SM would be a second round).
-  // 93 tokens at 16 heads: 11 us without, 12.7 with one; 2,048 tokens: 35 and
-  // 41 us.
+  // two thirds of the SMs (half a unit more to each SM would be a second round)
+  // over few keys.  93 tokens at 16 heads: 11 us without, 12.7 with one; 2,048
+  // tokens: 34 and 39 us.  The bound on the keys (the rows of nine blocks, so that
+  // one prompt without a history stays below it) is there because the lengths
+  // are on the device, and one sequence may hold most keys.  Eight single tokens
+  // at 16 heads, contexts equal and all but one of 16 keys: 2,304 keys take 11
+  // and 33 us without a plan, 16 and 21 with one; 8,192 keys 19 and 101, 24 and 30.
   const long long whole = blocks * p.heads_v;
-  if (p.num_seqs <= kDirectSeqs && ((whole <= 2 * p.sm_count && p.n_k <= kMinSplit * kKeys) ||
-                           (whole <= p.sm_count && 3 * whole > 2 * p.sm_count)))
+  if (p.num_seqs <= kDirectSeqs &&
+      ((whole <= 2 * p.sm_count && p.n_k <= kMinSplit * kKeys) ||
+       (whole <= p.sm_count && 3 * whole > 2 * p.sm_count && p.n_k <= kDirectTiles * kKeys)))
     return launch_pdl(prompt_attention_kernel<true>, dim3(grid), dim3(kPromptThreads), kSmem, stream, 1, qn, qp, kn, kp,
                       v, p);
   // Splitting keys is for calls whose query rows make two rounds at most, and

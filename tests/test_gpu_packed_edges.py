@@ -1,5 +1,5 @@
 """Edges of the packed-prompt operators: rows that see no key beside values that
-are not finite, and default-stream handles."""
+are not finite, long contexts among short ones, and default-stream handles."""
 import numpy as np
 import pytest
 import torch
@@ -59,6 +59,34 @@ def test_rows_without_keys_beside_bad_values(cuda_lib, H, kv, q_lens, k_lens, ba
     assert torch.all(out[:none] == 0) and torch.all(torch.isneginf(lse[:none]))
     assert not torch.isfinite(out[none + 3:q_lens[0]]).any()
     assert torch.equal(out[q_lens[0]:], out0[q_lens[0]:]) and torch.equal(lse, lse0)
+
+
+# ----- one long context among short ones ---------------------------------------------
+def _close(x, out, lse):
+    n = sum(x["q_lens"])
+    ref, lref, tol, ltol = R.attention(*(x[k] for k in NAMES), x["q_lens"], x["k_lens"], SCALE)
+    assert R.worst(out[:n].cpu(), ref, tol) <= 1.0 and R.worst(lse[:n].cpu(), lref, ltol) <= 1.0
+
+
+@pytest.mark.parametrize("H,kv,n", [(16, 16, 7), (16, 16, 8), (16, 16, 9), (128, 8, 13), (128, 8, 19), (32, 32, 4)])
+def test_long_context_among_short_is_split(cuda_lib, H, kv, n):
+    """Single tokens whose units fill most of one round of SMs, one of them
+    behind a long context: its keys are spread over the SMs."""
+    k_lens = [100 + i for i in range(n)]
+    k_lens[n // 2] = 20000
+    x = _prompt([1] * n, k_lens, H=H, kv=kv, seed=3)
+    out, lse, words = _attend(x)
+    assert words[0] == mla.MLA_OK
+    assert words[3] >= 1  # split blocks
+    _close(x, out, lse)
+
+
+def test_long_context_of_a_padded_batch_is_split(cuda_lib):
+    """Query rows of no sequence do not hide that the few others stand behind a long context."""
+    x = _prompt((5,), (20000,), seed=4, extra_q=2043)
+    out, lse, words = _attend(x)
+    assert words[0] == mla.MLA_OK and words[3] >= 1
+    _close(x, out, lse)
 
 
 # ----- streams --------------------------------------------------------------------------
