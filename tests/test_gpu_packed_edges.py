@@ -1,5 +1,6 @@
 """Edges of the packed-prompt operators: rows that see no key beside values that
-are not finite, long contexts among short ones, and default-stream handles."""
+are not finite, long contexts among short ones, the expansion on both sides of
+its change of form, and default-stream handles."""
 import numpy as np
 import pytest
 import torch
@@ -87,6 +88,42 @@ def test_long_context_of_a_padded_batch_is_split(cuda_lib):
     out, lse, words = _attend(x)
     assert words[0] == mla.MLA_OK and words[3] >= 1
     _close(x, out, lse)
+
+
+# ----- the expansion on both sides of its change of form ------------------------------
+def _worst_expand(got, c, w):
+    """Largest error in units of its bound, all rows, in 64 bits on the GPU."""
+    bad = 0.0
+    wd, wa = w.double().flatten(0, 1).T, w.double().abs().flatten(0, 1).T
+    for i in range(0, len(c), 4096):
+        cd = c[i:i + 4096].double()
+        ref, mag = cd @ wd, cd.abs() @ wa
+        r = (got[i:i + 4096].double().flatten(1) - ref).abs() / (R.BF16 * ref.abs() + 512 * R.SUM * mag)
+        bad = max(bad, float(torch.nan_to_num(r, nan=float("inf")).max()))
+    return bad
+
+
+@pytest.mark.parametrize("n,H", [
+    (4096, 16), (4097, 16),      # weights resident up to 256 rows to a head, latents from there on
+    (5003, 16), (34893, 16),     # an odd end; several resident tiles to a pair of SMs
+    (8193, 32), (16461, 64), (32769, 128),
+])
+def test_expand_both_forms(cuda_lib, n, H):
+    g = W.generator(n + H)
+    c = W.draw_bf16((n, 512), 1.0, g).cuda()
+    uk, uv = W.draw_bf16((H, 128, 512), 0.02, g).cuda(), W.draw_bf16((H, 128, 512), 0.02, g).cuda()
+    d = mla.dims(H, 64)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    k_out = torch.full((n + 1, H, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    v_out = torch.full((n + 1, H, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    k, v = mla.expand_kv(d, c, uk, uv, k_nope=k_out[:n], v=v_out[:n], device_status=status)
+    assert mla.read_status_word(status) == mla.MLA_OK
+    assert _worst_expand(k, c, uk) <= 1.0 and _worst_expand(v, c, uv) <= 1.0
+    assert torch.all(k_out[n] == 7.0) and torch.all(v_out[n] == 7.0)
+    step = 200 * H + 7  # the same rows in calls with the weights resident: the same sums in the same order
+    for i in range(0, n, step):
+        k1, v1 = mla.expand_kv(d, c[i:i + step], uk, uv)
+        assert torch.equal(k[i:i + step], k1) and torch.equal(v[i:i + step], v1)
 
 
 # ----- streams --------------------------------------------------------------------------
