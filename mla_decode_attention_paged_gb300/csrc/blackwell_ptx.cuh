@@ -82,6 +82,15 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const 
   return mbar_try_wait(bar, parity) || mbar_wait_spin(bar, parity, abort, limit_ns);
 }
 
+// Waits for a phase until `end_ns`, whatever the abort flag says: for what a CTA
+// that gives up still has in flight.
+__device__ __forceinline__ bool mbar_wait_until(uint64_t* bar, uint32_t parity, uint64_t end_ns) {
+  do {
+    if (mbar_try_wait(bar, parity)) return true;
+  } while (global_timer_ns() < end_ns);
+  return false;
+}
+
 // ----- thread-block clusters ------------------------------------------------------
 __device__ __forceinline__ uint32_t cluster_ctarank() {
   uint32_t r;

@@ -23,7 +23,9 @@
 //
 // Warps: 0 TMA producer, 1 tensor memory and (in the leading CTA) MMA issue,
 // 2-5 epilogue.  Every wait is bounded: on timeout the CTA records
-// MLA_ERR_DEVICE_TIMEOUT, drains, frees its tensor memory and returns.
+// MLA_ERR_DEVICE_TIMEOUT and the pair ends together: once neither CTA issues any
+// more, their MMAs and copies in flight are waited for on their own barriers
+// (half a second at most), then tensor memory is freed.
 #include <atomic>
 
 #include "blackwell_ptx.cuh"
@@ -42,7 +44,8 @@ constexpr uint32_t kBox = 128 * 128;                  // [128 rows x 64 columns]
 constexpr uint32_t kOffRing = kKBlocks * kBox;        // after the resident operand
 constexpr uint32_t kOffMisc = kOffRing + kStages * kBox;
 constexpr uint32_t kSmem = kOffMisc + 256 + 1024;
-constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr uint64_t kWaitNs = 2000000000ull;           // 2 s
+constexpr uint64_t kDrainNs = 500000000ull;           // 0.5 s
 static_assert(kSmem <= 232448, "dynamic shared memory of one CTA");
 
 struct ExpandBarriers {
@@ -53,8 +56,11 @@ struct ExpandBarriers {
   uint64_t acc_empty[2];      // leading CTA: read by both CTAs' epilogues
   uint64_t drain;
   uint32_t tmem_base;
-  int abort;
+  int abort;                     // this CTA gave up
+  int pair_abort;                // a CTA of the pair did
+  uint32_t boxes[2], blocks[2];  // leading CTA: streamed boxes and resident blocks that each producer issued copies of
 };
+static_assert(sizeof(ExpandBarriers) <= 256, "shared memory behind the ring");
 
 __device__ __forceinline__ void fail(ExpandBarriers* B, int* status) {
   B->abort = 1;
@@ -103,6 +109,9 @@ __device__ __forceinline__ void tma2_load_2d(void* dst, const CUtensorMap* map, 
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+__device__ __forceinline__ void store_cluster(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 // kRowsResident: latents resident, weights streamed; else the other way round.
 template <bool kRowsResident>
 __global__ void __launch_bounds__(kExpThreads, 1)
@@ -126,7 +135,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
       mbar_init(&B->acc_empty[i], 8);  // one lane of each epilogue warp of both CTAs
     }
     mbar_init(&B->drain, 1);
-    B->abort = 0;
+    B->abort = B->pair_abort = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -176,6 +185,8 @@ __global__ void __launch_bounds__(kExpThreads, 1)
       }
     }
     if (!ok) fail(B, p.status);
+    store_cluster(mapa_shared(smem_u32(&B->boxes[rank]), 0), k);
+    store_cluster(mapa_shared(smem_u32(&B->blocks[rank]), 0), nr);
   } else if (warp == 1 && rank == 0) {
     // ------------------------------------------------------------ MMA issue
     constexpr uint32_t idesc = idesc_bf16_f32(256, 256, false, false);
@@ -269,15 +280,31 @@ __global__ void __launch_bounds__(kExpThreads, 1)
   }
   // ---------------------------------------------------------------- teardown
   __syncthreads();
-  if (warp == 1) mbar_wait(&B->drain, 0, abort_flag, kWaitNs);  // both CTAs: the commits arrive in both
-  if (B->abort) {  // copies already issued land before the shared memory is released
-    const uint64_t t0 = global_timer_ns();
-    while (global_timer_ns() - t0 < 20000) {
-    }
+  if (warp == 1) {  // both CTAs: the commits arrive in both
+    if (!mbar_wait(&B->drain, 0, abort_flag, kWaitNs)) fail(B, p.status);
+    __syncwarp();
+    if (lane < 2 && B->abort) store_cluster(mapa_shared(smem_u32(&B->pair_abort), lane), 1);
+    __syncwarp();
   }
   tc_fence_before();
-  cluster_sync();  // the peer's copies, MMAs and arrivals into this CTA are done
+  cluster_sync();  // the peer issues no more copies, MMAs and arrivals into this CTA; without an abort all are done
   tc_fence_after();
+  if (B->pair_abort) {
+    if (threadIdx.x == 0) {
+      const uint64_t end = global_timer_ns() + kDrainNs;
+      mbar_wait_until(&B->drain, 0, end);
+      if (rank == 0) {  // the last phase of each barrier that either CTA's copies count on; not to be met where only one issued them
+        for (uint32_t s = 0; s < kStages; ++s) {
+          const uint32_t k = max(B->boxes[0], B->boxes[1]), phases = (k + kStages - 1 - s) / kStages;
+          if (phases > 0) mbar_wait_until(&B->full[s], (phases - 1) & 1, end);
+        }
+        const uint32_t blocks = max(B->blocks[0], B->blocks[1]);
+        if (blocks > 0) mbar_wait_until(&B->res_full, (blocks - 1) & 1, end);
+      }
+    }
+    __syncwarp();
+    cluster_sync();
+  }
   if (warp == 1) tmem_dealloc2(tmem, 512);
 }
 

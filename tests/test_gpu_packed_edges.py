@@ -1,6 +1,8 @@
 """Edges of the packed-prompt operators: rows that see no key beside values that
 are not finite, long contexts among short ones, the expansion on both sides of
-its change of form, and default-stream handles."""
+its change of form, default-stream handles, and waits that run out."""
+import time
+
 import numpy as np
 import pytest
 import torch
@@ -145,3 +147,36 @@ def test_default_stream_by_handle(cuda_lib):
         k, v = mla.expand_kv(mla.dims(16, 64), c, w, w, stream=0)
     torch.cuda.synchronize()
     assert _stream_of(k) == 0 and _stream_of(v) == 0
+
+
+# ----- waits that run out -------------------------------------------------------------
+class _Injected:
+    """A copy that never completes in every call inside: waits run out after 2 s, and
+    what is in flight is waited for half a second more."""
+
+    def __enter__(self):
+        torch.cuda.synchronize()
+        mla.test_inject_wait_timeout(True)
+        self.t0 = time.monotonic()
+
+    def __exit__(self, *exc):
+        mla.test_inject_wait_timeout(False)
+        torch.cuda.synchronize()
+        self.seconds = time.monotonic() - self.t0
+
+
+@pytest.mark.parametrize("n,H", [(300, 16), (5003, 16), (40, 128)])  # either form; fewer units than pairs and more
+def test_expand_waits_for_what_is_in_flight(cuda_lib, n, H):
+    g = W.generator(n)
+    c = W.draw_bf16((n, 512), 1.0, g).cuda()
+    uk, uv = W.draw_bf16((H, 128, 512), 0.02, g).cuda(), W.draw_bf16((H, 128, 512), 0.02, g).cuda()
+    d = mla.dims(H, 64)
+    k0, v0 = mla.expand_kv(d, c, uk, uv)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    run = _Injected()
+    with run:
+        mla.expand_kv(d, c, uk, uv, device_status=status)
+    assert run.seconds >= 2.45
+    assert mla.read_status_word(status) == mla.MLA_ERR_DEVICE_TIMEOUT
+    k, v = mla.expand_kv(d, c, uk, uv)
+    assert torch.equal(k, k0) and torch.equal(v, v0)
