@@ -48,8 +48,9 @@
 // Warps: 0-3 softmax and epilogue of query tile 0, 4-7 of tile 1, 8 units and
 // key copies, 9 (which also owns tensor memory) and 10 query copies and MMA
 // issue for tiles 0 and 1, 11 value copies.  Every wait is bounded: on timeout
-// the CTA records MLA_ERR_DEVICE_TIMEOUT, drains, frees its tensor memory and
-// returns.
+// the CTA records MLA_ERR_DEVICE_TIMEOUT, waits for its products and copies in
+// flight on their own barriers (half a second at most), frees its tensor memory
+// and returns.
 #include <atomic>
 
 #include "blackwell_ptx.cuh"
@@ -72,6 +73,7 @@ constexpr uint32_t kSmem = kOffMisc + 2048 + 1024;  // + barriers, alignment sla
 constexpr int kPromptThreads = 384;
 constexpr uint32_t kColS = 0, kColO = 256;         // tensor memory columns: S x2, O x2
 constexpr uint64_t kWaitNs = 2000000000ull;        // 2 s
+constexpr uint64_t kDrainNs = 500000000ull;        // 0.5 s
 constexpr float kRescale = 8.f;                    // log2 units
 constexpr int kPlanThreads = 1024, kFewPlan = 128;
 constexpr int kPlanSeqs = 1024;                    // sequences whose offsets the plan holds in shared memory
@@ -326,6 +328,7 @@ struct PromptBarriers {
   int seq_end[kDirectSeqs];
   uint32_t tmem_base;
   int abort;
+  uint32_t k_tiles, v_tiles, q_tiles[2];  // key, value and query tiles that copies were issued of
 };
 static_assert(sizeof(PromptBarriers) <= 2048, "shared memory behind the ring");
 
@@ -550,7 +553,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (j >= 2 && !(ok = mbar_wait(&B->k_empty[j & 1], ((j - 2) >> 1) & 1, abort_flag, kWaitNs))) break;
         mbar_arrive_expect_tx(bar, 3 * kBox + (p.inject_wait_timeout && j == 0 ? 16 : 0));
         tma_load_3d(smem + kOffRing + (5 * j % kRing) * kBox, &map_kn, 0, g, key, bar);
-        if (j >= 2 && !(ok = mbar_wait(&B->v_empty[j & 1], ((j - 2) >> 1) & 1, abort_flag, kWaitNs))) break;
+        if (j >= 2 && !(ok = mbar_wait(&B->v_empty[j & 1], ((j - 2) >> 1) & 1, abort_flag, kWaitNs))) {
+          ++j;  // one of its boxes is on its way
+          break;
+        }
         tma_load_3d(smem + kOffRing + ((5 * j + 1) % kRing) * kBox, &map_kn, 64, g, key, bar);
         tma_load_2d(smem + kOffRing + ((5 * j + 2) % kRing) * kBox, &map_kp, 0, key, bar);
         if (!fetched) {
@@ -560,6 +566,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       }
       if (!fetched) after = fetch(u_after);
     }
+    B->k_tiles = j;
     if (!ok) fail(B, p.status);
   } else if ((warp == 9 || warp == 10) && elect_one()) {
     // ------------------------------------------------------------ MMA issue
@@ -717,9 +724,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         else pass_turn();
       }
     }
+    B->q_tiles[t] = nload;
     if (!ok) fail(B, p.status);
     mma_commit(&B->drain[t]);  // every MMA issued completes before teardown
-    mbar_wait(&B->drain[t], 0, abort_flag, kWaitNs);
+    if (!mbar_wait(&B->drain[t], 0, abort_flag, kWaitNs)) fail(B, p.status);
   } else if (warp == 11 && lane == 0) {
     // ------------------------------------------------------------ value copies
     bool ok = true;
@@ -740,6 +748,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         tma_load_3d(smem + kOffRing + ((5 * j + 4) % kRing) * kBox, &map_v, 64, g, key, bar);
       }
     }
+    B->v_tiles = j;
     if (!ok) fail(B, p.status);
   } else if (warp < 8) {
     // ------------------------------------------------------------ softmax, epilogue
@@ -918,10 +927,21 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   __syncwarp();
   // ---------------------------------------------------------------- teardown
   __syncthreads();
-  if (B->abort) {  // copies already issued land before the shared memory is released
-    const uint64_t t0 = global_timer_ns();
-    while (global_timer_ns() - t0 < 20000) {
+  if (B->abort) {  // products complete, and copies land, before tensor and shared memory are released
+    if (threadIdx.x == 0) {
+      const uint64_t end = global_timer_ns() + kDrainNs;
+      // The last phase of a barrier; the phases before are complete, or it would not have begun.
+      auto last = [&](uint64_t* bar, uint32_t phases) {
+        if (phases > 0) mbar_wait_until(bar, (phases - 1) & 1, end);
+      };
+      for (uint32_t i = 0; i < 2; ++i) {
+        last(&B->drain[i], 1);
+        last(&B->q_full[i], B->q_tiles[i]);
+        last(&B->k_full[i], (B->k_tiles + 1 - i) / 2);
+        last(&B->v_full[i], (B->v_tiles + 1 - i) / 2);
+      }
     }
+    __syncthreads();
   }
   tc_fence_after();
   if (warp == 9) tmem_dealloc(tmem, 512);

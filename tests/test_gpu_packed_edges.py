@@ -180,3 +180,21 @@ def test_expand_waits_for_what_is_in_flight(cuda_lib, n, H):
     assert mla.read_status_word(status) == mla.MLA_ERR_DEVICE_TIMEOUT
     k, v = mla.expand_kv(d, c, uk, uv)
     assert torch.equal(k, k0) and torch.equal(v, v0)
+
+
+@pytest.mark.parametrize("q_lens,k_lens", [
+    ((93,), (93,)),              # no plan
+    ((300, 2), (300, 3000)),     # planned, split
+    ((3000,), (3000,)),          # planned, whole blocks
+])
+def test_prompt_waits_for_what_is_in_flight(cuda_lib, q_lens, k_lens):
+    x = {k: v.cuda() if torch.is_tensor(v) else v for k, v in _prompt(q_lens, k_lens, seed=6).items()}
+    out0, lse0, words = _attend(x)
+    assert words[0] == mla.MLA_OK
+    run = _Injected()
+    with run:
+        _, _, words = _attend(x)
+    assert run.seconds >= 2.45
+    assert words[0] == mla.MLA_ERR_DEVICE_TIMEOUT
+    out, lse, words = _attend(x)
+    assert words[0] == mla.MLA_OK and torch.equal(out, out0) and torch.equal(lse, lse0)
