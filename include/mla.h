@@ -395,7 +395,9 @@ size_t mla_prompt_attention_workspace_size(const mla_dims* dims, int32_t num_seq
  * none if that is negative.  For head h with g = h / (H / num_kv_heads):
  *   s_j = softmax_scale * (q_nope[i][h] . k_nope[j][g] + q_pe[i][h] . k_pe[j])
  *   out[i][h] = sum_j softmax(s)_j v[j][g],  lse[i][h] = ln sum_j exp(s_j)
- * A query that sees no key gets out = 0 and lse = -inf.
+ * A query that sees no key, or only scores of minus infinity, gets out = 0 and
+ * lse = -inf.  Scores, maximum and sum are fp32; a weight is rounded to bf16 for
+ * its product with the value, and these are accumulated in fp32.
  *
  *   q_nope      bf16 [n_q, H, 128];  q_pe bf16 [n_q, H, 64], rotated
  *   k_nope      bf16 [n_k, num_kv_heads, 128];  k_pe bf16 [n_k, 64], rotated,
@@ -419,6 +421,13 @@ size_t mla_prompt_attention_workspace_size(const mla_dims* dims, int32_t num_seq
  * inputs are 16-byte aligned, out 32-byte aligned.
  * Results are bit-identical between runs; calls sharing one workspace must not
  * overlap on the device.  dims' page_size and cache_dtype are not used.
+ *
+ * The keys of a long block of query rows are cut into pieces, and spread over the
+ * SMs, only as long as all pieces times the heads (fewer where heads share rows)
+ * are at most twice the SMs: with 16 key/value heads on 152 SMs, batches of 19
+ * sequences and more are not cut.  A long context among short ones then takes
+ * one SM to a head: one token behind 100,000 keys beside 18 behind 1,000 takes
+ * 1.2 ms, beside seven 0.22 ms; such a sequence is better run in a call of its own.
  */
 int mla_prompt_attention(const mla_dims* dims, const void* q_nope, const void* q_pe, int32_t n_q, const void* k_nope,
                          const void* k_pe, const void* v, int32_t n_k, int32_t num_kv_heads, const int32_t* cu_q,
@@ -496,7 +505,9 @@ int mla_set_timing_events(mla_event_t start, mla_event_t stop);
  * limit (about 2 s), and the kernel records MLA_ERR_DEVICE_TIMEOUT in the
  * workspace status word, releases its resources and returns; the device and
  * the context stay usable.  mla_expand_kv (its first weight or latent copy) and
- * mla_prompt_attention (its first key tile) take part the same way.  Nothing faults, traps or hangs.  Process-wide; 0
+ * mla_prompt_attention (its first key tile) take part the same way; a CTA of
+ * theirs that gives up waits for its copies in flight, here until that wait's
+ * own limit of half a second.  Nothing faults, traps or hangs.  Process-wide; 0
  * (the default) disables it.  Returns MLA_OK. */
 int mla_test_inject_wait_timeout(int32_t enable);
 

@@ -64,6 +64,19 @@ def test_rows_without_keys_beside_bad_values(cuda_lib, H, kv, q_lens, k_lens, ba
     assert torch.equal(out[q_lens[0]:], out0[q_lens[0]:]) and torch.equal(lse, lse0)
 
 
+def test_scores_of_minus_infinity(cuda_lib):
+    """A row whose visible scores are all -inf has no weight to give: 0 and -inf, as a row that sees no key."""
+    x = _prompt((200, 2), (200, 3000), seed=2)
+    x["q_nope"][..., 0] = 1.0
+    x["k_nope"][:70, 5, 0] = float("-inf")        # one head: rows 0 .. 69 see nothing else
+    x["k_nope"][200:, 7, 0] = float("-inf")       # all keys of the second sequence, which are split
+    out, lse, words = _attend(x)
+    assert words[0] == mla.MLA_OK and words[3] > 0
+    for rows, h in ((slice(0, 70), 5), (slice(200, 202), 7)):
+        assert torch.all(out[rows, h] == 0) and torch.all(torch.isneginf(lse[rows, h]))
+    assert torch.isfinite(out).all() and torch.isfinite(lse[70:200, 5]).all()
+
+
 # ----- one long context among short ones ---------------------------------------------
 def _close(x, out, lse):
     n = sum(x["q_lens"])
