@@ -30,8 +30,10 @@
 // Softmax: one thread per query row, online in fp32 and base 2.  The running
 // maximum only has to bound the scores within 8 (log2 units); a tile that
 // breaks the bound raises it and rescales O and the sum.  P is rounded to bf16
-// for the MMA (at most 2^-8 relative per weight, averaged over the keys); the
-// sum takes the unrounded fp32 weights.
+// for the MMA, whose operands have one type (at most 2^-8 relative per weight,
+// averaged over the keys: 0.0017 off the formula as a 2-norm over 93 and 16,384
+// tokens alike, 0.0016 and 0.0017 with fp32 weights, most of it the output's own
+// rounding); the sum takes the unrounded fp32 weights.
 //
 // Measured (16,384 tokens, 16 heads: 1.37 TFLOP): 864 us, 1,590 TFLOP/s, 84% of
 // the measured bf16 peak (from 1,582 us).  What each step gave: one MMA warp per
@@ -41,7 +43,7 @@
 // leave the pipe idle while the next unit's first keys land and its first softmax
 // runs: 24 ragged prompts of 1 to 2,048 tokens run at 128 us (970 TFLOP/s), 14%
 // of it the masked halves of the diagonal tiles.
-// Few rows behind long contexts (26 behind 32,768 and 20,011 keys) take 98 us,
+// Few rows behind long contexts (26 behind 32,768 and 20,011 keys) take 97 us,
 // 4.5 TB/s: one query tile at work, and a key tile's chain QK, softmax, PV takes
 // 2,930 cycles where its copies take 2,800.
 //
@@ -205,8 +207,11 @@ __global__ void __launch_bounds__(kThreads) prompt_plan_kernel(PromptParams p) {
   auto block_item = [&](int i, int b) {
     return make_item(p, cu_q[b], cu_q[b + 1], cu_k[b], cu_k[b + 1], i - block_start[b]);
   };
-  // more units than two rounds are never split, nor are short blocks: a piece
-  // would be little more than its start and merge
+  // short blocks are never split: a piece would be little more than its start and
+  // merge.  Nor are more units than two rounds, where equal lengths fill the SMs
+  // (24 single tokens behind 5,000 keys each at 16 heads: 204 us), at the cost
+  // of unequal ones: one behind 100,000 keys beside 19 behind 1,000 takes 1,200 us,
+  // beside nine, where it is split, 264.
   const int G = p.sm_count;
   if (kFew || (p.may_split && (long long)n * p.heads_v <= 2 * G && n <= kPromptMaxSplit)) {
     PromptItem it;
