@@ -65,10 +65,26 @@ typedef enum {
   MLA_CACHE_BF16 = 0,  /* cache rows are 576 bf16 values                                   */
   MLA_CACHE_INT8 = 1,  /* cache rows are 576 int8 codes plus fp32 (scale, zero point) per
                           row; value = scale * (code - zero_point)                          */
-  MLA_CACHE_FP8 = 2    /* cache rows are 576 FP8 E4M3 codes (1 sign, 4 exponent bits with
+  MLA_CACHE_FP8 = 2,   /* cache rows are 576 FP8 E4M3 codes (1 sign, 4 exponent bits with
                           bias 7, 3 mantissa bits; no infinities; 0x7F/0xFF are NaN) plus
                           one fp32 scale per row; value = scale * e4m3(code)                */
+  MLA_CACHE_FP4 = 4    /* cache rows are MLA_FP4_ROW_BYTES bytes: 576 FP4 E2M1 codes (1 sign,
+                          2 exponent bits with bias 1, 1 mantissa bit) and a power-of-two
+                          scale for every 32 of them; value = 2^(scale byte - 127) *
+                          e2m1(code)                                                        */
 } mla_cache_dtype;
+
+/* Row of an MLA_CACHE_FP4 cache (the elements and scales of the Open Compute
+ * Project's "Microscaling Formats", MXFP4):
+ *   bytes 0 .. 287    72 little-endian 32-bit words of 8 codes.  For i in 0 .. 3,
+ *                     value 8w + i of word w has its magnitude's code in bits
+ *                     4i .. 4i + 2 and its sign in bit 8i + 7; value 8w + 4 + i
+ *                     has them in bits 16 + 4i .. 16 + 4i + 2 and bit 8i + 3.
+ *                     Magnitudes of the codes 0 .. 7: 0, 0.5, 1, 1.5, 2, 3, 4, 6.
+ *   bytes 288 .. 305  scale bytes: byte 288 + j holds e + 127 for the scale 2^e
+ *                     of values 32j .. 32j + 31; 255 makes all of them NaN
+ *   bytes 306 .. 319  written as zero, not read                                 */
+#define MLA_FP4_ROW_BYTES 320
 
 /* Model dimensions.  This library implements kv_lora_rank = 512, rope_dim = 64,
  * qk_nope_dim = 128, v_head_dim = 128 (the DeepSeek-V2/V3 shapes of "Seven
@@ -108,11 +124,16 @@ int mla_check_dims(const mla_dims* dims);
  * all in IEEE fp32 round-to-nearest-even, and store (s, zp).  FP8 caches
  * take a = max |x|, s = a/448 (1 if 0) and code = the E4M3 value nearest
  * to x/s (ties to the even mantissa, magnitudes past 448 saturate, the sign
- * of zero kept), in IEEE fp32 round-to-nearest-even, and store s.
+ * of zero kept), in IEEE fp32 round-to-nearest-even, and store s.  FP4 caches
+ * take, for every 32 values, a = max |x|, the smallest power of two s >= 2^-127
+ * with a <= 6 s (byte 0 for a = 0) and code = the E2M1 value nearest to x/s (ties
+ * to the even code, the sign of zero kept): off by at most s, and by at most s/4
+ * below 2 s.  A block with an infinity or a NaN gets byte 255 and codes of 0.
  *
- *   cache            bf16, int8 or E4M3 (uint8) [num_pages, P, 576]
+ *   cache            bf16, int8 or E4M3 (uint8) [num_pages, P, 576], or FP4 rows
+ *                    [num_pages, P, MLA_FP4_ROW_BYTES bytes]
  *   cache_scale_zero fp32 [num_pages, P, 2] (INT8), fp32 [num_pages, P] (FP8),
- *                    NULL for bf16
+ *                    NULL for bf16 and FP4
  *   block_table      int32 [num_seqs, max_pages_per_seq]
  *   seq_ids, positions  int32 [n_tokens]
  *   c_kv             bf16 [n_tokens, 512];  k_pe bf16 [n_tokens, 64]
@@ -176,6 +197,9 @@ size_t mla_decode_workspace_size(const mla_dims* dims, int32_t batch, int32_t nu
  *               scaled scores.
  * Results are bit-identical between runs with the same inputs and the same
  * num_splits; calls sharing one workspace must not overlap on the device.
+ * FP4 caches are read through the FP8 format E5M2 (two mantissa bits: a code
+ * times its scale fits): exact for block scales 2^-15 .. 2^13; smaller blocks'
+ * values are rounded to multiples of 2^-16, larger ones' saturate at 57,344.
  */
 int mla_decode(const mla_dims* dims, const void* q_nope, const void* q_pe, const void* cache,
                const float* cache_scale_zero, int32_t num_pages, const int32_t* block_table,
@@ -343,7 +367,8 @@ int mla_decode_sparse(const mla_dims* dims, const void* q_nope, const void* q_pe
  *   c_kv        bf16 [n_rows, 512] latents;  k_pe bf16 [n_rows, 64] RoPE keys
  *               (rotated, as the append stored them); both 32-byte aligned.
  *               bf16 caches are copied bit for bit; 1-byte caches are
- *               dequantised in fp32 and rounded once to bf16.
+ *               dequantised in fp32 and rounded once to bf16; FP4 values are
+ *               exact in bf16 (past its largest value: infinity).
  *   device_status  optional int32 (device); a row whose position or page-table
  *               entry is out of range is left as it was, and that, decreasing
  *               offsets, or offsets outside [0, n_rows] store

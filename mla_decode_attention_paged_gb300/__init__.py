@@ -24,7 +24,7 @@ __all__ = [
     "set_timing_events", "status_string", "version",
     "MLA_OK", "MLA_ERR_INVALID_ARG", "MLA_ERR_UNSUPPORTED", "MLA_ERR_WORKSPACE", "MLA_ERR_CUDA",
     "MLA_ERR_DEVICE_TIMEOUT", "MLA_ERR_DEVICE_BOUNDS", "MLA_CACHE_BF16", "MLA_CACHE_INT8", "MLA_CACHE_FP8",
-    "MAX_Q_LEN", "MAX_TOP_K", "MAX_PREFILL_CHUNK", "MAX_PROMPT_SEQS",
+    "MLA_CACHE_FP4", "FP4_ROW_BYTES", "MAX_Q_LEN", "MAX_TOP_K", "MAX_PREFILL_CHUNK", "MAX_PROMPT_SEQS",
 ]
 
 MLA_OK = 0
@@ -37,6 +37,8 @@ MLA_ERR_DEVICE_BOUNDS = -6
 MLA_CACHE_BF16 = 0
 MLA_CACHE_INT8 = 1
 MLA_CACHE_FP8 = 2
+MLA_CACHE_FP4 = 4
+FP4_ROW_BYTES = 320  # MLA_FP4_ROW_BYTES in include/mla.h
 MAX_Q_LEN = 8  # MLA_MAX_Q_LEN in include/mla.h
 MAX_PREFILL_CHUNK = 2048  # MLA_MAX_PREFILL_CHUNK in include/mla.h
 MAX_TOP_K = 1 << 20  # MLA_MAX_TOP_K in include/mla.h
@@ -69,12 +71,14 @@ class Dims(ctypes.Structure):
 
 
 def dims(num_heads: int, page_size: int, int8: bool = False, kv_lora_rank: int = 512, rope_dim: int = 64,
-         qk_nope_dim: int = 128, v_head_dim: int = 128, fp8: bool = False) -> Dims:
+         qk_nope_dim: int = 128, v_head_dim: int = 128, fp8: bool = False, fp4: bool = False) -> Dims:
     """Model dimensions; ``int8`` / ``fp8`` select a 1-byte cache (INT8 codes, or
-    FP8 E4M3 codes held as uint8 or torch.float8_e4m3fn) with per-token scales."""
-    if int8 and fp8:
-        raise ValueError("int8 and fp8 are exclusive")
-    code = MLA_CACHE_INT8 if int8 else MLA_CACHE_FP8 if fp8 else MLA_CACHE_BF16
+    FP8 E4M3 codes held as uint8 or torch.float8_e4m3fn) with per-token scales,
+    ``fp4`` one of FP4 rows (uint8 [pages, page_size, FP4_ROW_BYTES]: E2M1 codes
+    and their scales, no scale tensor)."""
+    if bool(int8) + bool(fp8) + bool(fp4) > 1:
+        raise ValueError("int8, fp8 and fp4 are exclusive")
+    code = MLA_CACHE_INT8 if int8 else MLA_CACHE_FP8 if fp8 else MLA_CACHE_FP4 if fp4 else MLA_CACHE_BF16
     return Dims(num_heads, kv_lora_rank, rope_dim, qk_nope_dim, v_head_dim, page_size, code)
 
 
@@ -169,8 +173,13 @@ def _ptr(t: torch.Tensor | None, dtype=None, name="tensor", device=None):
 
 
 def _cache_ptrs(d: Dims, cache: torch.Tensor, scale_zero: torch.Tensor | None, device=None):
-    """Pointers of the cache rows (bf16 values, int8 codes, or E4M3 codes) and of
-    their per-token scales (None for bf16 caches)."""
+    """Pointers of the cache rows (bf16 values, int8 codes, E4M3 codes, or FP4
+    rows) and of their per-token scales (None for bf16 and FP4 caches)."""
+    if d.cache_dtype == MLA_CACHE_FP4:
+        p = _ptr(cache, torch.uint8, "cache", device)
+        if cache.dim() != 3 or cache.shape[1:] != (d.page_size, FP4_ROW_BYTES):
+            raise ValueError(f"cache must have shape [pages, {d.page_size}, {FP4_ROW_BYTES}], got {list(cache.shape)}")
+        return p, None
     if d.cache_dtype == MLA_CACHE_FP8:
         if isinstance(cache, torch.Tensor) and cache.dtype == torch.float8_e4m3fn:
             cache = cache.view(torch.uint8)
@@ -427,11 +436,12 @@ def cache_read(d: Dims, cache: torch.Tensor, scale_zero: torch.Tensor | None, bl
     code = d.cache_dtype
     if code == MLA_CACHE_FP8 and cache.dtype == torch.float8_e4m3fn:
         cache = cache.view(torch.uint8)
-    want = (torch.bfloat16, torch.int8, torch.uint8)[code] if 0 <= code <= 2 else torch.bfloat16
+    want = {MLA_CACHE_INT8: torch.int8, MLA_CACHE_FP8: torch.uint8, MLA_CACHE_FP4: torch.uint8}.get(code, torch.bfloat16)
+    width = FP4_ROW_BYTES if code == MLA_CACHE_FP4 else d.kv_lora_rank + d.rope_dim
     st = _call_on(
         dev, stream, _L().mla_cache_read, ctypes.byref(d),
-        _arg(cache, "cache", want, (pages, P, d.kv_lora_rank + d.rope_dim), dev),
-        None if code == MLA_CACHE_BF16 else
+        _arg(cache, "cache", want, (pages, P, width), dev),
+        None if code in (MLA_CACHE_BF16, MLA_CACHE_FP4) else
         _arg(scale_zero, "scale_zero", torch.float32, (pages, P, 2) if code == MLA_CACHE_INT8 else (pages, P), dev),
         pages, _arg(block_table, "block_table", torch.int32, (B, max_pages), dev), B, max_pages,
         None if starts is None else _arg(starts, "starts", torch.int32, (B,), dev),

@@ -89,6 +89,11 @@ __device__ __forceinline__ void causal_mask(float (&x)[HC], const DecodeParams& 
 // exp2(x - max) of a masked score is 0 rather than NaN, and below any score.
 constexpr float kEmptyRowMax = -1e30f;
 
+// Partial log-sum-exp of a row whose sum is not positive: a sum of 0 saw no
+// token; a NaN (from a NaN block of an FP4 row) becomes plus infinity, which the
+// merge turns into NaN outputs -- a NaN itself would lose its maximum.
+__device__ __forceinline__ float lse_of_no_sum(float l) { return l == 0.f ? -INFINITY : INFINITY; }
+
 // Physical page of token `tok` of sequence b (range-checked; out-of-range
 // entries are reported and replaced by page 0 to stay in bounds).
 __device__ __forceinline__ int page_of(const DecodeParams& p, int b, int tok) {
@@ -196,6 +201,40 @@ __device__ __forceinline__ void dequant16(uint4& lo, uint4& hi, float scale, flo
                   dequant_half2(lo.w, scale, nzs));
   hi = make_uint4(dequant_half2(hi.x, scale, nzs), dequant_half2(hi.y, scale, nzs), dequant_half2(hi.z, scale, nzs),
                   dequant_half2(hi.w, scale, nzs));
+}
+
+// ----- FP4 caches: codes expanded through E5M2 --------------------------------
+// E2M1 has one mantissa bit, E5M2 two, so a code times a power-of-two scale is an
+// E5M2 value as long as it lies in that format's range: exact for block scales
+// 2^-15 .. 2^13; below that the magnitudes round to multiples of 2^-16, above
+// it they saturate at 57,344.  An E5M2 byte is also the high byte of the fp16
+// of the same value, so one table serves both operand types.
+
+// The eight magnitudes of a block with this scale byte as E5M2 bytes, entry c
+// for code c; NaN for 255.
+__device__ __forceinline__ uint2 e2m1_table(uint32_t scale_byte) {
+  if (scale_byte == 255) return make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
+  const float s = __uint_as_float(scale_byte << 23);  // 2^-127 as 0: both give zeros
+  uint16_t a, b, c, d;
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(a) : "f"(0.5f * s), "f"(0.f));
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(b) : "f"(1.5f * s), "f"(s));
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(c) : "f"(3.f * s), "f"(2.f * s));
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(d) : "f"(6.f * s), "f"(4.f * s));
+  return make_uint2(a | (uint32_t(b) << 16), c | (uint32_t(d) << 16));
+}
+// Eight codes (a word of an FP4 row) to E5M2 bytes: values 0 .. 3 in `a`,
+// 4 .. 7 in `b`.  The codes' magnitude bits are the selectors of the permutation.
+__device__ __forceinline__ void e2m1_to_e5m2(uint32_t word, uint2 table, uint32_t& a, uint32_t& b) {
+  const uint32_t sel = word & 0x77777777u;
+  a = __byte_perm(table.x, table.y, sel) | (word & 0x80808080u);
+  b = __byte_perm(table.x, table.y, sel >> 16) | ((word << 4) & 0x80808080u);
+}
+// The same as fp16 values, value 0 in the low half of .x.
+__device__ __forceinline__ uint4 e2m1_to_f16(uint32_t word, uint2 table) {
+  uint32_t a, b;
+  e2m1_to_e5m2(word, table, a, b);
+  return make_uint4(__byte_perm(a, 0, 0x1404), __byte_perm(a, 0, 0x3424), __byte_perm(b, 0, 0x1404),
+                    __byte_perm(b, 0, 0x3424));
 }
 
 // ----- host side: tensor maps ----------------------------------------------

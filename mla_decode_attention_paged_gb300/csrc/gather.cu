@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(GatherParams p) 
   __syncthreads();
   // copy the rows: warp w takes entries w, w + 8, ...
   const size_t base_row = size_t(b) * p.pages_per_seq * P;
-  constexpr int kRowBytes = kCode == kCodeBf16 ? 1152 : 576, kPieces = kRowBytes / 16;
+  constexpr int kRowBytes = cache_row_bytes(kCode), kPieces = kRowBytes / 16;
   for (int e = warp; e < kGatherEntries; e += kGatherThreads / 32) {
     const int d = dest[e];
     if (d < 0) continue;
@@ -98,6 +98,7 @@ cudaError_t launch_gather(const GatherParams& p, int code, cudaStream_t stream) 
   const dim3 grid((p.top_k + kGatherEntries - 1) / kGatherEntries, p.batch);
   if (code == kCodeInt8) return launch_pdl(gather_kernel<kCodeInt8>, grid, dim3(kGatherThreads), 0, stream, 1, p);
   if (code == kCodeE4m3) return launch_pdl(gather_kernel<kCodeE4m3>, grid, dim3(kGatherThreads), 0, stream, 1, p);
+  if (code == kCodeE2m1) return launch_pdl(gather_kernel<kCodeE2m1>, grid, dim3(kGatherThreads), 0, stream, 1, p);
   return launch_pdl(gather_kernel<kCodeBf16>, grid, dim3(kGatherThreads), 0, stream, 1, p);
 }
 

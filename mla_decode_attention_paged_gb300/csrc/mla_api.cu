@@ -25,10 +25,16 @@ std::atomic<int> g_force_single_cta{0};
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-// Element code of the cache rows; 1-byte codes (INT8, FP8) carry per-token scales.
+// Element code of the cache rows; 1-byte codes (INT8, FP8) carry per-token
+// scales, FP4 rows hold their own.
 int cache_code(const mla_dims* d) {
-  return d->cache_dtype == MLA_CACHE_INT8 ? kCodeInt8 : d->cache_dtype == MLA_CACHE_FP8 ? kCodeE4m3 : kCodeBf16;
+  return d->cache_dtype == MLA_CACHE_INT8  ? kCodeInt8
+         : d->cache_dtype == MLA_CACHE_FP8 ? kCodeE4m3
+         : d->cache_dtype == MLA_CACHE_FP4 ? kCodeE2m1
+                                           : kCodeBf16;
 }
+// Whether the per-token parameters are in an array of their own.
+bool has_scales(int code) { return code == kCodeInt8 || code == kCodeE4m3; }
 // Bytes of per-token quantisation parameters: (scale, zero point) or a scale.
 size_t scale_bytes_per_row(int code) { return code == kCodeInt8 ? 8 : code == kCodeE4m3 ? 4 : 0; }
 
@@ -68,6 +74,7 @@ struct AttnChoice {
 };
 AttnChoice choose_attention(int rows, int code) {
   const bool byte = code != kCodeBf16;
+  if (code == kCodeE2m1) return {kAttnRows128, 128, decode_rows128_capacity(code)};
   const bool single = g_force_single_cta.load() != 0;
   const bool pair_groups = !byte && rows <= 64 && rows % 32 == 0;
   if (!single && (rows % 128 == 0 || (rows > 32 && !pair_groups))) {
@@ -97,6 +104,17 @@ int decode_rows(const mla_dims* d, const void* q_nope, const void* q_pe, const v
                 const void* W_UV, float softmax_scale, int32_t num_splits, void* workspace, size_t workspace_bytes,
                 void* out, float* lse_out, mla_stream_t stream, bool reset_status);
 
+// The fraction of f / (2 pi) in units of 2^-64 (f >= 0), to about one unit
+// where f is at most 1: 1 / (2 pi) as a sum of two doubles.
+uint64_t turn_fraction(double f) {
+  constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;
+  const double p = f * kHi, rest = std::fma(f, kHi, -p) + f * kLo, whole = std::floor(p);
+  if (!std::isfinite(p)) return 0;
+  // the difference is exact; p - whole < 1, so the first term fits and the second (|rest| < 2^-53 p) is added modulo 2^64
+  const double frac = p - whole;
+  return uint64_t(std::ldexp(frac, 64)) + uint64_t(int64_t(std::ldexp(std::fmod(rest, 0.25), 64)));
+}
+
 // Append parameters shared by mla_cache_append and mla_prefill (which then
 // set the token -> (sequence, position) mapping).
 AppendParams append_params(const mla_dims* d, void* cache, float* cache_scale_zero, int32_t num_pages,
@@ -116,8 +134,10 @@ AppendParams append_params(const mla_dims* d, void* cache, float* cache_scale_ze
   p.rope_theta = rope_theta;
   // the frequencies depend only on theta: one fp64 pow per pair here instead
   // of one per token and pair on the device's slow fp64 units
-  for (int i = 0; i < kRope / 2; ++i)
+  for (int i = 0; i < kRope / 2; ++i) {
     p.inv_freq[i] = rope_theta > 0.0 ? std::pow(rope_theta, -double(2 * i) / double(kRope)) : 0.0;
+    p.turn[i] = cache_code(d) == kCodeE2m1 ? turn_fraction(p.inv_freq[i]) : 0;
+  }
   p.n_tokens = n_tokens;
   p.num_seqs = num_seqs;
   p.max_pages = max_pages_per_seq;
@@ -150,7 +170,8 @@ int mla_check_dims(const mla_dims* d) {
   if (d->num_heads <= 0 || d->kv_lora_rank <= 0 || d->rope_dim <= 0 || d->qk_nope_dim <= 0 ||
       d->v_head_dim <= 0 || d->page_size <= 0)
     return MLA_ERR_INVALID_ARG;
-  if (d->cache_dtype != MLA_CACHE_BF16 && d->cache_dtype != MLA_CACHE_INT8 && d->cache_dtype != MLA_CACHE_FP8)
+  if (d->cache_dtype != MLA_CACHE_BF16 && d->cache_dtype != MLA_CACHE_INT8 && d->cache_dtype != MLA_CACHE_FP8 &&
+      d->cache_dtype != MLA_CACHE_FP4)
     return MLA_ERR_INVALID_ARG;
   if (d->kv_lora_rank != kLatent || d->rope_dim != kRope || d->qk_nope_dim != kNope || d->v_head_dim != kVDim)
     return MLA_ERR_UNSUPPORTED;
@@ -169,7 +190,7 @@ int mla_cache_append(const mla_dims* d, void* cache, float* cache_scale_zero, in
   if (n_tokens < 0 || num_pages <= 0 || num_seqs <= 0 || max_pages_per_seq <= 0) return MLA_ERR_INVALID_ARG;
   if (n_tokens == 0) return MLA_OK;
   const int code = cache_code(d);
-  const bool byte = code != kCodeBf16;
+  const bool byte = has_scales(code);
   if (!cache || !block_table || !seq_ids || !positions || !c_kv || !k_pe) return MLA_ERR_INVALID_ARG;
   if (byte && !cache_scale_zero) return MLA_ERR_INVALID_ARG;
   if (!aligned(cache, 16) || !aligned(c_kv, 16) || !aligned(k_pe, 4) || !aligned(block_table, 4) ||
@@ -239,7 +260,7 @@ int mla_prefill(const mla_dims* d, void* cache, float* cache_scale_zero, int32_t
   if (st != MLA_OK) return st;
   if (batch <= 0 || num_pages <= 0 || max_pages_per_seq <= 0 || chunk < 1 || chunk > MLA_MAX_PREFILL_CHUNK)
     return MLA_ERR_INVALID_ARG;
-  const bool byte = cache_code(d) != kCodeBf16;
+  const bool byte = has_scales(cache_code(d));
   if (!cache || !block_table || !seq_lens || !c_kv || !k_pe || (byte && !cache_scale_zero)) return MLA_ERR_INVALID_ARG;
   if (!aligned(c_kv, 16) || !aligned(k_pe, 4) || (byte && !aligned(cache_scale_zero, 16)))
     return MLA_ERR_INVALID_ARG;
@@ -283,7 +304,7 @@ int decode_rows(const mla_dims* d, const void* q_nope, const void* q_pe, const v
   int st = mla_check_dims(d);
   if (st != MLA_OK) return st;
   const int code = cache_code(d);
-  const bool byte = code != kCodeBf16;
+  const bool byte = has_scales(code);
   if (batch <= 0 || num_pages <= 0 || max_pages_per_seq <= 0 || num_splits < 0) return MLA_ERR_INVALID_ARG;
   if (q_len < 1 || q_len > MLA_MAX_PREFILL_CHUNK) return MLA_ERR_INVALID_ARG;
   // query rows of the call: keeps every grid (absorption, merge) and row index in range
@@ -327,7 +348,7 @@ int decode_rows(const mla_dims* d, const void* q_nope, const void* q_pe, const v
   ap.cols = batch * q_len;
   ap.max_len = max_pages_per_seq * d->page_size;
   ap.num_splits = S;
-  if (launch_absorb(ap, byte, s) != cudaSuccess) return MLA_ERR_CUDA;
+  if (launch_absorb(ap, code != kCodeBf16, s) != cudaSuccess) return MLA_ERR_CUDA;
 
   DecodeParams dp;
   dp.q_full = ap.q_full;
@@ -396,7 +417,7 @@ SparseLayout sparse_layout(const mla_dims* d, int batch, int top_k, size_t decod
   const size_t rows = size_t(batch) * L.pps * d->page_size;
   size_t off = 0;
   L.decode = off;      off = align256(off + decode_bytes);
-  L.cache = off;       off = align256(off + rows * (code == kCodeBf16 ? 1152 : 576));
+  L.cache = off;       off = align256(off + rows * cache_row_bytes(code));
   L.scale_zero = off;  off = align256(off + rows * scale_bytes_per_row(code));
   L.table = off;       off = align256(off + size_t(batch) * L.pps * 4);
   L.lens = off;        off = align256(off + size_t(batch) * 4);
@@ -456,7 +477,7 @@ int mla_decode_sparse(const mla_dims* d, const void* q_nope, const void* q_pe, c
   int st = mla_check_dims(d);
   if (st != MLA_OK) return st;
   const int code = cache_code(d);
-  const bool byte = code != kCodeBf16;
+  const bool byte = has_scales(code);
   if (batch <= 0 || num_pages <= 0 || max_pages_per_seq <= 0 || num_splits < 0) return MLA_ERR_INVALID_ARG;
   if (top_k < 1 || top_k > MLA_MAX_TOP_K || !token_indices || !aligned(token_indices, 4)) return MLA_ERR_INVALID_ARG;
   if (!cache || !block_table || !seq_lens || (byte && !cache_scale_zero)) return MLA_ERR_INVALID_ARG;
@@ -508,7 +529,7 @@ int mla_cache_read(const mla_dims* d, const void* cache, const float* cache_scal
   if (n_rows < 0 || num_pages <= 0 || num_seqs <= 0 || max_pages_per_seq <= 0) return MLA_ERR_INVALID_ARG;
   if (n_rows == 0) return MLA_OK;
   const int code = cache_code(d);
-  const bool byte = code != kCodeBf16;
+  const bool byte = has_scales(code);
   if (!cache || !block_table || !cu_rows || !c_kv || !k_pe || (byte && !cache_scale_zero)) return MLA_ERR_INVALID_ARG;
   if (!aligned(cache, 16) || !aligned(c_kv, 32) || !aligned(k_pe, 32) || !aligned(block_table, 4) ||
       !aligned(cu_rows, 4) || (starts && !aligned(starts, 4)) || (device_status && !aligned(device_status, 4)) ||

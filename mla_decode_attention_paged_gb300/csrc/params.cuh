@@ -9,9 +9,20 @@
 namespace mla {
 
 // Element type of the cached rows (mla_cache_dtype): bf16 values, INT8 codes
-// with a per-token (scale, zero point), or FP8 E4M3 codes with a per-token
-// scale.
-enum CacheCode : int { kCodeBf16 = 0, kCodeInt8 = 1, kCodeE4m3 = 2 };
+// with a per-token (scale, zero point), FP8 E4M3 codes with a per-token
+// scale, or FP4 E2M1 codes with a power-of-two scale per 32 values in the row.
+enum CacheCode : int { kCodeBf16 = 0, kCodeInt8 = 1, kCodeE4m3 = 2, kCodeE2m1 = 3 };
+
+// FP4 rows (MLA_CACHE_FP4): 18 blocks of 32 codes, 16 bytes each, then their
+// scale bytes (2^(byte - 127); 255: NaN), then zeros up to whole sectors.
+constexpr int kFp4Blocks = kRow / 32;        // 18
+constexpr int kFp4Scales = kFp4Blocks * 16;  // offset of the scale bytes: 288
+constexpr int kFp4RowBytes = 320;
+
+// Bytes of one cached row without per-token parameters kept elsewhere.
+constexpr int cache_row_bytes(int code) {
+  return code == kCodeBf16 ? 2 * kRow : code == kCodeE2m1 ? kFp4RowBytes : kRow;
+}
 
 // Multi-token decode (q_len query tokens per sequence) runs the same kernels
 // over "rows": row v = t * heads_w + h of a sequence is query token t, head
@@ -42,7 +53,7 @@ struct AbsorbParams {
 // order into pages_per_seq pages of the gathered cache (sequence b owns pages
 // [b pages_per_seq, (b + 1) pages_per_seq)), its length and page-table row.
 struct GatherParams {
-  const void* cache;         // bf16, int8 or e4m3 [num_pages, P, 576]
+  const void* cache;         // bf16, int8 or e4m3 [num_pages, P, 576], or FP4 rows [num_pages, P, 320 bytes]
   const float* scale_zero;   // [num_pages, P, 2] (INT8) or [num_pages, P] (FP8)
   const int* block_table;    // [B, max_pages]
   const int* seq_lens;       // [B]
@@ -56,7 +67,7 @@ struct GatherParams {
 };
 
 struct AppendParams {
-  void* cache;                   // bf16, int8 or e4m3 [num_pages, P, 576]
+  void* cache;                   // bf16, int8 or e4m3 [num_pages, P, 576], or FP4 rows [num_pages, P, 320 bytes]
   float* scale_zero;             // [num_pages, P, 2] (INT8) or [num_pages, P] (FP8)
   const int* block_table;        // [num_seqs, max_pages]
   const int* seq_ids;            // [N]   (chunk == 0)
@@ -69,12 +80,13 @@ struct AppendParams {
   int* status;                   // optional
   double rope_theta;
   double inv_freq[kRope / 2];    // theta^(-2i/64), evaluated on the host in fp64
+  uint64_t turn[kRope / 2];      // FP4: the fraction of inv_freq / (2 pi) in units of 2^-64
   int n_tokens, num_seqs, max_pages, num_pages, page_size;
 };
 
 // Packed rows read back out of the cache (mla_cache_read).
 struct CacheReadParams {
-  const void* cache;         // bf16, int8 or e4m3 [num_pages, P, 576]
+  const void* cache;         // bf16, int8 or e4m3 [num_pages, P, 576], or FP4 rows [num_pages, P, 320 bytes]
   const float* scale_zero;   // [num_pages, P, 2] (INT8) or [num_pages, P] (FP8)
   const int* block_table;    // [num_seqs, max_pages]
   const int* starts;         // [num_seqs] first position, or null: 0
