@@ -1,0 +1,627 @@
+// decode_fp4.cu -- split-KV MLA decode attention over FP4 caches for groups of
+// 16 or 32 query rows (16 or 32 heads, or heads x tokens of multi-token decode),
+// on the FP8 tensor cores.
+//
+// What it computes ("The Weight Absorption Trick"; "Seven Ways LLMs Handle
+// Attention", section 5; "Flash-Decoding and FlashInfer"; "The Architecture of
+// Memory", "Leveraging Tensor Cores and Asynchronous Prefetching": caches of 2
+// to 4 bits on the tensor cores): for one head group of one sequence and one
+// contiguous range of its tokens, with q_full[h] = [W^UK_h^T q_nope_h | q_pe_h]
+// (576 wide) and the cached rows c_t = [latent | RoPE key] (576 wide),
+//     s[t][h] = scale * q_full[h] . c_t
+//     o_lat[h] = sum_t softmax(s[., h])_t * c_t[0:512]
+// and emits o_lat (normalised within the range) with the range's lse.
+//
+// Why FP8 operands.  A row of 320 bytes is 3.6 times shorter than a bf16 row, so
+// what bounds a 16-head decode is no longer HBM alone: an SM's share of it, 22
+// bytes a cycle, is a row every 14 cycles, and a row expanded to 16 bits costs
+// shared memory (128 bytes a cycle) 1,152 bytes written and 2,176 read by the two
+// products, 26 cycles.  E2M1 times a power of two is an E5M2 value (see
+// decode_common.cuh), so the row is expanded to 576 bytes and costs half of that,
+// and exactly.  The other operands are fp32 values split into FP8 terms that
+// stand side by side in the MMA's N extent (16 heads fill an eighth of it: the
+// MMA's time is its A operand's way through shared memory):
+//   Q: two E4M3 terms, q = 2^-k (hi + lo / 16), k per head: off by at most 2^-8
+//      of a value, as bf16 is (half of that on average)
+//   P: three E5M2 terms, hi + mid + lo = the weight's fp16 value exactly down to
+//      2^-19 of the running maximum and to 2^-30 of it below: as many bits as the
+//      1-byte caches' weights
+// Products as in decode_tc.cu, with the 128 tokens of a tile as M:
+//     S^T [128 tok x 2 HC] = C_tile [128 x 576] * [Q_hi | Q_lo]^T          (K-major)
+//     O^T [512 x 3 HC] += C_tile^T [512 x 128] * [P_hi | P_mid | P_lo]^T   (MN-major)
+//
+// Warp roles (448 threads; 576 for 32 rows):
+//   first 4 (8) warps  softmax, one thread per token row of S^T and 16 heads; Q of
+//                      each segment; epilogue
+//   next 8 warps       expansion: the tile's rows from global memory into registers,
+//                      a tile ahead (40 KB in flight per SM), then through byte
+//                      permutations into one of two operand slots
+//   last 2 warps       TMEM and QK issuer; PV issuer
+// Every wait is bounded: on timeout the CTA records MLA_ERR_DEVICE_TIMEOUT,
+// drains, frees its tensor memory and returns.
+#include <atomic>
+#include <cuda_fp16.h>
+
+#include "blackwell_ptx.cuh"
+#include "decode_common.cuh"
+#include "params.cuh"
+
+namespace mla {
+namespace {
+
+using namespace ptx;
+using namespace dc;
+
+constexpr int kExpWarps = 8;
+constexpr int kSlots = 2;
+constexpr uint32_t kLatBox = kTile * 128;                 // [128 tokens x 128 latent columns] E5M2, SW128: one O^T chunk
+constexpr uint32_t kRopeBox = 4 * kLatBox;                // offset of [128 tokens x 64 RoPE columns] E5M2, SW64
+constexpr uint32_t kSlotBytes = kRopeBox + kTile * kRope;  // 72 KB
+constexpr uint64_t kWaitLimitNs = 2000000000ull;          // 2 s
+constexpr float kRescaleThreshold = 2.f;                  // log2 units
+constexpr float kWeightBits = 13.f;                       // a weight is 2^13 at the running maximum, 2^15 at most
+
+template <int HC>
+struct Fp4Cfg {
+  static constexpr int kSoftWarps = HC / 4;
+  static constexpr int kThreads = 32 * (kSoftWarps + kExpWarps + 2);
+  static constexpr int kNQ = 2 * HC, kNP = 3 * HC;          // N of the products
+  static constexpr uint32_t kQBox = kNQ * 128;              // [2 HC rows x 128 columns] E4M3, SW128
+  static constexpr uint32_t kQBytes = 4 * kQBox + kNQ * 64;  // + [2 HC rows x 64 RoPE columns], SW64
+  static constexpr uint32_t kPBytes = kTile * kNP;          // P^T core matrices: 16 rows x 8 tokens, 128 bytes each
+  static constexpr uint32_t kOffQ = kSlots * kSlotBytes;
+  static constexpr uint32_t kOffP = kOffQ + kQBytes;
+  static constexpr uint32_t kOffLut = kOffP + 2 * kPBytes;  // magnitudes by scale byte
+  static constexpr uint32_t kOffMisc = kOffLut + 256 * 8;
+  static constexpr uint32_t kMiscBytes = 256 + 15 * HC * 4;
+  static constexpr uint32_t kSmem = kOffMisc + kMiscBytes + 1024;  // +1024: base alignment slack
+  static constexpr uint32_t kColS = 0;                       // + buf * 2 HC
+  static constexpr uint32_t kColO = 128, kColOStep = HC == 16 ? 64 : 96, kTmemCols = 512;
+  static_assert(kSmem <= 232448, "dynamic shared memory of one CTA");
+  static_assert(kColO + 3 * kColOStep + kNP <= kTmemCols && 2 * kNQ <= int(kColO), "tensor memory");
+};
+
+struct Fp4Barriers {
+  uint64_t full[kSlots], empty[kSlots];  // operands expanded; PV has read them
+  uint64_t q_full, s_full[2], s_free[2], p_full[2], pv_done[2], o_full, o_free, drain[2];
+  uint32_t tmem_base;
+  int abort;
+};
+static_assert(sizeof(Fp4Barriers) <= 256, "barriers");
+
+__device__ __forceinline__ void fail(Fp4Barriers* B, int* status) {
+  B->abort = 1;
+  set_status(status, MLA_ERR_DEVICE_TIMEOUT);
+}
+
+// OR over the 128 threads of a softmax group (named barrier 1 + group).
+__device__ __forceinline__ bool group_any(int group, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %2, 0;\n\t"
+      "bar.red.or.pred q, %1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(group + 1), "r"(uint32_t(pred))
+      : "memory");
+  return r != 0;
+}
+
+// Instruction descriptor, kind::f8f6f4, fp32 accumulator (bits 4-5 = 1): A is
+// E5M2 (bits 7-9 = 1), B E5M2 or E4M3 (bits 10-12 = 1 or 0), the rest as for f16.
+constexpr uint32_t idesc_f8(int M, int N, bool mn_major, bool b_e5m2) {
+  return (1u << 4) | (1u << 7) | (uint32_t(b_e5m2) << 10) | (uint32_t(mn_major) << 15) | (uint32_t(mn_major) << 16) |
+         (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
+}
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Two fp32 values to E4M3, `lo` in the low byte.
+__device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// Read-once data.
+__device__ __forceinline__ uint4 ld_stream(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+// 32 codes (16 bytes of a row) to 32 E5M2 bytes.
+__device__ __forceinline__ void expand_block(uint4 v, uint2 table, uint4& lo, uint4& hi) {
+  e2m1_to_e5m2(v.x, table, lo.x, lo.y);
+  e2m1_to_e5m2(v.y, table, lo.z, lo.w);
+  e2m1_to_e5m2(v.z, table, hi.x, hi.y);
+  e2m1_to_e5m2(v.w, table, hi.z, hi.w);
+}
+
+// kCausal: multi-token decode (q_len > 1) masks each row's later positions on a
+// sequence's last tiles.
+template <int HC, bool kCausal>
+__global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(DecodeParams p) {
+  using C = Fp4Cfg<HC>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Fp4Barriers* B = reinterpret_cast<Fp4Barriers*>(smem + C::kOffMisc);
+  // [2][HC][4] maxima, [HC][4] sums, [HC] 1 / l, [2][HC] scale of Q's terms
+  float* red = reinterpret_cast<float*>(smem + C::kOffMisc + 256);
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kQkWarp = C::kSoftWarps + kExpWarps, kPvWarp = kQkWarp + 1;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      // the test hook: one arrival more than the first tile gets
+      mbar_init(&B->full[i], kExpWarps + (p.inject_wait_timeout && i == 0 ? 1 : 0));
+      mbar_init(&B->empty[i], 1);
+    }
+    mbar_init(&B->q_full, 32 * C::kSoftWarps);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&B->s_full[i], 1);
+      mbar_init(&B->s_free[i], 32 * C::kSoftWarps);
+      mbar_init(&B->p_full[i], 32 * C::kSoftWarps);
+      mbar_init(&B->pv_done[i], 1);
+      mbar_init(&B->drain[i], 1);
+    }
+    mbar_init(&B->o_full, 1);
+    mbar_init(&B->o_free, 32 * C::kSoftWarps);
+    B->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kQkWarp) {
+    tmem_alloc(&B->tmem_base, C::kTmemCols);
+    tmem_relinquish();
+  }
+  if (threadIdx.x < 256) reinterpret_cast<uint2*>(smem + C::kOffLut)[threadIdx.x] = e2m1_table(threadIdx.x);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = B->tmem_base;
+  griddep_wait();  // the plan and Q come from the kernel before
+  griddep_launch_dependents();
+
+  const int G = p.num_groups, g = blockIdx.x % G, cp = blockIdx.x / G, Cp = gridDim.x / G;
+  const long long S = p.status[1];  // effective split count from the plan
+  const long long pa = (cp * S) / Cp, pb = ((cp + 1) * S) / Cp;
+  const volatile int* abort_flag = &B->abort;
+
+  if (warp >= C::kSoftWarps && warp < kQkWarp) {
+    // ------------------------------------------------------------ expansion
+    // Thread (r0, j) takes block 4c + j of rows r0 and r0 + 64, c = 0 .. 3, and
+    // piece j of the rows' tails (RoPE blocks 16 and 17, scales 0 - 15, scales
+    // 16 and 17): four lanes read 64 bytes of a row, and their stores and those
+    // of the next row's lanes go to distinct banks.  A piece's register is
+    // loaded again, for the next tile, as soon as it has been expanded.
+    const int e = threadIdx.x - 32 * C::kSoftWarps, j = e & 3, r0 = e >> 2;
+    const int lane2 = (lane & ~3) + 2, lane3 = lane2 + 1;
+    const uint2* lut = reinterpret_cast<const uint2*>(smem + C::kOffLut);
+    const uint8_t* cache = static_cast<const uint8_t*>(p.cache) + 16 * j;
+    TileWalkerT<true> walk;
+    walk.init(p.tile_start, p.seg_base, p.len, p.batch, int(S), pa, pb);
+    TileInfo t;
+    // valid rows of the current, the next and the tile behind it; page ids of the last
+    int v0 = 0, v1 = 0, v2 = 0, tok1 = 0, tok2 = 0, pg1[2], pg2[2];
+    auto look = [&](int& valid, int& tok, int (&pg)[2]) {
+      valid = 0;
+      tok = 0;
+      pg[0] = pg[1] = 0;
+      if (!walk.next(t)) return;
+      valid = t.valid;
+      tok = t.tile * kTile + r0;
+      const int* bt = p.block_table + size_t(t.b) * p.max_pages;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (r0 + 64 * i < valid) pg[i] = __ldg(bt + (tok + 64 * i) / p.page_size);
+    };
+    auto row_of = [&](int tok, int page) -> const uint8_t* {
+      if (uint32_t(page) >= uint32_t(p.num_pages)) {
+        report_bad_page(p.status);
+        page = 0;
+      }
+      return cache + (size_t(page) * p.page_size + tok % p.page_size) * kFp4RowBytes;
+    };
+    uint4 v[2][5];
+    look(v0, tok1, pg1);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const bool in = r0 + 64 * i < v0;
+      const uint8_t* row = in ? row_of(tok1 + 64 * i, pg1[i]) : nullptr;
+#pragma unroll
+      for (int c = 0; c < 5; ++c) v[i][c] = in ? ld_stream(row + 64 * c) : make_uint4(0, 0, 0, 0);
+    }
+    look(v1, tok1, pg1);
+    bool ok = true;
+    for (uint32_t k = 0; v0 > 0; ++k) {
+      const uint32_t slot = k % kSlots;
+      uint8_t* base = smem + slot * kSlotBytes;
+      look(v2, tok2, pg2);
+      ok = __all_sync(0xffffffffu, mbar_wait(&B->empty[slot], ((k / kSlots) & 1) ^ 1, abort_flag, kWaitLimitNs));
+      if (!ok) break;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = r0 + 64 * i;
+        const bool in = r < v0, next = r < v1;
+        const uint8_t* row = next ? row_of(tok1 + 64 * i, pg1[i]) : nullptr;
+        const uint32_t tail[5] = {__shfl_sync(0xffffffffu, v[i][4].x, lane2), __shfl_sync(0xffffffffu, v[i][4].y, lane2),
+                                  __shfl_sync(0xffffffffu, v[i][4].z, lane2), __shfl_sync(0xffffffffu, v[i][4].w, lane2),
+                                  __shfl_sync(0xffffffffu, v[i][4].x, lane3)};
+        // rows at and past the tile's valid length are written as zeros
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint2 tab = in ? lut[(tail[c] >> (8 * j)) & 255] : make_uint2(0, 0);
+          uint4 lo, hi;
+          expand_block(v[i][c], tab, lo, hi);
+          uint8_t* dst = base + c * kLatBox + r * 128;
+          *reinterpret_cast<uint4*>(dst + (((2 * j) ^ (r & 7)) << 4)) = lo;
+          *reinterpret_cast<uint4*>(dst + (((2 * j + 1) ^ (r & 7)) << 4)) = hi;
+          if (next) v[i][c] = ld_stream(row + 64 * c);
+        }
+        if (j < 2) {
+          const uint2 tab = in ? lut[(tail[4] >> (8 * j)) & 255] : make_uint2(0, 0);
+          uint4 lo, hi;
+          expand_block(v[i][4], tab, lo, hi);
+          uint8_t* dst = base + kRopeBox + r * 64;
+          *reinterpret_cast<uint4*>(dst + (((2 * j) ^ ((r >> 1) & 3)) << 4)) = lo;
+          *reinterpret_cast<uint4*>(dst + (((2 * j + 1) ^ ((r >> 1) & 3)) << 4)) = hi;
+        }
+        if (next) v[i][4] = ld_stream(row + 256);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&B->full[slot]);
+      v0 = v1;
+      v1 = v2;
+      tok1 = tok2;
+      pg1[0] = pg2[0];
+      pg1[1] = pg2[1];
+    }
+    if (!ok) fail(B, p.status);
+  } else if (warp == kQkWarp && lane == 0) {
+    // ------------------------------------------------------------ QK issuer
+    TileWalkerT<true> walk;
+    walk.init(p.tile_start, p.seg_base, p.len, p.batch, int(S), pa, pb);
+    constexpr uint32_t id_qk = idesc_f8(128, C::kNQ, false, false);
+    constexpr uint64_t kDescK = smem_desc(0, 16, 1024, kSwizzle128B);   // K-major SW128 (8-row groups of 1 KB)
+    constexpr uint64_t kDescRope = smem_desc(0, 16, 512, kSwizzle64B);  // K-major SW64 (8-row groups of 512 B)
+    uint32_t k = 0, seg = 0;
+    TileInfo t;
+    bool ok = true;
+    while (ok && walk.next(t)) {
+      const uint32_t slot = k % kSlots, buf = k & 1;
+      // every softmax thread has read tile k - 2's scores
+      if (k >= 2 && !(ok = mbar_wait(&B->s_free[buf], ((k - 2) >> 1) & 1, abort_flag, kWaitLimitNs))) break;
+      if (t.first && !(ok = mbar_wait(&B->q_full, seg++ & 1, abort_flag, kWaitLimitNs))) break;
+      if (!(ok = mbar_wait(&B->full[slot], (k / kSlots) & 1, abort_flag, kWaitLimitNs))) break;
+      tc_fence_after();
+      const uint32_t d = tmem + C::kColS + buf * C::kNQ, a = sbase + slot * kSlotBytes, q = sbase + C::kOffQ;
+#pragma unroll
+      for (int kk = 0; kk < 16; ++kk)
+        mma_f8(d, kDescK | desc_addr(a + (kk >> 2) * kLatBox + 32 * (kk & 3)),
+               kDescK | desc_addr(q + (kk >> 2) * C::kQBox + 32 * (kk & 3)), id_qk, kk > 0);
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk)
+        mma_f8(d, kDescRope | desc_addr(a + kRopeBox + 32 * kk), kDescRope | desc_addr(q + 4 * C::kQBox + 32 * kk), id_qk, 1);
+      mma_commit(&B->s_full[buf]);
+      ++k;
+    }
+    if (!ok) fail(B, p.status);
+    mma_commit(&B->drain[0]);  // every MMA this thread issued completes before teardown
+    mbar_wait_until(&B->drain[0], 0, global_timer_ns() + kWaitLimitNs / 4);
+  } else if (warp == kPvWarp && lane == 0) {
+    // ------------------------------------------------------------ PV issuer
+    TileWalkerT<true> walk;
+    walk.init(p.tile_start, p.seg_base, p.len, p.batch, int(S), pa, pb);
+    constexpr uint32_t id_pv = idesc_f8(128, C::kNP, true, true);
+    constexpr uint64_t kDescMN = smem_desc(0, kLatBox, 1024, kSwizzle128B);  // MN-major SW128: 128 columns, 8-token groups
+    constexpr uint64_t kDescP = smem_desc(0, 128, 2048, kSwizzleNone);       // P^T core matrices
+    uint32_t k = 0, seg = 0;
+    TileInfo t;
+    bool ok = true;
+    while (ok && walk.next(t)) {
+      const uint32_t slot = k % kSlots, buf = k & 1;
+      if (!(ok = mbar_wait(&B->p_full[buf], (k >> 1) & 1, abort_flag, kWaitLimitNs))) break;
+      if (t.first && seg > 0 && !(ok = mbar_wait(&B->o_free, (seg - 1) & 1, abort_flag, kWaitLimitNs))) break;
+      tc_fence_after();
+      const int nk = (t.valid + 31) >> 5;
+      const uint32_t a = sbase + slot * kSlotBytes, b = sbase + C::kOffP + buf * C::kPBytes;
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c)
+        for (int kk = 0; kk < nk; ++kk)
+          mma_f8(tmem + C::kColO + c * C::kColOStep, kDescMN | desc_addr(a + c * kLatBox + 4096 * kk),
+                 kDescP | desc_addr(b + 512 * kk), id_pv, !(t.first && kk == 0));
+      mma_commit(&B->empty[slot]);
+      mma_commit(&B->pv_done[buf]);
+      if (t.last) {
+        mma_commit(&B->o_full);
+        ++seg;
+      }
+      ++k;
+    }
+    if (!ok) fail(B, p.status);
+    mma_commit(&B->drain[1]);
+    mbar_wait_until(&B->drain[1], 0, global_timer_ns() + kWaitLimitNs / 4);
+  } else if (warp < C::kSoftWarps) {
+    // ------------------------------------------------------------ Q, softmax, epilogue
+    // Group c (four warps) has heads 16c .. 16c + 15 of the head group; thread st
+    // of it the token row st of S^T (its TMEM lane).
+    const int c = warp >> 2, q4 = warp & 3, st = threadIdx.x & 127;
+    const uint32_t lane_off = uint32_t(q4 * 32) << 16;
+    float* qscale = red + 13 * HC + 16 * c;  // + (segment & 1) * HC
+    TileWalkerT<true> walk;
+    walk.init(p.tile_start, p.seg_base, p.len, p.batch, int(S), pa, pb);
+    // Q of a segment's sequence as two E4M3 terms: eight threads per head, each
+    // every eighth chunk of eight values.  Every QK MMA of the previous segment
+    // has completed: this thread saw the s_full of its last tile.
+    auto load_q = [&](int b, uint32_t seg) {
+      const int hl = st >> 3, i8 = st & 7, row_hi = 16 * c + hl, row_lo = HC + row_hi;
+      const uint4* src = reinterpret_cast<const uint4*>(p.q_full + (size_t(b) * p.heads + g * HC + row_hi) * kRow) + i8;
+      uint4 u[9];
+      float top = 0.f;
+#pragma unroll
+      for (int i = 0; i < 9; ++i) {
+        u[i] = src[8 * i];
+        const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float2 f = unpack_f16x2(w[x]);
+          top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+      }
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      // up to a power of two in [128, 256): 2^(7 - floor(log2 top)) (fp16 values: 2^-24 .. 2^16)
+      const int ex = top > 0.f ? int(__float_as_uint(top) >> 23) - 127 : 7;
+      const float up = __uint_as_float(uint32_t(127 + 7 - ex) << 23), down = __uint_as_float(uint32_t(127 - 7 + ex) << 23);
+      if (i8 == 0) qscale[(seg & 1) * HC + hl] = down * p.scale_log2;
+#pragma unroll
+      for (int i = 0; i < 9; ++i) {
+        const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+        uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          float2 f = unpack_f16x2(w[x]);
+          f.x *= up;
+          f.y *= up;
+          const uint32_t a = pack_e4m3x2(f.x, f.y);
+          const float2 fa = unpack_f16x2(e4m3x2_to_half2(a));
+          hi[x >> 1] |= a << (16 * (x & 1));
+          lo[x >> 1] |= pack_e4m3x2(16.f * (f.x - fa.x), 16.f * (f.y - fa.y)) << (16 * (x & 1));
+        }
+        // chunk i8 + 8 i: 16 chunks to a box, two to a 16-byte piece
+        const int ch = i8 + 8 * (i & 1), piece = ch >> 1;
+        uint8_t* box = smem + C::kOffQ + (i >> 1) * C::kQBox;
+#pragma unroll
+        for (int term = 0; term < 2; ++term) {
+          const int row = term ? row_lo : row_hi;
+          uint8_t* dst = i < 8 ? box + row * 128 + ((piece ^ (row & 7)) << 4) : box + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
+          *reinterpret_cast<uint2*>(dst + 8 * (ch & 1)) = term ? make_uint2(lo[0], lo[1]) : make_uint2(hi[0], hi[1]);
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&B->q_full);
+    };
+    float m_run[16], l_run[16];  // m_run: the running maximum less kWeightBits
+    uint32_t k = 0, seg = 0;
+    TileInfo t, tn;
+    bool have = walk.next(t);
+    int len_b = walk.len_b;
+    if (have) load_q(t.b, 0);
+    while (have) {
+      const uint32_t buf = k & 1;
+      const bool valid = st < t.valid;
+      bool ok = mbar_wait(&B->s_full[buf], (k >> 1) & 1, abort_flag, kWaitLimitNs);
+      if (k >= 2) ok = ok && mbar_wait(&B->pv_done[buf], ((k - 2) >> 1) & 1, abort_flag, kWaitLimitNs);
+      tc_fence_after();
+      // the first tile of a segment: every thread's qscale must be there
+      if (t.first) group_any(c, false);
+      float x[16];
+      {
+        float lo[16];
+        tmem_ld16(tmem + lane_off + C::kColS + buf * C::kNQ + 16 * c, x);
+        tmem_ld16(tmem + lane_off + C::kColS + buf * C::kNQ + HC + 16 * c, lo);
+        tc_fence_before();
+        mbar_arrive(&B->s_free[buf]);
+        const float4* qs = reinterpret_cast<const float4*>(qscale + (seg & 1) * HC);
+#pragma unroll
+        for (int h4 = 0; h4 < 4; ++h4) {
+          const float4 s = qs[h4];
+          x[4 * h4] = fmaf(lo[4 * h4], 0.0625f, x[4 * h4]) * s.x;
+          x[4 * h4 + 1] = fmaf(lo[4 * h4 + 1], 0.0625f, x[4 * h4 + 1]) * s.y;
+          x[4 * h4 + 2] = fmaf(lo[4 * h4 + 2], 0.0625f, x[4 * h4 + 2]) * s.z;
+          x[4 * h4 + 3] = fmaf(lo[4 * h4 + 3], 0.0625f, x[4 * h4 + 3]) * s.w;
+        }
+      }
+      if (!valid) {
+#pragma unroll
+        for (int h = 0; h < 16; ++h) x[h] = -INFINITY;
+      }
+      if (kCausal && causal_tile(p, t, len_b)) {
+        const int pos = t.tile * kTile + st - (len_b - p.q_len);  // against the query token's number
+#pragma unroll
+        for (int h = 0; h < 16; ++h)
+          if (pos > (g * HC + 16 * c + h) / p.heads_w) x[h] = -INFINITY;
+      }
+      // Running max: as in decode_tc.cu it only has to bound the scores, here to
+      // within a factor of 4, so that the weights use E5M2's range down.
+      bool over = false;
+      if (!t.first) {
+#pragma unroll
+        for (int h = 0; h < 16; ++h) over |= x[h] > m_run[h] + (kWeightBits + kRescaleThreshold);
+      }
+      float alpha[16];
+      bool rescale = false;
+      if (t.first || group_any(c, over || !ok)) {
+        float* rm = red + buf * 4 * HC + 64 * c;
+        {
+          float tmp[16];
+#pragma unroll
+          for (int h = 0; h < 16; ++h) tmp[h] = x[h];
+          const float wm = warp_transpose_reduce<16, true>(tmp, lane);
+          if (!(lane & 1)) rm[(lane >> 1) * 4 + q4] = wm;
+        }
+        if (group_any(c, !ok)) break;
+#pragma unroll
+        for (int h = 0; h < 16; ++h) {
+          const float4 m4 = reinterpret_cast<const float4*>(rm)[h];
+          const float mt = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
+          alpha[h] = 1.f;
+          if (t.first) {
+            m_run[h] = fmaxf(mt, kEmptyRowMax) - kWeightBits;  // a row masked in the whole tile stays empty
+            l_run[h] = 0.f;
+          } else if (mt > m_run[h] + (kWeightBits + kRescaleThreshold)) {
+            alpha[h] = exp2f(m_run[h] - (mt - kWeightBits));
+            m_run[h] = mt - kWeightBits;
+            l_run[h] *= alpha[h];
+            rescale = true;
+          }
+        }
+      }
+      if (rescale) {
+        // uniform across the group.  QK of this tile may have been issued
+        // before PV of the previous one: wait for that PV first.
+        const bool ok3 = mbar_wait(&B->pv_done[(k - 1) & 1], ((k - 1) >> 1) & 1, abort_flag, kWaitLimitNs);
+        tc_fence_after();
+        if (group_any(c, !ok3)) break;
+#pragma unroll 1
+        for (int i = 0; i < 12; ++i) {  // chunk i / 3, term i % 3
+          float v[16];
+          const uint32_t a = tmem + lane_off + C::kColO + (i / 3) * C::kColOStep + (i % 3) * HC + 16 * c;
+          tmem_ld16(a, v);
+#pragma unroll
+          for (int h = 0; h < 16; ++h) v[h] *= alpha[h];
+          tmem_st16(a, v);
+        }
+        tmem_st_wait();
+      }
+      // weights -> P^T, three E5M2 terms of the fp16 value: the high byte rounded
+      // to nearest, the same of what is left, and the rest (at most three bits)
+      {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float a = ex2_ftz(x[2 * i] - m_run[2 * i]), b = ex2_ftz(x[2 * i + 1] - m_run[2 * i + 1]);
+          l_run[2 * i] += a;
+          l_run[2 * i + 1] += b;
+          w[i] = pack_f16x2(a, b);
+        }
+        uint8_t* pt = smem + C::kOffP + buf * C::kPBytes + c * 2048 + (st >> 3) * 128 + (st & 7) * 16;
+#pragma unroll
+        for (int term = 0; term < 3; ++term) {
+          uint32_t h[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            h[i] = term < 2 ? (w[i] + 0x00800080u) & 0xff00ff00u : w[i];
+            if (term < 2) w[i] = sub_f16x2(w[i], h[i]);
+          }
+          *reinterpret_cast<uint4*>(pt + term * (HC / 16) * 2048) =
+              make_uint4(__byte_perm(h[0], h[1], 0x7531), __byte_perm(h[2], h[3], 0x7531),
+                         __byte_perm(h[4], h[5], 0x7531), __byte_perm(h[6], h[7], 0x7531));
+        }
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      mbar_arrive(&B->p_full[buf]);
+      const bool have_next = walk.next(tn);
+      if (t.last) {
+        if (have_next) load_q(tn.b, seg + 1);
+        const bool ok2 = mbar_wait(&B->o_full, seg & 1, abort_flag, kWaitLimitNs);
+        tc_fence_after();
+        float* rl = red + 8 * HC + 64 * c;  // [16][4] sums
+        {
+          float tmp[16];
+#pragma unroll
+          for (int h = 0; h < 16; ++h) tmp[h] = l_run[h];
+          const float ls = warp_transpose_reduce<16, false>(tmp, lane);
+          if (!(lane & 1)) rl[(lane >> 1) * 4 + q4] = ls;
+        }
+        if (group_any(c, !ok2)) break;
+        float* rinv = red + 12 * HC + 16 * c;
+        float l = 0.f, il = 0.f;
+        if (st < 16) {  // thread h divides for head h
+          const float4 l4 = reinterpret_cast<const float4*>(rl)[st];
+          l = (l4.x + l4.y) + (l4.z + l4.w);
+          il = l > 0.f ? 1.f / l : l;  // 0: a row with no visible token; NaN stays
+          rinv[st] = il;
+        }
+        group_any(c, false);
+        const int row0 = g * HC + 16 * c;
+        float* dst = p.partial_o + (size_t(t.seg) * p.heads + row0) * kLatent + st;
+#pragma unroll 1
+        for (int ch = 0; ch < 4; ++ch) {
+          float v[16], v2[16];
+          const uint32_t a = tmem + lane_off + C::kColO + ch * C::kColOStep + 16 * c;
+          tmem_ld16(a, v);
+          tmem_ld16(a + HC, v2);
+#pragma unroll
+          for (int h = 0; h < 16; ++h) v[h] += v2[h];
+          tmem_ld16(a + 2 * HC, v2);
+#pragma unroll
+          for (int h = 0; h < 16; ++h) dst[h * kLatent + ch * 128] = (v[h] + v2[h]) * rinv[h];
+        }
+        tc_fence_before();
+        mbar_arrive(&B->o_free);
+        if (st < 16) {  // thread h writes head h's lse
+          float mh = 0.f;
+#pragma unroll
+          for (int h = 0; h < 16; ++h)
+            if (st == h) mh = m_run[h];
+          p.partial_lse[size_t(t.seg) * p.heads + row0 + st] = l > 0.f ? (mh + log2f(l)) * kLn2 : lse_of_no_sum(l);
+        }
+        ++seg;
+      }
+      t = tn;
+      len_b = walk.len_b;
+      have = have_next;
+      ++k;
+    }
+  }
+  // ---------------------------------------------------------------- teardown
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kQkWarp) tmem_dealloc(tmem, C::kTmemCols);
+}
+
+template <int HC>
+cudaError_t launch_fp4(const DecodeParams& p, int grid, cudaStream_t stream) {
+  using C = Fp4Cfg<HC>;
+  static std::atomic<bool> attr[128];  // per device: attributes set (zero-initialised)
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 128 || !attr[dev]) {
+    for (auto* k : {decode_fp4_kernel<HC, false>, decode_fp4_kernel<HC, true>}) {
+      const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::kSmem));
+      if (e != cudaSuccess) return e;
+    }
+    if (dev >= 0 && dev < 128) attr[dev] = true;
+  }
+  auto* kernel = p.q_len > 1 ? decode_fp4_kernel<HC, true> : decode_fp4_kernel<HC, false>;
+  return launch_pdl(kernel, dim3(grid), dim3(C::kThreads), C::kSmem, stream, 1, p);
+}
+
+}  // namespace
+
+cudaError_t launch_decode_fp4(const DecodeParams& p, int hc, int grid, cudaStream_t stream) {
+  return hc == 16 ? launch_fp4<16>(p, grid, stream) : launch_fp4<32>(p, grid, stream);
+}
+
+}  // namespace mla

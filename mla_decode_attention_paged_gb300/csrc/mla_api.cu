@@ -68,13 +68,15 @@ mla_dims row_dims(const mla_dims* d, int q_len) {
 // 16/32-head CTA-pair kernel, 1-byte caches (and devices that cannot place
 // pairs) on single CTAs.  `units` = attention units resident at once (pairs
 // or CTAs).
-enum AttnKind { kAttnRows128, kAttnPair, kAttnSingle };
+enum AttnKind { kAttnRows128, kAttnPair, kAttnSingle, kAttnFp4 };
 struct AttnChoice {
   int kind, hc, units;
 };
 AttnChoice choose_attention(int rows, int code) {
   const bool byte = code != kCodeBf16;
-  if (code == kCodeE2m1) return {kAttnRows128, 128, decode_rows128_capacity(code)};
+  if (code == kCodeE2m1)
+    return rows <= 64 ? AttnChoice{kAttnFp4, rows % 32 == 0 ? 32 : 16, sm_count()}
+                      : AttnChoice{kAttnRows128, 128, decode_rows128_capacity(code)};
   const bool single = g_force_single_cta.load() != 0;
   const bool pair_groups = !byte && rows <= 64 && rows % 32 == 0;
   if (!single && (rows % 128 == 0 || (rows > 32 && !pair_groups))) {
@@ -380,6 +382,7 @@ int decode_rows(const mla_dims* d, const void* q_nope, const void* q_pe, const v
   if (ev0 && ev1 && cudaEventRecord(ev0, s) != cudaSuccess) return MLA_ERR_CUDA;
   const cudaError_t le = attn.kind == kAttnRows128 ? launch_decode_rows128(dp, code, per_group_used, s)
                          : attn.kind == kAttnPair  ? launch_decode_pair(dp, hc, per_group_used, s)
+                         : attn.kind == kAttnFp4   ? launch_decode_fp4(dp, hc, per_group_used * groups, s)
                                                    : launch_decode_tc(dp, hc, code, per_group_used * groups, s);
   if (le != cudaSuccess) return MLA_ERR_CUDA;
   if (ev0 && ev1 && cudaEventRecord(ev1, s) != cudaSuccess) return MLA_ERR_CUDA;

@@ -186,6 +186,8 @@ cudaError_t launch_prompt_attention(PromptParams p, cudaStream_t stream);
 cudaError_t launch_gather(const GatherParams& p, int code, cudaStream_t stream);
 cudaError_t launch_decode_tc(const DecodeParams& p, int hc, int code, int grid, cudaStream_t stream);
 int decode_head_group(int heads, bool byte_cache);
+// FP4 caches, groups of 16 or 32 query rows: one CTA per SM.
+cudaError_t launch_decode_fp4(const DecodeParams& p, int hc, int grid, cudaStream_t stream);
 // Launches `kernel` with programmatic dependent launch (and, if cluster_x > 1,
 // thread-block clusters of cluster_x CTAs).  The kernels of the decode step
 // (append, absorb, attention, merge + up-projection) set up their shared

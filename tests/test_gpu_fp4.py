@@ -279,8 +279,9 @@ def test_decode_running_maximum(cuda_lib, H, order):
     flat = x["cache"].view(-1, 320)
     for t in range(n):
         flat[int(x["table"][0, t // 64]) * 64 + t % 64] = torch.from_numpy(enc[t])
-    # the key's first value alone makes the score, in the first CTA's partial: one rounding
-    score = SCALE * np.abs(F.decode_rows(enc)[:, 512]).max()
+    # the key's first value alone makes the score, in the first CTA's partial: one
+    # rounding (up to 64 rows run on single CTAs and round no scores)
+    score = SCALE * np.abs(F.decode_rows(enc)[:, 512]).max() if H > 64 else 0.0
     _check(x, score=score)
     _check(x, splits=5, score=score)
 
