@@ -30,13 +30,13 @@
 //     S^T [128 tok x 2 HC] = C_tile [128 x 576] * [Q_hi | Q_lo]^T          (K-major)
 //     O^T [512 x 3 HC] += C_tile^T [512 x 128] * [P_hi | P_mid | P_lo]^T   (MN-major)
 //
-// Warp roles (448 threads; 576 for 32 rows):
+// Warp roles (512 threads; 640 for 32 rows):
 //   first 4 (8) warps  softmax, one thread per token row of S^T and 16 heads; Q of
 //                      each segment; epilogue
 //   next 8 warps       expansion: the tile's rows from global memory into registers,
 //                      a tile ahead (40 KB in flight per SM), then through byte
 //                      permutations into one of two operand slots
-//   last 2 warps       TMEM and QK issuer; PV issuer
+//   last 4 warps       TMEM and QK issuer; PV issuer; two without work
 // Every wait is bounded: on timeout the CTA records MLA_ERR_DEVICE_TIMEOUT,
 // drains, frees its tensor memory and returns.
 #include <atomic>
@@ -58,13 +58,13 @@ constexpr uint32_t kLatBox = kTile * 128;                 // [128 tokens x 128 l
 constexpr uint32_t kRopeBox = 4 * kLatBox;                // offset of [128 tokens x 64 RoPE columns] E5M2, SW64
 constexpr uint32_t kSlotBytes = kRopeBox + kTile * kRope;  // 72 KB
 constexpr uint64_t kWaitLimitNs = 2000000000ull;          // 2 s
-constexpr float kRescaleThreshold = 2.f;                  // log2 units
-constexpr float kWeightBits = 13.f;                       // a weight is 2^13 at the running maximum, 2^15 at most
+constexpr float kRescaleThreshold = 5.f;                  // log2 units
+constexpr float kWeightBits = 10.f;                       // a weight is 2^10 at the running maximum, 2^15 at most
 
 template <int HC>
 struct Fp4Cfg {
   static constexpr int kSoftWarps = HC / 4;
-  static constexpr int kThreads = 32 * (kSoftWarps + kExpWarps + 2);
+  static constexpr int kThreads = 32 * (kSoftWarps + kExpWarps + 4);
   static constexpr int kNQ = 2 * HC, kNP = 3 * HC;          // N of the products
   static constexpr uint32_t kQBox = kNQ * 128;              // [2 HC rows x 128 columns] E4M3, SW128
   static constexpr uint32_t kQBytes = 4 * kQBox + kNQ * 64;  // + [2 HC rows x 64 RoPE columns], SW64
@@ -73,7 +73,7 @@ struct Fp4Cfg {
   static constexpr uint32_t kOffP = kOffQ + kQBytes;
   static constexpr uint32_t kOffLut = kOffP + 2 * kPBytes;  // magnitudes by scale byte
   static constexpr uint32_t kOffMisc = kOffLut + 256 * 8;
-  static constexpr uint32_t kMiscBytes = 256 + 15 * HC * 4;
+  static constexpr uint32_t kMiscBytes = 256 + 17 * HC * 4;
   static constexpr uint32_t kSmem = kOffMisc + kMiscBytes + 1024;  // +1024: base alignment slack
   static constexpr uint32_t kColS = 0;                       // + buf * 2 HC
   static constexpr uint32_t kColO = 128, kColOStep = HC == 16 ? 64 : 96, kTmemCols = 512;
@@ -82,7 +82,7 @@ struct Fp4Cfg {
 };
 
 struct Fp4Barriers {
-  uint64_t full[kSlots], empty[kSlots];  // operands expanded; PV has read them
+  uint64_t full[kSlots][2], empty[kSlots];  // latent boxes 0 and 1 expanded, the others; PV has read the slot
   uint64_t q_full, s_full[2], s_free[2], p_full[2], pv_done[2], o_full, o_free, drain[2];
   uint32_t tmem_base;
   int abort;
@@ -163,16 +163,17 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Fp4Barriers* B = reinterpret_cast<Fp4Barriers*>(smem + C::kOffMisc);
-  // [2][HC][4] maxima, [HC][4] sums, [HC] 1 / l, [2][HC] scale of Q's terms
+  // [2][HC][4] maxima, [HC][4] sums, [HC] 1 / l, [2][HC] scale of Q's terms, [HC]
+  // running maxima less kWeightBits, [HC] factors of a rescale
   float* red = reinterpret_cast<float*>(smem + C::kOffMisc + 256);
   const uint32_t sbase = smem_u32(smem);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
   constexpr int kQkWarp = C::kSoftWarps + kExpWarps, kPvWarp = kQkWarp + 1;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSlots; ++i) {
-      // the test hook: one arrival more than the first tile gets
-      mbar_init(&B->full[i], kExpWarps + (p.inject_wait_timeout && i == 0 ? 1 : 0));
+      // the test hook: one arrival more than the first box gets
+      for (int c = 0; c < 2; ++c) mbar_init(&B->full[i][c], kExpWarps + (p.inject_wait_timeout && i + c == 0 ? 1 : 0));
       mbar_init(&B->empty[i], 1);
     }
     mbar_init(&B->q_full, 32 * C::kSoftWarps);
@@ -207,47 +208,52 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
 
   if (warp >= C::kSoftWarps && warp < kQkWarp) {
     // ------------------------------------------------------------ expansion
-    // Thread (r0, j) takes block 4c + j of rows r0 and r0 + 64, c = 0 .. 3, and
-    // piece j of the rows' tails (RoPE blocks 16 and 17, scales 0 - 15, scales
-    // 16 and 17): four lanes read 64 bytes of a row, and their stores and those
-    // of the next row's lanes go to distinct banks.  A piece's register is
-    // loaded again, for the next tile, as soon as it has been expanded.
-    const int e = threadIdx.x - 32 * C::kSoftWarps, j = e & 3, r0 = e >> 2;
+    // A warp has rows 8w .. 8w + 7 and the 8 behind 64 + 8w, each of one page.
+    // Thread (r, j) takes block 4c + j of rows r and r + 64, c = 0 .. 3, and piece
+    // j of their tails (RoPE blocks 16 and 17, scales 0 - 15, scales 16 and 17):
+    // four lanes read 64 bytes of a row, and their stores and those of the next
+    // row's lanes go to distinct banks.  A piece's registers are loaded again,
+    // for the next tile, as soon as it has been expanded.
+    const int w8 = 8 * (warp - C::kSoftWarps), j = lane & 3, r = w8 + (lane >> 2);
     const int lane2 = (lane & ~3) + 2, lane3 = lane2 + 1;
-    const uint2* lut = reinterpret_cast<const uint2*>(smem + C::kOffLut);
-    const uint8_t* cache = static_cast<const uint8_t*>(p.cache) + 16 * j;
+    // the block's two 16-byte pieces in its row of a latent and of the RoPE box
+    const uint32_t at0 = r * 128 + (((2 * j) ^ (r & 7)) << 4), at1 = at0 ^ 16;
+    const uint32_t rope0 = kRopeBox + r * 64 + (((2 * j) ^ ((r >> 1) & 3)) << 4), rope1 = rope0 ^ 16;
+    const uint8_t* lut = smem + C::kOffLut;
+    const uint8_t* cache = static_cast<const uint8_t*>(p.cache) + (lane >> 2) * kFp4RowBytes + 16 * j;
+    const uint32_t byte_j = 0x4440 + j;  // byte j of a word
+    const int page_log2 = __ffs(p.page_size) - 1;
     TileWalkerT<true> walk;
     walk.init(p.tile_start, p.seg_base, p.len, p.batch, int(S), pa, pb);
-    TileInfo t;
-    // valid rows of the current, the next and the tile behind it; page ids of the last
-    int v0 = 0, v1 = 0, v2 = 0, tok1 = 0, tok2 = 0, pg1[2], pg2[2];
+    // valid rows of the current tile, the next and the one behind it (0: none);
+    // position of the warp's first row and its two pages in the latter two
+    int v0 = 0, v1 = 0, v2 = 0, tok1 = 0, tok2 = 0, pg1[2] = {}, pg2[2] = {};
     auto look = [&](int& valid, int& tok, int (&pg)[2]) {
+      TileInfo t;
       valid = 0;
-      tok = 0;
-      pg[0] = pg[1] = 0;
       if (!walk.next(t)) return;
       valid = t.valid;
-      tok = t.tile * kTile + r0;
+      tok = t.tile * kTile + w8;
       const int* bt = p.block_table + size_t(t.b) * p.max_pages;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        if (r0 + 64 * i < valid) pg[i] = __ldg(bt + (tok + 64 * i) / p.page_size);
+        if (w8 + 64 * i < valid) pg[i] = __ldg(bt + ((tok + 64 * i) >> page_log2));
     };
     auto row_of = [&](int tok, int page) -> const uint8_t* {
       if (uint32_t(page) >= uint32_t(p.num_pages)) {
         report_bad_page(p.status);
         page = 0;
       }
-      return cache + (size_t(page) * p.page_size + tok % p.page_size) * kFp4RowBytes;
+      return cache + ((size_t(page) << page_log2) + (tok & (p.page_size - 1))) * kFp4RowBytes;
     };
+    // scale bytes of 0 (values of 0) where there is no row
     uint4 v[2][5];
     look(v0, tok1, pg1);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const bool in = r0 + 64 * i < v0;
-      const uint8_t* row = in ? row_of(tok1 + 64 * i, pg1[i]) : nullptr;
+      const uint8_t* row = w8 + 64 * i < v0 ? row_of(tok1 + 64 * i, pg1[i]) : nullptr;
 #pragma unroll
-      for (int c = 0; c < 5; ++c) v[i][c] = in ? ld_stream(row + 64 * c) : make_uint4(0, 0, 0, 0);
+      for (int c = 0; c < 5; ++c) v[i][c] = r + 64 * i < v0 ? ld_stream(row + 64 * c) : make_uint4(0, 0, 0, 0);
     }
     look(v1, tok1, pg1);
     bool ok = true;
@@ -255,40 +261,44 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
       const uint32_t slot = k % kSlots;
       uint8_t* base = smem + slot * kSlotBytes;
       look(v2, tok2, pg2);
+      const uint8_t* row[2];
+      uint32_t at[2][5];  // where the blocks' magnitudes are in the table
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        row[i] = w8 + 64 * i < v1 ? row_of(tok1 + 64 * i, pg1[i]) : nullptr;
+        const uint32_t tail[5] = {
+            __shfl_sync(0xffffffffu, v[i][4].x, lane2), __shfl_sync(0xffffffffu, v[i][4].y, lane2),
+            __shfl_sync(0xffffffffu, v[i][4].z, lane2), __shfl_sync(0xffffffffu, v[i][4].w, lane2),
+            __shfl_sync(0xffffffffu, v[i][4].x, lane3)};
+#pragma unroll
+        for (int c = 0; c < 5; ++c) at[i][c] = __byte_perm(tail[c], 0, byte_j) * 8;
+      }
       ok = __all_sync(0xffffffffu, mbar_wait(&B->empty[slot], ((k / kSlots) & 1) ^ 1, abort_flag, kWaitLimitNs));
       if (!ok) break;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = r0 + 64 * i;
-        const bool in = r < v0, next = r < v1;
-        const uint8_t* row = next ? row_of(tok1 + 64 * i, pg1[i]) : nullptr;
-        const uint32_t tail[5] = {__shfl_sync(0xffffffffu, v[i][4].x, lane2), __shfl_sync(0xffffffffu, v[i][4].y, lane2),
-                                  __shfl_sync(0xffffffffu, v[i][4].z, lane2), __shfl_sync(0xffffffffu, v[i][4].w, lane2),
-                                  __shfl_sync(0xffffffffu, v[i][4].x, lane3)};
-        // rows at and past the tile's valid length are written as zeros
+      for (int c = 0; c < 5; ++c) {
+        if (c < 4 || j < 2) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint2 tab = in ? lut[(tail[c] >> (8 * j)) & 255] : make_uint2(0, 0);
-          uint4 lo, hi;
-          expand_block(v[i][c], tab, lo, hi);
-          uint8_t* dst = base + c * kLatBox + r * 128;
-          *reinterpret_cast<uint4*>(dst + (((2 * j) ^ (r & 7)) << 4)) = lo;
-          *reinterpret_cast<uint4*>(dst + (((2 * j + 1) ^ (r & 7)) << 4)) = hi;
-          if (next) v[i][c] = ld_stream(row + 64 * c);
+          for (int i = 0; i < 2; ++i) {
+            uint4 lo, hi;
+            expand_block(v[i][c], *reinterpret_cast<const uint2*>(lut + at[i][c]), lo, hi);
+            uint8_t* dst = base + (c < 4 ? c * kLatBox + 64 * 128 * i : 64 * 64 * i);
+            *reinterpret_cast<uint4*>(dst + (c < 4 ? at0 : rope0)) = lo;
+            *reinterpret_cast<uint4*>(dst + (c < 4 ? at1 : rope1)) = hi;
+          }
         }
-        if (j < 2) {
-          const uint2 tab = in ? lut[(tail[4] >> (8 * j)) & 255] : make_uint2(0, 0);
-          uint4 lo, hi;
-          expand_block(v[i][4], tab, lo, hi);
-          uint8_t* dst = base + kRopeBox + r * 64;
-          *reinterpret_cast<uint4*>(dst + (((2 * j) ^ ((r >> 1) & 3)) << 4)) = lo;
-          *reinterpret_cast<uint4*>(dst + (((2 * j + 1) ^ ((r >> 1) & 3)) << 4)) = hi;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (r + 64 * i < v1) v[i][c] = ld_stream(row[i] + 64 * c);
+          else if (c == 4) v[i][c] = make_uint4(0, 0, 0, 0);
         }
-        if (next) v[i][4] = ld_stream(row + 256);
+        if (c == 1 || c == 4) {
+          // no proxy fence here: it would wait for the loads in flight.  The QK
+          // issuer, which acquires these writes, fences for them.
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&B->full[slot][c >> 2]);
+        }
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&B->full[slot]);
       v0 = v1;
       v1 = v2;
       tok1 = tok2;
@@ -296,71 +306,99 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
       pg1[1] = pg2[1];
     }
     if (!ok) fail(B, p.status);
-  } else if (warp == kQkWarp && lane == 0) {
-    // ------------------------------------------------------------ QK issuer
-    TileWalkerT<true> walk;
-    walk.init(p.tile_start, p.seg_base, p.len, p.batch, int(S), pa, pb);
-    constexpr uint32_t id_qk = idesc_f8(128, C::kNQ, false, false);
-    constexpr uint64_t kDescK = smem_desc(0, 16, 1024, kSwizzle128B);   // K-major SW128 (8-row groups of 1 KB)
-    constexpr uint64_t kDescRope = smem_desc(0, 16, 512, kSwizzle64B);  // K-major SW64 (8-row groups of 512 B)
-    uint32_t k = 0, seg = 0;
-    TileInfo t;
-    bool ok = true;
-    while (ok && walk.next(t)) {
-      const uint32_t slot = k % kSlots, buf = k & 1;
-      // every softmax thread has read tile k - 2's scores
-      if (k >= 2 && !(ok = mbar_wait(&B->s_free[buf], ((k - 2) >> 1) & 1, abort_flag, kWaitLimitNs))) break;
-      if (t.first && !(ok = mbar_wait(&B->q_full, seg++ & 1, abort_flag, kWaitLimitNs))) break;
-      if (!(ok = mbar_wait(&B->full[slot], (k / kSlots) & 1, abort_flag, kWaitLimitNs))) break;
-      tc_fence_after();
-      const uint32_t d = tmem + C::kColS + buf * C::kNQ, a = sbase + slot * kSlotBytes, q = sbase + C::kOffQ;
+  } else if (warp >= kQkWarp) {
+    // Whole warps wait and compute addresses, one lane issues: with everything
+    // uniform a product costs a few instructions (with a single lane in the
+    // role, 190 cycles each).
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, kWaitLimitNs)) != 0;
+    };
+    if (warp == kQkWarp) {
+      // ------------------------------------------------------------ QK issuer
+      TileWalkerT<true> walk;
+      walk.init(p.tile_start, p.seg_base, p.len, p.batch, int(S), pa, pb);
+      constexpr uint32_t id_qk = idesc_f8(128, C::kNQ, false, false);
+      constexpr uint64_t kDescK = smem_desc(0, 16, 1024, kSwizzle128B);   // K-major SW128 (8-row groups of 1 KB)
+      constexpr uint64_t kDescRope = smem_desc(0, 16, 512, kSwizzle64B);  // K-major SW64 (8-row groups of 512 B)
+      const uint64_t q = desc_addr(sbase + C::kOffQ);  // (no sum of addresses here leaves the descriptors' 14-bit field)
+      uint32_t k = 0, seg = 0;
+      TileInfo t;
+      bool ok = true;
+      while (walk.next(t)) {
+        const uint32_t slot = k % kSlots, buf = k & 1;
+        // every softmax thread has read tile k - 2's scores
+        if (k >= 2 && !(ok = wait(&B->s_free[buf], ((k - 2) >> 1) & 1))) break;
+        if (t.first && !(ok = wait(&B->q_full, seg++ & 1))) break;
+        const uint32_t d = tmem + C::kColS + buf * C::kNQ;
+        const uint64_t a = desc_addr(sbase + slot * kSlotBytes);
 #pragma unroll
-      for (int kk = 0; kk < 16; ++kk)
-        mma_f8(d, kDescK | desc_addr(a + (kk >> 2) * kLatBox + 32 * (kk & 3)),
-               kDescK | desc_addr(q + (kk >> 2) * C::kQBox + 32 * (kk & 3)), id_qk, kk > 0);
+        for (int c = 0; c < 5; ++c) {
+          if (c == 0 || c == 2) {
+            if (!(ok = wait(&B->full[slot][c >> 1], (k / kSlots) & 1))) break;
+            fence_proxy_async_smem();  // the expansion's writes, for this warp's and the PV issuer's products
+            tc_fence_after();
+          }
+          if (elect_one()) {
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk)
-        mma_f8(d, kDescRope | desc_addr(a + kRopeBox + 32 * kk), kDescRope | desc_addr(q + 4 * C::kQBox + 32 * kk), id_qk, 1);
-      mma_commit(&B->s_full[buf]);
-      ++k;
-    }
-    if (!ok) fail(B, p.status);
-    mma_commit(&B->drain[0]);  // every MMA this thread issued completes before teardown
-    mbar_wait_until(&B->drain[0], 0, global_timer_ns() + kWaitLimitNs / 4);
-  } else if (warp == kPvWarp && lane == 0) {
-    // ------------------------------------------------------------ PV issuer
-    TileWalkerT<true> walk;
-    walk.init(p.tile_start, p.seg_base, p.len, p.batch, int(S), pa, pb);
-    constexpr uint32_t id_pv = idesc_f8(128, C::kNP, true, true);
-    constexpr uint64_t kDescMN = smem_desc(0, kLatBox, 1024, kSwizzle128B);  // MN-major SW128: 128 columns, 8-token groups
-    constexpr uint64_t kDescP = smem_desc(0, 128, 2048, kSwizzleNone);       // P^T core matrices
-    uint32_t k = 0, seg = 0;
-    TileInfo t;
-    bool ok = true;
-    while (ok && walk.next(t)) {
-      const uint32_t slot = k % kSlots, buf = k & 1;
-      if (!(ok = mbar_wait(&B->p_full[buf], (k >> 1) & 1, abort_flag, kWaitLimitNs))) break;
-      if (t.first && seg > 0 && !(ok = mbar_wait(&B->o_free, (seg - 1) & 1, abort_flag, kWaitLimitNs))) break;
-      tc_fence_after();
-      const int nk = (t.valid + 31) >> 5;
-      const uint32_t a = sbase + slot * kSlotBytes, b = sbase + C::kOffP + buf * C::kPBytes;
-#pragma unroll 1
-      for (int c = 0; c < 4; ++c)
-        for (int kk = 0; kk < nk; ++kk)
-          mma_f8(tmem + C::kColO + c * C::kColOStep, kDescMN | desc_addr(a + c * kLatBox + 4096 * kk),
-                 kDescP | desc_addr(b + 512 * kk), id_pv, !(t.first && kk == 0));
-      mma_commit(&B->empty[slot]);
-      mma_commit(&B->pv_done[buf]);
-      if (t.last) {
-        mma_commit(&B->o_full);
-        ++seg;
+            for (int kk = 0; kk < (c < 4 ? 4 : 2); ++kk)
+              mma_f8(d, (c < 4 ? kDescK : kDescRope) + a + (c * kLatBox + 32 * kk) / 16,
+                     (c < 4 ? kDescK : kDescRope) + q + (c * C::kQBox + 32 * kk) / 16, id_qk, c + kk > 0);
+            if (c == 4) mma_commit(&B->s_full[buf]);
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        ++k;
       }
-      ++k;
+      if (!ok) fail(B, p.status);
+      if (elect_one()) {  // every product this lane issued completes before teardown
+        mma_commit(&B->drain[0]);
+        mbar_wait_until(&B->drain[0], 0, global_timer_ns() + kWaitLimitNs / 4);
+      }
+      __syncwarp();
+    } else if (warp == kPvWarp) {
+      // ------------------------------------------------------------ PV issuer
+      TileWalkerT<true> walk;
+      walk.init(p.tile_start, p.seg_base, p.len, p.batch, int(S), pa, pb);
+      constexpr uint32_t id_pv = idesc_f8(128, C::kNP, true, true);
+      constexpr uint64_t kDescMN = smem_desc(0, kLatBox, 1024, kSwizzle128B);  // MN-major SW128: 128 columns, 8-token groups
+      constexpr uint64_t kDescP = smem_desc(0, 128, 2048, kSwizzleNone);       // P^T core matrices
+      uint32_t k = 0, seg = 0;
+      TileInfo t;
+      bool ok = true;
+      while (walk.next(t)) {
+        const uint32_t slot = k % kSlots, buf = k & 1;
+        if (!(ok = wait(&B->p_full[buf], (k >> 1) & 1))) break;
+        if (t.first && seg > 0 && !(ok = wait(&B->o_free, (seg - 1) & 1))) break;
+        tc_fence_after();
+        const int nk = (t.valid + 31) >> 5;
+        const uint64_t a = kDescMN + desc_addr(sbase + slot * kSlotBytes);
+        const uint64_t b = kDescP + desc_addr(sbase + C::kOffP + buf * C::kPBytes);
+        const uint32_t later = !t.first;
+        if (elect_one()) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t d = tmem + C::kColO + c * C::kColOStep;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              if (kk < nk) mma_f8(d, a + (c * kLatBox + 4096 * kk) / 16, b + 512 * kk / 16, id_pv, kk > 0 ? 1u : later);
+          }
+          mma_commit(&B->empty[slot]);
+          mma_commit(&B->pv_done[buf]);
+          if (t.last) mma_commit(&B->o_full);
+        }
+        __syncwarp();
+        if (t.last) ++seg;
+        ++k;
+      }
+      if (!ok) fail(B, p.status);
+      if (elect_one()) {
+        mma_commit(&B->drain[1]);
+        mbar_wait_until(&B->drain[1], 0, global_timer_ns() + kWaitLimitNs / 4);
+      }
+      __syncwarp();
     }
-    if (!ok) fail(B, p.status);
-    mma_commit(&B->drain[1]);
-    mbar_wait_until(&B->drain[1], 0, global_timer_ns() + kWaitLimitNs / 4);
-  } else if (warp < C::kSoftWarps) {
+  } else {
     // ------------------------------------------------------------ Q, softmax, epilogue
     // Group c (four warps) has heads 16c .. 16c + 15 of the head group; thread st
     // of it the token row st of S^T (its TMEM lane).
@@ -420,7 +458,9 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
       fence_proxy_async_smem();
       mbar_arrive(&B->q_full);
     };
-    float m_run[16], l_run[16];  // m_run: the running maximum less kWeightBits
+    float* m_run = red + 15 * HC + 16 * c;  // kept once for the group's threads
+    float* alpha = red + 16 * HC + 16 * c;
+    float l_run[16];
     uint32_t k = 0, seg = 0;
     TileInfo t, tn;
     bool have = walk.next(t);
@@ -462,13 +502,17 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
           if (pos > (g * HC + 16 * c + h) / p.heads_w) x[h] = -INFINITY;
       }
       // Running max: as in decode_tc.cu it only has to bound the scores, here to
-      // within a factor of 4, so that the weights use E5M2's range down.
+      // within 2^5, so that the weights keep E5M2's range down.
       bool over = false;
       if (!t.first) {
 #pragma unroll
-        for (int h = 0; h < 16; ++h) over |= x[h] > m_run[h] + (kWeightBits + kRescaleThreshold);
+        for (int h4 = 0; h4 < 4; ++h4) {
+          const float4 m = reinterpret_cast<const float4*>(m_run)[h4];
+          constexpr float kTop = kWeightBits + kRescaleThreshold;
+          over |= x[4 * h4] > m.x + kTop || x[4 * h4 + 1] > m.y + kTop || x[4 * h4 + 2] > m.z + kTop ||
+                  x[4 * h4 + 3] > m.w + kTop;
+        }
       }
-      float alpha[16];
       bool rescale = false;
       if (t.first || group_any(c, over || !ok)) {
         float* rm = red + buf * 4 * HC + 64 * c;
@@ -480,25 +524,31 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
           if (!(lane & 1)) rm[(lane >> 1) * 4 + q4] = wm;
         }
         if (group_any(c, !ok)) break;
-#pragma unroll
-        for (int h = 0; h < 16; ++h) {
-          const float4 m4 = reinterpret_cast<const float4*>(rm)[h];
-          const float mt = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
-          alpha[h] = 1.f;
+        if (st < 16) {  // thread h: head h's maximum over the tile
+          const float4 m4 = reinterpret_cast<const float4*>(rm)[st];
+          const float mt = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w)), old = m_run[st];
+          float a = 1.f;
           if (t.first) {
-            m_run[h] = fmaxf(mt, kEmptyRowMax) - kWeightBits;  // a row masked in the whole tile stays empty
-            l_run[h] = 0.f;
-          } else if (mt > m_run[h] + (kWeightBits + kRescaleThreshold)) {
-            alpha[h] = exp2f(m_run[h] - (mt - kWeightBits));
-            m_run[h] = mt - kWeightBits;
-            l_run[h] *= alpha[h];
+            m_run[st] = fmaxf(mt, kEmptyRowMax) - kWeightBits;  // a row masked in the whole tile stays empty
+          } else if (mt > old + (kWeightBits + kRescaleThreshold)) {
+            a = exp2f(old - (mt - kWeightBits));
+            m_run[st] = mt - kWeightBits;
             rescale = true;
           }
+          alpha[st] = a;
+        }
+        rescale = group_any(c, rescale);
+        if (t.first) {
+#pragma unroll
+          for (int h = 0; h < 16; ++h) l_run[h] = 0.f;
+        } else {
+#pragma unroll
+          for (int h = 0; h < 16; ++h) l_run[h] *= alpha[h];
         }
       }
       if (rescale) {
-        // uniform across the group.  QK of this tile may have been issued
-        // before PV of the previous one: wait for that PV first.
+        // QK of this tile may have been issued before PV of the previous one:
+        // wait for that PV first
         const bool ok3 = mbar_wait(&B->pv_done[(k - 1) & 1], ((k - 1) >> 1) & 1, abort_flag, kWaitLimitNs);
         tc_fence_after();
         if (group_any(c, !ok3)) break;
@@ -518,11 +568,16 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
       {
         uint32_t w[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float a = ex2_ftz(x[2 * i] - m_run[2 * i]), b = ex2_ftz(x[2 * i + 1] - m_run[2 * i + 1]);
-          l_run[2 * i] += a;
-          l_run[2 * i + 1] += b;
-          w[i] = pack_f16x2(a, b);
+        for (int h4 = 0; h4 < 4; ++h4) {
+          const float4 m = reinterpret_cast<const float4*>(m_run)[h4];
+          const float e0 = ex2_ftz(x[4 * h4] - m.x), e1 = ex2_ftz(x[4 * h4 + 1] - m.y);
+          const float e2 = ex2_ftz(x[4 * h4 + 2] - m.z), e3 = ex2_ftz(x[4 * h4 + 3] - m.w);
+          l_run[4 * h4] += e0;
+          l_run[4 * h4 + 1] += e1;
+          l_run[4 * h4 + 2] += e2;
+          l_run[4 * h4 + 3] += e3;
+          w[2 * h4] = pack_f16x2(e0, e1);
+          w[2 * h4 + 1] = pack_f16x2(e2, e3);
         }
         uint8_t* pt = smem + C::kOffP + buf * C::kPBytes + c * 2048 + (st >> 3) * 128 + (st & 7) * 16;
 #pragma unroll
@@ -581,11 +636,7 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
         tc_fence_before();
         mbar_arrive(&B->o_free);
         if (st < 16) {  // thread h writes head h's lse
-          float mh = 0.f;
-#pragma unroll
-          for (int h = 0; h < 16; ++h)
-            if (st == h) mh = m_run[h];
-          p.partial_lse[size_t(t.seg) * p.heads + row0 + st] = l > 0.f ? (mh + log2f(l)) * kLn2 : lse_of_no_sum(l);
+          p.partial_lse[size_t(t.seg) * p.heads + row0 + st] = l > 0.f ? (m_run[st] + log2f(l)) * kLn2 : lse_of_no_sum(l);
         }
         ++seg;
       }
