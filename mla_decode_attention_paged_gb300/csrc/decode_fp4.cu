@@ -36,7 +36,7 @@
 //   next 8 warps       expansion: the tile's rows from global memory into registers,
 //                      a tile ahead (40 KB in flight per SM), then through byte
 //                      permutations into one of two operand slots
-//   last 4 warps       TMEM and QK issuer; PV issuer; two without work
+//   last 4 warps       TMEM and QK issuer; PV issuer; L2 prefetch; one without work
 // Every wait is bounded: on timeout the CTA records MLA_ERR_DEVICE_TIMEOUT,
 // drains, frees its tensor memory and returns.
 #include <atomic>
@@ -52,8 +52,9 @@ namespace {
 using namespace ptx;
 using namespace dc;
 
-constexpr int kExpWarps = 8;
 constexpr int kSlots = 2;
+constexpr int kAhead = 4;                                 // tiles between the page lookup and the expansion
+constexpr int kRing = 8;                                  // tiles of looked-up pages kept
 constexpr uint32_t kLatBox = kTile * 128;                 // [128 tokens x 128 latent columns] E5M2, SW128: one O^T chunk
 constexpr uint32_t kRopeBox = 4 * kLatBox;                // offset of [128 tokens x 64 RoPE columns] E5M2, SW64
 constexpr uint32_t kSlotBytes = kRopeBox + kTile * kRope;  // 72 KB
@@ -63,7 +64,10 @@ constexpr float kWeightBits = 10.f;                       // a weight is 2^10 at
 
 template <int HC>
 struct Fp4Cfg {
-  static constexpr int kSoftWarps = HC / 4;
+  // 16 rows: groups of 8 heads and one cached row to an expansion thread; 32
+  // rows: 16 heads, two rows (36 warps would be the other way)
+  static constexpr int kHeads = HC / 2, kSoftWarps = 8;
+  static constexpr int kRowsPer = HC == 16 ? 1 : 2, kExpWarps = 16 / kRowsPer;
   static constexpr int kThreads = 32 * (kSoftWarps + kExpWarps + 4);
   static constexpr int kNQ = 2 * HC, kNP = 3 * HC;          // N of the products
   static constexpr uint32_t kQBox = kNQ * 128;              // [2 HC rows x 128 columns] E4M3, SW128
@@ -73,7 +77,7 @@ struct Fp4Cfg {
   static constexpr uint32_t kOffP = kOffQ + kQBytes;
   static constexpr uint32_t kOffLut = kOffP + 2 * kPBytes;  // magnitudes by scale byte
   static constexpr uint32_t kOffMisc = kOffLut + 256 * 8;
-  static constexpr uint32_t kMiscBytes = 256 + 17 * HC * 4;
+  static constexpr uint32_t kMiscBytes = 1024 + 17 * HC * 4;
   static constexpr uint32_t kSmem = kOffMisc + kMiscBytes + 1024;  // +1024: base alignment slack
   static constexpr uint32_t kColS = 0;                       // + buf * 2 HC
   static constexpr uint32_t kColO = 128, kColOStep = HC == 16 ? 64 : 96, kTmemCols = 512;
@@ -82,12 +86,17 @@ struct Fp4Cfg {
 };
 
 struct Fp4Barriers {
-  uint64_t full[kSlots][2], empty[kSlots];  // latent boxes 0 and 1 expanded, the others; PV has read the slot
+  // RoPE and latent boxes 0 and 1 expanded, boxes 2 and 3; PV has read boxes 0 and 1, 2 and 3
+  uint64_t full[kSlots][2], empty[kSlots][2];
   uint64_t q_full, s_full[2], s_free[2], p_full[2], pv_done[2], o_full, o_free, drain[2];
+  uint64_t ring_full[kRing];
   uint32_t tmem_base;
   int abort;
+  int expanding;               // the tile that the expansion is at
+  int valid[kRing];            // rows of a tile, 0 behind the last
+  const uint8_t* page[kRing][kTile / 16];  // first row of each of its pages
 };
-static_assert(sizeof(Fp4Barriers) <= 256, "barriers");
+static_assert(sizeof(Fp4Barriers) <= 1024, "barriers and page ring");
 
 __device__ __forceinline__ void fail(Fp4Barriers* B, int* status) {
   B->abort = 1;
@@ -108,6 +117,39 @@ __device__ __forceinline__ bool group_any(int group, bool pred) {
   return r != 0;
 }
 
+// Reduces 8 or 16 values per lane over a warp, each lane keeping half of them a
+// round; every lane gets that of value lane / (32 / N).
+template <int N, bool kMax>
+__device__ __forceinline__ float warp_reduce(float (&v)[N], int lane) {
+  if constexpr (N == 16) {
+    return warp_transpose_reduce<16, kMax>(v, lane);
+  } else {
+    static_assert(N == 8, "8 or 16 values per lane");
+#pragma unroll
+    for (int w = 4, o = 16; w >= 1; w >>= 1, o >>= 1) {
+      const bool upper = lane & o;
+#pragma unroll
+      for (int i = 0; i < w; ++i) {
+        const float keep = upper ? v[i + w] : v[i], send = upper ? v[i] : v[i + w];
+        const float got = __shfl_xor_sync(0xffffffffu, send, o);
+        v[i] = kMax ? fmaxf(keep, got) : keep + got;
+      }
+    }
+#pragma unroll
+    for (int o = 2; o > 0; o >>= 1) {
+      const float got = __shfl_xor_sync(0xffffffffu, v[0], o);
+      v[0] = kMax ? fmaxf(v[0], got) : v[0] + got;
+    }
+    return v[0];
+  }
+}
+// N (8 or 16) tensor memory columns.
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t a, float (&v)[N]) {
+  if constexpr (N == 16) tmem_ld16(a, v);
+  else tmem_ld8(a, v);
+}
+
 // Instruction descriptor, kind::f8f6f4, fp32 accumulator (bits 4-5 = 1): A is
 // E5M2 (bits 7-9 = 1), B E5M2 or E4M3 (bits 10-12 = 1 or 0), the rest as for f16.
 constexpr uint32_t idesc_f8(int M, int N, bool mn_major, bool b_e5m2) {
@@ -122,6 +164,18 @@ __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+template <int N>
+__device__ __forceinline__ void tmem_store(uint32_t a, const float (&v)[N]) {
+  if constexpr (N == 16) {
+    tmem_st16(a, v);
+  } else {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(a),
+                 "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
+                 "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
+                 "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7]))
+                 : "memory");
+  }
 }
 // Two fp32 values to E4M3, `lo` in the low byte.
 __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
@@ -165,17 +219,18 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
   Fp4Barriers* B = reinterpret_cast<Fp4Barriers*>(smem + C::kOffMisc);
   // [2][HC][4] maxima, [HC][4] sums, [HC] 1 / l, [2][HC] scale of Q's terms, [HC]
   // running maxima less kWeightBits, [HC] factors of a rescale
-  float* red = reinterpret_cast<float*>(smem + C::kOffMisc + 256);
+  float* red = reinterpret_cast<float*>(smem + C::kOffMisc + 1024);
   const uint32_t sbase = smem_u32(smem);
   const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
-  constexpr int kQkWarp = C::kSoftWarps + kExpWarps, kPvWarp = kQkWarp + 1;
+  constexpr int kQkWarp = C::kSoftWarps + C::kExpWarps, kPvWarp = kQkWarp + 1;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSlots; ++i) {
       // the test hook: one arrival more than the first box gets
-      for (int c = 0; c < 2; ++c) mbar_init(&B->full[i][c], kExpWarps + (p.inject_wait_timeout && i + c == 0 ? 1 : 0));
-      mbar_init(&B->empty[i], 1);
+      for (int c = 0; c < 2; ++c) mbar_init(&B->full[i][c], C::kExpWarps + (p.inject_wait_timeout && i + c == 0 ? 1 : 0));
+      for (int c = 0; c < 2; ++c) mbar_init(&B->empty[i][c], 1);
     }
+    for (int i = 0; i < kRing; ++i) mbar_init(&B->ring_full[i], 1);
     mbar_init(&B->q_full, 32 * C::kSoftWarps);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&B->s_full[i], 1);
@@ -187,6 +242,7 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
     mbar_init(&B->o_full, 1);
     mbar_init(&B->o_free, 32 * C::kSoftWarps);
     B->abort = 0;
+    B->expanding = 0;
     fence_mbar_init();
   }
   if (warp == kQkWarp) {
@@ -208,64 +264,49 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
 
   if (warp >= C::kSoftWarps && warp < kQkWarp) {
     // ------------------------------------------------------------ expansion
-    // A warp has rows 8w .. 8w + 7 and the 8 behind 64 + 8w, each of one page.
-    // Thread (r, j) takes block 4c + j of rows r and r + 64, c = 0 .. 3, and piece
-    // j of their tails (RoPE blocks 16 and 17, scales 0 - 15, scales 16 and 17):
-    // four lanes read 64 bytes of a row, and their stores and those of the next
-    // row's lanes go to distinct banks.  A piece's registers are loaded again,
-    // for the next tile, as soon as it has been expanded.
+    // A warp has rows 8w .. 8w + 7 (two to a thread: and the 8 behind 64 + 8w),
+    // each of one page.  Thread (r, j) takes block 4c + j of row r, c = 0 .. 3, and
+    // piece j of its tail (RoPE blocks 16 and 17, scales 0 - 15, scales 16 and
+    // 17): four lanes read 64 bytes of a row, and their stores and those of the
+    // next row's lanes go to distinct banks.  A piece's registers are loaded
+    // again, for the next tile, as soon as it has been expanded.
+    constexpr int R = C::kRowsPer;
     const int w8 = 8 * (warp - C::kSoftWarps), j = lane & 3, r = w8 + (lane >> 2);
     const int lane2 = (lane & ~3) + 2, lane3 = lane2 + 1;
     // the block's two 16-byte pieces in its row of a latent and of the RoPE box
     const uint32_t at0 = r * 128 + (((2 * j) ^ (r & 7)) << 4), at1 = at0 ^ 16;
     const uint32_t rope0 = kRopeBox + r * 64 + (((2 * j) ^ ((r >> 1) & 3)) << 4), rope1 = rope0 ^ 16;
     const uint8_t* lut = smem + C::kOffLut;
-    const uint8_t* cache = static_cast<const uint8_t*>(p.cache) + (lane >> 2) * kFp4RowBytes + 16 * j;
     const uint32_t byte_j = 0x4440 + j;  // byte j of a word
+    // where this thread's first row is, from its page's first, and the others' pages
     const int page_log2 = __ffs(p.page_size) - 1;
-    TileWalkerT<true> walk;
-    walk.init(p.tile_start, p.seg_base, p.len, p.batch, int(S), pa, pb);
-    // valid rows of the current tile, the next and the one behind it (0: none);
-    // position of the warp's first row and its two pages in the latter two
-    int v0 = 0, v1 = 0, v2 = 0, tok1 = 0, tok2 = 0, pg1[2] = {}, pg2[2] = {};
-    auto look = [&](int& valid, int& tok, int (&pg)[2]) {
-      TileInfo t;
-      valid = 0;
-      if (!walk.next(t)) return;
-      valid = t.valid;
-      tok = t.tile * kTile + w8;
-      const int* bt = p.block_table + size_t(t.b) * p.max_pages;
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (w8 + 64 * i < valid) pg[i] = __ldg(bt + ((tok + 64 * i) >> page_log2));
-    };
-    auto row_of = [&](int tok, int page) -> const uint8_t* {
-      if (uint32_t(page) >= uint32_t(p.num_pages)) {
-        report_bad_page(p.status);
-        page = 0;
-      }
-      return cache + ((size_t(page) << page_log2) + (tok & (p.page_size - 1))) * kFp4RowBytes;
-    };
-    // scale bytes of 0 (values of 0) where there is no row
-    uint4 v[2][5];
-    look(v0, tok1, pg1);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint8_t* row = w8 + 64 * i < v0 ? row_of(tok1 + 64 * i, pg1[i]) : nullptr;
-#pragma unroll
-      for (int c = 0; c < 5; ++c) v[i][c] = r + 64 * i < v0 ? ld_stream(row + 64 * c) : make_uint4(0, 0, 0, 0);
-    }
-    look(v1, tok1, pg1);
+    const uint32_t row_off = (r & (p.page_size - 1)) * kFp4RowBytes + 16 * j;
+    // the pages of tile k; scale bytes of 0 (values of 0) where there is no row
+    const uint8_t* row[R];
     bool ok = true;
-    for (uint32_t k = 0; v0 > 0; ++k) {
+    auto look = [&](uint32_t k) -> int {
+      const int e = k % kRing;
+      ok = __all_sync(0xffffffffu, mbar_wait(&B->ring_full[e], (k / kRing) & 1, abort_flag, kWaitLimitNs));
+      if (!ok) return 0;
+#pragma unroll
+      for (int i = 0; i < R; ++i) row[i] = B->page[e][(w8 + 64 * i) >> page_log2] + row_off;
+      return B->valid[e];
+    };
+    uint4 v[R][5];
+    int v0 = look(0), v1 = 0;
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int c = 0; c < 5; ++c) v[i][c] = r + 64 * i < v0 ? ld_stream(row[i] + 64 * c) : make_uint4(0, 0, 0, 0);
+    for (uint32_t k = 0; v0 > 0; ++k, v0 = v1) {
       const uint32_t slot = k % kSlots;
       uint8_t* base = smem + slot * kSlotBytes;
-      look(v2, tok2, pg2);
-      const uint8_t* row[2];
-      uint32_t at[2][5];  // where the blocks' magnitudes are in the table
+      if (threadIdx.x == 32 * C::kSoftWarps) *reinterpret_cast<volatile int*>(&B->expanding) = int(k);
+      v1 = look(k + 1);
+      if (!ok) break;
+      uint32_t at[R][5];  // where the blocks' magnitudes are in the table
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        row[i] = w8 + 64 * i < v1 ? row_of(tok1 + 64 * i, pg1[i]) : nullptr;
+      for (int i = 0; i < R; ++i) {
         const uint32_t tail[5] = {
             __shfl_sync(0xffffffffu, v[i][4].x, lane2), __shfl_sync(0xffffffffu, v[i][4].y, lane2),
             __shfl_sync(0xffffffffu, v[i][4].z, lane2), __shfl_sync(0xffffffffu, v[i][4].w, lane2),
@@ -273,13 +314,17 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
 #pragma unroll
         for (int c = 0; c < 5; ++c) at[i][c] = __byte_perm(tail[c], 0, byte_j) * 8;
       }
-      ok = __all_sync(0xffffffffu, mbar_wait(&B->empty[slot], ((k / kSlots) & 1) ^ 1, abort_flag, kWaitLimitNs));
-      if (!ok) break;
+      // the tails first: their registers are the first that the next tile needs
 #pragma unroll
-      for (int c = 0; c < 5; ++c) {
+      for (int cc = 0; cc < 5; ++cc) {
+        const int c = cc == 0 ? 4 : cc - 1;
+        if (c == 4 || c == 2) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&B->empty[slot][c & 2 ? 1 : 0], ((k / kSlots) & 1) ^ 1, abort_flag, kWaitLimitNs));
+          if (!ok) break;
+        }
         if (c < 4 || j < 2) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
+          for (int i = 0; i < R; ++i) {
             uint4 lo, hi;
             expand_block(v[i][c], *reinterpret_cast<const uint2*>(lut + at[i][c]), lo, hi);
             uint8_t* dst = base + (c < 4 ? c * kLatBox + 64 * 128 * i : 64 * 64 * i);
@@ -288,22 +333,18 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
           }
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < R; ++i) {
           if (r + 64 * i < v1) v[i][c] = ld_stream(row[i] + 64 * c);
           else if (c == 4) v[i][c] = make_uint4(0, 0, 0, 0);
         }
-        if (c == 1 || c == 4) {
+        if (c == 1 || c == 3) {
           // no proxy fence here: it would wait for the loads in flight.  The QK
           // issuer, which acquires these writes, fences for them.
           __syncwarp();
-          if (lane == 0) mbar_arrive(&B->full[slot][c >> 2]);
+          if (lane == 0) mbar_arrive(&B->full[slot][c >> 1]);
         }
       }
-      v0 = v1;
-      v1 = v2;
-      tok1 = tok2;
-      pg1[0] = pg2[0];
-      pg1[1] = pg2[1];
+      if (!ok) break;
     }
     if (!ok) fail(B, p.status);
   } else if (warp >= kQkWarp) {
@@ -332,18 +373,22 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
         const uint32_t d = tmem + C::kColS + buf * C::kNQ;
         const uint64_t a = desc_addr(sbase + slot * kSlotBytes);
 #pragma unroll
-        for (int c = 0; c < 5; ++c) {
-          if (c == 0 || c == 2) {
-            if (!(ok = wait(&B->full[slot][c >> 1], (k / kSlots) & 1))) break;
-            fence_proxy_async_smem();  // the expansion's writes, for this warp's and the PV issuer's products
-            tc_fence_after();
-          }
+        for (int half = 0; half < 2; ++half) {
+          if (!(ok = wait(&B->full[slot][half], (k / kSlots) & 1))) break;
+          fence_proxy_async_smem();  // the expansion's writes, for this warp's and the PV issuer's products
+          tc_fence_after();
           if (elect_one()) {
+            if (half == 0) {
 #pragma unroll
-            for (int kk = 0; kk < (c < 4 ? 4 : 2); ++kk)
-              mma_f8(d, (c < 4 ? kDescK : kDescRope) + a + (c * kLatBox + 32 * kk) / 16,
-                     (c < 4 ? kDescK : kDescRope) + q + (c * C::kQBox + 32 * kk) / 16, id_qk, c + kk > 0);
-            if (c == 4) mma_commit(&B->s_full[buf]);
+              for (int kk = 0; kk < 2; ++kk)
+                mma_f8(d, kDescRope + a + (kRopeBox + 32 * kk) / 16, kDescRope + q + (4 * C::kQBox + 32 * kk) / 16, id_qk, kk);
+            }
+#pragma unroll
+            for (int kk = 8 * half; kk < 8 * half + 8; ++kk) {
+              const uint32_t box = kk >> 2, col = 32 * (kk & 3);
+              mma_f8(d, kDescK + a + (box * kLatBox + col) / 16, kDescK + q + (box * C::kQBox + col) / 16, id_qk, 1);
+            }
+            if (half == 1) mma_commit(&B->s_full[buf]);
           }
           __syncwarp();
         }
@@ -382,8 +427,8 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               if (kk < nk) mma_f8(d, a + (c * kLatBox + 4096 * kk) / 16, b + 512 * kk / 16, id_pv, kk > 0 ? 1u : later);
+            if (c & 1) mma_commit(&B->empty[slot][c >> 1]);
           }
-          mma_commit(&B->empty[slot]);
           mma_commit(&B->pv_done[buf]);
           if (t.last) mma_commit(&B->o_full);
         }
@@ -397,27 +442,59 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
         mbar_wait_until(&B->drain[1], 0, global_timer_ns() + kWaitLimitNs / 4);
       }
       __syncwarp();
+    } else if (warp == kPvWarp + 1) {
+      // ------------------------------------------------------------ page lookup
+      // Where the rows of tile k + kAhead are when the expansion is at tile k (it
+      // reads the ring a tile ahead), and those rows' way into L2.
+      TileWalkerT<true> walk;
+      walk.init(p.tile_start, p.seg_base, p.len, p.batch, int(S), pa, pb);
+      const volatile int* at = &B->expanding;
+      const int page_log2 = __ffs(p.page_size) - 1;
+      TileInfo t;
+      bool more = true, ok = true;
+      for (int k = 0; more; ++k) {
+        const uint64_t t0 = global_timer_ns();
+        while (*at + kAhead < k && (ok = !*abort_flag && global_timer_ns() - t0 < kWaitLimitNs)) __nanosleep(64);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        more = walk.next(t);
+        const int e = k % kRing, first = lane << page_log2;
+        if (more && first < t.valid) {
+          int page = __ldg(p.block_table + size_t(t.b) * p.max_pages + ((t.tile * kTile) >> page_log2) + lane);
+          if (uint32_t(page) >= uint32_t(p.num_pages)) {
+            report_bad_page(p.status);
+            page = 0;
+          }
+          const uint8_t* rows = static_cast<const uint8_t*>(p.cache) + (size_t(page) << page_log2) * kFp4RowBytes;
+          B->page[e][lane] = rows;
+          if (k > 0) prefetch_l2(rows, min(p.page_size, t.valid - first) * kFp4RowBytes);
+        }
+        if (lane == 0) B->valid[e] = more ? t.valid : 0;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&B->ring_full[e]);
+      }
     }
   } else {
     // ------------------------------------------------------------ Q, softmax, epilogue
-    // Group c (four warps) has heads 16c .. 16c + 15 of the head group; thread st
-    // of it the token row st of S^T (its TMEM lane).
+    // Group c (four warps) has heads NH c .. NH (c + 1) - 1 of the head group; thread
+    // st of it the token row st of S^T (its TMEM lane).
+    constexpr int NH = C::kHeads;
     const int c = warp >> 2, q4 = warp & 3, st = threadIdx.x & 127;
     const uint32_t lane_off = uint32_t(q4 * 32) << 16;
-    float* qscale = red + 13 * HC + 16 * c;  // + (segment & 1) * HC
+    float* qscale = red + 13 * HC + NH * c;  // + (segment & 1) * HC
     TileWalkerT<true> walk;
     walk.init(p.tile_start, p.seg_base, p.len, p.batch, int(S), pa, pb);
     // Q of a segment's sequence as two E4M3 terms: eight threads per head, each
     // every eighth chunk of eight values.  Every QK MMA of the previous segment
     // has completed: this thread saw the s_full of its last tile.
     auto load_q = [&](int b, uint32_t seg) {
-      const int hl = st >> 3, i8 = st & 7, row_hi = 16 * c + hl, row_lo = HC + row_hi;
-      const uint4* src = reinterpret_cast<const uint4*>(p.q_full + (size_t(b) * p.heads + g * HC + row_hi) * kRow) + i8;
-      uint4 u[9];
+      constexpr int T = 128 / NH, N = (72 + T - 1) / T;  // threads per head, chunks of eight values each
+      const int hl = st / T, i0 = st % T, row_hi = NH * c + hl, row_lo = HC + row_hi;
+      const uint4* src = reinterpret_cast<const uint4*>(p.q_full + (size_t(b) * p.heads + g * HC + row_hi) * kRow);
+      uint4 u[N];
       float top = 0.f;
 #pragma unroll
-      for (int i = 0; i < 9; ++i) {
-        u[i] = src[8 * i];
+      for (int i = 0; i < N; ++i) {
+        u[i] = i0 + T * i < 72 ? src[i0 + T * i] : make_uint4(0, 0, 0, 0);
         const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
@@ -426,13 +503,15 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
         }
       }
 #pragma unroll
-      for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      for (int o = T / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       // up to a power of two in [128, 256): 2^(7 - floor(log2 top)) (fp16 values: 2^-24 .. 2^16)
       const int ex = top > 0.f ? int(__float_as_uint(top) >> 23) - 127 : 7;
       const float up = __uint_as_float(uint32_t(127 + 7 - ex) << 23), down = __uint_as_float(uint32_t(127 - 7 + ex) << 23);
-      if (i8 == 0) qscale[(seg & 1) * HC + hl] = down * p.scale_log2;
+      if (i0 == 0) qscale[(seg & 1) * HC + hl] = down * p.scale_log2;
 #pragma unroll
-      for (int i = 0; i < 9; ++i) {
+      for (int i = 0; i < N; ++i) {
+        const int chunk = i0 + T * i;
+        if (chunk >= 72) break;
         const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
         uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
@@ -445,22 +524,22 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
           hi[x >> 1] |= a << (16 * (x & 1));
           lo[x >> 1] |= pack_e4m3x2(16.f * (f.x - fa.x), 16.f * (f.y - fa.y)) << (16 * (x & 1));
         }
-        // chunk i8 + 8 i: 16 chunks to a box, two to a 16-byte piece
-        const int ch = i8 + 8 * (i & 1), piece = ch >> 1;
-        uint8_t* box = smem + C::kOffQ + (i >> 1) * C::kQBox;
+        // 16 chunks to a box, two to a 16-byte piece
+        const int piece = (chunk & 15) >> 1;
+        uint8_t* box = smem + C::kOffQ + (chunk >> 4) * C::kQBox + 8 * (chunk & 1);
 #pragma unroll
         for (int term = 0; term < 2; ++term) {
           const int row = term ? row_lo : row_hi;
-          uint8_t* dst = i < 8 ? box + row * 128 + ((piece ^ (row & 7)) << 4) : box + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
-          *reinterpret_cast<uint2*>(dst + 8 * (ch & 1)) = term ? make_uint2(lo[0], lo[1]) : make_uint2(hi[0], hi[1]);
+          uint8_t* dst = chunk < 64 ? box + row * 128 + ((piece ^ (row & 7)) << 4) : box + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
+          *reinterpret_cast<uint2*>(dst) = term ? make_uint2(lo[0], lo[1]) : make_uint2(hi[0], hi[1]);
         }
       }
       fence_proxy_async_smem();
       mbar_arrive(&B->q_full);
     };
-    float* m_run = red + 15 * HC + 16 * c;  // kept once for the group's threads
-    float* alpha = red + 16 * HC + 16 * c;
-    float l_run[16];
+    float* m_run = red + 15 * HC + NH * c;  // kept once for the group's threads
+    float* alpha = red + 16 * HC + NH * c;
+    float l_run[NH];
     uint32_t k = 0, seg = 0;
     TileInfo t, tn;
     bool have = walk.next(t);
@@ -474,16 +553,16 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
       tc_fence_after();
       // the first tile of a segment: every thread's qscale must be there
       if (t.first) group_any(c, false);
-      float x[16];
+      float x[NH];
       {
-        float lo[16];
-        tmem_ld16(tmem + lane_off + C::kColS + buf * C::kNQ + 16 * c, x);
-        tmem_ld16(tmem + lane_off + C::kColS + buf * C::kNQ + HC + 16 * c, lo);
+        float lo[NH];
+        tmem_load<NH>(tmem + lane_off + C::kColS + buf * C::kNQ + NH * c, x);
+        tmem_load<NH>(tmem + lane_off + C::kColS + buf * C::kNQ + HC + NH * c, lo);
         tc_fence_before();
         mbar_arrive(&B->s_free[buf]);
         const float4* qs = reinterpret_cast<const float4*>(qscale + (seg & 1) * HC);
 #pragma unroll
-        for (int h4 = 0; h4 < 4; ++h4) {
+        for (int h4 = 0; h4 < NH / 4; ++h4) {
           const float4 s = qs[h4];
           x[4 * h4] = fmaf(lo[4 * h4], 0.0625f, x[4 * h4]) * s.x;
           x[4 * h4 + 1] = fmaf(lo[4 * h4 + 1], 0.0625f, x[4 * h4 + 1]) * s.y;
@@ -493,20 +572,20 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
       }
       if (!valid) {
 #pragma unroll
-        for (int h = 0; h < 16; ++h) x[h] = -INFINITY;
+        for (int h = 0; h < NH; ++h) x[h] = -INFINITY;
       }
       if (kCausal && causal_tile(p, t, len_b)) {
         const int pos = t.tile * kTile + st - (len_b - p.q_len);  // against the query token's number
 #pragma unroll
-        for (int h = 0; h < 16; ++h)
-          if (pos > (g * HC + 16 * c + h) / p.heads_w) x[h] = -INFINITY;
+        for (int h = 0; h < NH; ++h)
+          if (pos > (g * HC + NH * c + h) / p.heads_w) x[h] = -INFINITY;
       }
       // Running max: as in decode_tc.cu it only has to bound the scores, here to
       // within 2^5, so that the weights keep E5M2's range down.
       bool over = false;
       if (!t.first) {
 #pragma unroll
-        for (int h4 = 0; h4 < 4; ++h4) {
+        for (int h4 = 0; h4 < NH / 4; ++h4) {
           const float4 m = reinterpret_cast<const float4*>(m_run)[h4];
           constexpr float kTop = kWeightBits + kRescaleThreshold;
           over |= x[4 * h4] > m.x + kTop || x[4 * h4 + 1] > m.y + kTop || x[4 * h4 + 2] > m.z + kTop ||
@@ -515,16 +594,16 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
       }
       bool rescale = false;
       if (t.first || group_any(c, over || !ok)) {
-        float* rm = red + buf * 4 * HC + 64 * c;
+        float* rm = red + buf * 4 * HC + 4 * NH * c;
         {
-          float tmp[16];
+          float tmp[NH];
 #pragma unroll
-          for (int h = 0; h < 16; ++h) tmp[h] = x[h];
-          const float wm = warp_transpose_reduce<16, true>(tmp, lane);
-          if (!(lane & 1)) rm[(lane >> 1) * 4 + q4] = wm;
+          for (int h = 0; h < NH; ++h) tmp[h] = x[h];
+          const float wm = warp_reduce<NH, true>(tmp, lane);
+          if (lane % (32 / NH) == 0) rm[lane / (32 / NH) * 4 + q4] = wm;
         }
         if (group_any(c, !ok)) break;
-        if (st < 16) {  // thread h: head h's maximum over the tile
+        if (st < NH) {  // thread h: head h's maximum over the tile
           const float4 m4 = reinterpret_cast<const float4*>(rm)[st];
           const float mt = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w)), old = m_run[st];
           float a = 1.f;
@@ -540,10 +619,10 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
         rescale = group_any(c, rescale);
         if (t.first) {
 #pragma unroll
-          for (int h = 0; h < 16; ++h) l_run[h] = 0.f;
+          for (int h = 0; h < NH; ++h) l_run[h] = 0.f;
         } else {
 #pragma unroll
-          for (int h = 0; h < 16; ++h) l_run[h] *= alpha[h];
+          for (int h = 0; h < NH; ++h) l_run[h] *= alpha[h];
         }
       }
       if (rescale) {
@@ -554,21 +633,21 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
         if (group_any(c, !ok3)) break;
 #pragma unroll 1
         for (int i = 0; i < 12; ++i) {  // chunk i / 3, term i % 3
-          float v[16];
-          const uint32_t a = tmem + lane_off + C::kColO + (i / 3) * C::kColOStep + (i % 3) * HC + 16 * c;
-          tmem_ld16(a, v);
+          float v[NH];
+          const uint32_t a = tmem + lane_off + C::kColO + (i / 3) * C::kColOStep + (i % 3) * HC + NH * c;
+          tmem_load<NH>(a, v);
 #pragma unroll
-          for (int h = 0; h < 16; ++h) v[h] *= alpha[h];
-          tmem_st16(a, v);
+          for (int h = 0; h < NH; ++h) v[h] *= alpha[h];
+          tmem_store<NH>(a, v);
         }
         tmem_st_wait();
       }
       // weights -> P^T, three E5M2 terms of the fp16 value: the high byte rounded
       // to nearest, the same of what is left, and the rest (at most three bits)
       {
-        uint32_t w[8];
+        uint32_t w[NH / 2];
 #pragma unroll
-        for (int h4 = 0; h4 < 4; ++h4) {
+        for (int h4 = 0; h4 < NH / 4; ++h4) {
           const float4 m = reinterpret_cast<const float4*>(m_run)[h4];
           const float e0 = ex2_ftz(x[4 * h4] - m.x), e1 = ex2_ftz(x[4 * h4 + 1] - m.y);
           const float e2 = ex2_ftz(x[4 * h4 + 2] - m.z), e3 = ex2_ftz(x[4 * h4 + 3] - m.w);
@@ -579,18 +658,25 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
           w[2 * h4] = pack_f16x2(e0, e1);
           w[2 * h4 + 1] = pack_f16x2(e2, e3);
         }
-        uint8_t* pt = smem + C::kOffP + buf * C::kPBytes + c * 2048 + (st >> 3) * 128 + (st & 7) * 16;
+        // head n of a term is byte n % 16 of its row in core matrix n / 16
+        uint8_t* pt = smem + C::kOffP + buf * C::kPBytes + (NH * c / 16) * 2048 + NH * c % 16 + (st >> 3) * 128 + (st & 7) * 16;
 #pragma unroll
         for (int term = 0; term < 3; ++term) {
-          uint32_t h[8];
+          uint32_t o[NH / 4];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            h[i] = term < 2 ? (w[i] + 0x00800080u) & 0xff00ff00u : w[i];
-            if (term < 2) w[i] = sub_f16x2(w[i], h[i]);
+          for (int i = 0; i < NH / 4; ++i) {
+            uint32_t h[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              uint32_t& x2 = w[2 * i + e];
+              h[e] = term < 2 ? (x2 + 0x00800080u) & 0xff00ff00u : x2;
+              if (term < 2) x2 = sub_f16x2(x2, h[e]);
+            }
+            o[i] = __byte_perm(h[0], h[1], 0x7531);
           }
-          *reinterpret_cast<uint4*>(pt + term * (HC / 16) * 2048) =
-              make_uint4(__byte_perm(h[0], h[1], 0x7531), __byte_perm(h[2], h[3], 0x7531),
-                         __byte_perm(h[4], h[5], 0x7531), __byte_perm(h[6], h[7], 0x7531));
+          uint8_t* dst = pt + term * (HC / 16) * 2048;
+          if constexpr (NH == 16) *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+          else *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1]);
         }
       }
       fence_proxy_async_smem();
@@ -601,41 +687,41 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
         if (have_next) load_q(tn.b, seg + 1);
         const bool ok2 = mbar_wait(&B->o_full, seg & 1, abort_flag, kWaitLimitNs);
         tc_fence_after();
-        float* rl = red + 8 * HC + 64 * c;  // [16][4] sums
+        float* rl = red + 8 * HC + 4 * NH * c;  // [NH][4] sums
         {
-          float tmp[16];
+          float tmp[NH];
 #pragma unroll
-          for (int h = 0; h < 16; ++h) tmp[h] = l_run[h];
-          const float ls = warp_transpose_reduce<16, false>(tmp, lane);
-          if (!(lane & 1)) rl[(lane >> 1) * 4 + q4] = ls;
+          for (int h = 0; h < NH; ++h) tmp[h] = l_run[h];
+          const float ls = warp_reduce<NH, false>(tmp, lane);
+          if (lane % (32 / NH) == 0) rl[lane / (32 / NH) * 4 + q4] = ls;
         }
         if (group_any(c, !ok2)) break;
-        float* rinv = red + 12 * HC + 16 * c;
+        float* rinv = red + 12 * HC + NH * c;
         float l = 0.f, il = 0.f;
-        if (st < 16) {  // thread h divides for head h
+        if (st < NH) {  // thread h divides for head h
           const float4 l4 = reinterpret_cast<const float4*>(rl)[st];
           l = (l4.x + l4.y) + (l4.z + l4.w);
           il = l > 0.f ? 1.f / l : l;  // 0: a row with no visible token; NaN stays
           rinv[st] = il;
         }
         group_any(c, false);
-        const int row0 = g * HC + 16 * c;
+        const int row0 = g * HC + NH * c;
         float* dst = p.partial_o + (size_t(t.seg) * p.heads + row0) * kLatent + st;
 #pragma unroll 1
         for (int ch = 0; ch < 4; ++ch) {
-          float v[16], v2[16];
-          const uint32_t a = tmem + lane_off + C::kColO + ch * C::kColOStep + 16 * c;
-          tmem_ld16(a, v);
-          tmem_ld16(a + HC, v2);
+          float v[NH], v2[NH];
+          const uint32_t a = tmem + lane_off + C::kColO + ch * C::kColOStep + NH * c;
+          tmem_load<NH>(a, v);
+          tmem_load<NH>(a + HC, v2);
 #pragma unroll
-          for (int h = 0; h < 16; ++h) v[h] += v2[h];
-          tmem_ld16(a + 2 * HC, v2);
+          for (int h = 0; h < NH; ++h) v[h] += v2[h];
+          tmem_load<NH>(a + 2 * HC, v2);
 #pragma unroll
-          for (int h = 0; h < 16; ++h) dst[h * kLatent + ch * 128] = (v[h] + v2[h]) * rinv[h];
+          for (int h = 0; h < NH; ++h) dst[h * kLatent + ch * 128] = (v[h] + v2[h]) * rinv[h];
         }
         tc_fence_before();
         mbar_arrive(&B->o_free);
-        if (st < 16) {  // thread h writes head h's lse
+        if (st < NH) {  // thread h writes head h's lse
           p.partial_lse[size_t(t.seg) * p.heads + row0 + st] = l > 0.f ? (m_run[st] + log2f(l)) * kLn2 : lse_of_no_sum(l);
         }
         ++seg;
