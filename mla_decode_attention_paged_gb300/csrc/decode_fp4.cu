@@ -64,10 +64,8 @@ constexpr float kWeightBits = 10.f;                       // a weight is 2^10 at
 
 template <int HC>
 struct Fp4Cfg {
-  // 16 rows: groups of 8 heads and one cached row to an expansion thread; 32
-  // rows: 16 heads, two rows (36 warps would be the other way)
-  static constexpr int kHeads = HC / 2, kSoftWarps = 8;
-  static constexpr int kRowsPer = HC == 16 ? 1 : 2, kExpWarps = 16 / kRowsPer;
+  static constexpr int kHeads = HC / 2, kSoftWarps = 8;     // two softmax groups
+  static constexpr int kRowsPer = 2, kExpWarps = 16 / kRowsPer;  // cached rows to an expansion thread
   static constexpr int kThreads = 32 * (kSoftWarps + kExpWarps + 4);
   static constexpr int kNQ = 2 * HC, kNP = 3 * HC;          // N of the products
   static constexpr uint32_t kQBox = kNQ * 128;              // [2 HC rows x 128 columns] E4M3, SW128
@@ -276,7 +274,7 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
     // the block's two 16-byte pieces in its row of a latent and of the RoPE box
     const uint32_t at0 = r * 128 + (((2 * j) ^ (r & 7)) << 4), at1 = at0 ^ 16;
     const uint32_t rope0 = kRopeBox + r * 64 + (((2 * j) ^ ((r >> 1) & 3)) << 4), rope1 = rope0 ^ 16;
-    const uint8_t* lut = smem + C::kOffLut;
+    const uint2* lut = reinterpret_cast<const uint2*>(smem + C::kOffLut);
     const uint32_t byte_j = 0x4440 + j;  // byte j of a word
     // where this thread's first row is, from its page's first, and the others' pages
     const int page_log2 = __ffs(p.page_size) - 1;
@@ -304,7 +302,9 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
       if (threadIdx.x == 32 * C::kSoftWarps) *reinterpret_cast<volatile int*>(&B->expanding) = int(k);
       v1 = look(k + 1);
       if (!ok) break;
-      uint32_t at[R][5];  // where the blocks' magnitudes are in the table
+      // the blocks' scale bytes, and whether any is outside 2^-13 .. 2^13
+      uint32_t sc[R][5];
+      bool far = false;
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         const uint32_t tail[5] = {
@@ -312,7 +312,10 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
             __shfl_sync(0xffffffffu, v[i][4].z, lane2), __shfl_sync(0xffffffffu, v[i][4].w, lane2),
             __shfl_sync(0xffffffffu, v[i][4].x, lane3)};
 #pragma unroll
-        for (int c = 0; c < 5; ++c) at[i][c] = __byte_perm(tail[c], 0, byte_j) * 8;
+        for (int c = 0; c < 5; ++c) {
+          sc[i][c] = __byte_perm(tail[c], 0, byte_j);
+          far |= sc[i][c] - (127 - 13) > 26;
+        }
       }
       // the tails first: their registers are the first that the next tile needs
 #pragma unroll
@@ -326,7 +329,12 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
 #pragma unroll
           for (int i = 0; i < R; ++i) {
             uint4 lo, hi;
-            expand_block(v[i][c], *reinterpret_cast<const uint2*>(lut + at[i][c]), lo, hi);
+            // the magnitudes' E5M2 bytes: within that range a scale adds to the
+            // exponents, four to each byte and step (0 stays 0)
+            uint2 tab = make_uint2(sc[i][c] * 0x04040400u + (0x3e3c3800u - 127u * 0x04040400u),
+                                   sc[i][c] * 0x04040404u + (0x46444240u - 127u * 0x04040404u));
+            if (far) tab = lut[sc[i][c]];
+            expand_block(v[i][c], tab, lo, hi);
             uint8_t* dst = base + (c < 4 ? c * kLatBox + 64 * 128 * i : 64 * 64 * i);
             *reinterpret_cast<uint4*>(dst + (c < 4 ? at0 : rope0)) = lo;
             *reinterpret_cast<uint4*>(dst + (c < 4 ? at1 : rope1)) = hi;
@@ -539,7 +547,25 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
     };
     float* m_run = red + 15 * HC + NH * c;  // kept once for the group's threads
     float* alpha = red + 16 * HC + NH * c;
-    float l_run[NH];
+    // 8 heads: copies of m_run and qscale in registers (as loads of one address
+    // by all lanes they cost shared memory four wavefronts each); 16: none to spare
+    constexpr bool kCopies = NH == 8;
+    float l_run[NH], mr[kCopies ? NH : 4], qs[kCopies ? NH : 4];
+    auto load_copies = [&](float (&dst)[kCopies ? NH : 4], const float* src) {
+#pragma unroll
+      for (int h4 = 0; h4 < (kCopies ? NH / 4 : 1); ++h4) {
+        const float4 m = reinterpret_cast<const float4*>(src)[h4];
+        dst[4 * h4] = m.x;
+        dst[4 * h4 + 1] = m.y;
+        dst[4 * h4 + 2] = m.z;
+        dst[4 * h4 + 3] = m.w;
+      }
+    };
+    // four values of one of them, for heads 4 h4 .. 4 h4 + 3
+    auto four = [&](const float (&copy)[kCopies ? NH : 4], const float* src, int h4) -> float4 {
+      if constexpr (kCopies) return make_float4(copy[4 * h4], copy[4 * h4 + 1], copy[4 * h4 + 2], copy[4 * h4 + 3]);
+      else return reinterpret_cast<const float4*>(src)[h4];
+    };
     uint32_t k = 0, seg = 0;
     TileInfo t, tn;
     bool have = walk.next(t);
@@ -552,7 +578,10 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
       if (k >= 2) ok = ok && mbar_wait(&B->pv_done[buf], ((k - 2) >> 1) & 1, abort_flag, kWaitLimitNs);
       tc_fence_after();
       // the first tile of a segment: every thread's qscale must be there
-      if (t.first) group_any(c, false);
+      if (t.first) {
+        group_any(c, false);
+        if (kCopies) load_copies(qs, qscale + (seg & 1) * HC);
+      }
       float x[NH];
       {
         float lo[NH];
@@ -560,10 +589,9 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
         tmem_load<NH>(tmem + lane_off + C::kColS + buf * C::kNQ + HC + NH * c, lo);
         tc_fence_before();
         mbar_arrive(&B->s_free[buf]);
-        const float4* qs = reinterpret_cast<const float4*>(qscale + (seg & 1) * HC);
 #pragma unroll
         for (int h4 = 0; h4 < NH / 4; ++h4) {
-          const float4 s = qs[h4];
+          const float4 s = four(qs, qscale + (seg & 1) * HC, h4);
           x[4 * h4] = fmaf(lo[4 * h4], 0.0625f, x[4 * h4]) * s.x;
           x[4 * h4 + 1] = fmaf(lo[4 * h4 + 1], 0.0625f, x[4 * h4 + 1]) * s.y;
           x[4 * h4 + 2] = fmaf(lo[4 * h4 + 2], 0.0625f, x[4 * h4 + 2]) * s.z;
@@ -586,7 +614,7 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
       if (!t.first) {
 #pragma unroll
         for (int h4 = 0; h4 < NH / 4; ++h4) {
-          const float4 m = reinterpret_cast<const float4*>(m_run)[h4];
+          const float4 m = four(mr, m_run, h4);
           constexpr float kTop = kWeightBits + kRescaleThreshold;
           over |= x[4 * h4] > m.x + kTop || x[4 * h4 + 1] > m.y + kTop || x[4 * h4 + 2] > m.z + kTop ||
                   x[4 * h4 + 3] > m.w + kTop;
@@ -617,6 +645,7 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
           alpha[st] = a;
         }
         rescale = group_any(c, rescale);
+        if (kCopies) load_copies(mr, m_run);
         if (t.first) {
 #pragma unroll
           for (int h = 0; h < NH; ++h) l_run[h] = 0.f;
@@ -648,7 +677,7 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
         uint32_t w[NH / 2];
 #pragma unroll
         for (int h4 = 0; h4 < NH / 4; ++h4) {
-          const float4 m = reinterpret_cast<const float4*>(m_run)[h4];
+          const float4 m = four(mr, m_run, h4);
           const float e0 = ex2_ftz(x[4 * h4] - m.x), e1 = ex2_ftz(x[4 * h4 + 1] - m.y);
           const float e2 = ex2_ftz(x[4 * h4 + 2] - m.z), e3 = ex2_ftz(x[4 * h4 + 3] - m.w);
           l_run[4 * h4] += e0;
