@@ -172,6 +172,30 @@ def _ptr(t: torch.Tensor | None, dtype=None, name="tensor", device=None):
     return t.data_ptr()
 
 
+def _on(t: torch.Tensor, dtype, index: int, name: str) -> int:
+    """Pointer of a contiguous tensor of this type on CUDA device ``index`` (_ptr
+    with its common case first: these checks are most of a small call's host time)."""
+    try:
+        if t.dtype is dtype and t.get_device() == index and index >= 0 and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    if t is None:
+        raise TypeError(f"{name} must be a torch.Tensor")
+    return _ptr(t, dtype, name, torch.device("cuda", index) if index >= 0 else None)
+
+
+def _index(t: torch.Tensor, name: str = "q_nope") -> int:
+    """CUDA device of a tensor."""
+    _ptr(t, None, name)
+    return t.get_device()
+
+
+def _workspace(t: torch.Tensor, index: int) -> tuple[int, int]:
+    """Pointer and bytes of a workspace tensor of any type."""
+    return _on(t, t.dtype if isinstance(t, torch.Tensor) else None, index, "workspace"), t.nbytes
+
+
 def _cache_ptrs(d: Dims, cache: torch.Tensor, scale_zero: torch.Tensor | None, device=None):
     """Pointers of the cache rows (bf16 values, int8 codes, E4M3 codes, or FP4
     rows) and of their per-token scales (None for bf16 and FP4 caches)."""
@@ -205,13 +229,15 @@ def cache_append(d: Dims, cache: torch.Tensor, scale_zero: torch.Tensor | None, 
                  seq_ids: torch.Tensor, positions: torch.Tensor, c_kv: torch.Tensor, k_pe: torch.Tensor,
                  rope_theta: float = 10000.0, device_status: torch.Tensor | None = None, stream=None) -> None:
     """mla_cache_append: write new tokens' rows into the paged cache (in place)."""
-    dev = cache.device
-    st = _L().mla_cache_append(
-        ctypes.byref(d), *_cache_ptrs(d, cache, scale_zero, dev), cache.shape[0],
-        _ptr(block_table, torch.int32, "block_table", dev), block_table.shape[0], block_table.shape[1],
-        _ptr(seq_ids, torch.int32, "seq_ids", dev), _ptr(positions, torch.int32, "positions", dev),
-        seq_ids.numel(), _ptr(c_kv, torch.bfloat16, "c_kv", dev), _ptr(k_pe, torch.bfloat16, "k_pe", dev),
-        float(rope_theta), _ptr(device_status, torch.int32, "device_status", dev), _stream(stream))
+    dev, i32, bf16 = cache.device, torch.int32, torch.bfloat16
+    cache_p, scale_p = _cache_ptrs(d, cache, scale_zero, dev)
+    at = dev.index
+    st = _call_on(
+        dev, stream, _L().mla_cache_append, ctypes.byref(d), cache_p, scale_p, cache.shape[0],
+        _on(block_table, i32, at, "block_table"), block_table.shape[0], block_table.shape[1],
+        _on(seq_ids, i32, at, "seq_ids"), _on(positions, i32, at, "positions"), seq_ids.numel(),
+        _on(c_kv, bf16, at, "c_kv"), _on(k_pe, bf16, at, "k_pe"), float(rope_theta),
+        None if device_status is None else _on(device_status, i32, at, "device_status"))
     _check(st, "mla_cache_append")
 
 
@@ -244,14 +270,13 @@ def decode(d: Dims, q_nope, q_pe, cache, scale_zero, block_table, seq_lens, W_UK
         out = torch.empty((B, d.num_heads, d.v_head_dim), dtype=torch.bfloat16, device=dev)
     if lse_out is None and want_lse:
         lse_out = torch.empty((B, d.num_heads), dtype=torch.float32, device=dev)
-    st = _L().mla_decode(
-        ctypes.byref(d), _ptr(q_nope, torch.bfloat16, "q_nope"), _ptr(q_pe, torch.bfloat16, "q_pe", dev),
-        *_cache_ptrs(d, cache, scale_zero, dev), cache.shape[0],
-        _ptr(block_table, torch.int32, "block_table", dev), block_table.shape[1],
-        _ptr(seq_lens, torch.int32, "seq_lens", dev), B, _ptr(W_UK, torch.bfloat16, "W_UK", dev),
-        _ptr(W_UV, torch.bfloat16, "W_UV", dev), float(softmax_scale), int(num_splits),
-        _ptr(workspace, None, "workspace", dev), workspace.numel() * workspace.element_size(),
-        _ptr(out, torch.bfloat16, "out", dev), _ptr(lse_out, torch.float32, "lse_out", dev), _stream(stream))
+    at, i32, bf16 = _index(q_nope), torch.int32, torch.bfloat16
+    st = _call_on(
+        dev, stream, _L().mla_decode, ctypes.byref(d), _on(q_nope, bf16, at, "q_nope"), _on(q_pe, bf16, at, "q_pe"),
+        *_cache_ptrs(d, cache, scale_zero, dev), cache.shape[0], _on(block_table, i32, at, "block_table"),
+        block_table.shape[1], _on(seq_lens, i32, at, "seq_lens"), B, _on(W_UK, bf16, at, "W_UK"),
+        _on(W_UV, bf16, at, "W_UV"), float(softmax_scale), int(num_splits), *_workspace(workspace, at),
+        _on(out, bf16, at, "out"), None if lse_out is None else _on(lse_out, torch.float32, at, "lse_out"))
     _check(st, "mla_decode")
     return out, lse_out
 
@@ -279,14 +304,14 @@ def decode_multi(d: Dims, q_nope, q_pe, cache, scale_zero, block_table, seq_lens
         out = torch.empty((B, T, d.num_heads, d.v_head_dim), dtype=torch.bfloat16, device=dev)
     if lse_out is None and want_lse:
         lse_out = torch.empty((B, T, d.num_heads), dtype=torch.float32, device=dev)
-    st = _L().mla_decode_multi(
-        ctypes.byref(d), _ptr(q_nope, torch.bfloat16, "q_nope"), _ptr(q_pe, torch.bfloat16, "q_pe", dev),
-        *_cache_ptrs(d, cache, scale_zero, dev), cache.shape[0],
-        _ptr(block_table, torch.int32, "block_table", dev), block_table.shape[1],
-        _ptr(seq_lens, torch.int32, "seq_lens", dev), B, T, _ptr(W_UK, torch.bfloat16, "W_UK", dev),
-        _ptr(W_UV, torch.bfloat16, "W_UV", dev), float(softmax_scale), int(num_splits),
-        _ptr(workspace, None, "workspace", dev), workspace.numel() * workspace.element_size(),
-        _ptr(out, torch.bfloat16, "out", dev), _ptr(lse_out, torch.float32, "lse_out", dev), _stream(stream))
+    at, i32, bf16 = _index(q_nope), torch.int32, torch.bfloat16
+    st = _call_on(
+        dev, stream, _L().mla_decode_multi, ctypes.byref(d), _on(q_nope, bf16, at, "q_nope"),
+        _on(q_pe, bf16, at, "q_pe"), *_cache_ptrs(d, cache, scale_zero, dev), cache.shape[0],
+        _on(block_table, i32, at, "block_table"), block_table.shape[1], _on(seq_lens, i32, at, "seq_lens"), B, T,
+        _on(W_UK, bf16, at, "W_UK"), _on(W_UV, bf16, at, "W_UV"), float(softmax_scale), int(num_splits),
+        *_workspace(workspace, at), _on(out, bf16, at, "out"),
+        None if lse_out is None else _on(lse_out, torch.float32, at, "lse_out"))
     _check(st, "mla_decode_multi")
     return out, lse_out
 
@@ -316,14 +341,14 @@ def prefill(d: Dims, cache, scale_zero, block_table, seq_lens, c_kv, k_pe, q_nop
     if lse_out is None and want_lse:
         lse_out = torch.empty((B, T, d.num_heads), dtype=torch.float32, device=dev)
     cache_p, scale_p = _cache_ptrs(d, cache, scale_zero, dev)
-    st = _L().mla_prefill(
-        ctypes.byref(d), cache_p, scale_p, cache.shape[0], _ptr(block_table, torch.int32, "block_table", dev),
-        block_table.shape[1], _ptr(seq_lens, torch.int32, "seq_lens", dev), B, T,
-        _ptr(c_kv, torch.bfloat16, "c_kv", dev), _ptr(k_pe, torch.bfloat16, "k_pe", dev), float(rope_theta),
-        _ptr(q_nope, torch.bfloat16, "q_nope", dev), _ptr(q_pe, torch.bfloat16, "q_pe", dev),
-        _ptr(W_UK, torch.bfloat16, "W_UK", dev), _ptr(W_UV, torch.bfloat16, "W_UV", dev), float(softmax_scale),
-        int(num_splits), _ptr(workspace, None, "workspace", dev), workspace.numel() * workspace.element_size(),
-        _ptr(out, torch.bfloat16, "out", dev), _ptr(lse_out, torch.float32, "lse_out", dev), _stream(stream))
+    at, i32, bf16 = _index(q_nope), torch.int32, torch.bfloat16
+    st = _call_on(
+        dev, stream, _L().mla_prefill, ctypes.byref(d), cache_p, scale_p, cache.shape[0],
+        _on(block_table, i32, at, "block_table"), block_table.shape[1], _on(seq_lens, i32, at, "seq_lens"), B, T,
+        _on(c_kv, bf16, at, "c_kv"), _on(k_pe, bf16, at, "k_pe"), float(rope_theta), _on(q_nope, bf16, at, "q_nope"),
+        _on(q_pe, bf16, at, "q_pe"), _on(W_UK, bf16, at, "W_UK"), _on(W_UV, bf16, at, "W_UV"), float(softmax_scale),
+        int(num_splits), *_workspace(workspace, at), _on(out, bf16, at, "out"),
+        None if lse_out is None else _on(lse_out, torch.float32, at, "lse_out"))
     _check(st, "mla_prefill")
     return out, lse_out
 
@@ -350,14 +375,14 @@ def decode_sparse(d: Dims, q_nope, q_pe, cache, scale_zero, block_table, seq_len
         out = torch.empty((B, d.num_heads, d.v_head_dim), dtype=torch.bfloat16, device=dev)
     if lse_out is None and want_lse:
         lse_out = torch.empty((B, d.num_heads), dtype=torch.float32, device=dev)
-    st = _L().mla_decode_sparse(
-        ctypes.byref(d), _ptr(q_nope, torch.bfloat16, "q_nope"), _ptr(q_pe, torch.bfloat16, "q_pe", dev),
-        *_cache_ptrs(d, cache, scale_zero, dev), cache.shape[0],
-        _ptr(block_table, torch.int32, "block_table", dev), block_table.shape[1],
-        _ptr(seq_lens, torch.int32, "seq_lens", dev), B, _ptr(token_indices, torch.int32, "token_indices", dev), K,
-        _ptr(W_UK, torch.bfloat16, "W_UK", dev), _ptr(W_UV, torch.bfloat16, "W_UV", dev), float(softmax_scale),
-        int(num_splits), _ptr(workspace, None, "workspace", dev), workspace.numel() * workspace.element_size(),
-        _ptr(out, torch.bfloat16, "out", dev), _ptr(lse_out, torch.float32, "lse_out", dev), _stream(stream))
+    at, i32, bf16 = _index(q_nope), torch.int32, torch.bfloat16
+    st = _call_on(
+        dev, stream, _L().mla_decode_sparse, ctypes.byref(d), _on(q_nope, bf16, at, "q_nope"),
+        _on(q_pe, bf16, at, "q_pe"), *_cache_ptrs(d, cache, scale_zero, dev), cache.shape[0],
+        _on(block_table, i32, at, "block_table"), block_table.shape[1], _on(seq_lens, i32, at, "seq_lens"), B,
+        _on(token_indices, i32, at, "token_indices"), K, _on(W_UK, bf16, at, "W_UK"), _on(W_UV, bf16, at, "W_UV"),
+        float(softmax_scale), int(num_splits), *_workspace(workspace, at), _on(out, bf16, at, "out"),
+        None if lse_out is None else _on(lse_out, torch.float32, at, "lse_out"))
     _check(st, "mla_decode_sparse")
     return out, lse_out
 

@@ -112,9 +112,8 @@ uint64_t turn_fraction(double f) {
   constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;
   const double p = f * kHi, rest = std::fma(f, kHi, -p) + f * kLo, whole = std::floor(p);
   if (!std::isfinite(p)) return 0;
-  // the difference is exact; p - whole < 1, so the first term fits and the second (|rest| < 2^-53 p) is added modulo 2^64
-  const double frac = p - whole;
-  return uint64_t(std::ldexp(frac, 64)) + uint64_t(int64_t(std::ldexp(std::fmod(rest, 0.25), 64)));
+  // p - whole is exact and below 1; |rest| < 2^-53 p is added modulo 2^64
+  return uint64_t((p - whole) * 0x1p64) + uint64_t(int64_t((std::fabs(rest) < 0.25 ? rest : std::fmod(rest, 0.25)) * 0x1p64));
 }
 
 // Append parameters shared by mla_cache_append and mla_prefill (which then
