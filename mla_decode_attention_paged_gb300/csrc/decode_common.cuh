@@ -207,8 +207,7 @@ __device__ __forceinline__ void dequant16(uint4& lo, uint4& hi, float scale, flo
 // E2M1 has one mantissa bit, E5M2 two, so a code times a power-of-two scale is an
 // E5M2 value as long as it lies in that format's range: exact for block scales
 // 2^-15 .. 2^13; below that the magnitudes round to multiples of 2^-16, above
-// it they saturate at 57,344.  An E5M2 byte is also the high byte of the fp16
-// of the same value, so one table serves both operand types.
+// it they saturate at 57,344.
 
 // The eight magnitudes of a block with this scale byte as E5M2 bytes, entry c
 // for code c; NaN for 255.
@@ -229,14 +228,6 @@ __device__ __forceinline__ void e2m1_to_e5m2(uint32_t word, uint2 table, uint32_
   a = __byte_perm(table.x, table.y, sel) | (word & 0x80808080u);
   b = __byte_perm(table.x, table.y, sel >> 16) | ((word << 4) & 0x80808080u);
 }
-// The same as fp16 values, value 0 in the low half of .x.
-__device__ __forceinline__ uint4 e2m1_to_f16(uint32_t word, uint2 table) {
-  uint32_t a, b;
-  e2m1_to_e5m2(word, table, a, b);
-  return make_uint4(__byte_perm(a, 0, 0x1404), __byte_perm(a, 0, 0x3424), __byte_perm(b, 0, 0x1404),
-                    __byte_perm(b, 0, 0x3424));
-}
-
 // ----- host side: tensor maps ----------------------------------------------
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,

@@ -1,6 +1,7 @@
-// decode_fp4.cu -- split-KV MLA decode attention over FP4 caches for groups of
-// 16 or 32 query rows (16 or 32 heads, or heads x tokens of multi-token decode),
-// on the FP8 tensor cores.
+// decode_fp4.cu -- split-KV MLA decode attention over FP4 caches, on the FP8 tensor
+// cores, for groups of 16 or 32 query rows (heads, or heads x tokens of
+// multi-token decode and prefill; 16 rows are a group, more go in groups of 32
+// of which the last may be half empty).
 //
 // What it computes ("The Weight Absorption Trick"; "Seven Ways LLMs Handle
 // Attention", section 5; "Flash-Decoding and FlashInfer"; "The Architecture of
@@ -58,15 +59,23 @@ constexpr int kRing = 8;                                  // tiles of looked-up 
 constexpr uint32_t kLatBox = kTile * 128;                 // [128 tokens x 128 latent columns] E5M2, SW128: one O^T chunk
 constexpr uint32_t kRopeBox = 4 * kLatBox;                // offset of [128 tokens x 64 RoPE columns] E5M2, SW64
 constexpr uint32_t kSlotBytes = kRopeBox + kTile * kRope;  // 72 KB
-constexpr uint64_t kWaitLimitNs = 2000000000ull;          // 2 s
+constexpr uint32_t kWaitLimitNs = 2000000000u;            // 2 s
 constexpr float kRescaleThreshold = 5.f;                  // log2 units
 constexpr float kWeightBits = 10.f;                       // a weight is 2^10 at the running maximum, 2^15 at most
 
 template <int HC>
 struct Fp4Cfg {
   static constexpr int kHeads = HC / 2, kSoftWarps = 8;     // two softmax groups
-  static constexpr int kRowsPer = 2, kExpWarps = 16 / kRowsPer;  // cached rows to an expansion thread
+  // expansion: four lanes to a cached row, the rows of a half tile to the eight
+  // warps; 16 query rows: both halves at once, 32: one after the other
+  static constexpr int kExpWarps = 8, kHalves = HC == 16 ? 2 : 1;
   static constexpr int kThreads = 32 * (kSoftWarps + kExpWarps + 4);
+  // registers of a thread at the launch, and of each role (setmaxnreg)
+  static constexpr bool kSplitRegs = HC == 32;
+  static constexpr int kRegs = 96;
+  static constexpr int kSoftRegs = 136, kExpRegs = 64, kIssueRegs = 80;
+  static_assert(!kSplitRegs || 32 * (kSoftWarps * kSoftRegs + kExpWarps * kExpRegs + 4 * kIssueRegs) <= kThreads * kRegs,
+                "setmaxnreg shares out what the block was launched with");
   static constexpr int kNQ = 2 * HC, kNP = 3 * HC;          // N of the products
   static constexpr uint32_t kQBox = kNQ * 128;              // [2 HC rows x 128 columns] E4M3, SW128
   static constexpr uint32_t kQBytes = 4 * kQBox + kNQ * 64;  // + [2 HC rows x 64 RoPE columns], SW64
@@ -191,6 +200,29 @@ __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
+// A warpgroup's registers per thread from here on.
+template <bool kSplit, int N, int kFrom>
+__device__ __forceinline__ void set_max_regs() {
+  if constexpr (kSplit && N > kFrom) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+  if constexpr (kSplit && N < kFrom) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+// A bounded wait.  Where registers are shared out it is inline, since a function
+// call has registers of its own, and short, since the roles' loops share the
+// instruction caches; else it calls (16 rows: 106 us by calls, 111 inline, 121 with
+// a longer loop inline).
+template <bool kInline>
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, const volatile int* abort) {
+  if constexpr (!kInline) return mbar_wait(bar, parity, abort, kWaitLimitNs);
+  if (mbar_try_wait(bar, parity)) return true;
+  uint32_t t0, t1;  // nanoseconds; the low word wraps after 4.3 s
+  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t0));
+#pragma unroll 1
+  do {
+    if (mbar_try_wait(bar, parity)) return true;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t1));
+  } while (!*abort && t1 - t0 < kWaitLimitNs);
+  return false;
+}
 // Read-once data.
 __device__ __forceinline__ uint4 ld_stream(const uint8_t* p) {
   uint4 v;
@@ -262,13 +294,14 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
 
   if (warp >= C::kSoftWarps && warp < kQkWarp) {
     // ------------------------------------------------------------ expansion
-    // A warp has rows 8w .. 8w + 7 (two to a thread: and the 8 behind 64 + 8w),
-    // each of one page.  Thread (r, j) takes block 4c + j of row r, c = 0 .. 3, and
-    // piece j of its tail (RoPE blocks 16 and 17, scales 0 - 15, scales 16 and
-    // 17): four lanes read 64 bytes of a row, and their stores and those of the
-    // next row's lanes go to distinct banks.  A piece's registers are loaded
-    // again, for the next tile, as soon as it has been expanded.
-    constexpr int R = C::kRowsPer;
+    set_max_regs<C::kSplitRegs, C::kExpRegs, C::kRegs>();
+    // A warp has 8 rows of a half tile, all of one page; thread (r, j) takes block
+    // 4c + j of its row, c = 0 .. 3, and piece j of the row's tail (RoPE blocks 16
+    // and 17, scales 0 - 15, scales 16 and 17): four lanes read 64 bytes of a row,
+    // and their stores and those of the next row's lanes go to distinct banks.  A
+    // piece's registers are loaded again, for the next rows, as soon as it has
+    // been expanded.
+    constexpr int R = C::kHalves;
     const int w8 = 8 * (warp - C::kSoftWarps), j = lane & 3, r = w8 + (lane >> 2);
     const int lane2 = (lane & ~3) + 2, lane3 = lane2 + 1;
     // the block's two 16-byte pieces in its row of a latent and of the RoPE box
@@ -276,32 +309,41 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
     const uint32_t rope0 = kRopeBox + r * 64 + (((2 * j) ^ ((r >> 1) & 3)) << 4), rope1 = rope0 ^ 16;
     const uint2* lut = reinterpret_cast<const uint2*>(smem + C::kOffLut);
     const uint32_t byte_j = 0x4440 + j;  // byte j of a word
-    // where this thread's first row is, from its page's first, and the others' pages
     const int page_log2 = __ffs(p.page_size) - 1;
-    const uint32_t row_off = (r & (p.page_size - 1)) * kFp4RowBytes + 16 * j;
-    // the pages of tile k; scale bytes of 0 (values of 0) where there is no row
     const uint8_t* row[R];
-    bool ok = true;
-    auto look = [&](uint32_t k) -> int {
-      const int e = k % kRing;
-      ok = __all_sync(0xffffffffu, mbar_wait(&B->ring_full[e], (k / kRing) & 1, abort_flag, kWaitLimitNs));
-      if (!ok) return 0;
+    // this thread's rows of half tile `half` (and the other) of the tile in ring entry e
+    auto look = [&](int e, int half) {
 #pragma unroll
-      for (int i = 0; i < R; ++i) row[i] = B->page[e][(w8 + 64 * i) >> page_log2] + row_off;
-      return B->valid[e];
+      for (int i = 0; i < R; ++i) {
+        const int at = w8 + 64 * (half + i);
+        row[i] = B->page[e][at >> page_log2] + (((at & (p.page_size - 1)) + (lane >> 2)) * kFp4RowBytes + 16 * j);
+      }
     };
+    // scale bytes of 0 (values of 0) where there is no row
+    bool ok = __all_sync(0xffffffffu, wait_for<C::kSplitRegs>(&B->ring_full[0], 0, abort_flag));
+    int v0 = ok ? B->valid[0] : 0, v1 = 0;
     uint4 v[R][5];
-    int v0 = look(0), v1 = 0;
+    look(0, 0);
 #pragma unroll
     for (int i = 0; i < R; ++i)
 #pragma unroll
       for (int c = 0; c < 5; ++c) v[i][c] = r + 64 * i < v0 ? ld_stream(row[i] + 64 * c) : make_uint4(0, 0, 0, 0);
-    for (uint32_t k = 0; v0 > 0; ++k, v0 = v1) {
-      const uint32_t slot = k % kSlots;
+    for (uint32_t it = 0; v0 > 0; ++it) {
+      const uint32_t k = R == 2 ? it : it >> 1, half = R == 2 ? 0 : it & 1, slot = k % kSlots;
+      const bool begins = R == 2 || half == 0, ends = R == 2 || half == 1;
       uint8_t* base = smem + slot * kSlotBytes;
-      if (threadIdx.x == 32 * C::kSoftWarps) *reinterpret_cast<volatile int*>(&B->expanding) = int(k);
-      v1 = look(k + 1);
-      if (!ok) break;
+      int left;  // of the next rows: this thread's row r + 64 i is there if it is below
+      if (begins && threadIdx.x == 32 * C::kSoftWarps) *reinterpret_cast<volatile int*>(&B->expanding) = int(k);
+      if (ends) {
+        const int e = (k + 1) % kRing;
+        ok = __all_sync(0xffffffffu, wait_for<C::kSplitRegs>(&B->ring_full[e], ((k + 1) / kRing) & 1, abort_flag));
+        if (!ok) break;
+        left = v1 = B->valid[e];
+        look(e, 0);
+      } else {
+        look(k % kRing, 1);
+        left = v0 - 64;
+      }
       // the blocks' scale bytes, and whether any is outside 2^-13 .. 2^13
       uint32_t sc[R][5];
       bool far = false;
@@ -317,35 +359,35 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
           far |= sc[i][c] - (127 - 13) > 26;
         }
       }
-      // the tails first: their registers are the first that the next tile needs
+      // the tails first: their registers are the first that the next rows need
 #pragma unroll
       for (int cc = 0; cc < 5; ++cc) {
         const int c = cc == 0 ? 4 : cc - 1;
-        if (c == 4 || c == 2) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&B->empty[slot][c & 2 ? 1 : 0], ((k / kSlots) & 1) ^ 1, abort_flag, kWaitLimitNs));
+        if ((c == 4 || c == 2) && begins) {
+          ok = __all_sync(0xffffffffu, wait_for<C::kSplitRegs>(&B->empty[slot][c & 2 ? 1 : 0], ((k / kSlots) & 1) ^ 1, abort_flag));
           if (!ok) break;
         }
         if (c < 4 || j < 2) {
 #pragma unroll
           for (int i = 0; i < R; ++i) {
-            uint4 lo, hi;
             // the magnitudes' E5M2 bytes: within that range a scale adds to the
             // exponents, four to each byte and step (0 stays 0)
             uint2 tab = make_uint2(sc[i][c] * 0x04040400u + (0x3e3c3800u - 127u * 0x04040400u),
                                    sc[i][c] * 0x04040404u + (0x46444240u - 127u * 0x04040404u));
             if (far) tab = lut[sc[i][c]];
+            uint4 lo, hi;
             expand_block(v[i][c], tab, lo, hi);
-            uint8_t* dst = base + (c < 4 ? c * kLatBox + 64 * 128 * i : 64 * 64 * i);
+            uint8_t* dst = base + (c < 4 ? c * kLatBox + 64 * 128 * (half + i) : 64 * 64 * (half + i));
             *reinterpret_cast<uint4*>(dst + (c < 4 ? at0 : rope0)) = lo;
             *reinterpret_cast<uint4*>(dst + (c < 4 ? at1 : rope1)) = hi;
           }
         }
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-          if (r + 64 * i < v1) v[i][c] = ld_stream(row[i] + 64 * c);
+          if (r + 64 * i < left) v[i][c] = ld_stream(row[i] + 64 * c);
           else if (c == 4) v[i][c] = make_uint4(0, 0, 0, 0);
         }
-        if (c == 1 || c == 3) {
+        if ((c == 1 || c == 3) && ends) {
           // no proxy fence here: it would wait for the loads in flight.  The QK
           // issuer, which acquires these writes, fences for them.
           __syncwarp();
@@ -353,14 +395,16 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
         }
       }
       if (!ok) break;
+      if (ends) v0 = v1;
     }
     if (!ok) fail(B, p.status);
   } else if (warp >= kQkWarp) {
+    set_max_regs<C::kSplitRegs, C::kIssueRegs, C::kRegs>();
     // Whole warps wait and compute addresses, one lane issues: with everything
     // uniform a product costs a few instructions (with a single lane in the
     // role, 190 cycles each).
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, kWaitLimitNs)) != 0;
+      return __all_sync(0xffffffffu, wait_for<C::kSplitRegs>(bar, parity, abort_flag)) != 0;
     };
     if (warp == kQkWarp) {
       // ------------------------------------------------------------ QK issuer
@@ -469,7 +513,7 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
         if (more && first < t.valid) {
           int page = __ldg(p.block_table + size_t(t.b) * p.max_pages + ((t.tile * kTile) >> page_log2) + lane);
           if (uint32_t(page) >= uint32_t(p.num_pages)) {
-            report_bad_page(p.status);
+            set_status(p.status, MLA_ERR_DEVICE_BOUNDS);
             page = 0;
           }
           const uint8_t* rows = static_cast<const uint8_t*>(p.cache) + (size_t(page) << page_log2) * kFp4RowBytes;
@@ -485,9 +529,12 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
     // ------------------------------------------------------------ Q, softmax, epilogue
     // Group c (four warps) has heads NH c .. NH (c + 1) - 1 of the head group; thread
     // st of it the token row st of S^T (its TMEM lane).
+    set_max_regs<C::kSplitRegs, C::kSoftRegs, C::kRegs>();
     constexpr int NH = C::kHeads;
     const int c = warp >> 2, q4 = warp & 3, st = threadIdx.x & 127;
     const uint32_t lane_off = uint32_t(q4 * 32) << 16;
+    // the last group of 32 may be half empty: rows of zeros that write nothing
+    const bool live = HC == 16 || g * HC + NH * c < p.heads;
     float* qscale = red + 13 * HC + NH * c;  // + (segment & 1) * HC
     TileWalkerT<true> walk;
     walk.init(p.tile_start, p.seg_base, p.len, p.batch, int(S), pa, pb);
@@ -502,7 +549,7 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
       float top = 0.f;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        u[i] = i0 + T * i < 72 ? src[i0 + T * i] : make_uint4(0, 0, 0, 0);
+        u[i] = live && i0 + T * i < 72 ? src[i0 + T * i] : make_uint4(0, 0, 0, 0);
         const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
@@ -574,8 +621,8 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
     while (have) {
       const uint32_t buf = k & 1;
       const bool valid = st < t.valid;
-      bool ok = mbar_wait(&B->s_full[buf], (k >> 1) & 1, abort_flag, kWaitLimitNs);
-      if (k >= 2) ok = ok && mbar_wait(&B->pv_done[buf], ((k - 2) >> 1) & 1, abort_flag, kWaitLimitNs);
+      bool ok = wait_for<C::kSplitRegs>(&B->s_full[buf], (k >> 1) & 1, abort_flag);
+      if (k >= 2) ok = ok && wait_for<C::kSplitRegs>(&B->pv_done[buf], ((k - 2) >> 1) & 1, abort_flag);
       tc_fence_after();
       // the first tile of a segment: every thread's qscale must be there
       if (t.first) {
@@ -657,7 +704,7 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
       if (rescale) {
         // QK of this tile may have been issued before PV of the previous one:
         // wait for that PV first
-        const bool ok3 = mbar_wait(&B->pv_done[(k - 1) & 1], ((k - 1) >> 1) & 1, abort_flag, kWaitLimitNs);
+        const bool ok3 = wait_for<C::kSplitRegs>(&B->pv_done[(k - 1) & 1], ((k - 1) >> 1) & 1, abort_flag);
         tc_fence_after();
         if (group_any(c, !ok3)) break;
 #pragma unroll 1
@@ -714,7 +761,7 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
       const bool have_next = walk.next(tn);
       if (t.last) {
         if (have_next) load_q(tn.b, seg + 1);
-        const bool ok2 = mbar_wait(&B->o_full, seg & 1, abort_flag, kWaitLimitNs);
+        const bool ok2 = wait_for<C::kSplitRegs>(&B->o_full, seg & 1, abort_flag);
         tc_fence_after();
         float* rl = red + 8 * HC + 4 * NH * c;  // [NH][4] sums
         {
@@ -746,11 +793,12 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
           for (int h = 0; h < NH; ++h) v[h] += v2[h];
           tmem_load<NH>(a + 2 * HC, v2);
 #pragma unroll
-          for (int h = 0; h < NH; ++h) dst[h * kLatent + ch * 128] = (v[h] + v2[h]) * rinv[h];
+          for (int h = 0; h < NH; ++h)
+            if (live) dst[h * kLatent + ch * 128] = (v[h] + v2[h]) * rinv[h];
         }
         tc_fence_before();
         mbar_arrive(&B->o_free);
-        if (st < NH) {  // thread h writes head h's lse
+        if (st < NH && live) {  // thread h writes head h's lse
           p.partial_lse[size_t(t.seg) * p.heads + row0 + st] = l > 0.f ? (m_run[st] + log2f(l)) * kLn2 : lse_of_no_sum(l);
         }
         ++seg;

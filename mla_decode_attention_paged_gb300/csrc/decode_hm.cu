@@ -2,7 +2,7 @@
 // (128 heads; or q_len x heads rows of multi-token decode and prefill; a
 // sequence's last group padded when its rows are not a multiple of 128) on
 // CTA pairs, with the query rows as the tensor-core MMA's M extent.  Serves
-// bf16, INT8, FP8 and FP4 caches.
+// bf16, INT8 and FP8 caches.
 //
 // What it computes ("The Weight Absorption Trick"; "Seven Ways LLMs Handle
 // Attention", section 5; "Flash-Decoding and FlashInfer"): for 128 rows h of
@@ -47,10 +47,7 @@
 // values ("KV Cache Optimization", section 3: x = s_t (code - zp_t), INT8;
 // x = s_t e4m3(code), FP8), each computed in fp32 and rounded once to fp16.
 // Q and P are fp16, and from there the sub-tile runs exactly as for a bf16
-// cache: the scale and zero point never reach the softmax.  FP4 caches take the
-// same road: a code word becomes 16 bytes of fp16 in eleven instructions (byte
-// permutations with the codes as selectors, see decode_common.cuh), exact for
-// block scales 2^-15 .. 2^13.
+// cache: the scale and zero point never reach the softmax.
 //
 // Warp roles (384 threads; 512 for 1-byte caches):
 //   warp 0       TMA producer: Q's RoPE part per segment; latent boxes 0-1 and
@@ -86,10 +83,6 @@ constexpr uint32_t kOffRopeBox = 4 * kLatBox;     // [64 tokens x 32 RoPE column
 // 1-byte caches: a code slot holds a sub-tile's 4 latent code blocks [64 x
 // 64 B], its RoPE codes [64 x 32 B] and its per-token (scale, zero point) or
 // scale
-// FP4: the CTA's 128 code bytes of every token [64 x 128 B] SW128, then the row's
-// tail [64 x 64 B] (both halves of the RoPE codes, the scale bytes); the rest of
-// the first slot holds the table of block magnitudes by scale byte
-constexpr uint32_t kFp4Tail = 8192, kFp4Lut = 12288;
 constexpr int kCodeSlots = 2;
 constexpr uint32_t kCodeRope = 4 * 4096, kCodeScl = kCodeRope + 64 * 32, kCodeSlotBytes = 19 * 1024;
 constexpr uint32_t kXBytes = kRowsG * kSub * 2;   // one sub-tile's partial scores, fp16
@@ -225,7 +218,6 @@ __global__ void __launch_bounds__(HmCfg<kCode != kCodeBf16>::kThreads, 1)
                      const __grid_constant__ CUtensorMap tmap_qrope, DecodeParams p) {
   constexpr bool kByte = kCode != kCodeBf16;
   constexpr bool kZp = kCode == kCodeInt8;
-  constexpr bool kFp4 = kCode == kCodeE2m1;
   using C = HmCfg<kByte>;
   extern __shared__ uint8_t smem_raw[];
   // the same offset in both CTAs: the peer's exchange buffers and barriers are found by mapa
@@ -266,8 +258,6 @@ __global__ void __launch_bounds__(HmCfg<kCode != kCodeBf16>::kThreads, 1)
     tmem_alloc(&B->tmem_base, kTmemCols);
     tmem_relinquish();
   }
-  const uint2* lut = reinterpret_cast<const uint2*>(smem + C::kOffCode + kFp4Lut);
-  if (kFp4 && threadIdx.x < 256) reinterpret_cast<uint2*>(smem + C::kOffCode + kFp4Lut)[threadIdx.x] = e2m1_table(threadIdx.x);
   tc_fence_before();
   cluster_sync();  // both CTAs' barriers exist before either sends to the other
   tc_fence_after();
@@ -318,14 +308,9 @@ __global__ void __launch_bounds__(HmCfg<kCode != kCodeBf16>::kThreads, 1)
         nxt.rows(p, nrows, false);
 #pragma unroll 1
         for (int i = 0; i < nxt.nb; ++i) {
-          if constexpr (kFp4) {
-            if (role == 0) tma_prefetch_2d(&tmap_lat, lat0 / 2, nrows[i]);
-            else tma_prefetch_2d(&tmap_rope, kLatent / 2, nrows[i]);
-          } else {
-            tma_prefetch_2d(&tmap_lat, lat0 + 128 * role, nrows[i]);
-            tma_prefetch_2d(&tmap_lat, lat0 + 128 * role + 64, nrows[i]);
-            if (role == 0) tma_prefetch_2d(&tmap_rope, rope0, nrows[i]);
-          }
+          tma_prefetch_2d(&tmap_lat, lat0 + 128 * role, nrows[i]);
+          tma_prefetch_2d(&tmap_lat, lat0 + 128 * role + 64, nrows[i]);
+          if (role == 0) tma_prefetch_2d(&tmap_rope, rope0, nrows[i]);
         }
       }
       const uint32_t rows_bytes = uint32_t(nb * box_rows);
@@ -346,22 +331,17 @@ __global__ void __launch_bounds__(HmCfg<kCode != kCodeBf16>::kThreads, 1)
         const uint32_t cs = k % kCodeSlots;
         if (!(ok = mbar_wait(&B->code_empty[cs], ((k / kCodeSlots) & 1) ^ 1, abort_flag, kWaitLimitNs))) break;
         uint8_t* code = smem + C::kOffCode + cs * kCodeSlotBytes;
-        const uint32_t bytes = rows_bytes * (kFp4 ? (role == 0 ? 128 : 64) : role == 0 ? 64 + 64 + 32 : 64 + 64 + sbytes);
+        const uint32_t bytes = rows_bytes * (role == 0 ? 64 + 64 + 32 : 64 + 64 + sbytes);
         mbar_arrive_expect_tx(&B->landed[cs], bytes + (p.inject_wait_timeout && k == 0 && role == 0 ? 16 : 0));
 #pragma unroll 1
         for (int i = 0; i < nb; ++i) {
-          if constexpr (kFp4) {
-            if (role == 0) tma_load_2d(code + i * box_rows * 128, &tmap_lat, lat0 / 2, rows[i], &B->landed[cs]);
-            else tma_load_2d(code + kFp4Tail + i * box_rows * 64, &tmap_rope, kLatent / 2, rows[i], &B->landed[cs]);
-          } else {
-            for (int q = 2 * role; q < 2 * role + 2; ++q)
-              tma_load_2d(code + q * 4096 + i * box_rows * 64, &tmap_lat, lat0 + 64 * q, rows[i], &B->landed[cs]);
-            if (role == 0)
-              tma_load_2d(code + kCodeRope + i * box_rows * 32, &tmap_rope, rope0, rows[i], &B->landed[cs]);
-            else
-              bulk_copy_g2s(code + kCodeScl + i * box_rows * sbytes, p.scale_zero + size_t(rows[i]) * (kZp ? 2 : 1),
-                            box_rows * sbytes, &B->landed[cs]);
-          }
+          for (int q = 2 * role; q < 2 * role + 2; ++q)
+            tma_load_2d(code + q * 4096 + i * box_rows * 64, &tmap_lat, lat0 + 64 * q, rows[i], &B->landed[cs]);
+          if (role == 0)
+            tma_load_2d(code + kCodeRope + i * box_rows * 32, &tmap_rope, rope0, rows[i], &B->landed[cs]);
+          else
+            bulk_copy_g2s(code + kCodeScl + i * box_rows * sbytes, p.scale_zero + size_t(rows[i]) * (kZp ? 2 : 1),
+                          box_rows * sbytes, &B->landed[cs]);
         }
       }
       ++k;
@@ -500,78 +480,48 @@ __global__ void __launch_bounds__(HmCfg<kCode != kCodeBf16>::kThreads, 1)
           ok = false;
           break;
         }
-        if constexpr (kFp4) {
-          // thread ct takes token ct % 64: four of the row's eight latent blocks
-          // (32 codes, 64 bytes of fp16 each) and, in the first half, its RoPE
-          // block; rows apart, the lanes of a warp read and write distinct banks
-          const int r = ct & 63, half = ct >> 6;
-          const bool in = r < s.valid;
-          const uint8_t* tail = code + kFp4Tail + r * 64;
-          const uint32_t scl = *reinterpret_cast<const uint32_t*>(tail + 32 + 8 * rank + 4 * half);
+        // the three tokens' scale and -zero point x scale (FP8: no zero point)
+        float sc[3], nz[3] = {0.f, 0.f, 0.f};
+        {
+          const float* scl = reinterpret_cast<const float*>(code + kCodeScl);
+          const int rows3[3] = {ra, ra + 32, rr};
+#pragma unroll
+          for (int j = 0; j < 3; ++j) {
+            if constexpr (kZp) {
+              const float2 a = reinterpret_cast<const float2*>(scl)[rows3[j]];
+              sc[j] = a.x;
+              nz[j] = -a.y * a.x;
+            } else {
+              sc[j] = scl[rows3[j]];
+            }
+          }
+        }
 #pragma unroll 1
-          for (int i = 0; i < 4; ++i) {
-            const int c = 4 * half + i;
-            const uint4 v = *reinterpret_cast<const uint4*>(code + r * 128 + ((c ^ (r & 7)) << 4));
-            const uint2 t = in ? lut[(scl >> (8 * i)) & 255] : make_uint2(0, 0);
-            uint8_t* row = base + (c >> 1) * kLatBox + r * 128;  // 128-byte rows, 128-byte swizzle
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              *reinterpret_cast<uint4*>(row + (((4 * (c & 1) + j) ^ (r & 7)) << 4)) = e2m1_to_f16(w[j], t);
+        for (int i = 0; i < 8; ++i) {  // latent chunk i: token ra + 32 (i & 1), block i / 2
+          const int c = ct + 128 * i, q = c >> 8, r = (c >> 2) & 63, ch = c & 3;
+          const uint4 v = *reinterpret_cast<const uint4*>(code + q * 4096 + r * 64 + ch * 16);
+          uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+          if (r < s.valid) {
+            if constexpr (kZp) expand_codes(v, lo, hi);
+            else expand_e4m3(v, lo, hi);
+            dequant16(lo, hi, (i & 1) ? sc[1] : sc[0], (i & 1) ? nz[1] : nz[0]);
           }
-          if (half == 0) {
-            const uint4 v = *reinterpret_cast<const uint4*>(tail + 16 * rank);
-            const uint2 t = in ? lut[tail[48 + rank]] : make_uint2(0, 0);
-            uint8_t* row = base + kOffRopeBox + r * 64;  // 64-byte rows, 64-byte swizzle
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              *reinterpret_cast<uint4*>(row + ((j ^ ((r >> 1) & 3)) << 4)) = e2m1_to_f16(w[j], t);
+          uint8_t* row = base + q * kLatBox + r * 128;  // 128-byte rows, 128-byte swizzle
+          *reinterpret_cast<uint4*>(row + (((2 * ch) ^ (r & 7)) << 4)) = lo;
+          *reinterpret_cast<uint4*>(row + (((2 * ch + 1) ^ (r & 7)) << 4)) = hi;
+        }
+        {  // RoPE chunk: token rr
+          const int r = rr, ch = ct & 1;
+          const uint4 v = *reinterpret_cast<const uint4*>(code + kCodeRope + r * 32 + ch * 16);
+          uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+          if (r < s.valid) {
+            if constexpr (kZp) expand_codes(v, lo, hi);
+            else expand_e4m3(v, lo, hi);
+            dequant16(lo, hi, sc[2], nz[2]);
           }
-        } else {
-          // the three tokens' scale and -zero point x scale (FP8: no zero point)
-          float sc[3], nz[3] = {0.f, 0.f, 0.f};
-          {
-            const float* scl = reinterpret_cast<const float*>(code + kCodeScl);
-            const int rows3[3] = {ra, ra + 32, rr};
-  #pragma unroll
-            for (int j = 0; j < 3; ++j) {
-              if constexpr (kZp) {
-                const float2 a = reinterpret_cast<const float2*>(scl)[rows3[j]];
-                sc[j] = a.x;
-                nz[j] = -a.y * a.x;
-              } else {
-                sc[j] = scl[rows3[j]];
-              }
-            }
-          }
-  #pragma unroll 1
-          for (int i = 0; i < 8; ++i) {  // latent chunk i: token ra + 32 (i & 1), block i / 2
-            const int c = ct + 128 * i, q = c >> 8, r = (c >> 2) & 63, ch = c & 3;
-            const uint4 v = *reinterpret_cast<const uint4*>(code + q * 4096 + r * 64 + ch * 16);
-            uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-            if (r < s.valid) {
-              if constexpr (kZp) expand_codes(v, lo, hi);
-              else expand_e4m3(v, lo, hi);
-              dequant16(lo, hi, (i & 1) ? sc[1] : sc[0], (i & 1) ? nz[1] : nz[0]);
-            }
-            uint8_t* row = base + q * kLatBox + r * 128;  // 128-byte rows, 128-byte swizzle
-            *reinterpret_cast<uint4*>(row + (((2 * ch) ^ (r & 7)) << 4)) = lo;
-            *reinterpret_cast<uint4*>(row + (((2 * ch + 1) ^ (r & 7)) << 4)) = hi;
-          }
-          {  // RoPE chunk: token rr
-            const int r = rr, ch = ct & 1;
-            const uint4 v = *reinterpret_cast<const uint4*>(code + kCodeRope + r * 32 + ch * 16);
-            uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-            if (r < s.valid) {
-              if constexpr (kZp) expand_codes(v, lo, hi);
-              else expand_e4m3(v, lo, hi);
-              dequant16(lo, hi, sc[2], nz[2]);
-            }
-            uint8_t* row = base + kOffRopeBox + r * 64;  // 64-byte rows, 64-byte swizzle
-            *reinterpret_cast<uint4*>(row + (((2 * ch) ^ ((r >> 1) & 3)) << 4)) = lo;
-            *reinterpret_cast<uint4*>(row + (((2 * ch + 1) ^ ((r >> 1) & 3)) << 4)) = hi;
-          }
+          uint8_t* row = base + kOffRopeBox + r * 64;  // 64-byte rows, 64-byte swizzle
+          *reinterpret_cast<uint4*>(row + (((2 * ch) ^ ((r >> 1) & 3)) << 4)) = lo;
+          *reinterpret_cast<uint4*>(row + (((2 * ch + 1) ^ ((r >> 1) & 3)) << 4)) = hi;
         }
         fence_proxy_async_smem();
         converters_sync();
@@ -809,9 +759,7 @@ __global__ void __launch_bounds__(HmCfg<kCode != kCodeBf16>::kThreads, 1)
         tc_fence_before();
         mbar_arrive(&B->o_free);
         if (rank == 0 && c == 0 && live)
-          p.partial_lse[size_t(s.seg) * p.heads + row] = l_row > 0.f ? (m_run + log2f(l_row)) * kLn2
-                                                         : kFp4      ? lse_of_no_sum(l_row)
-                                                                     : -INFINITY;
+          p.partial_lse[size_t(s.seg) * p.heads + row] = l_row > 0.f ? (m_run + log2f(l_row)) * kLn2 : -INFINITY;
         soft_sync();  // the sums are read before the next sub-tile writes its maxima there
         ++seg;
       }
@@ -844,16 +792,12 @@ cudaError_t launch_hm(const DecodeParams& p, int clusters_per_group, cudaStream_
   const uint64_t rows = uint64_t(p.num_pages) * p.page_size, qrows = uint64_t(p.batch) * p.heads;
   const uint32_t box_rows = p.page_size < kSub ? p.page_size : kSub;
   const int eb = kByte ? 1 : 2;
-  if (kCode == kCodeE2m1) {
-    if (!make_map_2d(&ml, p.cache, 1, kFp4RowBytes, rows, 128, box_rows, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_map_2d(&mr, p.cache, 1, kFp4RowBytes, rows, 64, box_rows, CU_TENSOR_MAP_SWIZZLE_NONE))
-      return cudaErrorInvalidValue;
-  } else if (!make_map_2d(&ml, p.cache, eb, kRow, rows, 64, box_rows,
+  if (!make_map_2d(&ml, p.cache, eb, kRow, rows, 64, box_rows,
                    kByte ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_map_2d(&mr, p.cache, eb, kRow, rows, 32, box_rows,
-                   kByte ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_64B))
+                   kByte ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_64B) ||
+      !make_map_2d(&mqr, p.q_full, 2, kRow, qrows, 32, kRowsG, CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
-  if (!make_map_2d(&mqr, p.q_full, 2, kRow, qrows, 32, kRowsG, CU_TENSOR_MAP_SWIZZLE_64B)) return cudaErrorInvalidValue;
   static std::atomic<bool> attr[128];  // per device: attributes set (zero-initialised)
   int dev = 0;
   cudaGetDevice(&dev);
@@ -905,16 +849,13 @@ int hm_capacity() {  // CTA pairs of this kernel that can be resident at once on
 }  // namespace
 
 int decode_rows128_capacity(int code) {
-  return code == kCodeInt8   ? hm_capacity<kCodeInt8>()
-         : code == kCodeE4m3 ? hm_capacity<kCodeE4m3>()
-         : code == kCodeE2m1 ? hm_capacity<kCodeE2m1>()
-                             : hm_capacity<kCodeBf16>();
+  return code == kCodeInt8 ? hm_capacity<kCodeInt8>() : code == kCodeE4m3 ? hm_capacity<kCodeE4m3>()
+                                                                          : hm_capacity<kCodeBf16>();
 }
 
 cudaError_t launch_decode_rows128(const DecodeParams& p, int code, int clusters_per_group, cudaStream_t stream) {
   return code == kCodeInt8   ? launch_hm<kCodeInt8>(p, clusters_per_group, stream)
          : code == kCodeE4m3 ? launch_hm<kCodeE4m3>(p, clusters_per_group, stream)
-         : code == kCodeE2m1 ? launch_hm<kCodeE2m1>(p, clusters_per_group, stream)
                              : launch_hm<kCodeBf16>(p, clusters_per_group, stream);
 }
 

@@ -75,8 +75,7 @@ struct AttnChoice {
 AttnChoice choose_attention(int rows, int code) {
   const bool byte = code != kCodeBf16;
   if (code == kCodeE2m1)
-    return rows <= 64 ? AttnChoice{kAttnFp4, rows % 32 == 0 ? 32 : 16, sm_count()}
-                      : AttnChoice{kAttnRows128, 128, decode_rows128_capacity(code)};
+    return {kAttnFp4, rows == 16 ? 16 : 32, sm_count()};
   const bool single = g_force_single_cta.load() != 0;
   const bool pair_groups = !byte && rows <= 64 && rows % 32 == 0;
   if (!single && (rows % 128 == 0 || (rows > 32 && !pair_groups))) {
