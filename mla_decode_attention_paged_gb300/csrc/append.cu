@@ -27,12 +27,41 @@ __device__ __forceinline__ uint32_t e4m3x2_rn_sat(float first, float second) {
 // ----- FP4 rows ------------------------------------------------------------------
 // A code is a quarter of its block's largest value away from the next, so a
 // rotated value that lands on the other side of its bf16 rounding can change by
-// that much.  The rotation of FP4 rows is therefore exact to about 2^-32: the
+// that much.  The rotation of FP4 rows is therefore exact to about 2^-30: the
 // angle as a 64-bit fraction of a turn (pos times the frequency, modulo 2^64:
 // two integer multiply-adds, where fp64 takes 64 times the issue slots of fp32
-// on this part), sine and cosine as sums of two fp32 values, and one rounding
-// to bf16.  Against the fp64 rotation about one value in 10^6 differs (fp32
-// sine and cosine: one in 10^4).
+// on this part), sine and cosine from a table of 256 angles, each a sum of two
+// floats, and the angle that is left, and one rounding to bf16.  Against the fp64
+// rotation less than one value in 10^6 differs (fp32 sine and cosine: one in
+// 10^4).
+struct alignas(16) SinCos {
+  float sh, sl, ch, cl;  // sine and cosine as hi + lo
+};
+struct TurnTable {
+  SinCos at[256];
+};
+// Sines and cosines of i / 256 turns, by their Taylor series in double around the nearest quarter.
+constexpr TurnTable make_turn_table() {
+  TurnTable t = {};
+  for (int i = 0; i < 256; ++i) {
+    const int quarter = (i + 32) / 64;
+    const double x = (i - 64 * quarter) * (6.283185307179586476925286766559 / 256);
+    double s = 0, c = 0, term = 1;
+    for (int n = 0; n < 24; ++n) {  // term = x^n / n!
+      if (n % 2 == 0) c += n % 4 == 0 ? term : -term;
+      else s += n % 4 == 1 ? term : -term;
+      term = term * x / (n + 1);
+    }
+    const double sine = quarter % 4 == 0 ? s : quarter % 4 == 1 ? c : quarter % 4 == 2 ? -s : -c;
+    const double cosine = quarter % 4 == 0 ? c : quarter % 4 == 1 ? -s : quarter % 4 == 2 ? -c : s;
+    t.at[i].sh = float(sine);
+    t.at[i].sl = float(sine - double(float(sine)));
+    t.at[i].ch = float(cosine);
+    t.at[i].cl = float(cosine - double(float(cosine)));
+  }
+  return t;
+}
+__device__ const TurnTable kTurns = make_turn_table();
 
 // The product a * b as a rounded value and its rounding error.
 __device__ __forceinline__ float mul_err(float a, float b, float& err) {
@@ -40,67 +69,23 @@ __device__ __forceinline__ float mul_err(float a, float b, float& err) {
   err = __fmaf_rn(a, b, -p);
   return p;
 }
-// hi + lo = a + b, for |a| >= |b| or a = 0.
-__device__ __forceinline__ float add_err(float a, float b, float& err) {
-  const float s = __fadd_rn(a, b);
-  err = __fadd_rn(b, -__fadd_rn(s, -a));
-  return s;
-}
 
-// Sine and cosine of `phase` / 2^64 turns, each as hi + lo.  The phase goes to
-// the nearest quarter turn; the remainder x, |x| <= pi / 4, through the Taylor
-// series with the leading terms in two floats (the fp32 terms behind them are
-// below 0.006 of the result).
-__device__ __forceinline__ void sincos_turns(uint64_t phase, float& sh, float& sl, float& ch, float& cl) {
-  const uint32_t quarter = uint32_t((phase + (1ull << 61)) >> 62);  // 0 .. 4, modulo 4 below
-  const int64_t r = int64_t(phase - (uint64_t(quarter) << 62));     // in [-2^61, 2^61)
-  const float a = float(int32_t(r >> 38)), b = float(int32_t((r >> 14) & 0xffffff));
-  // x = a 2 pi 2^-26 + b 2 pi 2^-50, the first constant as two floats
-  constexpr double kTwoPi = 6.283185307179586476925286766559;
-  constexpr float kC1 = float(kTwoPi / (1 << 26)), kC1l = float(kTwoPi / (1 << 26) - double(kC1));
-  constexpr float kC2 = float(kTwoPi / (1 << 26) / (1 << 24));
-  float xl, e;
-  const float p = mul_err(a, kC1, e);
-  const float xh = add_err(p, __fmaf_rn(b, kC2, __fmaf_rn(a, kC1l, e)), xl);
-  // z = x^2, w = x^3, q = x^4
-  float zl, wl, ql;
-  const float zh = mul_err(xh, xh, zl);
-  zl = __fmaf_rn(2.f * xh, xl, zl);
-  const float wh = mul_err(zh, xh, wl);
-  wl = __fmaf_rn(zh, xl, __fmaf_rn(zl, xh, wl));
-  const float qh = mul_err(zh, zh, ql);
-  ql = __fmaf_rn(2.f * zh, zl, ql);
-  // sin x = x + x^3 (-1/6 + z/120 - z^2/5040 + z^3/362880 - z^4/39916800)
-  constexpr float k6 = float(-1.0 / 6), k6l = float(-1.0 / 6 - double(k6));
-  const float ts = zh * __fmaf_rn(zh, __fmaf_rn(zh, __fmaf_rn(zh, -1.f / 39916800.f, 1.f / 362880.f), -1.f / 5040.f),
-                                  1.f / 120.f);
-  float fl, pl;
-  const float fs = add_err(k6, ts, fl);
-  fl = __fadd_rn(fl, k6l);
-  const float ps = mul_err(wh, fs, pl);
-  pl = __fmaf_rn(wh, fl, __fmaf_rn(wl, fs, pl));
-  float s_lo;
-  const float s_hi = add_err(xh, ps, s_lo);
-  s_lo = __fadd_rn(s_lo, __fadd_rn(pl, xl));
-  // cos x = 1 - z/2 + x^4 (1/24 - z/720 + z^2/40320 - z^3/3628800 + z^4/479001600)
-  constexpr float k24 = float(1.0 / 24), k24l = float(1.0 / 24 - double(k24));
-  const float tc = zh * __fmaf_rn(zh, __fmaf_rn(zh, __fmaf_rn(zh, 1.f / 479001600.f, -1.f / 3628800.f), 1.f / 40320.f),
-                                  -1.f / 720.f);
-  const float fc = add_err(k24, tc, fl);
-  fl = __fadd_rn(fl, k24l);
-  const float pc = mul_err(qh, fc, pl);
-  pl = __fmaf_rn(qh, fl, __fmaf_rn(ql, fc, pl));
-  float h_lo, c_lo;
-  const float h_hi = add_err(1.f, -0.5f * zh, h_lo);
-  const float c_hi = add_err(h_hi, pc, c_lo);
-  c_lo = __fadd_rn(c_lo, __fadd_rn(pl, __fmaf_rn(-0.5f, zl, h_lo)));
-  const bool swap = quarter & 1, neg_s = quarter & 2, neg_c = (quarter + 1) & 2;
-  sh = swap ? c_hi : s_hi;
-  sl = swap ? c_lo : s_lo;
-  ch = swap ? s_hi : c_hi;
-  cl = swap ? s_lo : c_lo;
-  if (neg_s) { sh = -sh; sl = -sl; }
-  if (neg_c) { ch = -ch; cl = -cl; }
+// Sine and cosine of `phase` / 2^64 turns, each as hi + lo with lo up to 0.0124:
+// the nearest of the table's angles a, and b = what is left, at most 1 / 512
+// turn: sin(a + b) = sin a + (sin a (cos b - 1) + cos a sin b), and so on.  The
+// fp32 terms in brackets are below 0.0125, off by 2^-30.
+__device__ __forceinline__ SinCos sincos_turns(uint64_t phase, const SinCos* table) {
+  const uint64_t near = phase + (1ull << 55);
+  const SinCos a = table[near >> 56];
+  constexpr float kStep = 6.283185307179586476925286766559 / (1ll << 40);
+  const float b = float(int32_t(uint32_t(near >> 24) ^ 0x80000000u)) * kStep, b2 = b * b;
+  const float sb = __fmaf_rn(b * b2, -1.f / 6.f, b), cb = b2 * __fmaf_rn(b2, 1.f / 24.f, -0.5f);  // cb: cos b - 1
+  SinCos r;
+  r.sh = a.sh;
+  r.sl = __fmaf_rn(a.sh, cb, __fmaf_rn(a.ch, sb, a.sl));
+  r.ch = a.ch;
+  r.cl = __fmaf_rn(a.ch, cb, __fmaf_rn(-a.sh, sb, a.cl));
+  return r;
 }
 
 // x a + y b rounded once to bf16, for bf16 x and y and two-float a and b.
@@ -118,8 +103,12 @@ __device__ __forceinline__ __nv_bfloat16 dot2_bf16(float x, float ah, float al, 
   return __float2bfloat16_rn(__uint_as_float(bits));
 }
 
-// The larger of two packed pairs of 16-bit magnitudes, each half by itself.
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
+// The larger magnitudes of two packed pairs of bf16 values, NaN where either is.
+__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 m = __hmax2_nan(__habs2(*reinterpret_cast<const __nv_bfloat162*>(&a)),
+                                       __habs2(*reinterpret_cast<const __nv_bfloat162*>(&b)));
+  return *reinterpret_cast<const uint32_t*>(&m);
+}
 
 // The scale byte of a block whose largest magnitude has these bf16 bits: the
 // smallest power of two s with largest <= 6 s = 1.5 * 2^2 s, at least 2^-127;
@@ -132,6 +121,16 @@ __device__ __forceinline__ uint32_t fp4_scale_byte(uint32_t top) {
 // 1 / scale (0 for 255: every code of such a block is 0).
 __device__ __forceinline__ float fp4_inv_scale(uint32_t byte) {
   return byte == 255 ? 0.f : __uint_as_float((254 - byte) << 23);
+}
+// Two fp32 values to E2M1 codes, the first in the low four bits (the rest undefined).
+__device__ __forceinline__ uint32_t e2m1x2_rn_sat(float first, float second) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "mov.b32 %0, {a, a, a, a};\n\t}"
+      : "=r"(r)
+      : "f"(first), "f"(second));
+  return r;
 }
 // Eight fp32 values to E2M1 codes (nearest, ties to even), value i in bits 4i .. 4i + 3.
 __device__ __forceinline__ uint32_t e2m1x8_rn_sat(const float (&v)[8]) {
@@ -155,20 +154,20 @@ __device__ __forceinline__ uint32_t fp4_word(const uint32_t (&x)[4], float inv) 
   float v[8];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    v[2 * j] = __uint_as_float((x[j] & 0x7fff) << 16) * inv;
-    v[2 * j + 1] = __uint_as_float(x[j] & 0x7fff0000) * inv;
+    v[2 * j] = __uint_as_float(x[j] << 16) * inv;
+    v[2 * j + 1] = __uint_as_float(x[j] & 0xffff0000u) * inv;
   }
   const uint32_t lo = __byte_perm(x[0], x[1], 0x7531) & 0x80808080u, hi = __byte_perm(x[2], x[3], 0x7531) & 0x80808080u;
-  return e2m1x8_rn_sat(v) | lo | (hi >> 4);
+  return (e2m1x8_rn_sat(v) & 0x77777777u) | lo | (hi >> 4);
 }
 
 // Quantises and stores one row: lane l has latents [16l, 16l + 16) and the
 // rotated pair l of the RoPE key.
 __device__ __forceinline__ void store_fp4_row(uint8_t* dst, const uint4& c0, const uint4& c1, uint32_t pair, int lane) {
   const uint32_t x0[4] = {c0.x, c0.y, c0.z, c0.w}, x1[4] = {c1.x, c1.y, c1.z, c1.w};
-  uint32_t top2 = 0;
+  uint32_t top2 = max_abs_bf16x2(x0[0], x1[0]);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) top2 = max_u16x2(top2, max_u16x2(x0[j] & 0x7fff7fffu, x1[j] & 0x7fff7fffu));
+  for (int j = 1; j < 4; ++j) top2 = max_abs_bf16x2(top2, max_abs_bf16x2(x0[j], x1[j]));
   uint32_t top = max(top2 & 0xffff, top2 >> 16);
   top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));  // the block's other half
   const uint32_t scale = fp4_scale_byte(top);
@@ -182,9 +181,13 @@ __device__ __forceinline__ void store_fp4_row(uint8_t* dst, const uint4& c0, con
   for (int o = 8; o > 0; o >>= 1) rtop = max(rtop, __shfl_xor_sync(0xffffffffu, rtop, o));
   const uint32_t rscale = fp4_scale_byte(rtop);
   const int g = lane & 3;
-  // the lane's pair is values 2g and 2g + 1 of the word
-  const uint32_t xr[4] = {g == 0 ? pair : 0, g == 1 ? pair : 0, g == 2 ? pair : 0, g == 3 ? pair : 0};
-  uint32_t wr = rscale == 255 ? 0 : fp4_word(xr, fp4_inv_scale(rscale));
+  // the lane's pair is values 2g and 2g + 1 of the word: byte g, and the signs'
+  // bits 16g + 7 and 16g + 15 (g < 2) or 16g - 29 and 16g - 21
+  const float rinv = fp4_inv_scale(rscale);
+  uint32_t wr = 0;
+  if (rscale != 255)
+    wr = ((e2m1x2_rn_sat(__uint_as_float(pair << 16) * rinv, __uint_as_float(pair & 0xffff0000u) * rinv) & 0x77) << (8 * g)) |
+         (((pair >> 15 & 1) | (pair >> 31 << 8)) << (g < 2 ? 16 * g + 7 : 16 * g - 29));
   wr |= __shfl_xor_sync(0xffffffffu, wr, 1);
   wr |= __shfl_xor_sync(0xffffffffu, wr, 2);
   if (g == 0) reinterpret_cast<uint32_t*>(dst + 256)[lane >> 2] = wr;
@@ -199,6 +202,73 @@ __device__ __forceinline__ void store_fp4_row(uint8_t* dst, const uint4& c0, con
   if (lane == 1) reinterpret_cast<uint4*>(dst + kFp4Scales)[1] = make_uint4(r16 | (r17 << 8), 0, 0, 0);
 }
 
+// Position of token i and its cache row; false (and reported) if its sequence,
+// position or page-table entry is out of range.
+__device__ __forceinline__ bool locate(const AppendParams& p, int i, int lane, int& pos, size_t& row) {
+  const int b = p.chunk > 0 ? i / p.chunk : p.seq_ids[i];
+  // 64-bit: a length near the int32 limits must not wrap into a valid position
+  const long long pos64 = p.chunk > 0 ? (long long)p.seq_lens[b] - p.chunk + i % p.chunk : p.positions[i];
+  const int page_log2 = __ffs(p.page_size) - 1;
+  bool ok = b >= 0 && b < p.num_seqs && pos64 >= 0 && pos64 < ((long long)p.max_pages << page_log2);
+  pos = int(pos64);  // in [0, max_pages * P) once ok
+  int page = -1;
+  if (ok) {
+    page = p.block_table[size_t(b) * p.max_pages + (pos >> page_log2)];
+    ok = page >= 0 && page < p.num_pages;
+  }
+  if (!ok && lane == 0) set_status(p.status, MLA_ERR_DEVICE_BOUNDS);
+  row = (size_t(page) << page_log2) + (pos & (p.page_size - 1));
+  return ok;
+}
+
+// FP4: a warp takes T tokens, the next one's values on their way while it works
+// on one.  Lane l owns latent values [16l, 16l + 16) and RoPE pair l.  Bound by
+// instructions (rotation, quantisation, packing) rather than memory (1,472 bytes a
+// token).
+template <int T>
+__global__ void __launch_bounds__(256) append_fp4_kernel(AppendParams p) {
+  __shared__ SinCos shared_turns[T > 1 ? 256 : 1];
+  const SinCos* turns = kTurns.at;
+  if constexpr (T > 1) {  // 256 threads; gathers of 16 bytes are cheaper in shared memory
+    shared_turns[threadIdx.x] = kTurns.at[threadIdx.x];
+    turns = shared_turns;
+    __syncthreads();
+  }
+  ptx::griddep_wait();
+  ptx::griddep_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int i0 = (blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * T;
+  if (i0 >= p.n_tokens) return;
+  const uint64_t turn = p.turn[lane];
+  uint4 c0, c1;
+  __nv_bfloat162 kp;
+  auto load = [&](int i) {
+    const uint4* src = reinterpret_cast<const uint4*>(p.c_kv + size_t(i) * kLatent) + 2 * lane;
+    c0 = src[0];
+    c1 = src[1];
+    kp = reinterpret_cast<const __nv_bfloat162*>(p.k_pe + size_t(i) * kRope)[lane];
+  };
+  load(i0);
+#pragma unroll 1
+  for (int t = 0; t < T && i0 + t < p.n_tokens; ++t) {
+    const uint4 x0 = c0, x1 = c1;
+    const __nv_bfloat162 k = kp;
+    if (t + 1 < T && i0 + t + 1 < p.n_tokens) load(i0 + t + 1);
+    int pos;
+    size_t row;
+    if (!locate(p, i0 + t, lane, pos, row)) continue;
+    __nv_bfloat162 kr = k;
+    if (p.rotate) {
+      const SinCos r = sincos_turns(uint64_t(pos) * turn, turns);
+      const float a = __low2float(k), b = __high2float(k);
+      kr.x = dot2_bf16(a, r.ch, r.cl, -b, r.sh, r.sl);
+      kr.y = dot2_bf16(a, r.sh, r.sl, b, r.ch, r.cl);
+    }
+    store_fp4_row(static_cast<uint8_t*>(p.cache) + row * kFp4RowBytes, x0, x1, *reinterpret_cast<const uint32_t*>(&kr),
+                  lane);
+  }
+}
+
 // One warp per token.  Lane l owns latent values [16l, 16l + 16) and RoPE pair l.
 template <int kCode>
 __global__ void __launch_bounds__(256) append_kernel(AppendParams p) {
@@ -207,25 +277,15 @@ __global__ void __launch_bounds__(256) append_kernel(AppendParams p) {
   const int lane = threadIdx.x & 31;
   const int i = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (i >= p.n_tokens) return;
-  const int b = p.chunk > 0 ? i / p.chunk : p.seq_ids[i];
-  // 64-bit: a length near the int32 limits must not wrap into a valid position
-  const long long pos64 = p.chunk > 0 ? (long long)p.seq_lens[b] - p.chunk + i % p.chunk : p.positions[i];
-  bool ok = b >= 0 && b < p.num_seqs && pos64 >= 0 && pos64 / p.page_size < p.max_pages;
-  const int pos = int(pos64);  // in [0, max_pages * P) once ok
-  int page = -1;
-  if (ok) {
-    page = p.block_table[size_t(b) * p.max_pages + pos / p.page_size];
-    ok = page >= 0 && page < p.num_pages;
-  }
-  if (!ok) {
-    if (lane == 0) set_status(p.status, MLA_ERR_DEVICE_BOUNDS);
-    return;
-  }
-  const size_t row = size_t(page) * p.page_size + pos % p.page_size;
-
-  // latent part: 16 bf16 per lane, two 16-byte loads
+  // latent part: 16 bf16 per lane, two 16-byte loads; RoPE pair `lane`.  They do
+  // not wait for the page lookup.
   const uint4* src = reinterpret_cast<const uint4*>(p.c_kv + size_t(i) * kLatent) + 2 * lane;
   uint4 c0 = src[0], c1 = src[1];
+  const __nv_bfloat162 kp = reinterpret_cast<const __nv_bfloat162*>(p.k_pe + size_t(i) * kRope)[lane];
+
+  int pos;
+  size_t row;
+  if (!locate(p, i, lane, pos, row)) return;
 
   // RoPE pair `lane`: angle = pos * theta^(-2 lane / 64) in fp64 (up to
   // ~2^31 rad), reduced modulo 2 pi in fp64 to [-pi, pi]; sine, cosine and
@@ -233,20 +293,7 @@ __global__ void __launch_bounds__(256) append_kernel(AppendParams p) {
   // fp64 sincos per lane kept the few SMs an append runs on busy for
   // microseconds (the fp64 units are a small fraction of this part's), and
   // the reduced fp32 result stays far inside the bf16 rounding.
-  const __nv_bfloat162 kp = reinterpret_cast<const __nv_bfloat162*>(p.k_pe + size_t(i) * kRope)[lane];
   __nv_bfloat162 kr = kp;
-  if constexpr (kCode == kCodeE2m1) {
-    if (p.rope_theta > 0.0) {
-      float sh, sl, ch, cl;
-      sincos_turns(uint64_t(pos) * p.turn[lane], sh, sl, ch, cl);
-      const float x0 = __low2float(kp), x1 = __high2float(kp);
-      kr.x = dot2_bf16(x0, ch, cl, -x1, sh, sl);
-      kr.y = dot2_bf16(x0, sh, sl, x1, ch, cl);
-    }
-    store_fp4_row(static_cast<uint8_t*>(p.cache) + row * kFp4RowBytes, c0, c1, *reinterpret_cast<const uint32_t*>(&kr),
-                  lane);
-    return;
-  }
   if (p.rope_theta > 0.0) {
     constexpr double kTwoPi = 6.283185307179586476925286766559, kInvTwoPi = 0.15915494309189533576888376337251;
     const double ang = __dmul_rn(double(pos), p.inv_freq[lane]);
@@ -346,7 +393,11 @@ cudaError_t launch_append(const AppendParams& p, int code, cudaStream_t stream) 
   const int grid = (p.n_tokens + warps - 1) / warps;
   if (code == kCodeInt8) return launch_pdl(append_kernel<kCodeInt8>, dim3(grid), dim3(warps * 32), 0, stream, 1, p);
   if (code == kCodeE4m3) return launch_pdl(append_kernel<kCodeE4m3>, dim3(grid), dim3(warps * 32), 0, stream, 1, p);
-  if (code == kCodeE2m1) return launch_pdl(append_kernel<kCodeE2m1>, dim3(grid), dim3(warps * 32), 0, stream, 1, p);
+  if (code == kCodeE2m1) {
+    if (p.n_tokens < 2048) return launch_pdl(append_fp4_kernel<1>, dim3(grid), dim3(warps * 32), 0, stream, 1, p);
+    constexpr int T = 4;
+    return launch_pdl(append_fp4_kernel<T>, dim3((p.n_tokens + 8 * T - 1) / (8 * T)), dim3(256), 0, stream, 1, p);
+  }
   return launch_pdl(append_kernel<kCodeBf16>, dim3(grid), dim3(warps * 32), 0, stream, 1, p);
 }
 

@@ -132,6 +132,7 @@ AppendParams append_params(const mla_dims* d, void* cache, float* cache_scale_ze
   p.k_pe = static_cast<const __nv_bfloat16*>(k_pe);
   p.status = device_status;
   p.rope_theta = rope_theta;
+  p.rotate = rope_theta > 0.0;
   // the frequencies depend only on theta: one fp64 pow per pair here instead
   // of one per token and pair on the device's slow fp64 units
   for (int i = 0; i < kRope / 2; ++i) {

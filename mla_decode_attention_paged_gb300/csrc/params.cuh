@@ -81,6 +81,7 @@ struct AppendParams {
   double rope_theta;
   double inv_freq[kRope / 2];    // theta^(-2i/64), evaluated on the host in fp64
   uint64_t turn[kRope / 2];      // FP4: the fraction of inv_freq / (2 pi) in units of 2^-64
+  int rotate;                    // FP4: rope_theta > 0
   int n_tokens, num_seqs, max_pages, num_pages, page_size;
 };
 
