@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
     const uint32_t at0 = r * 128 + (((2 * j) ^ (r & 7)) << 4), at1 = at0 ^ 16;
     const uint32_t rope0 = kRopeBox + r * 64 + (((2 * j) ^ ((r >> 1) & 3)) << 4), rope1 = rope0 ^ 16;
     const uint2* lut = reinterpret_cast<const uint2*>(smem + C::kOffLut);
-    const uint32_t byte_j = 0x4440 + j;  // byte j of a word
+    const uint32_t byte_j = 0x4440 + j, byte_r = 0x4440 + (j & 1);  // bytes j and j % 2 of a word
     const int page_log2 = __ffs(p.page_size) - 1;
     const uint8_t* row[R];
     // this thread's rows of half tile `half` (and the other) of the tile in ring entry e
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
             __shfl_sync(0xffffffffu, v[i][4].x, lane3)};
 #pragma unroll
         for (int c = 0; c < 5; ++c) {
-          sc[i][c] = __byte_perm(tail[c], 0, byte_j);
+          sc[i][c] = __byte_perm(tail[c], 0, c < 4 ? byte_j : byte_r);
           far |= sc[i][c] - (127 - 13) > 26;
         }
       }
@@ -507,7 +507,10 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
       for (int k = 0; more; ++k) {
         const uint64_t t0 = global_timer_ns();
         while (*at + kAhead < k && (ok = !*abort_flag && global_timer_ns() - t0 < kWaitLimitNs)) __nanosleep(64);
-        if (!__all_sync(0xffffffffu, ok)) break;
+        if (!__all_sync(0xffffffffu, ok)) {
+          fail(B, p.status);
+          break;
+        }
         more = walk.next(t);
         const int e = k % kRing, first = lane << page_log2;
         if (more && first < t.valid) {
