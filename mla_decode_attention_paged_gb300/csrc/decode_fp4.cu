@@ -22,8 +22,9 @@
 // and exactly.  The other operands are fp32 values split into FP8 terms that
 // stand side by side in the MMA's N extent (16 heads fill an eighth of it: the
 // MMA's time is its A operand's way through shared memory):
-//   Q: two E4M3 terms, q = 2^-k (hi + lo / 16), k per head: off by at most 2^-8
-//      of a value, as bf16 is (half of that on average)
+//   Q: two E4M3 terms, q = 2^-k (hi + lo / 16): off by at most 2^-8 of a value, as
+//      bf16 is (half of that on average), and by at most 2^-22 of the largest of
+//      the 8 or 16 heads that share k
 //   P: three E5M2 terms, hi + mid + lo = the weight's fp16 value exactly down to
 //      2^-19 of the running maximum and to 2^-30 of it below: as many bits as the
 //      1-byte caches' weights
@@ -247,8 +248,8 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Fp4Barriers* B = reinterpret_cast<Fp4Barriers*>(smem + C::kOffMisc);
-  // [2][HC][4] maxima, [HC][4] sums, [HC] 1 / l, [2][HC] scale of Q's terms, [HC]
-  // running maxima less kWeightBits, [HC] factors of a rescale
+  // [2][HC][4] maxima, [HC][4] sums, [HC] 1 / l, [2 groups][2][4] largest values of
+  // Q, [HC] running maxima less kWeightBits, [HC] factors of a rescale
   float* red = reinterpret_cast<float*>(smem + C::kOffMisc + 1024);
   const uint32_t sbase = smem_u32(smem);
   const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
@@ -538,12 +539,13 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
     const uint32_t lane_off = uint32_t(q4 * 32) << 16;
     // the last group of 32 may be half empty: rows of zeros that write nothing
     const bool live = HC == 16 || g * HC + NH * c < p.heads;
-    float* qscale = red + 13 * HC + NH * c;  // + (segment & 1) * HC
+    float* qtop = red + 13 * HC + 8 * c;  // [2 segments' parity][4] largest magnitude by warp
     TileWalkerT<true> walk;
     walk.init(p.tile_start, p.seg_base, p.len, p.batch, int(S), pa, pb);
     // Q of a segment's sequence as two E4M3 terms: eight threads per head, each
     // every eighth chunk of eight values.  Every QK MMA of the previous segment
     // has completed: this thread saw the s_full of its last tile.
+    float qs = 0.f, qs_next = 0.f;  // what a sum of Q's terms is multiplied by, this segment and the next
     auto load_q = [&](int b, uint32_t seg) {
       constexpr int T = 128 / NH, N = (72 + T - 1) / T;  // threads per head, chunks of eight values each
       const int hl = st / T, i0 = st % T, row_hi = NH * c + hl, row_lo = HC + row_hi;
@@ -561,11 +563,15 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
         }
       }
 #pragma unroll
-      for (int o = T / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      if (lane == 0) qtop[4 * (seg & 1) + q4] = top;
+      group_any(c, false);
+      const float4 top4 = *reinterpret_cast<const float4*>(qtop + 4 * (seg & 1));
+      top = fmaxf(fmaxf(top4.x, top4.y), fmaxf(top4.z, top4.w));
       // up to a power of two in [128, 256): 2^(7 - floor(log2 top)) (fp16 values: 2^-24 .. 2^16)
       const int ex = top > 0.f ? int(__float_as_uint(top) >> 23) - 127 : 7;
       const float up = __uint_as_float(uint32_t(127 + 7 - ex) << 23), down = __uint_as_float(uint32_t(127 - 7 + ex) << 23);
-      if (i0 == 0) qscale[(seg & 1) * HC + hl] = down * p.scale_log2;
+      qs_next = down * p.scale_log2;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const int chunk = i0 + T * i;
@@ -597,24 +603,14 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
     };
     float* m_run = red + 15 * HC + NH * c;  // kept once for the group's threads
     float* alpha = red + 16 * HC + NH * c;
-    // 8 heads: copies of m_run and qscale in registers (as loads of one address
-    // by all lanes they cost shared memory four wavefronts each); 16: none to spare
+    // 8 heads: a copy of m_run in registers (loads of one address by all lanes cost
+    // shared memory four wavefronts each); 16: none to spare
     constexpr bool kCopies = NH == 8;
-    float l_run[NH], mr[kCopies ? NH : 4], qs[kCopies ? NH : 4];
-    auto load_copies = [&](float (&dst)[kCopies ? NH : 4], const float* src) {
-#pragma unroll
-      for (int h4 = 0; h4 < (kCopies ? NH / 4 : 1); ++h4) {
-        const float4 m = reinterpret_cast<const float4*>(src)[h4];
-        dst[4 * h4] = m.x;
-        dst[4 * h4 + 1] = m.y;
-        dst[4 * h4 + 2] = m.z;
-        dst[4 * h4 + 3] = m.w;
-      }
-    };
-    // four values of one of them, for heads 4 h4 .. 4 h4 + 3
-    auto four = [&](const float (&copy)[kCopies ? NH : 4], const float* src, int h4) -> float4 {
-      if constexpr (kCopies) return make_float4(copy[4 * h4], copy[4 * h4 + 1], copy[4 * h4 + 2], copy[4 * h4 + 3]);
-      else return reinterpret_cast<const float4*>(src)[h4];
+    float l_run[NH], mr[kCopies ? NH : 4];
+    // m_run of heads 4 h4 .. 4 h4 + 3
+    auto m_four = [&](int h4) -> float4 {
+      if constexpr (kCopies) return make_float4(mr[4 * h4], mr[4 * h4 + 1], mr[4 * h4 + 2], mr[4 * h4 + 3]);
+      else return reinterpret_cast<const float4*>(m_run)[h4];
     };
     uint32_t k = 0, seg = 0;
     TileInfo t, tn;
@@ -627,56 +623,57 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
       bool ok = wait_for<C::kSplitRegs>(&B->s_full[buf], (k >> 1) & 1, abort_flag);
       if (k >= 2) ok = ok && wait_for<C::kSplitRegs>(&B->pv_done[buf], ((k - 2) >> 1) & 1, abort_flag);
       tc_fence_after();
-      // the first tile of a segment: every thread's qscale must be there
-      if (t.first) {
-        group_any(c, false);
-        if (kCopies) load_copies(qs, qscale + (seg & 1) * HC);
-      }
-      float x[NH];
-      {
+      if (t.first) qs = qs_next;
+      // The weights' exponents y: the scores in log2 units less m_run.
+      float y[NH];
+      auto sums = [&](float (&s)[NH]) {  // q . c, times 2^k
         float lo[NH];
-        tmem_load<NH>(tmem + lane_off + C::kColS + buf * C::kNQ + NH * c, x);
+        tmem_load<NH>(tmem + lane_off + C::kColS + buf * C::kNQ + NH * c, s);
         tmem_load<NH>(tmem + lane_off + C::kColS + buf * C::kNQ + HC + NH * c, lo);
-        tc_fence_before();
-        mbar_arrive(&B->s_free[buf]);
 #pragma unroll
-        for (int h4 = 0; h4 < NH / 4; ++h4) {
-          const float4 s = four(qs, qscale + (seg & 1) * HC, h4);
-          x[4 * h4] = fmaf(lo[4 * h4], 0.0625f, x[4 * h4]) * s.x;
-          x[4 * h4 + 1] = fmaf(lo[4 * h4 + 1], 0.0625f, x[4 * h4 + 1]) * s.y;
-          x[4 * h4 + 2] = fmaf(lo[4 * h4 + 2], 0.0625f, x[4 * h4 + 2]) * s.z;
-          x[4 * h4 + 3] = fmaf(lo[4 * h4 + 3], 0.0625f, x[4 * h4 + 3]) * s.w;
+        for (int h = 0; h < NH; ++h) s[h] = fmaf(lo[h], 0.0625f, s[h]);
+      };
+      auto mask = [&](float (&s)[NH]) {
+        if (!valid) {
+#pragma unroll
+          for (int h = 0; h < NH; ++h) s[h] = -INFINITY;
         }
-      }
-      if (!valid) {
+        if (kCausal && causal_tile(p, t, len_b)) {
+          const int pos = t.tile * kTile + st - (len_b - p.q_len);  // against the query token's number
 #pragma unroll
-        for (int h = 0; h < NH; ++h) x[h] = -INFINITY;
-      }
-      if (kCausal && causal_tile(p, t, len_b)) {
-        const int pos = t.tile * kTile + st - (len_b - p.q_len);  // against the query token's number
-#pragma unroll
-        for (int h = 0; h < NH; ++h)
-          if (pos > (g * HC + NH * c + h) / p.heads_w) x[h] = -INFINITY;
-      }
+          for (int h = 0; h < NH; ++h)
+            if (pos > (g * HC + NH * c + h) / p.heads_w) s[h] = -INFINITY;
+        }
+      };
       // Running max: as in decode_tc.cu it only has to bound the scores, here to
       // within 2^5, so that the weights keep E5M2's range down.
       bool over = false;
       if (!t.first) {
+        sums(y);
 #pragma unroll
         for (int h4 = 0; h4 < NH / 4; ++h4) {
-          const float4 m = four(mr, m_run, h4);
-          constexpr float kTop = kWeightBits + kRescaleThreshold;
-          over |= x[4 * h4] > m.x + kTop || x[4 * h4 + 1] > m.y + kTop || x[4 * h4 + 2] > m.z + kTop ||
-                  x[4 * h4 + 3] > m.w + kTop;
+          const float4 m = m_four(h4);
+          y[4 * h4] = fmaf(y[4 * h4], qs, -m.x);
+          y[4 * h4 + 1] = fmaf(y[4 * h4 + 1], qs, -m.y);
+          y[4 * h4 + 2] = fmaf(y[4 * h4 + 2], qs, -m.z);
+          y[4 * h4 + 3] = fmaf(y[4 * h4 + 3], qs, -m.w);
         }
+        mask(y);
+#pragma unroll
+        for (int h = 0; h < NH; ++h) over |= y[h] > kWeightBits + kRescaleThreshold;
       }
       bool rescale = false;
       if (t.first || group_any(c, over || !ok)) {
+        // exactly: the scores themselves, once more
+        sums(y);
+#pragma unroll
+        for (int h = 0; h < NH; ++h) y[h] *= qs;
+        mask(y);
         float* rm = red + buf * 4 * HC + 4 * NH * c;
         {
           float tmp[NH];
 #pragma unroll
-          for (int h = 0; h < NH; ++h) tmp[h] = x[h];
+          for (int h = 0; h < NH; ++h) tmp[h] = y[h];
           const float wm = warp_reduce<NH, true>(tmp, lane);
           if (lane % (32 / NH) == 0) rm[lane / (32 / NH) * 4 + q4] = wm;
         }
@@ -695,15 +692,16 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
           alpha[st] = a;
         }
         rescale = group_any(c, rescale);
-        if (kCopies) load_copies(mr, m_run);
-        if (t.first) {
 #pragma unroll
-          for (int h = 0; h < NH; ++h) l_run[h] = 0.f;
-        } else {
-#pragma unroll
-          for (int h = 0; h < NH; ++h) l_run[h] *= alpha[h];
+        for (int h = 0; h < NH; ++h) {
+          const float m = m_run[h];
+          if (kCopies) mr[h % (kCopies ? NH : 4)] = m;
+          y[h] -= m;
+          l_run[h] = t.first ? 0.f : l_run[h] * alpha[h];
         }
       }
+      tc_fence_before();
+      mbar_arrive(&B->s_free[buf]);
       if (rescale) {
         // QK of this tile may have been issued before PV of the previous one:
         // wait for that PV first
@@ -727,9 +725,8 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
         uint32_t w[NH / 2];
 #pragma unroll
         for (int h4 = 0; h4 < NH / 4; ++h4) {
-          const float4 m = four(mr, m_run, h4);
-          const float e0 = ex2_ftz(x[4 * h4] - m.x), e1 = ex2_ftz(x[4 * h4 + 1] - m.y);
-          const float e2 = ex2_ftz(x[4 * h4 + 2] - m.z), e3 = ex2_ftz(x[4 * h4 + 3] - m.w);
+          const float e0 = ex2_ftz(y[4 * h4]), e1 = ex2_ftz(y[4 * h4 + 1]);
+          const float e2 = ex2_ftz(y[4 * h4 + 2]), e3 = ex2_ftz(y[4 * h4 + 3]);
           l_run[4 * h4] += e0;
           l_run[4 * h4 + 1] += e1;
           l_run[4 * h4 + 2] += e2;
