@@ -74,7 +74,7 @@ struct Fp4Cfg {
   // registers of a thread at the launch, and of each role (setmaxnreg)
   static constexpr bool kSplitRegs = HC == 32;
   static constexpr int kRegs = 96;
-  static constexpr int kSoftRegs = 136, kExpRegs = 64, kIssueRegs = 80;
+  static constexpr int kSoftRegs = 128, kExpRegs = 72, kIssueRegs = 80;
   static_assert(!kSplitRegs || 32 * (kSoftWarps * kSoftRegs + kExpWarps * kExpRegs + 4 * kIssueRegs) <= kThreads * kRegs,
                 "setmaxnreg shares out what the block was launched with");
   static constexpr int kNQ = 2 * HC, kNP = 3 * HC;          // N of the products
@@ -606,7 +606,7 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
     // 8 heads: a copy of m_run in registers (loads of one address by all lanes cost
     // shared memory four wavefronts each); 16: none to spare
     constexpr bool kCopies = NH == 8;
-    float l_run[NH], mr[kCopies ? NH : 4];
+    float l_run[NH], mr[kCopies ? NH : 4] = {};
     // m_run of heads 4 h4 .. 4 h4 + 3
     auto m_four = [&](int h4) -> float4 {
       if constexpr (kCopies) return make_float4(mr[4 * h4], mr[4 * h4 + 1], mr[4 * h4 + 2], mr[4 * h4 + 3]);
