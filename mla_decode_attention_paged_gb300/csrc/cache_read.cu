@@ -5,11 +5,11 @@
 // cu_rows[b + 1] and is the cached row at position starts[b] + r - cu_rows[b].
 // bf16 caches: a copy; INT8: scale * (code - zero point); FP8: scale *
 // e4m3(code); FP4: block scale * e2m1(code); each in fp32 with one rounding to
-// bf16 ("KV Cache Optimization", section 3; FP4 values are exact).  These are the latents that W^UK and W^UV expand to keys and
-// values, so the outputs have the append's input layout: latents [n, 512] and
-// rotated RoPE keys [n, 64].
+// bf16 ("KV Cache Optimization", section 3; FP4 values are exact).  These are the
+// latents that W^UK and W^UV expand to keys and values, so the outputs have the
+// append's input layout: latents [n, 512] and rotated RoPE keys [n, 64].
 //
-// Bound by memory: 1,152 / 584 / 580 bytes read and 1,152 written per row.  A
+// Bound by memory: 1,152 / 584 / 580 / 306 bytes read and 1,152 written per row.  A
 // CTA resolves its rows first (one thread per row: binary search in cu_rows,
 // then the page-table entry), then all threads move 16-byte source pieces with
 // every load of the CTA issued before its first store.  A 1-byte piece becomes

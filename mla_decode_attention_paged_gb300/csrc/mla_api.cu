@@ -58,24 +58,27 @@ mla_dims row_dims(const mla_dims* d, int q_len) {
 }
 
 // The attention kernel for `rows` query rows per sequence (heads, or
-// q_len x heads): more than 32 rows run on the 128-row CTA-pair kernel (any
-// cache format; rows that are not a multiple of 128 pad the last group,
+// q_len x heads): more than 32 rows run on the 128-row CTA-pair kernel (bf16
+// and 1-byte caches; rows that are not a multiple of 128 pad the last group,
 // which still reads each tile once where the 16/32-row kernels would read it
 // once per group), except bf16 rows that make one or two 32-row groups of
 // the 16/32-head CTA-pair kernel (measured on the V2-Lite batch at 4 tokens
 // x 16 heads: 0.510 ms as two 32-row groups, 0.544 ms as one padded group;
 // at 6 tokens 0.754 against 0.547 ms).  The rest: bf16 caches on the
 // 16/32-head CTA-pair kernel, 1-byte caches (and devices that cannot place
-// pairs) on single CTAs.  `units` = attention units resident at once (pairs
-// or CTAs).
+// pairs) on single CTAs.  FP4 caches run on a kernel of their own for any rows: 16
+// as one group, more in groups of 32, which cost less a row (a batch of 32 x 32,768
+// tokens: 106 us for 16 rows, 140 for 32).  On the 128-row kernel, which expanded
+// them to fp16, the same batch took 607 us, and 128 heads over 128 x 8,192 tokens 607
+// against 490.  `units` = attention units resident at
+// once (pairs or CTAs).
 enum AttnKind { kAttnRows128, kAttnPair, kAttnSingle, kAttnFp4 };
 struct AttnChoice {
   int kind, hc, units;
 };
 AttnChoice choose_attention(int rows, int code) {
   const bool byte = code != kCodeBf16;
-  if (code == kCodeE2m1)
-    return {kAttnFp4, rows == 16 ? 16 : 32, sm_count()};
+  if (code == kCodeE2m1) return {kAttnFp4, rows == 16 ? 16 : 32, sm_count()};
   const bool single = g_force_single_cta.load() != 0;
   const bool pair_groups = !byte && rows <= 64 && rows % 32 == 0;
   if (!single && (rows % 128 == 0 || (rows > 32 && !pair_groups))) {

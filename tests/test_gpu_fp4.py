@@ -245,6 +245,17 @@ def test_decode_multi(cuda_lib, H, T):
     _check(_decode_inputs(H, 64, [T, 1, 128 + T - 1, 127, 129, 520, 0], seed=H + T, T=T))
 
 
+@pytest.mark.parametrize("H,T", [(16, 1), (32, 1), (16, 2)])
+def test_decode_all_empty(cuda_lib, H, T):
+    """A batch of nothing: zeros and minus infinity, written."""
+    x = _decode_inputs(H, 64, [0, 0, 0], seed=1, T=T)
+    q = x["q_nope"].shape[:-1]
+    out = torch.full(q + (128,), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full(q, 7.0, device="cuda")
+    _, _, st = _run(x, out=out, lse_out=lse)
+    assert st == mla.MLA_OK and not out.any() and torch.isneginf(lse).all()
+
+
 def test_decode_long(cuda_lib):
     x = _decode_inputs(16, 64, [20011, 5000], seed=4)
     a, la = _check(x)
