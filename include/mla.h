@@ -200,6 +200,11 @@ size_t mla_decode_workspace_size(const mla_dims* dims, int32_t batch, int32_t nu
  * FP4 caches are read through the FP8 format E5M2 (two mantissa bits: a code
  * times its scale fits): exact for block scales 2^-15 .. 2^13; smaller blocks'
  * values are rounded to multiples of 2^-16, larger ones' saturate at 57,344.
+ * Their queries (q_lat and q_pe) are rounded to fp16, then to a sum of two E4M3
+ * values with one power of two for 8 heads (16 query rows) or 16: off by at most
+ * 2^-8 of the value and 2^-22 of the largest of those heads.  A NaN block makes the
+ * query rows that see its row NaN (out and lse) and no others; a query past fp16's
+ * range, infinite or NaN its own head.
  */
 int mla_decode(const mla_dims* dims, const void* q_nope, const void* q_pe, const void* cache,
                const float* cache_scale_zero, int32_t num_pages, const int32_t* block_table,
@@ -299,8 +304,8 @@ size_t mla_prefill_workspace_size(const mla_dims* dims, int32_t batch, int32_t c
  * a sequence run in groups of 128 rows, each group on the MMA's M extent
  * against 64-token sub-tiles of the sequence's pages (a group of fewer rows
  * is padded; chunk * H of 32 or 64 rows on bf16 caches runs as 32-row
- * groups).  Each group streams its sequence's pages, from L2 after the
- * first.
+ * groups; FP4 caches run in groups of 32 rows against 128-token tiles).
+ * Each group streams its sequence's pages, from L2 after the first.
  */
 int mla_prefill(const mla_dims* dims, void* cache, float* cache_scale_zero, int32_t num_pages,
                 const int32_t* block_table, int32_t max_pages_per_seq, const int32_t* seq_lens, int32_t batch,

@@ -42,7 +42,7 @@
 //   warp 18      pages of the tiles to come, and their rows' way into L2
 //   warp 19      no work
 // Measured, 32 sequences of 32,768 tokens (1,048,576 rows of 320 bytes): 106 us at 16
-// heads (3.2 TB/s), 140 us at 32 (2.4 TB/s, 522 TFLOP/s), 487 us for 128 x 8,192
+// heads (3.2 TB/s), 137 us at 32 (2.4 TB/s, 533 TFLOP/s), 487 us for 128 x 8,192
 // tokens at 128 heads (600 TFLOP/s).  At 16 rows the L1 and shared-memory data pipe
 // bounds it: 3,330 wavefronts a tile (1,900 of loads and stores, 1,424 of the
 // products' operands) in about 3,800 cycles; at 32 rows the chain expansion, QK,
@@ -207,6 +207,12 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// Two fp16 values as they are, infinities as NaN (x + 0 x).
+__device__ __forceinline__ uint32_t nan_of_inf_f16x2(uint32_t x) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %1;" : "=r"(r) : "r"(x), "r"(0u));
   return r;
 }
 // A warpgroup's registers per thread from here on.
@@ -563,11 +569,17 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         u[i] = live && i0 + T * i < 72 ? src[i0 + T * i] : make_uint4(0, 0, 0, 0);
+        // E4M3 has no infinity: one in a query makes its head NaN, not the largest finite
+        // value, and has no part in the scale.  Here for 32 rows, below for 16 (137 and
+        // 106 us a batch; the other way round 141 and 108)
+        if (HC == 32)
+          u[i] = make_uint4(nan_of_inf_f16x2(u[i].x), nan_of_inf_f16x2(u[i].y), nan_of_inf_f16x2(u[i].z), nan_of_inf_f16x2(u[i].w));
         const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           const float2 f = unpack_f16x2(w[x]);
-          top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+          const float a = fmaxf(fabsf(f.x), fabsf(f.y));  // passes over NaN
+          if (HC == 32 || a < 65536.f) top = fmaxf(top, a);
         }
       }
 #pragma unroll
@@ -576,7 +588,7 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
       group_any(c, false);
       const float4 top4 = *reinterpret_cast<const float4*>(qtop + 4 * (seg & 1));
       top = fmaxf(fmaxf(top4.x, top4.y), fmaxf(top4.z, top4.w));
-      // up to a power of two in [128, 256): 2^(7 - floor(log2 top)) (fp16 values: 2^-24 .. 2^16)
+      // up to a power of two in [128, 256): 2^(7 - floor(log2 top)) (fp16 values: 2^-24 .. 2^15)
       const int ex = top > 0.f ? int(__float_as_uint(top) >> 23) - 127 : 7;
       const float up = __uint_as_float(uint32_t(127 + 7 - ex) << 23), down = __uint_as_float(uint32_t(127 - 7 + ex) << 23);
       qs_next = down * p.scale_log2;
@@ -588,7 +600,7 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
         uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          float2 f = unpack_f16x2(w[x]);
+          float2 f = unpack_f16x2(HC == 32 ? w[x] : nan_of_inf_f16x2(w[x]));
           f.x *= up;
           f.y *= up;
           const uint32_t a = pack_e4m3x2(f.x, f.y);
@@ -634,6 +646,7 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
       if (t.first) qs = qs_next;
       // The weights' exponents y: the scores in log2 units less m_run.
       float y[NH];
+      bool nan_row = false;  // a hidden row gave a NaN score
       auto sums = [&](float (&s)[NH]) {  // q . c, times 2^k
         float lo[NH];
         tmem_load<NH>(tmem + lane_off + C::kColS + buf * C::kNQ + NH * c, s);
@@ -650,7 +663,10 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
           const int pos = t.tile * kTile + st - (len_b - p.q_len);  // against the query token's number
 #pragma unroll
           for (int h = 0; h < NH; ++h)
-            if (pos > (g * HC + NH * c + h) / p.heads_w) s[h] = -INFINITY;
+            if (pos > (g * HC + NH * c + h) / p.heads_w) {
+              nan_row |= s[h] != s[h];
+              s[h] = -INFINITY;
+            }
         }
       };
       // Running max: as in decode_tc.cu it only has to bound the scores, here to
@@ -761,6 +777,21 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
           uint8_t* dst = pt + term * (HC / 16) * 2048;
           if constexpr (NH == 16) *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
           else *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1]);
+        }
+      }
+      if (kCausal && nan_row) {
+        // A NaN in a hidden row would pass its weight of 0 in PV.  Rows that see it
+        // have a NaN weight and sum already, so its pieces become zeros (QK of the
+        // tile has read them, PV waits for this thread).  A NaN query gets here too
+        // and changes nothing.
+        const uint32_t slot = k % kSlots;
+        uint8_t* row = smem + slot * kSlotBytes + st * 128;
+        // acquires the expansion's writes (these phases have completed)
+        for (int half = 0; half < 2; ++half) mbar_try_wait(&B->full[slot][half], (k / kSlots) & 1);
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i) {  // a piece is half a block: all NaN or none
+          uint4* piece = reinterpret_cast<uint4*>(row + (i >> 3) * kLatBox + 16 * (i & 7));
+          if ((piece->x & 0x7f) == 0x7f) *piece = make_uint4(0, 0, 0, 0);
         }
       }
       fence_proxy_async_smem();

@@ -330,6 +330,74 @@ def test_decode_tails_do_not_matter(cuda_lib):
             assert torch.equal(a[b], c[b]) and torch.equal(la[b], lc[b])
 
 
+@pytest.mark.parametrize("H", [16, 32, 96])
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), 1e30, float("nan")])
+def test_decode_infinite_query(cuda_lib, H, value):
+    """A query value past fp16, infinite or NaN makes its own head NaN; the heads
+    that share its scale keep their results."""
+    x = _decode_inputs(H, 32, [200, 1, 517], seed=31)
+    ref, lref = _reference(x)
+    x["q_pe"][0, 5, 9] = x["q_pe"][2, H - 1, 63] = value
+    out, lse, st = _run(x)
+    assert st == mla.MLA_OK
+    bad = torch.zeros((3, H), dtype=torch.bool)
+    bad[0, 5] = bad[2, H - 1] = True
+    assert torch.isnan(out[bad]).all() and torch.isnan(lse[bad]).all()
+    assert_parity(out, lse, ref, lref, [(b, h) for b in range(3) for h in range(H) if not bad[b, h]])
+
+
+@pytest.mark.parametrize("H", [16, 32, 64])
+def test_decode_heads_far_apart(cuda_lib, H):
+    """Heads share the scale of their query terms: sizes from 1 to 2^-15 of the largest."""
+    x = _decode_inputs(H, 64, [300, 77], seed=32)
+    size = 2.0 ** -(torch.arange(H) % 16).view(1, H, 1)
+    x["q_nope"], x["q_pe"] = x["q_nope"] * size.to(torch.bfloat16), x["q_pe"] * size.to(torch.bfloat16)
+    _check(x)
+
+
+@pytest.mark.parametrize("H,T,where", [(16, 2, "latent"), (16, 3, "latent"), (32, 2, "latent"), (16, 8, "both"),
+                                       (128, 2, "latent"), (32, 4, "rope")])
+def test_hidden_nan_rows(cuda_lib, H, T, where):
+    """A NaN block reaches the query tokens that see its row and no others."""
+    lens = [300, 128 + T, 2 * T + 1]
+    x = _decode_inputs(H, 64, lens, seed=33, T=T)
+    ref, lref = _reference(x)
+    blocks = {"latent": [288 + 3], "rope": [288 + 17], "both": list(range(288, 306))}[where]
+    for b, n in enumerate(lens):  # the last query token's row
+        page = int(x["table"][b, (n - 1) // 64])
+        x["cache"][page, (n - 1) % 64, blocks] = 255
+    out, lse, st = _run(x)
+    assert st == mla.MLA_OK
+    assert torch.isnan(out[:, T - 1]).all() and torch.isnan(lse[:, T - 1]).all()
+    R = (T - 1) * H
+    assert_parity(out.view(3, T * H, 128), lse.view(3, T * H), ref, lref, [(b, r) for b in range(3) for r in range(R)])
+
+
+def test_prefill_hidden_nan(cuda_lib):
+    """A NaN in a chunk's token 40: queries 0 .. 39 are as without it, 40 .. are NaN."""
+    H, P, T, n = 16, 64, 90, 150
+    x = _decode_inputs(H, P, [n], seed=34)
+    g = W.generator(35)
+    c, k = W.draw_bf16((1, T, 512), 1.0, g), W.draw_bf16((1, T, 64), 1.0, g)
+    q, qp = W.draw_bf16((1, T, H, 128), 2.0, g).cuda(), W.draw_bf16((1, T, H, 64), 2.0, g).cuda()
+    uk, uv = x["W_UK"].cuda(), x["W_UV"].cuda()
+
+    def run(c):
+        cache = x["cache"].cuda()
+        ws = torch.empty(mla.prefill_workspace_size(x["d"], 1, T, 0), dtype=torch.uint8, device="cuda")
+        out, lse = mla.prefill(x["d"], cache, None, x["table"].cuda(), _lens([n]).cuda(), c.cuda(), k.cuda(), q, qp,
+                               uk, uv, SCALE, workspace=ws)
+        assert mla.read_device_status(ws) == mla.MLA_OK
+        return out[0], lse[0]
+
+    clean, lclean = run(c)
+    assert torch.isfinite(clean).all() and torch.isfinite(lclean).all()
+    c[0, 40, 100] = float("nan")
+    out, lse = run(c)
+    assert torch.equal(out[:40], clean[:40]) and torch.equal(lse[:40], lclean[:40])
+    assert torch.isnan(out[40:]).all() and torch.isnan(lse[40:]).all()
+
+
 def test_decode_pages_shuffled(cuda_lib):
     """The same rows under another page table give the same bits."""
     x = _decode_inputs(16, 32, [900, 33, 260], seed=37)
