@@ -41,12 +41,12 @@
 //   warp 16      tensor memory and QK issuer;  warp 17  PV issuer
 //   warp 18      pages of the tiles to come, and their rows' way into L2
 //   warp 19      no work
-// Measured, 32 sequences of 32,768 tokens (1,048,576 rows of 320 bytes): 106 us at 16
-// heads (3.2 TB/s), 137 us at 32 (2.4 TB/s, 533 TFLOP/s), 487 us for 128 x 8,192
-// tokens at 128 heads (600 TFLOP/s).  At 16 rows the L1 and shared-memory data pipe
+// Measured, 32 sequences of 32,768 tokens (1,048,576 rows of 320 bytes): 102 us at 16
+// heads (3.3 TB/s), 133 us at 32 (2.5 TB/s, 549 TFLOP/s), 461 us for 128 x 8,192
+// tokens at 128 heads (634 TFLOP/s).  At 16 rows the L1 and shared-memory data pipe
 // bounds it: 3,330 wavefronts a tile (1,900 of loads and stores, 1,424 of the
-// products' operands) in about 3,800 cycles; at 32 rows the chain expansion, QK,
-// softmax, PV through two slots, about 5,000 cycles a tile for 3,980 wavefronts.
+// products' operands) in about 3,600 cycles; at 32 rows the chain expansion, QK,
+// softmax, PV through two slots, about 4,700 cycles a tile for 3,980 wavefronts.
 // Every wait is bounded: on timeout the CTA records MLA_ERR_DEVICE_TIMEOUT,
 // drains, frees its tensor memory and returns.
 #include <atomic>
@@ -166,6 +166,35 @@ __device__ __forceinline__ void tmem_load(uint32_t a, float (&v)[N]) {
   else tmem_ld8(a, v);
 }
 
+// The same of three places `step` columns apart, with one wait.
+template <int N>
+__device__ __forceinline__ void tmem_load3(uint32_t a, uint32_t step, float (&v)[3][N]) {
+  static_assert(N == 8 || N == 16, "8 or 16 columns");
+  uint32_t r[3][N];
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    uint32_t* x = r[i];
+    if constexpr (N == 16)
+      asm volatile(
+          "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+          : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7]),
+            "=r"(x[8]), "=r"(x[9]), "=r"(x[10]), "=r"(x[11]), "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15])
+          : "r"(a + i * step));
+    else
+      asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                   : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7])
+                   : "r"(a + i * step));
+  }
+  tmem_ld_wait();
+#pragma unroll
+  for (int i = 0; i < 3; ++i)
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      asm volatile("" : "+r"(r[i][n]));  // valid from the wait on
+      v[i][n] = __uint_as_float(r[i][n]);
+    }
+}
+
 // Instruction descriptor, kind::f8f6f4, fp32 accumulator (bits 4-5 = 1): A is
 // E5M2 (bits 7-9 = 1), B E5M2 or E4M3 (bits 10-12 = 1 or 0), the rest as for f16.
 constexpr uint32_t idesc_f8(int M, int N, bool mn_major, bool b_e5m2) {
@@ -193,10 +222,21 @@ __device__ __forceinline__ void tmem_store(uint32_t a, const float (&v)[N]) {
                  : "memory");
   }
 }
-// Two fp32 values to E4M3, `lo` in the low byte.
-__device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
+// Two fp16 values to E4M3.
+__device__ __forceinline__ uint32_t e4m3x2_of_f16x2(uint32_t x) {
   uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// The larger magnitudes; a NaN gives way to the other value.
+__device__ __forceinline__ uint32_t max_abs_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b & 0x7fff7fffu));
   return r;
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -223,8 +263,8 @@ __device__ __forceinline__ void set_max_regs() {
 }
 // A bounded wait.  Where registers are shared out it is inline, since a function
 // call has registers of its own, and short, since the roles' loops share the
-// instruction caches; else it calls (16 rows: 106 us by calls, 111 inline, 121 with
-// a longer loop inline).
+// instruction caches; else it calls (16 rows, when the batch above took 106 us by
+// calls: 111 inline, 121 with a longer loop inline).
 template <bool kInline>
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, const volatile int* abort) {
   if constexpr (!kInline) return mbar_wait(bar, parity, abort, kWaitLimitNs);
@@ -252,6 +292,41 @@ __device__ __forceinline__ void expand_block(uint4 v, uint2 table, uint4& lo, ui
   e2m1_to_e5m2(v.y, table, lo.z, lo.w);
   e2m1_to_e5m2(v.z, table, hi.x, hi.y);
   e2m1_to_e5m2(v.w, table, hi.z, hi.w);
+}
+
+// A CTA's walker at its first tile, as TileWalkerT::init leaves it: a warp divides for
+// several lanes at once and searches 32 ways, and all warps run one copy of this
+// code (with a copy in each role and serial divisions the first tile's scores came
+// 0.6 us later; one decode of 93 tokens 14.3 -> 12.3 us with what load_q does).
+__device__ __forceinline__ void walk_start(TileWalkerT<true>& w, const DecodeParams& p, int cp, int Cp, int lane) {
+  const int* ts = p.tile_start;
+  const long long S = p.status[1], W = ts[p.batch];  // effective split count and tiles, from the plan
+  w.tile_start = ts;
+  w.seg_base = p.seg_base;
+  w.len = p.len;
+  w.W = W;
+  w.S = S;
+  const long long part = (cp + (lane & 1)) * S / Cp;  // first partition of this CTA, of the next
+  const long long pa = __shfl_sync(0xffffffffu, part, 0), pb = __shfl_sync(0xffffffffu, part, 1);
+  const long long unit = part_start(lane == 1 ? pa + 1 : lane == 2 ? pb : pa, W, S);
+  w.p = pa;
+  w.u = w.p_start = __shfl_sync(0xffffffffu, unit, 0);
+  w.p_next = __shfl_sync(0xffffffffu, unit, 1);
+  w.u_end = __shfl_sync(0xffffffffu, unit, 2);
+  w.s_b = w.e_b = 0;
+  w.b = w.len_b = w.seg_b = 0;
+  if (w.u >= w.u_end) return;
+  // the sequences that end at or before unit u: below(i) = tile_start[i + 1] <= u is
+  // true for those and for no other; each round looks at the last of 32 ranges
+  int lo = 0, hi = p.batch;
+  while (lo < hi) {
+    const int step = (hi - lo + 31) >> 5, i = lo + step * (lane + 1) - 1;
+    const bool below = i < hi && ts[i + 1] <= w.u;
+    lo += step * __popc(__ballot_sync(0xffffffffu, below));
+    hi = min(hi, lo + step - 1);
+  }
+  w.b = lo;
+  w.enter_sequence_body();
 }
 
 // kCausal: multi-token decode (q_len > 1) masks each row's later positions on a
@@ -287,7 +362,7 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
     mbar_init(&B->o_full, 1);
     mbar_init(&B->o_free, 32 * C::kSoftWarps);
     B->abort = 0;
-    B->expanding = 0;
+    B->expanding = 1 - kAhead;  // two tiles first, the others' way into L2 once the first is here
     fence_mbar_init();
   }
   if (warp == kQkWarp) {
@@ -303,8 +378,8 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
   griddep_launch_dependents();
 
   const int G = p.num_groups, g = blockIdx.x % G, cp = blockIdx.x / G, Cp = gridDim.x / G;
-  const long long S = p.status[1];  // effective split count from the plan
-  const long long pa = (cp * S) / Cp, pb = ((cp + 1) * S) / Cp;
+  TileWalkerT<true> start;
+  walk_start(start, p, cp, Cp, lane);
   const volatile int* abort_flag = &B->abort;
 
   if (warp >= C::kSoftWarps && warp < kQkWarp) {
@@ -348,7 +423,6 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
       const bool begins = R == 2 || half == 0, ends = R == 2 || half == 1;
       uint8_t* base = smem + slot * kSlotBytes;
       int left;  // of the next rows: this thread's row r + 64 i is there if it is below
-      if (begins && threadIdx.x == 32 * C::kSoftWarps) *reinterpret_cast<volatile int*>(&B->expanding) = int(k);
       if (ends) {
         const int e = (k + 1) % kRing;
         ok = __all_sync(0xffffffffu, wait_for<C::kSplitRegs>(&B->ring_full[e], ((k + 1) / kRing) & 1, abort_flag));
@@ -374,6 +448,7 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
           far |= sc[i][c] - (127 - 13) > 26;
         }
       }
+      if (begins && threadIdx.x == 32 * C::kSoftWarps) *reinterpret_cast<volatile int*>(&B->expanding) = int(k);
       // the tails first: their registers are the first that the next rows need
 #pragma unroll
       for (int cc = 0; cc < 5; ++cc) {
@@ -423,8 +498,7 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
     };
     if (warp == kQkWarp) {
       // ------------------------------------------------------------ QK issuer
-      TileWalkerT<true> walk;
-      walk.init(p.tile_start, p.seg_base, p.len, p.batch, int(S), pa, pb);
+      TileWalkerT<true> walk = start;
       constexpr uint32_t id_qk = idesc_f8(128, C::kNQ, false, false);
       constexpr uint64_t kDescK = smem_desc(0, 16, 1024, kSwizzle128B);   // K-major SW128 (8-row groups of 1 KB)
       constexpr uint64_t kDescRope = smem_desc(0, 16, 512, kSwizzle64B);  // K-major SW64 (8-row groups of 512 B)
@@ -470,8 +544,7 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
       __syncwarp();
     } else if (warp == kPvWarp) {
       // ------------------------------------------------------------ PV issuer
-      TileWalkerT<true> walk;
-      walk.init(p.tile_start, p.seg_base, p.len, p.batch, int(S), pa, pb);
+      TileWalkerT<true> walk = start;
       constexpr uint32_t id_pv = idesc_f8(128, C::kNP, true, true);
       constexpr uint64_t kDescMN = smem_desc(0, kLatBox, 1024, kSwizzle128B);  // MN-major SW128: 128 columns, 8-token groups
       constexpr uint64_t kDescP = smem_desc(0, 128, 2048, kSwizzleNone);       // P^T core matrices
@@ -513,8 +586,7 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
       // ------------------------------------------------------------ page lookup
       // Where the rows of tile k + kAhead are when the expansion is at tile k (it
       // reads the ring a tile ahead), and those rows' way into L2.
-      TileWalkerT<true> walk;
-      walk.init(p.tile_start, p.seg_base, p.len, p.batch, int(S), pa, pb);
+      TileWalkerT<true> walk = start;
       const volatile int* at = &B->expanding;
       const int page_log2 = __ffs(p.page_size) - 1;
       TileInfo t;
@@ -553,9 +625,8 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
     const uint32_t lane_off = uint32_t(q4 * 32) << 16;
     // the last group of 32 may be half empty: rows of zeros that write nothing
     const bool live = HC == 16 || g * HC + NH * c < p.heads;
-    float* qtop = red + 13 * HC + 8 * c;  // [2 segments' parity][4] largest magnitude by warp
-    TileWalkerT<true> walk;
-    walk.init(p.tile_start, p.seg_base, p.len, p.batch, int(S), pa, pb);
+    uint32_t* qtop = reinterpret_cast<uint32_t*>(red + 13 * HC + 8 * c);  // [2 segments' parity][4] largest magnitude by warp
+    TileWalkerT<true> walk = start;
     // Q of a segment's sequence as two E4M3 terms: eight threads per head, each
     // every eighth chunk of eight values.  Every QK MMA of the previous segment
     // has completed: this thread saw the s_full of its last tile.
@@ -565,33 +636,29 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
       const int hl = st / T, i0 = st % T, row_hi = NH * c + hl, row_lo = HC + row_hi;
       const uint4* src = reinterpret_cast<const uint4*>(p.q_full + (size_t(b) * p.heads + g * HC + row_hi) * kRow);
       uint4 u[N];
-      float top = 0.f;
+      uint32_t top2 = 0;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         u[i] = live && i0 + T * i < 72 ? src[i0 + T * i] : make_uint4(0, 0, 0, 0);
         // E4M3 has no infinity: one in a query makes its head NaN, not the largest finite
-        // value, and has no part in the scale.  Here for 32 rows, below for 16 (137 and
-        // 106 us a batch; the other way round 141 and 108)
-        if (HC == 32)
-          u[i] = make_uint4(nan_of_inf_f16x2(u[i].x), nan_of_inf_f16x2(u[i].y), nan_of_inf_f16x2(u[i].z), nan_of_inf_f16x2(u[i].w));
-        const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const float2 f = unpack_f16x2(w[x]);
-          const float a = fmaxf(fabsf(f.x), fabsf(f.y));  // passes over NaN
-          if (HC == 32 || a < 65536.f) top = fmaxf(top, a);
-        }
+        // value, and has no part in the scale
+        u[i] = make_uint4(nan_of_inf_f16x2(u[i].x), nan_of_inf_f16x2(u[i].y), nan_of_inf_f16x2(u[i].z), nan_of_inf_f16x2(u[i].w));
+        top2 = max_abs_f16x2(max_abs_f16x2(max_abs_f16x2(max_abs_f16x2(top2, u[i].x), u[i].y), u[i].z), u[i].w);
       }
+      uint32_t top = max(top2 & 0xffff, top2 >> 16);  // of magnitudes, in fp16 bits
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
       if (lane == 0) qtop[4 * (seg & 1) + q4] = top;
       group_any(c, false);
-      const float4 top4 = *reinterpret_cast<const float4*>(qtop + 4 * (seg & 1));
-      top = fmaxf(fmaxf(top4.x, top4.y), fmaxf(top4.z, top4.w));
-      // up to a power of two in [128, 256): 2^(7 - floor(log2 top)) (fp16 values: 2^-24 .. 2^15)
-      const int ex = top > 0.f ? int(__float_as_uint(top) >> 23) - 127 : 7;
-      const float up = __uint_as_float(uint32_t(127 + 7 - ex) << 23), down = __uint_as_float(uint32_t(127 - 7 + ex) << 23);
-      qs_next = down * p.scale_log2;
+      const uint4 top4 = *reinterpret_cast<const uint4*>(qtop + 4 * (seg & 1));
+      top = max(max(top4.x, top4.y), max(top4.z, top4.w));
+      // up to a power of two in [128, 256): by 2^(7 - floor(log2 top)), at most 2^30
+      // (fp16 values: 2^-24 .. 2^15), in two steps that fp16 holds; what becomes
+      // subnormal is below 2^-21 of the largest value
+      const float ftop = __half2float(__ushort_as_half(uint16_t(top)));
+      const int shift = top > 0 ? min(30, 7 + 127 - int(__float_as_uint(ftop) >> 23)) : 0, shift0 = min(shift, 15);
+      const uint32_t up0 = uint32_t(15 + shift0) * 0x04000400u, up1 = uint32_t(15 + shift - shift0) * 0x04000400u;
+      qs_next = __uint_as_float(uint32_t(127 - shift) << 23) * p.scale_log2;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const int chunk = i0 + T * i;
@@ -600,13 +667,11 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
         uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          float2 f = unpack_f16x2(HC == 32 ? w[x] : nan_of_inf_f16x2(w[x]));
-          f.x *= up;
-          f.y *= up;
-          const uint32_t a = pack_e4m3x2(f.x, f.y);
-          const float2 fa = unpack_f16x2(e4m3x2_to_half2(a));
+          const uint32_t f = mul_f16x2(mul_f16x2(w[x], up0), up1);
+          const uint32_t a = e4m3x2_of_f16x2(f);
+          const uint32_t rest = sub_f16x2(f, e4m3x2_to_half2(a));  // exact, as is 16 times it
           hi[x >> 1] |= a << (16 * (x & 1));
-          lo[x >> 1] |= pack_e4m3x2(16.f * (f.x - fa.x), 16.f * (f.y - fa.y)) << (16 * (x & 1));
+          lo[x >> 1] |= e4m3x2_of_f16x2(mul_f16x2(rest, 0x4c004c00u)) << (16 * (x & 1));
         }
         // 16 chunks to a box, two to a 16-byte piece
         const int piece = (chunk & 15) >> 1;
@@ -824,16 +889,11 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
         float* dst = p.partial_o + (size_t(t.seg) * p.heads + row0) * kLatent + st;
 #pragma unroll 1
         for (int ch = 0; ch < 4; ++ch) {
-          float v[NH], v2[NH];
-          const uint32_t a = tmem + lane_off + C::kColO + ch * C::kColOStep + NH * c;
-          tmem_load<NH>(a, v);
-          tmem_load<NH>(a + HC, v2);
-#pragma unroll
-          for (int h = 0; h < NH; ++h) v[h] += v2[h];
-          tmem_load<NH>(a + 2 * HC, v2);
+          float v[3][NH];
+          tmem_load3<NH>(tmem + lane_off + C::kColO + ch * C::kColOStep + NH * c, HC, v);
 #pragma unroll
           for (int h = 0; h < NH; ++h)
-            if (live) dst[h * kLatent + ch * 128] = (v[h] + v2[h]) * rinv[h];
+            if (live) dst[h * kLatent + ch * 128] = ((v[0][h] + v[1][h]) + v[2][h]) * rinv[h];
         }
         tc_fence_before();
         mbar_arrive(&B->o_free);

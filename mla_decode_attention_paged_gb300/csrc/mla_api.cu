@@ -68,10 +68,9 @@ mla_dims row_dims(const mla_dims* d, int q_len) {
 // 16/32-head CTA-pair kernel, 1-byte caches (and devices that cannot place
 // pairs) on single CTAs.  FP4 caches run on a kernel of their own for any rows: 16
 // as one group, more in groups of 32, which cost less a row (a batch of 32 x 32,768
-// tokens: 106 us for 16 rows, 140 for 32).  On the 128-row kernel, which expanded
+// tokens: 102 us for 16 rows, 133 for 32).  On the 128-row kernel, which expanded
 // them to fp16, the same batch took 607 us, and 128 heads over 128 x 8,192 tokens 607
-// against 490.  `units` = attention units resident at
-// once (pairs or CTAs).
+// against 461.  `units` = attention units resident at once (pairs or CTAs).
 enum AttnKind { kAttnRows128, kAttnPair, kAttnSingle, kAttnFp4 };
 struct AttnChoice {
   int kind, hc, units;
