@@ -120,6 +120,19 @@ def test_many_short_sequences(cuda_lib, H):
     _check(_decode_inputs(H, 16, [int(n) for n in torch.randint(0, 4, (700,), generator=g)], seed=9))
 
 
+@pytest.mark.parametrize("H,B,splits", [(16, 33, 0), (16, 1057, 1), (16, 1057, 5000), (32, 1100, 0)])
+def test_many_empty_sequences(cuda_lib, H, B, splits):
+    """Runs of empty sequences between full ones: where each CTA starts is searched
+    for among 32, 32 x 32 and more."""
+    g = W.generator(10)
+    some = torch.rand(B, generator=g) < 0.1
+    some[0], some[-1] = False, False
+    lens = torch.where(some, torch.randint(1, 400, (B,), generator=g), torch.zeros(B, dtype=torch.int64))
+    x = _decode_inputs(H, 32, [int(n) for n in lens], seed=11)
+    out, lse = _check(x, splits)
+    assert not out[~some.cuda()].any() and torch.isneginf(lse[~some.cuda()]).all()
+
+
 @pytest.mark.parametrize("seed", range(12))
 def test_random_configuration(cuda_lib, seed):
     g = W.generator(1000 + seed)
