@@ -201,7 +201,8 @@ def _cache_ptrs(d: Dims, cache: torch.Tensor, scale_zero: torch.Tensor | None, d
     rows) and of their per-token scales (None for bf16 and FP4 caches)."""
     if d.cache_dtype == MLA_CACHE_FP4:
         p = _ptr(cache, torch.uint8, "cache", device)
-        if cache.dim() != 3 or cache.shape[1:] != (d.page_size, FP4_ROW_BYTES):
+        s = cache.shape
+        if len(s) != 3 or s[1] != d.page_size or s[2] != FP4_ROW_BYTES:
             raise ValueError(f"cache must have shape [pages, {d.page_size}, {FP4_ROW_BYTES}], got {list(cache.shape)}")
         return p, None
     if d.cache_dtype == MLA_CACHE_FP8:
@@ -232,9 +233,10 @@ def cache_append(d: Dims, cache: torch.Tensor, scale_zero: torch.Tensor | None, 
     dev, i32, bf16 = cache.device, torch.int32, torch.bfloat16
     cache_p, scale_p = _cache_ptrs(d, cache, scale_zero, dev)
     at = dev.index
+    table_p = _on(block_table, i32, at, "block_table")
+    table = block_table.shape
     st = _call_on(
-        dev, stream, _L().mla_cache_append, ctypes.byref(d), cache_p, scale_p, cache.shape[0],
-        _on(block_table, i32, at, "block_table"), block_table.shape[0], block_table.shape[1],
+        dev, stream, _L().mla_cache_append, ctypes.byref(d), cache_p, scale_p, cache.shape[0], table_p, table[0], table[1],
         _on(seq_ids, i32, at, "seq_ids"), _on(positions, i32, at, "positions"), seq_ids.numel(),
         _on(c_kv, bf16, at, "c_kv"), _on(k_pe, bf16, at, "k_pe"), float(rope_theta),
         None if device_status is None else _on(device_status, i32, at, "device_status"))
@@ -405,8 +407,9 @@ def _arg(t: torch.Tensor, name: str, dtype, shape: tuple, dev: torch.device) -> 
 def _dims_of(t: torch.Tensor, name: str, n: int):
     """Shape of an ``n``-dimensional CUDA tensor (the sizes the other arguments are checked against)."""
     try:
-        if t.is_cuda and len(t.shape) == n:
-            return t.shape
+        s = t.shape
+        if len(s) == n and t.is_cuda:
+            return s
     except AttributeError:
         pass
     if not isinstance(t, torch.Tensor):
@@ -414,6 +417,10 @@ def _dims_of(t: torch.Tensor, name: str, n: int):
     if t.dim() != n:
         raise ValueError(f"{name} must have {n} dimensions, got {list(t.shape)}")
     raise ValueError(f"{name} must be a CUDA tensor")
+
+
+# The type of a cache tensor by mla_cache_dtype, where it is not bf16.
+_CODES = {MLA_CACHE_INT8: torch.int8, MLA_CACHE_FP8: torch.uint8, MLA_CACHE_FP4: torch.uint8}
 
 
 def _call_on(dev: torch.device, stream, fn, *args) -> int:
@@ -446,33 +453,35 @@ def cache_read(d: Dims, cache: torch.Tensor, scale_zero: torch.Tensor | None, bl
     from position starts[b] (0 without ``starts``) on.  Returns (c_kv bf16
     [n_rows, 512], k_pe bf16 [n_rows, 64]); ``n_rows`` may be left out where
     an output is given."""
-    pages = _dims_of(cache, "cache", 3)[0]
+    i32, bf16 = torch.int32, torch.bfloat16
+    pages, page, row = _dims_of(cache, "cache", 3)
     B, max_pages = _dims_of(block_table, "block_table", 2)
     dev, P = cache.device, d.page_size
+    at = dev.index
     if n_rows is None:
         given = c_kv if c_kv is not None else k_pe
         if given is None:
             raise ValueError("n_rows is needed where neither c_kv nor k_pe is given")
         n_rows = _dims_of(given, "c_kv" if c_kv is not None else "k_pe", 2)[0]
     if c_kv is None:
-        c_kv = _new((n_rows, d.kv_lora_rank), torch.bfloat16, dev, stream)
+        c_kv = _new((n_rows, d.kv_lora_rank), bf16, dev, stream)
     if k_pe is None:
-        k_pe = _new((n_rows, d.rope_dim), torch.bfloat16, dev, stream)
+        k_pe = _new((n_rows, d.rope_dim), bf16, dev, stream)
     code = d.cache_dtype
     if code == MLA_CACHE_FP8 and cache.dtype == torch.float8_e4m3fn:
         cache = cache.view(torch.uint8)
-    want = {MLA_CACHE_INT8: torch.int8, MLA_CACHE_FP8: torch.uint8, MLA_CACHE_FP4: torch.uint8}.get(code, torch.bfloat16)
+    want = _CODES.get(code, bf16)
     width = FP4_ROW_BYTES if code == MLA_CACHE_FP4 else d.kv_lora_rank + d.rope_dim
     st = _call_on(
         dev, stream, _L().mla_cache_read, ctypes.byref(d),
-        _arg(cache, "cache", want, (pages, P, width), dev),
+        _on(cache, want, at, "cache") if page == P and row == width else _arg(cache, "cache", want, (pages, P, width), dev),
         None if code in (MLA_CACHE_BF16, MLA_CACHE_FP4) else
         _arg(scale_zero, "scale_zero", torch.float32, (pages, P, 2) if code == MLA_CACHE_INT8 else (pages, P), dev),
-        pages, _arg(block_table, "block_table", torch.int32, (B, max_pages), dev), B, max_pages,
-        None if starts is None else _arg(starts, "starts", torch.int32, (B,), dev),
-        _arg(cu_rows, "cu_rows", torch.int32, (B + 1,), dev), int(n_rows),
-        _arg(c_kv, "c_kv", torch.bfloat16, (n_rows, d.kv_lora_rank), dev),
-        _arg(k_pe, "k_pe", torch.bfloat16, (n_rows, d.rope_dim), dev),
+        pages, _on(block_table, i32, at, "block_table"), B, max_pages,
+        None if starts is None else _arg(starts, "starts", i32, (B,), dev),
+        _arg(cu_rows, "cu_rows", i32, (B + 1,), dev), int(n_rows),
+        _arg(c_kv, "c_kv", bf16, (n_rows, d.kv_lora_rank), dev),
+        _arg(k_pe, "k_pe", bf16, (n_rows, d.rope_dim), dev),
         None if device_status is None else _ptr(device_status, torch.int32, "device_status", dev))
     _check(st, "mla_cache_read")
     return c_kv, k_pe
