@@ -83,6 +83,7 @@ struct AppendParams {
   uint64_t turn[kRope / 2];      // FP4: the fraction of inv_freq / (2 pi) in units of 2^-64
   int rotate;                    // FP4: rope_theta > 0
   int n_tokens, num_seqs, max_pages, num_pages, page_size;
+  int run;                       // FP4: tokens of a warp (1 .. 32)
 };
 
 // Packed rows read back out of the cache (mla_cache_read).

@@ -180,6 +180,32 @@ def test_append_skips_bad_tokens(cuda_lib):
     assert np.array_equal(cache.cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("n", [2047, 2048, 2049, 13001, 50000, 194560, 194561])
+def test_append_many_tokens(cuda_lib, n):
+    """Every length of a warp's run of tokens, some of them out of range: rows from
+    400 different ones (not rotated), and nothing behind or between them."""
+    P, g = 64, W.generator(n)
+    pages = (n + P - 1) // P
+    some = _rows(400, g, 0.5)
+    pick = torch.randint(0, 400, (n,), generator=g)
+    pos = torch.arange(n, dtype=torch.int32)
+    bad = torch.rand(n, generator=g) < 0.01
+    bad[-1] = True
+    table = torch.randperm(pages, generator=g).to(torch.int32)
+    values = some[pick].cuda()
+    cache = torch.full((pages, P, 320), 0xAB, dtype=torch.uint8, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    mla.cache_append(mla.dims(16, P, fp4=True), cache, None, table.view(1, -1).cuda(),
+                     torch.zeros(n, dtype=torch.int32, device="cuda"), torch.where(bad, -1 - pos, pos).cuda(),
+                     values[:, :512].contiguous(), values[:, 512:].contiguous(), 0.0, device_status=status)
+    assert mla.read_status_word(status) == mla.MLA_ERR_DEVICE_BOUNDS
+    rows = torch.from_numpy(F.encode(some.double().numpy()))[pick]
+    rows[bad] = 0xAB
+    want = torch.full((pages * P, 320), 0xAB, dtype=torch.uint8)
+    want[table[pos // P].long() * P + pos % P] = rows
+    assert torch.equal(cache.cpu().view(-1, 320), want)
+
+
 # ----- read-back -------------------------------------------------------------------
 @pytest.mark.parametrize("P,lens,starts", [
     (16, (1,), None),
