@@ -129,6 +129,7 @@ int mla_check_dims(const mla_dims* dims);
  * with a <= 6 s (byte 0 for a = 0) and code = the E2M1 value nearest to x/s (ties
  * to the even code, the sign of zero kept): off by at most s, and by at most s/4
  * below 2 s.  A block with an infinity or a NaN gets byte 255 and codes of 0.
+ * (Their keys are rotated to about 2^-35 and rounded to fp32, then to bf16.)
  *
  *   cache            bf16, int8 or E4M3 (uint8) [num_pages, P, 576], or FP4 rows
  *                    [num_pages, P, MLA_FP4_ROW_BYTES bytes]

@@ -27,13 +27,13 @@ __device__ __forceinline__ uint32_t e4m3x2_rn_sat(float first, float second) {
 // ----- FP4 rows ------------------------------------------------------------------
 // A code is a quarter of its block's largest value away from the next, so a
 // rotated value that lands on the other side of its bf16 rounding can change by
-// that much.  The rotation of FP4 rows is therefore exact to about 2^-30: the
-// angle as a 64-bit fraction of a turn (pos times the frequency, modulo 2^64:
-// two integer multiply-adds, where fp64 takes 64 times the issue slots of fp32
-// on this part), sine and cosine from a table of 256 angles, each a sum of two
-// floats, and the angle that is left, and one rounding to bf16.  Against the fp64
-// rotation less than one value in 10^6 differs (fp32 sine and cosine: one in
-// 10^4).
+// that much.  The rotation of FP4 rows is therefore exact to about 2^-35 before it is
+// rounded, to fp32 and then to bf16: the angle as a 64-bit fraction of a turn (pos
+// times the frequency, modulo 2^64: two integer multiply-adds, where fp64 takes 64
+// times the issue slots of fp32 on this part), sine and cosine from a table of 256
+// angles, each a sum of two floats, and the angle that is left.  None of 8 million
+// blocks had another code than the fp64 rotation so rounded (with fp32 sine and
+// cosine, one value in 10^4).
 struct alignas(16) SinCos {
   float sh, sl, ch, cl;  // sine and cosine as hi + lo
 };
@@ -70,37 +70,47 @@ __device__ __forceinline__ float mul_err(float a, float b, float& err) {
   return p;
 }
 
-// Sine and cosine of `phase` / 2^64 turns, each as hi + lo with lo up to 0.0124:
-// the nearest of the table's angles a, and b = what is left, at most 1 / 512
-// turn: sin(a + b) = sin a + (sin a (cos b - 1) + cos a sin b), and so on.  The
-// fp32 terms in brackets are below 0.0125, off by 2^-30.
+// The sum of a and b as a rounded value and its rounding error, whichever is larger.
+__device__ __forceinline__ float add_err(float a, float b, float& err) {
+  const float s = __fadd_rn(a, b), t = __fadd_rn(s, -a);
+  err = __fadd_rn(__fadd_rn(a, -__fadd_rn(s, -t)), __fadd_rn(b, -t));
+  return s;
+}
+
+// Sine and cosine of `phase` / 2^64 turns, each as hi + lo with lo up to 2^-13: with
+// the nearest of the table's angles a, and b = what is left, at most 1 / 512 turn,
+// sin(a + b) = sin a + cos a sin b + sin a (cos b - 1), and so on.  b is a sum of two
+// floats and cos a sin b keeps its rounding error, so that what is rounded is below
+// 2^-13, by 2^-38.
 __device__ __forceinline__ SinCos sincos_turns(uint64_t phase, const SinCos* table) {
   const uint64_t near = phase + (1ull << 55);
   const SinCos a = table[near >> 56];
-  constexpr float kStep = 6.283185307179586476925286766559 / (1ll << 40);
-  const float b = float(int32_t(uint32_t(near >> 24) ^ 0x80000000u)) * kStep, b2 = b * b;
-  const float sb = __fmaf_rn(b * b2, -1.f / 6.f, b), cb = b2 * __fmaf_rn(b2, 1.f / 24.f, -0.5f);  // cb: cos b - 1
+  constexpr double kUnit = 6.283185307179586476925286766559 / (1ll << 32);  // 2^-32 turns
+  constexpr float kHi = float(kUnit), kLo = float(kUnit - double(kHi)), kLow = float(kUnit / (1ll << 32));
+  const float n = float(int(uint32_t(near >> 32) & 0xffffff) - 0x800000);  // exact
+  float b1;
+  const float b = mul_err(n, kHi, b1), b2 = b * b;
+  b1 += __fmaf_rn(n, kLo, float(uint32_t(near)) * kLow);
+  const float sb = __fmaf_rn(b * b2, -1.f / 6.f, b1), cb = b2 * __fmaf_rn(b2, 1.f / 24.f, -0.5f);  // sin b - b, cos b - 1
   SinCos r;
-  r.sh = a.sh;
-  r.sl = __fmaf_rn(a.sh, cb, __fmaf_rn(a.ch, sb, a.sl));
-  r.ch = a.ch;
-  r.cl = __fmaf_rn(a.ch, cb, __fmaf_rn(-a.sh, sb, a.cl));
+  float e, f;
+  const float u = mul_err(a.ch, b, e), v = mul_err(-a.sh, b, f);
+  e = __fmaf_rn(a.cl, b, e) + a.sl;
+  f = __fmaf_rn(-a.sl, b, f) + a.cl;
+  float g, h;
+  r.sh = add_err(a.sh, u, g);
+  r.ch = add_err(a.ch, v, h);
+  r.sl = __fmaf_rn(a.sh, cb, __fmaf_rn(a.ch, sb, e + g));
+  r.cl = __fmaf_rn(a.ch, cb, __fmaf_rn(-a.sh, sb, f + h));
   return r;
 }
 
-// x a + y b rounded once to bf16, for bf16 x and y and two-float a and b.
+// x a + y b rounded to fp32 and that to bf16, for bf16 x and y and two-float a and b.
 __device__ __forceinline__ __nv_bfloat16 dot2_bf16(float x, float ah, float al, float y, float bh, float bl) {
-  float ep, eq;
-  const float p = mul_err(x, ah, ep), q = mul_err(y, bh, eq);
-  // the sum of p and q and its error, whichever is larger
-  const float s = __fadd_rn(p, q), t = __fadd_rn(s, -p);
-  const float es = __fadd_rn(__fadd_rn(p, -__fadd_rn(s, -t)), __fadd_rn(q, -t));
+  float ep, eq, es;
+  const float p = mul_err(x, ah, ep), q = mul_err(y, bh, eq), s = add_err(p, q, es);
   const float low = __fadd_rn(es, __fadd_rn(__fmaf_rn(x, al, ep), __fmaf_rn(y, bl, eq)));
-  const float v = __fadd_rn(s, low), rest = __fadd_rn(low, -__fadd_rn(v, -s));
-  // where the fp32 sum sits on the border between two bf16 values, its own rounding error decides
-  uint32_t bits = __float_as_uint(v);
-  if ((bits & 0xffff) == 0x8000 && rest != 0.f) bits += (rest > 0.f) == (v > 0.f) ? 1 : -1;
-  return __float2bfloat16_rn(__uint_as_float(bits));
+  return __float2bfloat16_rn(__fadd_rn(s, low));
 }
 
 // The larger magnitudes of two packed pairs of bf16 values, NaN where either is.
@@ -225,7 +235,7 @@ __device__ __forceinline__ bool locate(const AppendParams& p, int i, bool report
 // look up side by side, the next one's values on their way while it works on one.
 // Lane l owns latent values [16l, 16l + 16) and RoPE pair l.  Bound by instructions
 // (rotation, quantisation, packing; about 350 a token) rather than memory (1,472 bytes
-// a token): 34,817 tokens 15.4 us, 3.3 TB/s (17.3 where each token was looked up in
+// a token): 34,817 tokens 15.6 us, 3.3 TB/s (17.3 where each token was looked up in
 // its turn, by a warp of four of them).
 template <bool kRuns>
 __global__ void __launch_bounds__(256) append_fp4_kernel(AppendParams p) {

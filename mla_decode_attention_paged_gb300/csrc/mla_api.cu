@@ -120,8 +120,8 @@ uint64_t turn_fraction(double f) {
 
 // Tokens of a warp of an FP4 append: so many that the blocks of 8 warps, 5 to an SM,
 // are there at once, or in as few rounds as runs of up to 32 tokens allow, all of them
-// full.  Against runs of 4 tokens: 2,048 tokens 5.0 -> 3.5 us, 16,384 11.6 -> 9.1, 34,817
-// 17.3 -> 15.4, 100,000 43.8 -> 39.3 (8,192 tokens 6.4 -> 6.8).
+// full.  Against runs of 4 tokens: 2,048 tokens 5.0 -> 3.5 us, 16,384 11.6 -> 9.2, 34,817
+// 17.3 -> 15.6, 100,000 43.8 -> 39.9 (8,192 tokens 6.4 -> 6.8).
 int append_run(int n_tokens) {
   const long long warps = 40ll * std::max(1, sm_count()), rounds = (n_tokens - 1) / (32 * warps) + 1;
   return int(std::max(2ll, (n_tokens - 1) / (rounds * warps) + 1));

@@ -64,10 +64,12 @@ def through_e5m2(x):
 
 
 def rotated(k_pe, positions, theta):
-    """bf16 values (as float64) of RoPE keys [n, 64] at their positions."""
+    """bf16 values (as float64) of RoPE keys [n, 64] at their positions: rounded to
+    fp32 and then to bf16."""
     if not theta > 0:
         return np.asarray(k_pe, np.float64)
-    return O.bf16_bits_to_f64(O.f64_to_bf16_bits(O.rope_rotate(np.asarray(k_pe, np.float64), np.asarray(positions), theta)))
+    x = O.rope_rotate(np.asarray(k_pe, np.float64), np.asarray(positions), theta).astype(np.float32)
+    return O.bf16_bits_to_f64(O.f64_to_bf16_bits(x.astype(np.float64)))
 
 
 def appended(cache, table, seq_ids, positions, c_kv, k_pe, theta, page):
