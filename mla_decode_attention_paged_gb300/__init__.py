@@ -267,11 +267,11 @@ def decode(d: Dims, q_nope, q_pe, cache, scale_zero, block_table, seq_lens, W_UK
     B = q_nope.shape[0]
     dev = q_nope.device
     if workspace is None:
-        workspace = torch.empty(decode_workspace_size(d, B, num_splits), dtype=torch.uint8, device=dev)
+        workspace = _new(decode_workspace_size(d, B, num_splits), torch.uint8, dev, stream)
     if out is None:
-        out = torch.empty((B, d.num_heads, d.v_head_dim), dtype=torch.bfloat16, device=dev)
+        out = _new((B, d.num_heads, d.v_head_dim), torch.bfloat16, dev, stream)
     if lse_out is None and want_lse:
-        lse_out = torch.empty((B, d.num_heads), dtype=torch.float32, device=dev)
+        lse_out = _new((B, d.num_heads), torch.float32, dev, stream)
     at, i32, bf16 = _index(q_nope), torch.int32, torch.bfloat16
     st = _call_on(
         dev, stream, _L().mla_decode, ctypes.byref(d), _on(q_nope, bf16, at, "q_nope"), _on(q_pe, bf16, at, "q_pe"),
@@ -301,11 +301,11 @@ def decode_multi(d: Dims, q_nope, q_pe, cache, scale_zero, block_table, seq_lens
     B, T = q_nope.shape[0], q_nope.shape[1]
     dev = q_nope.device
     if workspace is None:
-        workspace = torch.empty(decode_multi_workspace_size(d, B, T, num_splits), dtype=torch.uint8, device=dev)
+        workspace = _new(decode_multi_workspace_size(d, B, T, num_splits), torch.uint8, dev, stream)
     if out is None:
-        out = torch.empty((B, T, d.num_heads, d.v_head_dim), dtype=torch.bfloat16, device=dev)
+        out = _new((B, T, d.num_heads, d.v_head_dim), torch.bfloat16, dev, stream)
     if lse_out is None and want_lse:
-        lse_out = torch.empty((B, T, d.num_heads), dtype=torch.float32, device=dev)
+        lse_out = _new((B, T, d.num_heads), torch.float32, dev, stream)
     at, i32, bf16 = _index(q_nope), torch.int32, torch.bfloat16
     st = _call_on(
         dev, stream, _L().mla_decode_multi, ctypes.byref(d), _on(q_nope, bf16, at, "q_nope"),
@@ -337,11 +337,11 @@ def prefill(d: Dims, cache, scale_zero, block_table, seq_lens, c_kv, k_pe, q_nop
     B, T = q_nope.shape[0], q_nope.shape[1]
     dev = q_nope.device
     if workspace is None:
-        workspace = torch.empty(prefill_workspace_size(d, B, T, num_splits), dtype=torch.uint8, device=dev)
+        workspace = _new(prefill_workspace_size(d, B, T, num_splits), torch.uint8, dev, stream)
     if out is None:
-        out = torch.empty((B, T, d.num_heads, d.v_head_dim), dtype=torch.bfloat16, device=dev)
+        out = _new((B, T, d.num_heads, d.v_head_dim), torch.bfloat16, dev, stream)
     if lse_out is None and want_lse:
-        lse_out = torch.empty((B, T, d.num_heads), dtype=torch.float32, device=dev)
+        lse_out = _new((B, T, d.num_heads), torch.float32, dev, stream)
     cache_p, scale_p = _cache_ptrs(d, cache, scale_zero, dev)
     at, i32, bf16 = _index(q_nope), torch.int32, torch.bfloat16
     st = _call_on(
@@ -372,11 +372,11 @@ def decode_sparse(d: Dims, q_nope, q_pe, cache, scale_zero, block_table, seq_len
     B, K = token_indices.shape
     dev = q_nope.device
     if workspace is None:
-        workspace = torch.empty(decode_sparse_workspace_size(d, B, K, num_splits), dtype=torch.uint8, device=dev)
+        workspace = _new(decode_sparse_workspace_size(d, B, K, num_splits), torch.uint8, dev, stream)
     if out is None:
-        out = torch.empty((B, d.num_heads, d.v_head_dim), dtype=torch.bfloat16, device=dev)
+        out = _new((B, d.num_heads, d.v_head_dim), torch.bfloat16, dev, stream)
     if lse_out is None and want_lse:
-        lse_out = torch.empty((B, d.num_heads), dtype=torch.float32, device=dev)
+        lse_out = _new((B, d.num_heads), torch.float32, dev, stream)
     at, i32, bf16 = _index(q_nope), torch.int32, torch.bfloat16
     st = _call_on(
         dev, stream, _L().mla_decode_sparse, ctypes.byref(d), _on(q_nope, bf16, at, "q_nope"),
@@ -557,7 +557,7 @@ def decode_no_alloc(d: Dims, q_nope, q_pe, cache, scale_zero, block_table, seq_l
     B = q_nope.shape[0]
     dev = q_nope.device
     if out is None:
-        out = torch.empty((B, d.num_heads, d.v_head_dim), dtype=torch.bfloat16, device=dev)
+        out = _new((B, d.num_heads, d.v_head_dim), torch.bfloat16, dev, stream)
     st = _L().mla_decode_no_alloc(
         ctypes.byref(d), _ptr(q_nope, torch.bfloat16, "q_nope"), _ptr(q_pe, torch.bfloat16, "q_pe", dev),
         *_cache_ptrs(d, cache, scale_zero, dev), cache.shape[0],
@@ -576,9 +576,9 @@ def combine(d: Dims, partial_o: torch.Tensor, partial_lse: torch.Tensor, o_lat_o
     B, S, H, D = partial_o.shape
     dev = partial_o.device
     if o_lat_out is None:
-        o_lat_out = torch.empty((B, H, D), dtype=torch.float32, device=dev)
+        o_lat_out = _new((B, H, D), torch.float32, dev, stream)
     if lse_out is None:
-        lse_out = torch.empty((B, H), dtype=torch.float32, device=dev)
+        lse_out = _new((B, H), torch.float32, dev, stream)
     st = _L().mla_combine(ctypes.byref(d), _ptr(partial_o, torch.float32, "partial_o"),
                           _ptr(partial_lse, torch.float32, "partial_lse", dev), B, S,
                           _ptr(o_lat_out, torch.float32, "o_lat_out", dev), _ptr(lse_out, torch.float32, "lse_out", dev),
