@@ -185,10 +185,29 @@ def _on(t: torch.Tensor, dtype, index: int, name: str) -> int:
     return _ptr(t, dtype, name, torch.device("cuda", index) if index >= 0 else None)
 
 
+def _holds(t: torch.Tensor, dtype, index: int, name: str, n: int) -> int:
+    """_on of a tensor with at least the ``n`` elements that the call reads or writes."""
+    try:
+        if t.dtype is dtype and t.numel() >= n and t.get_device() == index and index >= 0 and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    p = _on(t, dtype, index, name)  # raises what is wrong, unless it is the size
+    if t.numel() < n:
+        raise ValueError(f"{name} has {t.numel()} elements, the call needs {n}")
+    return p
+
+
 def _index(t: torch.Tensor, name: str = "q_nope") -> int:
     """CUDA device of a tensor."""
     _ptr(t, None, name)
     return t.get_device()
+
+
+def _weights(d: Dims) -> tuple[int, int]:
+    """Elements of W_UK and of W_UV."""
+    n = d.num_heads * d.kv_lora_rank
+    return n * d.qk_nope_dim, n * d.v_head_dim
 
 
 def _workspace(t: torch.Tensor, index: int) -> tuple[int, int]:
@@ -196,24 +215,26 @@ def _workspace(t: torch.Tensor, index: int) -> tuple[int, int]:
     return _on(t, t.dtype if isinstance(t, torch.Tensor) else None, index, "workspace"), t.nbytes
 
 
-def _cache_ptrs(d: Dims, cache: torch.Tensor, scale_zero: torch.Tensor | None, device=None):
+# The type of a cache tensor by mla_cache_dtype, where it is not bf16.
+_CODES = {MLA_CACHE_INT8: torch.int8, MLA_CACHE_FP8: torch.uint8, MLA_CACHE_FP4: torch.uint8}
+
+
+def _cache_ptrs(d: Dims, cache: torch.Tensor, scale_zero: torch.Tensor | None, index: int):
     """Pointers of the cache rows (bf16 values, int8 codes, E4M3 codes, or FP4
     rows) and of their per-token scales (None for bf16 and FP4 caches)."""
-    if d.cache_dtype == MLA_CACHE_FP4:
-        p = _ptr(cache, torch.uint8, "cache", device)
-        s = cache.shape
+    code = d.cache_dtype
+    if code == MLA_CACHE_FP4:
+        p, s = _on(cache, torch.uint8, index, "cache"), cache.shape
         if len(s) != 3 or s[1] != d.page_size or s[2] != FP4_ROW_BYTES:
-            raise ValueError(f"cache must have shape [pages, {d.page_size}, {FP4_ROW_BYTES}], got {list(cache.shape)}")
+            raise ValueError(f"cache must have shape [pages, {d.page_size}, {FP4_ROW_BYTES}], got {list(s)}")
         return p, None
-    if d.cache_dtype == MLA_CACHE_FP8:
-        if isinstance(cache, torch.Tensor) and cache.dtype == torch.float8_e4m3fn:
-            cache = cache.view(torch.uint8)
-        want = torch.uint8
-    else:
-        want = torch.int8 if d.cache_dtype == MLA_CACHE_INT8 else torch.bfloat16
-    byte = d.cache_dtype != MLA_CACHE_BF16
-    return (_ptr(cache, want, "cache", device),
-            _ptr(scale_zero, torch.float32, "scale_zero", device) if byte else None)
+    if code == MLA_CACHE_FP8 and isinstance(cache, torch.Tensor) and cache.dtype == torch.float8_e4m3fn:
+        cache = cache.view(torch.uint8)
+    rows = cache.shape[0] * d.page_size
+    p = _holds(cache, _CODES.get(code, torch.bfloat16), index, "cache", rows * (d.kv_lora_rank + d.rope_dim))
+    if code == MLA_CACHE_BF16 or scale_zero is None:  # without its scales the library refuses a 1-byte cache
+        return p, None
+    return p, _holds(scale_zero, torch.float32, index, "scale_zero", rows * (2 if code == MLA_CACHE_INT8 else 1))
 
 
 def _stream(stream) -> int | None:
@@ -230,15 +251,14 @@ def cache_append(d: Dims, cache: torch.Tensor, scale_zero: torch.Tensor | None, 
                  seq_ids: torch.Tensor, positions: torch.Tensor, c_kv: torch.Tensor, k_pe: torch.Tensor,
                  rope_theta: float = 10000.0, device_status: torch.Tensor | None = None, stream=None) -> None:
     """mla_cache_append: write new tokens' rows into the paged cache (in place)."""
-    dev, i32, bf16 = cache.device, torch.int32, torch.bfloat16
-    cache_p, scale_p = _cache_ptrs(d, cache, scale_zero, dev)
-    at = dev.index
-    table_p = _on(block_table, i32, at, "block_table")
-    table = block_table.shape
+    dev, at, i32, bf16 = cache.device, cache.get_device(), torch.int32, torch.bfloat16
+    cache_p, scale_p = _cache_ptrs(d, cache, scale_zero, at)
+    table_p, table = _on(block_table, i32, at, "block_table"), block_table.shape
+    ids_p, n = _on(seq_ids, i32, at, "seq_ids"), seq_ids.numel()
     st = _call_on(
-        dev, stream, _L().mla_cache_append, ctypes.byref(d), cache_p, scale_p, cache.shape[0], table_p, table[0], table[1],
-        _on(seq_ids, i32, at, "seq_ids"), _on(positions, i32, at, "positions"), seq_ids.numel(),
-        _on(c_kv, bf16, at, "c_kv"), _on(k_pe, bf16, at, "k_pe"), float(rope_theta),
+        dev, stream, _L().mla_cache_append, ctypes.byref(d), cache_p, scale_p, cache.shape[0], table_p,
+        table[0], table[1], ids_p, _holds(positions, i32, at, "positions", n), n,
+        _holds(c_kv, bf16, at, "c_kv", n * d.kv_lora_rank), _holds(k_pe, bf16, at, "k_pe", n * d.rope_dim), float(rope_theta),
         None if device_status is None else _on(device_status, i32, at, "device_status"))
     _check(st, "mla_cache_append")
 
@@ -273,12 +293,16 @@ def decode(d: Dims, q_nope, q_pe, cache, scale_zero, block_table, seq_lens, W_UK
     if lse_out is None and want_lse:
         lse_out = _new((B, d.num_heads), torch.float32, dev, stream)
     at, i32, bf16 = _index(q_nope), torch.int32, torch.bfloat16
+    rows, max_pages = B * d.num_heads, block_table.shape[1]
+    uk, uv = _weights(d)
     st = _call_on(
-        dev, stream, _L().mla_decode, ctypes.byref(d), _on(q_nope, bf16, at, "q_nope"), _on(q_pe, bf16, at, "q_pe"),
-        *_cache_ptrs(d, cache, scale_zero, dev), cache.shape[0], _on(block_table, i32, at, "block_table"),
-        block_table.shape[1], _on(seq_lens, i32, at, "seq_lens"), B, _on(W_UK, bf16, at, "W_UK"),
-        _on(W_UV, bf16, at, "W_UV"), float(softmax_scale), int(num_splits), *_workspace(workspace, at),
-        _on(out, bf16, at, "out"), None if lse_out is None else _on(lse_out, torch.float32, at, "lse_out"))
+        dev, stream, _L().mla_decode, ctypes.byref(d), _holds(q_nope, bf16, at, "q_nope", rows * d.qk_nope_dim),
+        _holds(q_pe, bf16, at, "q_pe", rows * d.rope_dim), *_cache_ptrs(d, cache, scale_zero, at), cache.shape[0],
+        _holds(block_table, i32, at, "block_table", B * max_pages), max_pages,
+        _holds(seq_lens, i32, at, "seq_lens", B), B,
+        _holds(W_UK, bf16, at, "W_UK", uk), _holds(W_UV, bf16, at, "W_UV", uv), float(softmax_scale), int(num_splits),
+        *_workspace(workspace, at), _holds(out, bf16, at, "out", rows * d.v_head_dim),
+        None if lse_out is None else _holds(lse_out, torch.float32, at, "lse_out", rows))
     _check(st, "mla_decode")
     return out, lse_out
 
@@ -307,13 +331,16 @@ def decode_multi(d: Dims, q_nope, q_pe, cache, scale_zero, block_table, seq_lens
     if lse_out is None and want_lse:
         lse_out = _new((B, T, d.num_heads), torch.float32, dev, stream)
     at, i32, bf16 = _index(q_nope), torch.int32, torch.bfloat16
+    rows, max_pages = B * T * d.num_heads, block_table.shape[1]
+    uk, uv = _weights(d)
     st = _call_on(
-        dev, stream, _L().mla_decode_multi, ctypes.byref(d), _on(q_nope, bf16, at, "q_nope"),
-        _on(q_pe, bf16, at, "q_pe"), *_cache_ptrs(d, cache, scale_zero, dev), cache.shape[0],
-        _on(block_table, i32, at, "block_table"), block_table.shape[1], _on(seq_lens, i32, at, "seq_lens"), B, T,
-        _on(W_UK, bf16, at, "W_UK"), _on(W_UV, bf16, at, "W_UV"), float(softmax_scale), int(num_splits),
-        *_workspace(workspace, at), _on(out, bf16, at, "out"),
-        None if lse_out is None else _on(lse_out, torch.float32, at, "lse_out"))
+        dev, stream, _L().mla_decode_multi, ctypes.byref(d), _holds(q_nope, bf16, at, "q_nope", rows * d.qk_nope_dim),
+        _holds(q_pe, bf16, at, "q_pe", rows * d.rope_dim), *_cache_ptrs(d, cache, scale_zero, at), cache.shape[0],
+        _holds(block_table, i32, at, "block_table", B * max_pages), max_pages,
+        _holds(seq_lens, i32, at, "seq_lens", B), B, T,
+        _holds(W_UK, bf16, at, "W_UK", uk), _holds(W_UV, bf16, at, "W_UV", uv), float(softmax_scale), int(num_splits),
+        *_workspace(workspace, at), _holds(out, bf16, at, "out", rows * d.v_head_dim),
+        None if lse_out is None else _holds(lse_out, torch.float32, at, "lse_out", rows))
     _check(st, "mla_decode_multi")
     return out, lse_out
 
@@ -342,15 +369,20 @@ def prefill(d: Dims, cache, scale_zero, block_table, seq_lens, c_kv, k_pe, q_nop
         out = _new((B, T, d.num_heads, d.v_head_dim), torch.bfloat16, dev, stream)
     if lse_out is None and want_lse:
         lse_out = _new((B, T, d.num_heads), torch.float32, dev, stream)
-    cache_p, scale_p = _cache_ptrs(d, cache, scale_zero, dev)
     at, i32, bf16 = _index(q_nope), torch.int32, torch.bfloat16
+    cache_p, scale_p = _cache_ptrs(d, cache, scale_zero, at)
+    rows, max_pages = B * T * d.num_heads, block_table.shape[1]
+    uk, uv = _weights(d)
     st = _call_on(
         dev, stream, _L().mla_prefill, ctypes.byref(d), cache_p, scale_p, cache.shape[0],
-        _on(block_table, i32, at, "block_table"), block_table.shape[1], _on(seq_lens, i32, at, "seq_lens"), B, T,
-        _on(c_kv, bf16, at, "c_kv"), _on(k_pe, bf16, at, "k_pe"), float(rope_theta), _on(q_nope, bf16, at, "q_nope"),
-        _on(q_pe, bf16, at, "q_pe"), _on(W_UK, bf16, at, "W_UK"), _on(W_UV, bf16, at, "W_UV"), float(softmax_scale),
-        int(num_splits), *_workspace(workspace, at), _on(out, bf16, at, "out"),
-        None if lse_out is None else _on(lse_out, torch.float32, at, "lse_out"))
+        _holds(block_table, i32, at, "block_table", B * max_pages), max_pages,
+        _holds(seq_lens, i32, at, "seq_lens", B), B, T,
+        _holds(c_kv, bf16, at, "c_kv", B * T * d.kv_lora_rank), _holds(k_pe, bf16, at, "k_pe", B * T * d.rope_dim),
+        float(rope_theta), _holds(q_nope, bf16, at, "q_nope", rows * d.qk_nope_dim),
+        _holds(q_pe, bf16, at, "q_pe", rows * d.rope_dim), _holds(W_UK, bf16, at, "W_UK", uk),
+        _holds(W_UV, bf16, at, "W_UV", uv), float(softmax_scale), int(num_splits), *_workspace(workspace, at),
+        _holds(out, bf16, at, "out", rows * d.v_head_dim),
+        None if lse_out is None else _holds(lse_out, torch.float32, at, "lse_out", rows))
     _check(st, "mla_prefill")
     return out, lse_out
 
@@ -378,13 +410,16 @@ def decode_sparse(d: Dims, q_nope, q_pe, cache, scale_zero, block_table, seq_len
     if lse_out is None and want_lse:
         lse_out = _new((B, d.num_heads), torch.float32, dev, stream)
     at, i32, bf16 = _index(q_nope), torch.int32, torch.bfloat16
+    rows, max_pages = B * d.num_heads, block_table.shape[1]
+    uk, uv = _weights(d)
     st = _call_on(
-        dev, stream, _L().mla_decode_sparse, ctypes.byref(d), _on(q_nope, bf16, at, "q_nope"),
-        _on(q_pe, bf16, at, "q_pe"), *_cache_ptrs(d, cache, scale_zero, dev), cache.shape[0],
-        _on(block_table, i32, at, "block_table"), block_table.shape[1], _on(seq_lens, i32, at, "seq_lens"), B,
-        _on(token_indices, i32, at, "token_indices"), K, _on(W_UK, bf16, at, "W_UK"), _on(W_UV, bf16, at, "W_UV"),
-        float(softmax_scale), int(num_splits), *_workspace(workspace, at), _on(out, bf16, at, "out"),
-        None if lse_out is None else _on(lse_out, torch.float32, at, "lse_out"))
+        dev, stream, _L().mla_decode_sparse, ctypes.byref(d), _holds(q_nope, bf16, at, "q_nope", rows * d.qk_nope_dim),
+        _holds(q_pe, bf16, at, "q_pe", rows * d.rope_dim), *_cache_ptrs(d, cache, scale_zero, at), cache.shape[0],
+        _holds(block_table, i32, at, "block_table", B * max_pages), max_pages,
+        _holds(seq_lens, i32, at, "seq_lens", B), B, _on(token_indices, i32, at, "token_indices"), K,
+        _holds(W_UK, bf16, at, "W_UK", uk), _holds(W_UV, bf16, at, "W_UV", uv), float(softmax_scale), int(num_splits),
+        *_workspace(workspace, at), _holds(out, bf16, at, "out", rows * d.v_head_dim),
+        None if lse_out is None else _holds(lse_out, torch.float32, at, "lse_out", rows))
     _check(st, "mla_decode_sparse")
     return out, lse_out
 
@@ -417,10 +452,6 @@ def _dims_of(t: torch.Tensor, name: str, n: int):
     if t.dim() != n:
         raise ValueError(f"{name} must have {n} dimensions, got {list(t.shape)}")
     raise ValueError(f"{name} must be a CUDA tensor")
-
-
-# The type of a cache tensor by mla_cache_dtype, where it is not bf16.
-_CODES = {MLA_CACHE_INT8: torch.int8, MLA_CACHE_FP8: torch.uint8, MLA_CACHE_FP4: torch.uint8}
 
 
 def _call_on(dev: torch.device, stream, fn, *args) -> int:
@@ -558,14 +589,18 @@ def decode_no_alloc(d: Dims, q_nope, q_pe, cache, scale_zero, block_table, seq_l
     dev = q_nope.device
     if out is None:
         out = _new((B, d.num_heads, d.v_head_dim), torch.bfloat16, dev, stream)
+    at, i32, bf16 = _index(q_nope), torch.int32, torch.bfloat16
+    rows, max_pages = B * d.num_heads, block_table.shape[1]
+    uk, uv = _weights(d)
     st = _L().mla_decode_no_alloc(
-        ctypes.byref(d), _ptr(q_nope, torch.bfloat16, "q_nope"), _ptr(q_pe, torch.bfloat16, "q_pe", dev),
-        *_cache_ptrs(d, cache, scale_zero, dev), cache.shape[0],
-        _ptr(block_table, torch.int32, "block_table", dev), block_table.shape[1],
-        _ptr(seq_lens, torch.int32, "seq_lens", dev), B, _ptr(W_UK, torch.bfloat16, "W_UK", dev),
-        _ptr(W_UV, torch.bfloat16, "W_UV", dev), float(softmax_scale), int(num_splits),
-        _ptr(out, torch.bfloat16, "out", dev), _ptr(lse_out, torch.float32, "lse_out", dev),
-        _ptr(device_status, torch.int32, "device_status", dev), _stream(stream))
+        ctypes.byref(d), _holds(q_nope, bf16, at, "q_nope", rows * d.qk_nope_dim),
+        _holds(q_pe, bf16, at, "q_pe", rows * d.rope_dim), *_cache_ptrs(d, cache, scale_zero, at), cache.shape[0],
+        _holds(block_table, i32, at, "block_table", B * max_pages), max_pages,
+        _holds(seq_lens, i32, at, "seq_lens", B), B,
+        _holds(W_UK, bf16, at, "W_UK", uk), _holds(W_UV, bf16, at, "W_UV", uv), float(softmax_scale), int(num_splits),
+        _holds(out, bf16, at, "out", rows * d.v_head_dim),
+        None if lse_out is None else _holds(lse_out, torch.float32, at, "lse_out", rows),
+        None if device_status is None else _on(device_status, i32, at, "device_status"), _stream(stream))
     _check(st, "mla_decode_no_alloc")
     return out, lse_out
 
@@ -579,10 +614,12 @@ def combine(d: Dims, partial_o: torch.Tensor, partial_lse: torch.Tensor, o_lat_o
         o_lat_out = _new((B, H, D), torch.float32, dev, stream)
     if lse_out is None:
         lse_out = _new((B, H), torch.float32, dev, stream)
-    st = _L().mla_combine(ctypes.byref(d), _ptr(partial_o, torch.float32, "partial_o"),
-                          _ptr(partial_lse, torch.float32, "partial_lse", dev), B, S,
-                          _ptr(o_lat_out, torch.float32, "o_lat_out", dev), _ptr(lse_out, torch.float32, "lse_out", dev),
-                          _stream(stream))
+    at, f32 = _index(partial_o, "partial_o"), torch.float32
+    rows = B * d.num_heads
+    st = _L().mla_combine(ctypes.byref(d), _holds(partial_o, f32, at, "partial_o", rows * S * d.kv_lora_rank),
+                          _holds(partial_lse, f32, at, "partial_lse", rows * S), B, S,
+                          _holds(o_lat_out, f32, at, "o_lat_out", rows * d.kv_lora_rank),
+                          _holds(lse_out, f32, at, "lse_out", rows), _stream(stream))
     _check(st, "mla_combine")
     return o_lat_out, lse_out
 

@@ -1,5 +1,5 @@
 """CPU checks of what the binding does around a call of the library: the memory
-it allocates.  Nothing is launched (binding_calls)."""
+it allocates, and the tensors it refuses.  Nothing is launched (binding_calls)."""
 import pytest
 import torch
 
@@ -38,3 +38,47 @@ def test_what_a_call_allocates_is_its_streams(lib, monkeypatch, entry):
     # decode_no_alloc gives no log-sum-exp unless it gets the buffer
     assert made == [77] * (1 if entry == "decode_no_alloc" else len(buffers))
     assert lib.calls[-1][0] == "mla_" + entry and lib.calls[-1][1][-1] == 77
+
+
+SMALLER = {"cache_append": ["positions", "c_kv", "k_pe"],
+           "combine": ["partial_o", "partial_lse"]}
+DECODE = ["q_nope", "q_pe", "block_table", "seq_lens", "W_UK", "W_UV"]
+
+
+@pytest.mark.parametrize("cache_format", ["bf16", "int8", "fp8", "fp4"])
+@pytest.mark.parametrize("entry", ENTRIES)
+def test_tensors_too_small_for_the_call_are_refused(lib, cache_format, entry):
+    """Each tensor with less than the call reads or writes is refused before the
+    launch; larger ones, and the same elements in another shape, are not."""
+    d, calls = C.calls(cache_format)
+    tensors, buffers, rest = calls[entry]
+    given = {**tensors, **{k: v for k, v in buffers.items() if k != "workspace"}}
+    call = lambda **kw: getattr(mla, entry)(d, **{**tensors, **buffers, **rest, **kw})
+    call()
+    assert [name for name, _ in lib.calls] == ["mla_" + entry]
+    small = SMALLER.get(entry, DECODE + (["c_kv", "k_pe"] if entry == "prefill" else []))
+    small = small + [k for k in buffers if k != "workspace"] + (["scale_zero"] if tensors.get("scale_zero") is not None else [])
+    small = small + (["cache"] if "cache" in tensors else [])
+    for name in small:
+        t = given[name]
+        # one row less, with the sizes that the call takes from this tensor as they were
+        less = t.view(-1)[:t.numel() - 1]
+        if name in ("q_nope", "partial_o", "cache", "block_table"):
+            less = t[..., :-1].contiguous() if name != "block_table" else t[:-1]
+        with pytest.raises(ValueError):
+            call(**{name: less})
+        if name in ("q_nope", "cache", "partial_o", "block_table"):
+            continue
+        call(**{name: torch.cat([t.view(-1), t.view(-1)])})
+        call(**{name: t.view(-1)})
+    assert not [name for name, _ in lib.calls if name != "mla_" + entry]
+
+
+def test_sparse_lists_of_more_sequences_than_queries(lib):
+    """The batch is the lists'; queries, lengths and outputs of fewer sequences are refused."""
+    d, calls = C.calls()
+    tensors, buffers, rest = calls["decode_sparse"]
+    more = C.gpu(C.B + 1, C.TOP_K, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        mla.decode_sparse(d, **{**tensors, **buffers, **rest, "token_indices": more})
+    assert not lib.calls
