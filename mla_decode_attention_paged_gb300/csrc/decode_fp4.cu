@@ -914,6 +914,10 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
   if (warp == kQkWarp) tmem_dealloc(tmem, C::kTmemCols);
 }
 
+// Registers of a thread as a block's launch gives them out.
+constexpr int launch_registers(int regs) { return (regs + 7) / 8 * 8; }
+static_assert(launch_registers(88) == 88 && launch_registers(89) == 96 && launch_registers(96) == 96, "by eights");
+
 template <int HC>
 cudaError_t launch_fp4(const DecodeParams& p, int grid, cudaStream_t stream) {
   using C = Fp4Cfg<HC>;
@@ -922,8 +926,16 @@ cudaError_t launch_fp4(const DecodeParams& p, int grid, cudaStream_t stream) {
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 128 || !attr[dev]) {
     for (auto* k : {decode_fp4_kernel<HC, false>, decode_fp4_kernel<HC, true>}) {
-      const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::kSmem));
+      cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::kSmem));
       if (e != cudaSuccess) return e;
+      if (C::kSplitRegs) {
+        // setmaxnreg.inc waits, with no limit, for registers that the block was
+        // launched with: a build of fewer than the roles share out is not launched
+        cudaFuncAttributes a;
+        e = cudaFuncGetAttributes(&a, k);
+        if (e != cudaSuccess) return e;
+        if (launch_registers(a.numRegs) != C::kRegs) return cudaErrorLaunchOutOfResources;
+      }
     }
     if (dev >= 0 && dev < 128) attr[dev] = true;
   }
