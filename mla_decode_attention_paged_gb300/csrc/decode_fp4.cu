@@ -329,8 +329,8 @@ __device__ __forceinline__ void walk_start(TileWalkerT<true>& w, const DecodePar
   w.enter_sequence_body();
 }
 
-// kCausal: multi-token decode (q_len > 1) masks each row's later positions on a
-// sequence's last tiles.
+// kCausal: multi-token decode (q_len > 1, so groups of 32 rows) masks each row's
+// later positions on a sequence's last tiles.
 template <int HC, bool kCausal>
 __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(DecodeParams p) {
   using C = Fp4Cfg<HC>;
@@ -918,35 +918,35 @@ __global__ void __launch_bounds__(Fp4Cfg<HC>::kThreads, 1) decode_fp4_kernel(Dec
 constexpr int launch_registers(int regs) { return (regs + 7) / 8 * 8; }
 static_assert(launch_registers(88) == 88 && launch_registers(89) == 96 && launch_registers(96) == 96, "by eights");
 
-template <int HC>
+template <int HC, bool kCausal>
 cudaError_t launch_fp4(const DecodeParams& p, int grid, cudaStream_t stream) {
   using C = Fp4Cfg<HC>;
+  auto* kernel = decode_fp4_kernel<HC, kCausal>;
   static std::atomic<bool> attr[128];  // per device: attributes set (zero-initialised)
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 128 || !attr[dev]) {
-    for (auto* k : {decode_fp4_kernel<HC, false>, decode_fp4_kernel<HC, true>}) {
-      cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::kSmem));
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::kSmem));
+    if (e != cudaSuccess) return e;
+    if (C::kSplitRegs) {
+      // setmaxnreg.inc waits, with no limit, for registers that the block was
+      // launched with: a build of fewer than the roles share out is not launched
+      cudaFuncAttributes a;
+      e = cudaFuncGetAttributes(&a, kernel);
       if (e != cudaSuccess) return e;
-      if (C::kSplitRegs) {
-        // setmaxnreg.inc waits, with no limit, for registers that the block was
-        // launched with: a build of fewer than the roles share out is not launched
-        cudaFuncAttributes a;
-        e = cudaFuncGetAttributes(&a, k);
-        if (e != cudaSuccess) return e;
-        if (launch_registers(a.numRegs) != C::kRegs) return cudaErrorLaunchOutOfResources;
-      }
+      if (launch_registers(a.numRegs) != C::kRegs) return cudaErrorLaunchOutOfResources;
     }
     if (dev >= 0 && dev < 128) attr[dev] = true;
   }
-  auto* kernel = p.q_len > 1 ? decode_fp4_kernel<HC, true> : decode_fp4_kernel<HC, false>;
   return launch_pdl(kernel, dim3(grid), dim3(C::kThreads), C::kSmem, stream, 1, p);
 }
 
 }  // namespace
 
 cudaError_t launch_decode_fp4(const DecodeParams& p, int hc, int grid, cudaStream_t stream) {
-  return hc == 16 ? launch_fp4<16>(p, grid, stream) : launch_fp4<32>(p, grid, stream);
+  // 16 rows are the 16 heads of one token: no causal form
+  if (hc == 16) return launch_fp4<16, false>(p, grid, stream);
+  return p.q_len > 1 ? launch_fp4<32, true>(p, grid, stream) : launch_fp4<32, false>(p, grid, stream);
 }
 
 }  // namespace mla

@@ -62,3 +62,8 @@ def test_other_register_counts_are_not_launched(launch, q_len, registers):
 @pytest.mark.parametrize("registers", [89, 95, 96])
 def test_registers_are_given_out_by_eights(launch, registers):
     assert launch(32, 1, registers)[1] == [(32, 0)] * 2
+
+
+def test_only_forms_that_a_call_reaches(launch):
+    """16 rows are one token's (heads come by 16 or by 32): no causal form of them."""
+    assert launch(16, 1, REGISTERS)[0] == [(16, 0), (32, 0), (32, 1)]
