@@ -200,7 +200,8 @@ def _holds(t: torch.Tensor, dtype, index: int, name: str, n: int) -> int:
 
 def _index(t: torch.Tensor, name: str = "q_nope") -> int:
     """CUDA device of a tensor."""
-    _ptr(t, None, name)
+    if _ptr(t, None, name) is None:
+        raise TypeError(f"{name} must be a torch.Tensor")
     return t.get_device()
 
 
@@ -592,15 +593,15 @@ def decode_no_alloc(d: Dims, q_nope, q_pe, cache, scale_zero, block_table, seq_l
     at, i32, bf16 = _index(q_nope), torch.int32, torch.bfloat16
     rows, max_pages = B * d.num_heads, block_table.shape[1]
     uk, uv = _weights(d)
-    st = _L().mla_decode_no_alloc(
-        ctypes.byref(d), _holds(q_nope, bf16, at, "q_nope", rows * d.qk_nope_dim),
+    st = _call_on(
+        dev, stream, _L().mla_decode_no_alloc, ctypes.byref(d), _holds(q_nope, bf16, at, "q_nope", rows * d.qk_nope_dim),
         _holds(q_pe, bf16, at, "q_pe", rows * d.rope_dim), *_cache_ptrs(d, cache, scale_zero, at), cache.shape[0],
         _holds(block_table, i32, at, "block_table", B * max_pages), max_pages,
         _holds(seq_lens, i32, at, "seq_lens", B), B,
         _holds(W_UK, bf16, at, "W_UK", uk), _holds(W_UV, bf16, at, "W_UV", uv), float(softmax_scale), int(num_splits),
         _holds(out, bf16, at, "out", rows * d.v_head_dim),
         None if lse_out is None else _holds(lse_out, torch.float32, at, "lse_out", rows),
-        None if device_status is None else _on(device_status, i32, at, "device_status"), _stream(stream))
+        None if device_status is None else _on(device_status, i32, at, "device_status"))
     _check(st, "mla_decode_no_alloc")
     return out, lse_out
 
@@ -616,25 +617,24 @@ def combine(d: Dims, partial_o: torch.Tensor, partial_lse: torch.Tensor, o_lat_o
         lse_out = _new((B, H), torch.float32, dev, stream)
     at, f32 = _index(partial_o, "partial_o"), torch.float32
     rows = B * d.num_heads
-    st = _L().mla_combine(ctypes.byref(d), _holds(partial_o, f32, at, "partial_o", rows * S * d.kv_lora_rank),
-                          _holds(partial_lse, f32, at, "partial_lse", rows * S), B, S,
-                          _holds(o_lat_out, f32, at, "o_lat_out", rows * d.kv_lora_rank),
-                          _holds(lse_out, f32, at, "lse_out", rows), _stream(stream))
+    st = _call_on(
+        dev, stream, _L().mla_combine, ctypes.byref(d), _holds(partial_o, f32, at, "partial_o", rows * S * d.kv_lora_rank),
+        _holds(partial_lse, f32, at, "partial_lse", rows * S), B, S,
+        _holds(o_lat_out, f32, at, "o_lat_out", rows * d.kv_lora_rank), _holds(lse_out, f32, at, "lse_out", rows))
     _check(st, "mla_combine")
     return o_lat_out, lse_out
 
 
 def read_device_status(workspace: torch.Tensor, stream=None) -> int:
-    v = ctypes.c_int32(0)
-    _check(_L().mla_read_device_status(_ptr(workspace, None, "workspace"), ctypes.byref(v), _stream(stream)),
-           "mla_read_device_status")
+    v, at = ctypes.c_int32(0), _index(workspace, "workspace")
+    p, _ = _workspace(workspace, at)
+    _check(_call_on(workspace.device, stream, _L().mla_read_device_status, p, ctypes.byref(v)), "mla_read_device_status")
     return v.value
 
 
 def read_status_word(word: torch.Tensor, stream=None) -> int:
-    v = ctypes.c_int32(0)
-    _check(_L().mla_read_status_word(_ptr(word, torch.int32, "status word"), ctypes.byref(v), _stream(stream)),
-           "mla_read_status_word")
+    v, p = ctypes.c_int32(0), _on(word, torch.int32, _index(word, "status word"), "status word")
+    _check(_call_on(word.device, stream, _L().mla_read_status_word, p, ctypes.byref(v)), "mla_read_status_word")
     return v.value
 
 

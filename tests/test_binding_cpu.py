@@ -1,5 +1,5 @@
 """CPU checks of what the binding does around a call of the library: the memory
-it allocates, and the tensors it refuses.  Nothing is launched (binding_calls)."""
+it allocates, the tensors it refuses, and the device it calls on.  Nothing is launched (binding_calls)."""
 import pytest
 import torch
 
@@ -81,4 +81,31 @@ def test_sparse_lists_of_more_sequences_than_queries(lib):
     more = C.gpu(C.B + 1, C.TOP_K, dtype=torch.int32)
     with pytest.raises(ValueError):
         mla.decode_sparse(d, **{**tensors, **buffers, **rest, "token_indices": more})
+    assert not lib.calls
+
+
+@pytest.mark.parametrize("entry", ENTRIES + ["read_device_status", "read_status_word"])
+def test_calls_run_on_their_tensors_device(lib, monkeypatch, entry):
+    """With device 0 current, tensors of device 1: the call is made with device 1
+    current, on that device's stream where none is named."""
+    monkeypatch.setattr(C.OnGpu, "at", 1)
+    on = []
+    monkeypatch.setattr(mla, "_call_on", lambda dev, stream, fn, *args: on.append((dev, stream)) or fn(*args, stream))
+    d, calls = C.calls()
+    if entry in calls:
+        tensors, buffers, rest = calls[entry]
+        getattr(mla, entry)(d, **{**tensors, **buffers, **rest})
+    else:
+        getattr(mla, entry)(C.gpu(64, dtype=torch.int32))
+    assert on == [(torch.device("cuda", 1), None)]
+    assert [name for name, _ in lib.calls] == ["mla_" + entry]
+
+
+@pytest.mark.parametrize("entry", ["read_device_status", "read_status_word"])
+def test_a_status_is_read_from_a_tensor(lib, entry):
+    for bad in (None, 7):
+        with pytest.raises(TypeError):
+            getattr(mla, entry)(bad)
+    with pytest.raises(ValueError):
+        getattr(mla, entry)(torch.zeros(4, dtype=torch.int32))
     assert not lib.calls
