@@ -203,9 +203,10 @@ size_t mla_decode_workspace_size(const mla_dims* dims, int32_t batch, int32_t nu
  * values are rounded to multiples of 2^-16, larger ones' saturate at 57,344.
  * Their queries (q_lat and q_pe) are rounded to fp16, then to a sum of two E4M3
  * values with one power of two for 8 heads (16 query rows) or 16: off by at most
- * 2^-8 of the value and 2^-22 of the largest of those heads.  A NaN block makes the
- * query rows that see its row NaN (out and lse) and no others; a query past fp16's
- * range, infinite or NaN its own head.
+ * 2^-8 of the value or 2^-21 of the largest of those heads, whichever is more (from
+ * 2^-12 of that largest on: 2^-9 of the value, and bf16 values are held exactly).  A
+ * NaN block makes the query rows that see its row NaN (out and lse) and no others; a
+ * query past fp16's range, infinite or NaN its own head.
  */
 int mla_decode(const mla_dims* dims, const void* q_nope, const void* q_pe, const void* cache,
                const float* cache_scale_zero, int32_t num_pages, const int32_t* block_table,

@@ -22,9 +22,10 @@
 // and exactly.  The other operands are fp32 values split into FP8 terms that
 // stand side by side in the MMA's N extent (16 heads fill an eighth of it: the
 // MMA's time is its A operand's way through shared memory):
-//   Q: two E4M3 terms, q = 2^-k (hi + lo / 16): off by at most 2^-8 of a value, as
-//      bf16 is (half of that on average), and by at most 2^-22 of the largest of
-//      the 8 or 16 heads that share k
+//   Q: two E4M3 terms, q = 2^-k (hi + lo / 16): off by at most 2^-9 of a fp16 value,
+//      half of what bf16 is, and not at all of a bf16 value, as long as it is above
+//      2^-12 of the largest of the 8 or 16 heads that share k; below, by at most 2^-8
+//      of the value or 2^-21 of that largest
 //   P: three E5M2 terms, hi + mid + lo = the weight's fp16 value, exactly down to
 //      2^-16 of the running maximum and to 2^-26 of it below: as many bits as the
 //      1-byte caches' weights
