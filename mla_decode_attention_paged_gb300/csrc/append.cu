@@ -410,7 +410,12 @@ cudaError_t launch_append(const AppendParams& p, int code, cudaStream_t stream) 
   if (code == kCodeInt8) return launch_pdl(append_kernel<kCodeInt8>, dim3(grid), dim3(warps * 32), 0, stream, 1, p);
   if (code == kCodeE4m3) return launch_pdl(append_kernel<kCodeE4m3>, dim3(grid), dim3(warps * 32), 0, stream, 1, p);
   if (code == kCodeE2m1) {
-    if (p.n_tokens < 2048) return launch_pdl(append_fp4_kernel<false>, dim3(grid), dim3(warps * 32), 0, stream, 1, p);
+    // A token to a warp, or a run of them.  One / runs, us: 1,024 tokens 2.8 / 3.4, 2,048
+    // 3.1 / 3.4, 3,500 3.8 / 4.1, 4,096 4.1 / 4.2, 5,000 5.8 / 4.8, 6,080 5.9 / 4.9, 8,192
+    // 6.1 / 6.8, 12,160 7.6 / 7.0, 14,000 8.3 / 9.0, 18,240 10.2 / 9.2, 34,817 17.0 / 15.7.
+    // Runs take steps, one for each token more to a warp (6,081, 12,161, ...), and up to
+    // 18% more than one token a warp right behind such a step.
+    if (p.n_tokens <= 4096) return launch_pdl(append_fp4_kernel<false>, dim3(grid), dim3(warps * 32), 0, stream, 1, p);
     const int tokens = 8 * p.run;  // of a block
     return launch_pdl(append_fp4_kernel<true>, dim3((p.n_tokens - 1) / tokens + 1), dim3(256), 0, stream, 1, p);
   }

@@ -118,10 +118,10 @@ uint64_t turn_fraction(double f) {
   return uint64_t((p - whole) * 0x1p64) + uint64_t(int64_t((std::fabs(rest) < 0.25 ? rest : std::fmod(rest, 0.25)) * 0x1p64));
 }
 
-// Tokens of a warp of an FP4 append: so many that the blocks of 8 warps, 5 to an SM,
-// are there at once, or in as few rounds as runs of up to 32 tokens allow, all of them
-// full.  Against runs of 4 tokens: 2,048 tokens 5.0 -> 3.5 us, 16,384 11.6 -> 9.2, 34,817
-// 17.3 -> 15.6, 100,000 43.8 -> 39.9 (8,192 tokens 6.4 -> 6.8).
+// Tokens of a warp of an FP4 append of more than 4,096: so many that the blocks of 8
+// warps, 5 to an SM, are there at once, or in as few rounds as runs of up to 32 tokens
+// allow, all of them full.  Against runs of 4 tokens: 6,080 tokens 6.2 -> 4.9 us, 8,192
+// 6.3 -> 6.8, 16,384 11.1 -> 9.2, 34,817 16.7 -> 15.7, 100,000 43.8 -> 39.9.
 int append_run(int n_tokens) {
   const long long warps = 40ll * std::max(1, sm_count()), rounds = (n_tokens - 1) / (32 * warps) + 1;
   return int(std::max(2ll, (n_tokens - 1) / (rounds * warps) + 1));
