@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -205,14 +206,18 @@ def _index(t: torch.Tensor, name: str = "q_nope") -> int:
     return t.get_device()
 
 
-def _weights(d: Dims) -> tuple[int, int]:
-    """Elements of W_UK and of W_UV."""
-    n = d.num_heads * d.kv_lora_rank
-    return n * d.qk_nope_dim, n * d.v_head_dim
+# num_heads, kv_lora_rank, rope_dim, qk_nope_dim, v_head_dim, page_size and cache_dtype of a
+# Dims at once (cheaper than four fields by their names).
+_fields = struct.Struct("=7i").unpack_from
 
 
 def _workspace(t: torch.Tensor, index: int) -> tuple[int, int]:
     """Pointer and bytes of a workspace tensor of any type."""
+    try:
+        if t.get_device() == index and index >= 0 and t.is_contiguous():
+            return t.data_ptr(), t.nbytes
+    except AttributeError:
+        pass
     return _on(t, t.dtype if isinstance(t, torch.Tensor) else None, index, "workspace"), t.nbytes
 
 
@@ -220,19 +225,18 @@ def _workspace(t: torch.Tensor, index: int) -> tuple[int, int]:
 _CODES = {MLA_CACHE_INT8: torch.int8, MLA_CACHE_FP8: torch.uint8, MLA_CACHE_FP4: torch.uint8}
 
 
-def _cache_ptrs(d: Dims, cache: torch.Tensor, scale_zero: torch.Tensor | None, index: int):
+def _cache_ptrs(code: int, page: int, width: int, cache: torch.Tensor, scale_zero: torch.Tensor | None, index: int):
     """Pointers of the cache rows (bf16 values, int8 codes, E4M3 codes, or FP4
     rows) and of their per-token scales (None for bf16 and FP4 caches)."""
-    code = d.cache_dtype
     if code == MLA_CACHE_FP4:
         p, s = _on(cache, torch.uint8, index, "cache"), cache.shape
-        if len(s) != 3 or s[1] != d.page_size or s[2] != FP4_ROW_BYTES:
-            raise ValueError(f"cache must have shape [pages, {d.page_size}, {FP4_ROW_BYTES}], got {list(s)}")
+        if len(s) != 3 or s[1] != page or s[2] != FP4_ROW_BYTES:
+            raise ValueError(f"cache must have shape [pages, {page}, {FP4_ROW_BYTES}], got {list(s)}")
         return p, None
     if code == MLA_CACHE_FP8 and isinstance(cache, torch.Tensor) and cache.dtype == torch.float8_e4m3fn:
         cache = cache.view(torch.uint8)
-    rows = cache.shape[0] * d.page_size
-    p = _holds(cache, _CODES.get(code, torch.bfloat16), index, "cache", rows * (d.kv_lora_rank + d.rope_dim))
+    rows = cache.shape[0] * page
+    p = _holds(cache, _CODES.get(code, torch.bfloat16), index, "cache", rows * width)
     if code == MLA_CACHE_BF16 or scale_zero is None:  # without its scales the library refuses a 1-byte cache
         return p, None
     return p, _holds(scale_zero, torch.float32, index, "scale_zero", rows * (2 if code == MLA_CACHE_INT8 else 1))
@@ -252,14 +256,15 @@ def cache_append(d: Dims, cache: torch.Tensor, scale_zero: torch.Tensor | None, 
                  seq_ids: torch.Tensor, positions: torch.Tensor, c_kv: torch.Tensor, k_pe: torch.Tensor,
                  rope_theta: float = 10000.0, device_status: torch.Tensor | None = None, stream=None) -> None:
     """mla_cache_append: write new tokens' rows into the paged cache (in place)."""
+    _, R, rope, _, _, P, code = _fields(d)
     dev, at, i32, bf16 = cache.device, cache.get_device(), torch.int32, torch.bfloat16
-    cache_p, scale_p = _cache_ptrs(d, cache, scale_zero, at)
+    cache_p, scale_p = _cache_ptrs(code, P, R + rope, cache, scale_zero, at)
     table_p, table = _on(block_table, i32, at, "block_table"), block_table.shape
     ids_p, n = _on(seq_ids, i32, at, "seq_ids"), seq_ids.numel()
     st = _call_on(
         dev, stream, _L().mla_cache_append, ctypes.byref(d), cache_p, scale_p, cache.shape[0], table_p,
         table[0], table[1], ids_p, _holds(positions, i32, at, "positions", n), n,
-        _holds(c_kv, bf16, at, "c_kv", n * d.kv_lora_rank), _holds(k_pe, bf16, at, "k_pe", n * d.rope_dim), float(rope_theta),
+        _holds(c_kv, bf16, at, "c_kv", n * R), _holds(k_pe, bf16, at, "k_pe", n * rope), float(rope_theta),
         None if device_status is None else _on(device_status, i32, at, "device_status"))
     _check(st, "mla_cache_append")
 
@@ -285,24 +290,24 @@ def decode(d: Dims, q_nope, q_pe, cache, scale_zero, block_table, seq_lens, W_UK
 
     If ``workspace`` is None a uint8 buffer of the required size is taken from
     torch's allocator here (the library itself never allocates)."""
+    H, R, rope, nope, vdim, P, code = _fields(d)
     B = q_nope.shape[0]
     dev = q_nope.device
     if workspace is None:
         workspace = _new(decode_workspace_size(d, B, num_splits), torch.uint8, dev, stream)
     if out is None:
-        out = _new((B, d.num_heads, d.v_head_dim), torch.bfloat16, dev, stream)
+        out = _new((B, H, vdim), torch.bfloat16, dev, stream)
     if lse_out is None and want_lse:
-        lse_out = _new((B, d.num_heads), torch.float32, dev, stream)
-    at, i32, bf16 = _index(q_nope), torch.int32, torch.bfloat16
-    rows, max_pages = B * d.num_heads, block_table.shape[1]
-    uk, uv = _weights(d)
+        lse_out = _new((B, H), torch.float32, dev, stream)
+    at, i32, bf16 = q_nope.get_device(), torch.int32, torch.bfloat16
+    rows, max_pages = B * H, block_table.shape[1]
     st = _call_on(
-        dev, stream, _L().mla_decode, ctypes.byref(d), _holds(q_nope, bf16, at, "q_nope", rows * d.qk_nope_dim),
-        _holds(q_pe, bf16, at, "q_pe", rows * d.rope_dim), *_cache_ptrs(d, cache, scale_zero, at), cache.shape[0],
-        _holds(block_table, i32, at, "block_table", B * max_pages), max_pages,
+        dev, stream, _L().mla_decode, ctypes.byref(d), _holds(q_nope, bf16, at, "q_nope", rows * nope),
+        _holds(q_pe, bf16, at, "q_pe", rows * rope), *_cache_ptrs(code, P, R + rope, cache, scale_zero, at),
+        cache.shape[0], _holds(block_table, i32, at, "block_table", B * max_pages), max_pages,
         _holds(seq_lens, i32, at, "seq_lens", B), B,
-        _holds(W_UK, bf16, at, "W_UK", uk), _holds(W_UV, bf16, at, "W_UV", uv), float(softmax_scale), int(num_splits),
-        *_workspace(workspace, at), _holds(out, bf16, at, "out", rows * d.v_head_dim),
+        _holds(W_UK, bf16, at, "W_UK", H * nope * R), _holds(W_UV, bf16, at, "W_UV", H * vdim * R),
+        float(softmax_scale), int(num_splits), *_workspace(workspace, at), _holds(out, bf16, at, "out", rows * vdim),
         None if lse_out is None else _holds(lse_out, torch.float32, at, "lse_out", rows))
     _check(st, "mla_decode")
     return out, lse_out
@@ -323,24 +328,24 @@ def decode_multi(d: Dims, q_nope, q_pe, cache, scale_zero, block_table, seq_lens
     last q_len tokens of each cache, causal among themselves); q_nope bf16
     [B, T, H, 128], q_pe bf16 [B, T, H, 64].  Returns (out bf16 [B, T, H, 128],
     lse fp32 [B, T, H] or None)."""
+    H, R, rope, nope, vdim, P, code = _fields(d)
     B, T = q_nope.shape[0], q_nope.shape[1]
     dev = q_nope.device
     if workspace is None:
         workspace = _new(decode_multi_workspace_size(d, B, T, num_splits), torch.uint8, dev, stream)
     if out is None:
-        out = _new((B, T, d.num_heads, d.v_head_dim), torch.bfloat16, dev, stream)
+        out = _new((B, T, H, vdim), torch.bfloat16, dev, stream)
     if lse_out is None and want_lse:
-        lse_out = _new((B, T, d.num_heads), torch.float32, dev, stream)
-    at, i32, bf16 = _index(q_nope), torch.int32, torch.bfloat16
-    rows, max_pages = B * T * d.num_heads, block_table.shape[1]
-    uk, uv = _weights(d)
+        lse_out = _new((B, T, H), torch.float32, dev, stream)
+    at, i32, bf16 = q_nope.get_device(), torch.int32, torch.bfloat16
+    rows, max_pages = B * T * H, block_table.shape[1]
     st = _call_on(
-        dev, stream, _L().mla_decode_multi, ctypes.byref(d), _holds(q_nope, bf16, at, "q_nope", rows * d.qk_nope_dim),
-        _holds(q_pe, bf16, at, "q_pe", rows * d.rope_dim), *_cache_ptrs(d, cache, scale_zero, at), cache.shape[0],
-        _holds(block_table, i32, at, "block_table", B * max_pages), max_pages,
+        dev, stream, _L().mla_decode_multi, ctypes.byref(d), _holds(q_nope, bf16, at, "q_nope", rows * nope),
+        _holds(q_pe, bf16, at, "q_pe", rows * rope), *_cache_ptrs(code, P, R + rope, cache, scale_zero, at),
+        cache.shape[0], _holds(block_table, i32, at, "block_table", B * max_pages), max_pages,
         _holds(seq_lens, i32, at, "seq_lens", B), B, T,
-        _holds(W_UK, bf16, at, "W_UK", uk), _holds(W_UV, bf16, at, "W_UV", uv), float(softmax_scale), int(num_splits),
-        *_workspace(workspace, at), _holds(out, bf16, at, "out", rows * d.v_head_dim),
+        _holds(W_UK, bf16, at, "W_UK", H * nope * R), _holds(W_UV, bf16, at, "W_UV", H * vdim * R),
+        float(softmax_scale), int(num_splits), *_workspace(workspace, at), _holds(out, bf16, at, "out", rows * vdim),
         None if lse_out is None else _holds(lse_out, torch.float32, at, "lse_out", rows))
     _check(st, "mla_decode_multi")
     return out, lse_out
@@ -362,27 +367,27 @@ def prefill(d: Dims, cache, scale_zero, block_table, seq_lens, c_kv, k_pe, q_nop
     [B, chunk, 512] / k_pe bf16 [B, chunk, 64] into the cache, then attends
     q_nope bf16 [B, chunk, H, 128] / q_pe [B, chunk, H, 64] causally.  Returns
     (out bf16 [B, chunk, H, 128], lse fp32 [B, chunk, H] or None)."""
+    H, R, rope, nope, vdim, P, code = _fields(d)
     B, T = q_nope.shape[0], q_nope.shape[1]
     dev = q_nope.device
     if workspace is None:
         workspace = _new(prefill_workspace_size(d, B, T, num_splits), torch.uint8, dev, stream)
     if out is None:
-        out = _new((B, T, d.num_heads, d.v_head_dim), torch.bfloat16, dev, stream)
+        out = _new((B, T, H, vdim), torch.bfloat16, dev, stream)
     if lse_out is None and want_lse:
-        lse_out = _new((B, T, d.num_heads), torch.float32, dev, stream)
-    at, i32, bf16 = _index(q_nope), torch.int32, torch.bfloat16
-    cache_p, scale_p = _cache_ptrs(d, cache, scale_zero, at)
-    rows, max_pages = B * T * d.num_heads, block_table.shape[1]
-    uk, uv = _weights(d)
+        lse_out = _new((B, T, H), torch.float32, dev, stream)
+    at, i32, bf16 = q_nope.get_device(), torch.int32, torch.bfloat16
+    cache_p, scale_p = _cache_ptrs(code, P, R + rope, cache, scale_zero, at)
+    rows, max_pages = B * T * H, block_table.shape[1]
     st = _call_on(
         dev, stream, _L().mla_prefill, ctypes.byref(d), cache_p, scale_p, cache.shape[0],
         _holds(block_table, i32, at, "block_table", B * max_pages), max_pages,
         _holds(seq_lens, i32, at, "seq_lens", B), B, T,
-        _holds(c_kv, bf16, at, "c_kv", B * T * d.kv_lora_rank), _holds(k_pe, bf16, at, "k_pe", B * T * d.rope_dim),
-        float(rope_theta), _holds(q_nope, bf16, at, "q_nope", rows * d.qk_nope_dim),
-        _holds(q_pe, bf16, at, "q_pe", rows * d.rope_dim), _holds(W_UK, bf16, at, "W_UK", uk),
-        _holds(W_UV, bf16, at, "W_UV", uv), float(softmax_scale), int(num_splits), *_workspace(workspace, at),
-        _holds(out, bf16, at, "out", rows * d.v_head_dim),
+        _holds(c_kv, bf16, at, "c_kv", B * T * R), _holds(k_pe, bf16, at, "k_pe", B * T * rope),
+        float(rope_theta), _holds(q_nope, bf16, at, "q_nope", rows * nope),
+        _holds(q_pe, bf16, at, "q_pe", rows * rope), _holds(W_UK, bf16, at, "W_UK", H * nope * R),
+        _holds(W_UV, bf16, at, "W_UV", H * vdim * R), float(softmax_scale), int(num_splits), *_workspace(workspace, at),
+        _holds(out, bf16, at, "out", rows * vdim),
         None if lse_out is None else _holds(lse_out, torch.float32, at, "lse_out", rows))
     _check(st, "mla_prefill")
     return out, lse_out
@@ -402,24 +407,24 @@ def decode_sparse(d: Dims, q_nope, q_pe, cache, scale_zero, block_table, seq_len
     """mla_decode_sparse: attention over the listed positions of each sequence
     (token_indices int32 [B, top_k], -1 = padding).  Returns (out bf16
     [B, H, 128], lse fp32 [B, H] or None)."""
+    H, R, rope, nope, vdim, P, code = _fields(d)
     B, K = token_indices.shape
     dev = q_nope.device
     if workspace is None:
         workspace = _new(decode_sparse_workspace_size(d, B, K, num_splits), torch.uint8, dev, stream)
     if out is None:
-        out = _new((B, d.num_heads, d.v_head_dim), torch.bfloat16, dev, stream)
+        out = _new((B, H, vdim), torch.bfloat16, dev, stream)
     if lse_out is None and want_lse:
-        lse_out = _new((B, d.num_heads), torch.float32, dev, stream)
-    at, i32, bf16 = _index(q_nope), torch.int32, torch.bfloat16
-    rows, max_pages = B * d.num_heads, block_table.shape[1]
-    uk, uv = _weights(d)
+        lse_out = _new((B, H), torch.float32, dev, stream)
+    at, i32, bf16 = q_nope.get_device(), torch.int32, torch.bfloat16
+    rows, max_pages = B * H, block_table.shape[1]
     st = _call_on(
-        dev, stream, _L().mla_decode_sparse, ctypes.byref(d), _holds(q_nope, bf16, at, "q_nope", rows * d.qk_nope_dim),
-        _holds(q_pe, bf16, at, "q_pe", rows * d.rope_dim), *_cache_ptrs(d, cache, scale_zero, at), cache.shape[0],
-        _holds(block_table, i32, at, "block_table", B * max_pages), max_pages,
+        dev, stream, _L().mla_decode_sparse, ctypes.byref(d), _holds(q_nope, bf16, at, "q_nope", rows * nope),
+        _holds(q_pe, bf16, at, "q_pe", rows * rope), *_cache_ptrs(code, P, R + rope, cache, scale_zero, at),
+        cache.shape[0], _holds(block_table, i32, at, "block_table", B * max_pages), max_pages,
         _holds(seq_lens, i32, at, "seq_lens", B), B, _on(token_indices, i32, at, "token_indices"), K,
-        _holds(W_UK, bf16, at, "W_UK", uk), _holds(W_UV, bf16, at, "W_UV", uv), float(softmax_scale), int(num_splits),
-        *_workspace(workspace, at), _holds(out, bf16, at, "out", rows * d.v_head_dim),
+        _holds(W_UK, bf16, at, "W_UK", H * nope * R), _holds(W_UV, bf16, at, "W_UV", H * vdim * R),
+        float(softmax_scale), int(num_splits), *_workspace(workspace, at), _holds(out, bf16, at, "out", rows * vdim),
         None if lse_out is None else _holds(lse_out, torch.float32, at, "lse_out", rows))
     _check(st, "mla_decode_sparse")
     return out, lse_out
@@ -586,20 +591,21 @@ def decode_no_alloc(d: Dims, q_nope, q_pe, cache, scale_zero, block_table, seq_l
     """mla_decode_no_alloc: mla_decode on the library's fixed scratch array, for
     callers that cannot allocate device memory (outputs are still the
     caller's).  Returns (out, lse)."""
+    H, R, rope, nope, vdim, P, code = _fields(d)
     B = q_nope.shape[0]
     dev = q_nope.device
     if out is None:
-        out = _new((B, d.num_heads, d.v_head_dim), torch.bfloat16, dev, stream)
-    at, i32, bf16 = _index(q_nope), torch.int32, torch.bfloat16
-    rows, max_pages = B * d.num_heads, block_table.shape[1]
-    uk, uv = _weights(d)
+        out = _new((B, H, vdim), torch.bfloat16, dev, stream)
+    at, i32, bf16 = q_nope.get_device(), torch.int32, torch.bfloat16
+    rows, max_pages = B * H, block_table.shape[1]
     st = _call_on(
-        dev, stream, _L().mla_decode_no_alloc, ctypes.byref(d), _holds(q_nope, bf16, at, "q_nope", rows * d.qk_nope_dim),
-        _holds(q_pe, bf16, at, "q_pe", rows * d.rope_dim), *_cache_ptrs(d, cache, scale_zero, at), cache.shape[0],
-        _holds(block_table, i32, at, "block_table", B * max_pages), max_pages,
+        dev, stream, _L().mla_decode_no_alloc, ctypes.byref(d), _holds(q_nope, bf16, at, "q_nope", rows * nope),
+        _holds(q_pe, bf16, at, "q_pe", rows * rope), *_cache_ptrs(code, P, R + rope, cache, scale_zero, at),
+        cache.shape[0], _holds(block_table, i32, at, "block_table", B * max_pages), max_pages,
         _holds(seq_lens, i32, at, "seq_lens", B), B,
-        _holds(W_UK, bf16, at, "W_UK", uk), _holds(W_UV, bf16, at, "W_UV", uv), float(softmax_scale), int(num_splits),
-        _holds(out, bf16, at, "out", rows * d.v_head_dim),
+        _holds(W_UK, bf16, at, "W_UK", H * nope * R), _holds(W_UV, bf16, at, "W_UV", H * vdim * R),
+        float(softmax_scale), int(num_splits),
+        _holds(out, bf16, at, "out", rows * vdim),
         None if lse_out is None else _holds(lse_out, torch.float32, at, "lse_out", rows),
         None if device_status is None else _on(device_status, i32, at, "device_status"))
     _check(st, "mla_decode_no_alloc")
@@ -618,7 +624,8 @@ def combine(d: Dims, partial_o: torch.Tensor, partial_lse: torch.Tensor, o_lat_o
     at, f32 = _index(partial_o, "partial_o"), torch.float32
     rows = B * d.num_heads
     st = _call_on(
-        dev, stream, _L().mla_combine, ctypes.byref(d), _holds(partial_o, f32, at, "partial_o", rows * S * d.kv_lora_rank),
+        dev, stream, _L().mla_combine, ctypes.byref(d),
+        _holds(partial_o, f32, at, "partial_o", rows * S * d.kv_lora_rank),
         _holds(partial_lse, f32, at, "partial_lse", rows * S), B, S,
         _holds(o_lat_out, f32, at, "o_lat_out", rows * d.kv_lora_rank), _holds(lse_out, f32, at, "lse_out", rows))
     _check(st, "mla_combine")
