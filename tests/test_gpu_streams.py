@@ -63,3 +63,28 @@ def test_tensors_made_for_another_stream(cuda_lib, H, as_handle):
         for a, b in zip(got, want[name]):
             if b is not None:
                 assert _stream_of(a) == s.cuda_stream and torch.equal(a, b), name
+
+
+@pytest.mark.parametrize("named", ["current", "stream", "handle"])
+def test_captured_without_buffers(cuda_lib, named):
+    """A call captured with workspace and outputs left to the binding: they are the
+    graph's memory, and each replay gives the eager bits whatever is allocated and
+    filled outside it in between."""
+    calls = _calls(16)
+    want = {name: call(None) for name, (call, _) in calls.items()}
+    torch.cuda.synchronize()
+    for name, (call, size) in calls.items():
+        s = torch.cuda.Stream()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            got = call({"current": None, "stream": s, "handle": s.cuda_stream}[named])
+        for _ in range(3):
+            for t in got:
+                if t is not None:
+                    t.fill_(float("nan"))
+            for _ in range(20):
+                torch.empty(size, dtype=torch.uint8, device="cuda").fill_(0xFF)
+            graph.replay()
+            torch.cuda.synchronize()
+            for a, b in zip(got, want[name]):
+                assert b is None or torch.equal(a, b), name
