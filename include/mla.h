@@ -129,7 +129,9 @@ int mla_check_dims(const mla_dims* dims);
  * with a <= 6 s (byte 0 for a = 0) and code = the E2M1 value nearest to x/s (ties
  * to the even code, the sign of zero kept): off by at most s, and by at most s/4
  * below 2 s.  A block with an infinity or a NaN gets byte 255 and codes of 0.
- * (Their keys are rotated to about 2^-35 and rounded to fp32, then to bf16.)
+ * (Their keys are rotated to about 2^-35 below position 2^26, for the frequencies as
+ * fp64 has them -- the angle's error grows with the position, to 2^-31 at 2^30 -- and
+ * rounded to fp32, then to bf16.)
  *
  *   cache            bf16, int8 or E4M3 (uint8) [num_pages, P, 576], or FP4 rows
  *                    [num_pages, P, MLA_FP4_ROW_BYTES bytes]
@@ -141,7 +143,7 @@ int mla_check_dims(const mla_dims* dims);
  *   device_status    optional int32 (device); if a token's seq id, position
  *                    or page-table entry is out of range the token is
  *                    skipped and MLA_ERR_DEVICE_BOUNDS is stored here.
- * Two tokens mapping to one slot in the same call race (last writer wins).
+ * Two tokens mapping to one slot in the same call race: the row may hold parts of both.
  * n_tokens = 0 is a no-op.
  */
 int mla_cache_append(const mla_dims* dims, void* cache, float* cache_scale_zero, int32_t num_pages,

@@ -31,9 +31,11 @@ __device__ __forceinline__ uint32_t e4m3x2_rn_sat(float first, float second) {
 // rounded, to fp32 and then to bf16: the angle as a 64-bit fraction of a turn (pos
 // times the frequency, modulo 2^64: two integer multiply-adds, where fp64 takes 64
 // times the issue slots of fp32 on this part), sine and cosine from a table of 256
-// angles, each a sum of two floats, and the angle that is left.  None of 8 million
-// blocks had another code than the fp64 rotation so rounded (with fp32 sine and
-// cosine, one value in 10^4).
+// angles, each a sum of two floats, and the angle that is left.  The frequency is the
+// fp64 one, held to about 2^-64 turns, so that the angle is off by as many times the
+// position: 2^-35 radians at 2^26, 2^-31 at 2^30.  None of 8 million blocks had
+// another code than the fp64 rotation so rounded (with fp32 sine and cosine, one
+// value in 10^4).
 struct alignas(16) SinCos {
   float sh, sl, ch, cl;  // sine and cosine as hi + lo
 };

@@ -46,10 +46,13 @@
 // heads (3.3 TB/s), 133 us at 32 (2.5 TB/s, 549 TFLOP/s), 461 us for 128 x 8,192
 // tokens at 128 heads (634 TFLOP/s).  At 16 rows the L1 and shared-memory data pipe
 // bounds it: 3,330 wavefronts a tile (1,900 of loads and stores, 1,424 of the
-// products' operands) in about 3,600 cycles; at 32 rows the chain expansion, QK,
-// softmax, PV through two slots, about 4,700 cycles a tile for 3,980 wavefronts.
+// products' operands) in about 3,600 cycles, of the 1,900 about 990 for the rows'
+// loads, the expanded rows and the weights, the others not looked into one by one;
+// at 32 rows the chain expansion, QK, softmax, PV through two slots, about 4,700
+// cycles a tile for 3,980 wavefronts.
 // Every wait is bounded: on timeout the CTA records MLA_ERR_DEVICE_TIMEOUT,
-// drains, frees its tensor memory and returns.
+// drains, frees its tensor memory and returns.  (The wait of setmaxnreg is not: the
+// launch refuses a build that could not end it.)
 #include <atomic>
 #include <cuda_fp16.h>
 
